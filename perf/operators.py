@@ -185,7 +185,8 @@ def prepare(case, seed):
         n, mix = case["rows"], case["mix"]
         x = torch.randn((n, case["vocab"]), generator=g, device="cuda") * 2.5
         likely = torch.randint(0, case["vocab"], (n, 40), generator=g, device="cuda")
-        x.scatter_(1, likely, torch.rand((n, 40), generator=g, device="cuda") * 12 + 2)
+        # the larger of two values where a place comes twice: a plain scatter would take either
+        x.scatter_reduce_(1, likely, torch.rand((n, 40), generator=g, device="cuda") * 12 + 2, "amax")
         s["logits"] = x.to(dt)
         kinds = [mix if mix != "mixed" else rng.choice(["plain", "nucleus", "top", "least", "all", "greedy"]) for _ in range(n)]
         pick = lambda f, off, *names: [f() if k in names else off for k in kinds]  # noqa: E731
