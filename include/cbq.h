@@ -357,6 +357,174 @@ int cbq_matvec_static(const cbq_weights *W, const float *x_dev, int n, float *y_
 int cbq_weights_get_error(const cbq_weights *W, void *stream, unsigned int *code);
 int cbq_moe_get_error(const cbq_moe *L, void *stream, unsigned int *code);
 
+/* ---- between the products: positions, attention, sampling --------------
+ *
+ * What a verify step needs between its quantized products: the new tokens'
+ * rotary positions and their way into a paged cache, the attention of a tree
+ * of drafted tokens over that cache, and a token from each row of logits.
+ * These calls take no handle: every buffer, the workspace included, is the
+ * caller's, and errors found while a kernel runs are ORed into *err_dev
+ * (a caller's device word, zeroed by the caller; NULL: not reported).  They
+ * run on the current device.  Strides are in elements. */
+
+typedef enum {
+    CBQ_F32 = 0,
+    CBQ_BF16 = 1,
+    CBQ_F16 = 2
+} cbq_dtype;
+
+#define CBQ_DEVERR_BAD_SLOT 0x2u    /* a cache slot or page outside the cache: not written, or not seen */
+#define CBQ_DEVERR_BAD_LENGTH 0x4u  /* a sequence's tokens or length beyond the call's limits: cut to them */
+
+/* A paged cache of keys and values, on the device and the caller's.  Token t
+ * of page p of kv head h has its head_dim values of k at
+ * k + p*page_stride + t*tok_stride + h*head_stride (contiguous), and v alike.
+ * dtype CBQ_BF16 or CBQ_F16; 1 <= head_dim <= 256; page_size >= 1;
+ * n_pages * page_size < 2^31; strides >= 0. */
+typedef struct cbq_kv_cache {
+    void *k;
+    void *v;
+    int dtype;
+    int kv_heads;
+    int head_dim;
+    int page_size;
+    int64_t n_pages;
+    int64_t page_stride;
+    int64_t tok_stride;
+    int64_t head_stride;
+} cbq_kv_cache;
+
+/* How the rotary frequencies are scaled for contexts longer than orig_len. */
+#define CBQ_ROPE_NONE 0
+#define CBQ_ROPE_LINEAR 1
+#define CBQ_ROPE_BY_TURNS 2
+#define CBQ_ROPE_BY_INDEX 3
+/* Which values of the rotated part form pair i: (i, i + rot_dim/2), or
+ * (2i, 2i + 1). */
+#define CBQ_ROPE_HALF 0
+#define CBQ_ROPE_PAIRS 1
+#define CBQ_ROPE_MAX_DIM 1024 /* largest head_dim of cbq_rope */
+
+/* The table of a rotation, on the host: turns_host[i], i < rot_dim/2, is how
+ * many turns pair i makes from one position to the next,
+ *   t_i = base^(-2i/rot_dim) / (2 pi), scaled as `scaling` says:
+ *   NONE      t_i;
+ *   LINEAR    t_i / factor;
+ *   BY_TURNS  g t_i + (1-g) t_i/factor, g = clamp((t_i*orig_len - low) /
+ *             (high - low), 0, 1): pairs that make `high` turns or more over
+ *             orig_len positions stay, those under `low` are divided;
+ *   BY_INDEX  the same mix with g falling linearly in the index i, from 1 at
+ *             floor(i(high)) to 0 at ceil(i(low)), where i(r) is the index
+ *             whose pair makes r turns over orig_len (both ends clamped to
+ *             the table).
+ * In fp64.  The unused parameters of a scaling are ignored.
+ * Errors: EINVAL (null, rot_dim < 2, odd or > CBQ_ROPE_MAX_DIM, base <= 1 or
+ * not finite, factor <= 0, orig_len <= 0, not 0 < low < high). */
+int cbq_rope_turns(int rot_dim, double base, int scaling, double factor, double orig_len, double low, double high,
+                   double *turns_host);
+
+/* Rotary positions of x_dev: n_tok x heads x head_dim of `dtype`, value d of
+ * head h of token t at x_dev + t*x_tok_stride + h*x_head_stride + d; out_dev
+ * alike with its strides.  In each head the pairs (a, b) of the rot_dim
+ * values from rot_off on become
+ *   mscale * (a cos r - b sin r, a sin r + b cos r), r = 2 pi pos_t turns_i,
+ * the other values are copied.  pos_dev: n_tok int32; turns_dev: rot_dim/2
+ * fp64 (cbq_rope_turns).  The angle is reduced to a part of a turn in fp64,
+ * so far positions lose nothing; sine, cosine and the products are fp32,
+ * rounded once to `dtype`.  out_dev may be x_dev (with the same strides);
+ * otherwise the two must not overlap.  One launch on `stream`.
+ * Errors: EINVAL (null; n_tok < 1 or > 2^24; heads < 1 or > 65535; head_dim
+ * < 1 or > CBQ_ROPE_MAX_DIM; rot_dim < 2 or odd; rot_off < 0 or rot_off +
+ * rot_dim > head_dim; an unknown dtype or layout; negative strides, a pointer
+ * not aligned to its type, mscale not finite, in place with other strides),
+ * ECUDA, EDEVICE. */
+int cbq_rope(const void *x_dev, int dtype, int64_t n_tok, int heads, int head_dim, int64_t x_tok_stride,
+             int64_t x_head_stride, const int32_t *pos_dev, const double *turns_dev, int rot_dim, int rot_off,
+             int layout, float mscale, void *out_dev, int64_t out_tok_stride, int64_t out_head_stride, void *stream);
+
+/* New tokens on their way to attention, in one launch: the queries q_dev
+ * (n_tok x q_heads x head_dim) rotated into qout_dev (contiguous, of the
+ * cache's dtype), the keys k_dev (n_tok x kv_heads x head_dim) rotated into
+ * the cache, the values v_dev copied into it; all as cbq_rope, from `dtype`
+ * (any cbq_dtype), rounded once to the cache's.  k_dev and v_dev share their
+ * strides.  slots_dev: n_tok int64, the place of each token in the cache
+ * (page * page_size + token within it); a negative slot writes nothing, one
+ * beyond the cache writes nothing and sets CBQ_DEVERR_BAD_SLOT.  Two tokens
+ * with one slot race.  Errors as cbq_rope (head_dim is the cache's), and
+ * EINVAL for a bad cache. */
+int cbq_rope_append(const void *q_dev, const void *k_dev, const void *v_dev, int dtype, int64_t n_tok, int q_heads,
+                    int64_t q_tok_stride, int64_t q_head_stride, int64_t kv_tok_stride, int64_t kv_head_stride,
+                    const int32_t *pos_dev, const int64_t *slots_dev, const double *turns_dev, int rot_dim,
+                    int rot_off, int layout, float mscale, const cbq_kv_cache *cache, void *qout_dev,
+                    unsigned int *err_dev, void *stream);
+
+#define CBQ_TREE_MAX 64 /* drafted tokens of one sequence per call (bits of a mask) */
+
+/* Bytes of workspace cbq_tree_attention needs for these limits (at least 16;
+ * the same for every content of the device arrays).  Errors: EINVAL (null or
+ * out of the ranges below). */
+int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads,
+                                 int kv_heads, int head_dim, int64_t *bytes);
+
+/* Attention of each sequence's tree of drafted tokens over its paged cache.
+ * Sequence s has ctx_dev[s] committed tokens and the n_s = start_dev[s+1] -
+ * start_dev[s] drafted tokens (packed rows start_dev[s].. of q_dev; n_seq + 1
+ * int32 in start_dev); draft j sits in the cache right behind the committed
+ * ones, at place ctx_dev[s] + j (cbq_rope_append put it there).  Place p of
+ * sequence s is token p % page_size of page table_dev[s*table_width + p /
+ * page_size].  Draft i sees every committed token and those drafts j of its
+ * sequence whose bit j is set in mask_dev[start_dev[s] + i]:
+ *   out[i][h] = sum_p softmax_p(scale * q[i][h].k[p][g]) v[p][g],
+ *   g = h / (q_heads / kv_heads);  lse[i][h] = ln sum_p exp(scale * q.k).
+ * A row that sees nothing gives zeros and -inf.  What a row does not see,
+ * NaN and infinities included, does not touch it.  q_dev: total_tok x q_heads
+ * x head_dim of the cache's dtype, with strides; out_dev: total_tok x q_heads
+ * x head_dim, contiguous, out_dtype the cache's dtype or CBQ_F32; lse_dev:
+ * total_tok x q_heads fp32 or NULL.  Scores, running maxima and sums are
+ * fp32; the weights are rounded to the cache's 16 bits for the product with
+ * v.  max_tok and max_len bound n_s and ctx_dev[s] + n_s: they size the
+ * launch; a sequence beyond them, or beyond its table, is cut to them and
+ * sets CBQ_DEVERR_BAD_LENGTH; a page id outside the cache is not seen and
+ * sets CBQ_DEVERR_BAD_SLOT.  The result does not depend on timing (no
+ * atomics on it) but a row's last bits depend on max_len, by which the work
+ * is split.  ws_dev: 16-byte aligned, ws_bytes at least what
+ * cbq_tree_attention_workspace says, one call at a time.
+ * Errors: EINVAL (null; n_seq < 1 or > 65535; total_tok < 1 or > 2^24;
+ * max_tok outside 1..CBQ_TREE_MAX; max_len < 1 or >= 2^31; kv_heads < 1, > 256
+ * or no divisor of q_heads; q_heads > 1024; table_width < 1; scale not finite; a bad
+ * cache; a workspace too small or misaligned), ECUDA, EDEVICE. */
+int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
+                       const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
+                       const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,
+                       int64_t max_len, float scale, void *out_dev, int out_dtype, float *lse_dev, void *ws_dev,
+                       int64_t ws_bytes, unsigned int *err_dev, void *stream);
+
+#define CBQ_SAMPLE_MAX_V (1 << 18)
+
+/* One token from each of n rows of V logits (row c at logits_dev +
+ * c*row_stride, `dtype` any cbq_dtype) and one given number u in [0,1) per
+ * row.  With l the row's logits, T = temperature[c] and the order "larger
+ * logit first, of equal ones the lower index first":
+ *   w_i = exp((l_i - max l) / T);
+ *   top-k  keeps the first top_k[c] of the order (<= 0 or >= V: all);
+ *   top-p  keeps, of those, the shortest beginning of the order whose mass
+ *          reaches top_p[c] of theirs: i stays while the mass before it is
+ *          below top_p * mass (always the first; >= 1 or NaN: all);
+ *   min-p  keeps, of those, w_i >= min_p[c] (always the first);
+ *   ids[c] = the first index i whose cumulated kept mass, in the order of the
+ *          indices, exceeds u * (kept mass);  probs[c] = w_i / kept mass.
+ * T <= 0 or NaN takes the first of the order, with probability 1.  Logits of
+ * -inf and NaN are never taken; if a row has nothing else, ids[c] = -1 and
+ * probs[c] = 0.  Where +inf occurs only those logits have weight.  Weights
+ * are 2^-45 fixed-point numbers (each within 2^-39 of its value) summed in 64
+ * bits, so sums and choices are the same on every run; a weight under 2^-46
+ * has no mass.  temperature, top_k, top_p and min_p may be NULL (1, all, all,
+ * none); probs_dev may be NULL.  1 <= n <= 65535, 1 <= V <=
+ * CBQ_SAMPLE_MAX_V, row_stride >= V or n == 1, else EINVAL. */
+int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
+               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+               int32_t *ids_dev, float *probs_dev, void *stream);
+
 /* ---- checking entry points (used by the parity tests) ---------------- */
 
 /* Per-block int32 dots s_dev[c][r][b] (n x M x K/32) of W with plain int8

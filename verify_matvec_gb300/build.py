@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libcbq.so")
 OBJDIR = os.path.join(HERE, "_build")
-SOURCES = ["cbq_kernels.cu", "cbq_mmq.cu", "cbq_hc.cu", "cbq_api.cu"]
+SOURCES = ["cbq_kernels.cu", "cbq_mmq.cu", "cbq_hc.cu", "cbq_rope.cu", "cbq_attn.cu", "cbq_sample.cu", "cbq_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-Xptxas", "-v", "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -44,7 +44,8 @@ def _stale() -> bool:
     if not os.path.exists(OUT):
         return True
     t = os.path.getmtime(OUT)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "cbq.h"), __file__]
+    deps = [os.path.join(d, f) for d, _, files in os.walk(CSRC) for f in files]
+    deps += [os.path.join(INCLUDE, "cbq.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

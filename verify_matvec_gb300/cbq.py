@@ -32,10 +32,29 @@ CBQ_MAX_MMQ_COLS = 16
 CBQ_HC_NHC = 4
 CBQ_HC_MAX_ITERS = 1024
 CBQ_HC_MAX_N = 1 << 28
+CBQ_F32, CBQ_BF16, CBQ_F16 = 0, 1, 2
+CBQ_DEVERR_BAD_SLOT = 0x2
+CBQ_DEVERR_BAD_LENGTH = 0x4
+CBQ_ROPE_NONE, CBQ_ROPE_LINEAR, CBQ_ROPE_BY_TURNS, CBQ_ROPE_BY_INDEX = 0, 1, 2, 3
+CBQ_ROPE_HALF, CBQ_ROPE_PAIRS = 0, 1
+CBQ_ROPE_MAX_DIM = 1024
+CBQ_TREE_MAX = 64
+CBQ_SAMPLE_MAX_V = 1 << 18
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
+_F = ctypes.c_float
+_D = ctypes.c_double
+
+
+class cbq_kv_cache(ctypes.Structure):
+    """The C struct of the same name: a paged cache of keys and values."""
+    _fields_ = [("k", _P), ("v", _P), ("dtype", _I), ("kv_heads", _I), ("head_dim", _I), ("page_size", _I),
+                ("n_pages", _I64), ("page_stride", _I64), ("tok_stride", _I64), ("head_stride", _I64)]
+
+
+_KV = ctypes.POINTER(cbq_kv_cache)
 _SIGS = {
     "cbq_status_string": ([_I], ctypes.c_char_p),
     "cbq_last_cuda_error": ([], ctypes.c_char_p),
@@ -67,6 +86,14 @@ _SIGS = {
     "cbq_moe_debug_block_dots": ([_P, _I, _I, _P, _I, _P, _P], _I),
     "cbq_moe_set_debug": ([_P, _I], _I),
     "cbq_moe_set_stage_events": ([_P, _P, _P, _P], _I),
+    "cbq_rope_turns": ([_I, _D, _I, _D, _D, _D, _D, _P], _I),
+    "cbq_rope": ([_P, _I, _I64, _I, _I, _I64, _I64, _P, _P, _I, _I, _I, _F, _P, _I64, _I64, _P], _I),
+    "cbq_rope_append": ([_P, _P, _P, _I, _I64, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _I, _I, _I, _F, _KV, _P, _P,
+                         _P], _I),
+    "cbq_tree_attention_workspace": ([_I, _I64, _I, _I64, _I, _I, _I, ctypes.POINTER(_I64)], _I),
+    "cbq_tree_attention": ([_P, _I64, _I64, _I, _I64, _KV, _P, _I, _I, _P, _P, _P, _I, _I64, _F, _P, _I, _P, _P, _I64,
+                            _P, _P], _I),
+    "cbq_sample": ([_P, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "cbq_moe_debug_intermediate": ([_P, _I, _P, _P, _P, _P], _I),
 }
 
@@ -498,3 +525,178 @@ def cbq_debug_mmq_block_dots(W: Weights, qx, stream=None):
     _check(load().cbq_debug_mmq_block_dots(W.handle, _dev_ptr(qx, torch.int8, "qx"), n,
                                            _dev_ptr(s, torch.int32, "s"), _stream(stream)), "cbq_debug_mmq_block_dots")
     return s
+
+
+# ------------------------------------- positions, attention, sampling --
+
+_SCALINGS = {"none": CBQ_ROPE_NONE, "linear": CBQ_ROPE_LINEAR, "turns": CBQ_ROPE_BY_TURNS, "index": CBQ_ROPE_BY_INDEX}
+_LAYOUTS = {"half": CBQ_ROPE_HALF, "pairs": CBQ_ROPE_PAIRS}
+
+
+def _dtype(t, name):
+    torch = _torch()
+    code = {torch.float32: CBQ_F32, torch.bfloat16: CBQ_BF16, torch.float16: CBQ_F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _heads_ptr(t, name):
+    """Pointer of a CUDA tensor (tokens, heads, dim) whose last axis is contiguous."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be (tokens, heads, dim) with a contiguous last axis")
+    return t.data_ptr()
+
+
+def _cache(kc, vc):
+    """cbq_kv_cache of two CUDA tensors (pages, page_size, kv_heads, dim)."""
+    if not kc.is_cuda or not vc.is_cuda or kc.dtype != vc.dtype:
+        raise TypeError("kc and vc must be CUDA tensors of one dtype")
+    if kc.dim() != 4 or kc.shape != vc.shape or kc.stride() != vc.stride():
+        raise ValueError("kc and vc must be (pages, page_size, kv_heads, dim) of one shape and strides")
+    pages, page, heads, dim = kc.shape
+    sp, st, sh, sd = kc.stride()
+    if sd != 1 and dim != 1:
+        raise ValueError("the cache's last axis must be contiguous")
+    return cbq_kv_cache(kc.data_ptr(), vc.data_ptr(), _dtype(kc, "kc"), heads, dim, page, pages, sp, st, sh)
+
+
+def _opt_ptr(t, dtype, n, name):
+    """Pointer of an optional contiguous CUDA tensor of n values (None: null)."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} values")
+    return _dev_ptr(t, dtype, name)
+
+
+def cbq_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                   orig_len: float = 0.0, low: float = 1.0, high: float = 32.0, device=None):
+    """The fp64 table of a rotation (rot_dim/2 turns a position) on `device`
+    (default: the current CUDA device); scaling "none", "linear", "turns" or
+    "index"."""
+    torch = _torch()
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    t = np.empty(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    _check(load().cbq_rope_turns(int(rot_dim), base, _SCALINGS[scaling], factor, orig_len, low, high,
+                                 t.ctypes.data_as(_P)), "cbq_rope_turns")
+    return torch.from_numpy(t).to("cuda" if device is None else device)
+
+
+def cbq_rope(x, pos, turns, rot_off: int = 0, layout: str = "half", mscale: float = 1.0, out=None, stream=None):
+    """Rotary positions of x (tokens, heads, dim): 2 * len(turns) values of
+    each head from rot_off on turn, the others are copied; pos (tokens) int32,
+    turns fp64 (cbq_rope_turns).  out may be x."""
+    torch = _torch()
+    n, heads, dim = x.shape
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and dtype of x")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+    _check(load().cbq_rope(_heads_ptr(x, "x"), _dtype(x, "x"), n, heads, dim, x.stride(0), x.stride(1),
+                           _opt_ptr(pos, torch.int32, n, "pos"), _dev_ptr(turns, torch.float64, "turns"),
+                           2 * turns.numel(), rot_off, _LAYOUTS[layout], mscale, _heads_ptr(out, "out"),
+                           out.stride(0), out.stride(1), _stream(stream)), "cbq_rope")
+    return out
+
+
+def cbq_rope_append(q, k, v, pos, slots, turns, kc, vc, rot_off: int = 0, layout: str = "half", mscale: float = 1.0,
+                    out=None, err=None, stream=None):
+    """New tokens' q (tokens, q_heads, dim) rotated (returned, in the cache's
+    dtype), their k rotated and v copied into the paged cache kc, vc (pages,
+    page_size, kv_heads, dim) at slots (tokens) int64 (negative: not written).
+    err: an optional int32 tensor of one value for the CBQ_DEVERR_* bits."""
+    torch = _torch()
+    n, heads, dim = q.shape
+    c = _cache(kc, vc)
+    if k.shape != (n, c.kv_heads, dim) or v.shape != k.shape or dim != c.head_dim:
+        raise ValueError("k and v must be (tokens, kv_heads, dim) as the cache, dim as q")
+    if k.stride() != v.stride() or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one dtype, and k and v one set of strides")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=kc.dtype, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _check(load().cbq_rope_append(_heads_ptr(q, "q"), _heads_ptr(k, "k"), _heads_ptr(v, "v"), _dtype(q, "q"), n, heads,
+                                  q.stride(0), q.stride(1), k.stride(0), k.stride(1),
+                                  _opt_ptr(pos, torch.int32, n, "pos"), _opt_ptr(slots, torch.int64, n, "slots"),
+                                  _dev_ptr(turns, torch.float64, "turns"), 2 * turns.numel(), rot_off,
+                                  _LAYOUTS[layout], mscale, ctypes.byref(c), _dev_ptr(out, kc.dtype, "out"),
+                                  _opt_ptr(err, torch.int32, 1, "err"), _stream(stream)), "cbq_rope_append")
+    return out
+
+
+def cbq_tree_attention_workspace(n_seq: int, total_tok: int, max_tok: int, max_len: int, q_heads: int, kv_heads: int,
+                                 head_dim: int) -> int:
+    """Bytes of workspace of cbq_tree_attention for these limits."""
+    b = ctypes.c_int64()
+    _check(load().cbq_tree_attention_workspace(n_seq, total_tok, max_tok, max_len, q_heads, kv_heads, head_dim,
+                                               ctypes.byref(b)), "cbq_tree_attention_workspace")
+    return b.value
+
+
+def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len: int, scale: float | None = None,
+                       out=None, with_lse: bool = False, workspace=None, err=None, stream=None):
+    """Attention of each sequence's drafted tokens, packed in q (tokens,
+    q_heads, dim), over its committed tokens and those drafts its mask names,
+    in the paged cache kc, vc: table (sequences, width) int32 page ids, ctx
+    (sequences) int32 committed lengths, start (sequences + 1) int32 first rows,
+    mask (tokens) int64 bits.  scale: dim ** -0.5 if None.  Returns out, or
+    (out, lse) with with_lse.  workspace: a uint8 tensor of
+    cbq_tree_attention_workspace bytes (allocated when None)."""
+    torch = _torch()
+    n, heads, dim = q.shape
+    c = _cache(kc, vc)
+    if q.dtype != kc.dtype or dim != c.head_dim:
+        raise ValueError("q must have the cache's dtype and dim")
+    n_seq, width = table.shape
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out must be a contiguous CUDA tensor of the shape of q")
+    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if with_lse else None
+    if workspace is None:
+        workspace = torch.empty(cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim),
+                                dtype=torch.uint8, device=q.device)
+    _check(load().cbq_tree_attention(_heads_ptr(q, "q"), q.stride(0), q.stride(1), heads, n, ctypes.byref(c),
+                                     _dev_ptr(table, torch.int32, "table"), width, n_seq,
+                                     _opt_ptr(ctx, torch.int32, n_seq, "ctx"),
+                                     _opt_ptr(start, torch.int32, n_seq + 1, "start"),
+                                     _opt_ptr(mask, torch.int64, n, "mask"), max_tok, max_len,
+                                     dim ** -0.5 if scale is None else scale, out.data_ptr(), _dtype(out, "out"),
+                                     None if lse is None else lse.data_ptr(),
+                                     _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                     _opt_ptr(err, torch.int32, 1, "err"), _stream(stream)), "cbq_tree_attention")
+    return (out, lse) if with_lse else out
+
+
+def cbq_sample(logits, temperature, top_k, top_p, min_p, u, ids=None, probs=None, stream=None):
+    """One token from each row of logits (rows, V): temperature, top_p, min_p
+    and u (rows) fp32, top_k (rows) int32, each but u may be None.  Returns
+    ids int32 and the drawn tokens' probabilities among the kept ones."""
+    torch = _torch()
+    n, V = logits.shape
+    if not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.stride(1) != 1 and V != 1:
+        raise ValueError("logits must have a contiguous last axis")
+    if u is None:
+        raise ValueError("u must be given")
+    if ids is None:
+        ids = torch.empty(n, dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(n, dtype=torch.float32, device=logits.device)
+    f = torch.float32
+    _check(load().cbq_sample(logits.data_ptr(), _dtype(logits, "logits"), n, V, logits.stride(0),
+                             _opt_ptr(temperature, f, n, "temperature"), _opt_ptr(top_k, torch.int32, n, "top_k"),
+                             _opt_ptr(top_p, f, n, "top_p"), _opt_ptr(min_p, f, n, "min_p"), _opt_ptr(u, f, n, "u"),
+                             _opt_ptr(ids, torch.int32, n, "ids"), _opt_ptr(probs, f, n, "probs"), _stream(stream)),
+           "cbq_sample")
+    return ids, probs

@@ -4,10 +4,12 @@
 // cbq_kernels.cu.
 #include "cbq.h"
 #include "cbq_internal.h"
+#include "step/cbq_step.h"
 
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -712,6 +714,182 @@ int cbq_moe_debug_stall(cbq_moe *L, int mode) {
 int cbq_debug_mmq_stall(cbq_weights *W, int mode) {
     if (!W || mode < 0 || mode > 1) return CBQ_EINVAL;
     W->mq_stall = mode;
+    return CBQ_OK;
+}
+
+// ------------------------- positions, attention, sampling (no handle) ------
+
+namespace {
+
+bool known_dtype(int d) { return d == CBQ_F32 || d == CBQ_BF16 || d == CBQ_F16; }
+size_t dtype_bytes(int d) { return d == CBQ_F32 ? 4 : 2; }
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+bool good_cache(const cbq_kv_cache *c) {
+    return c && c->k && c->v && (c->dtype == CBQ_BF16 || c->dtype == CBQ_F16) && c->kv_heads >= 1 &&
+           c->kv_heads <= 256 && c->head_dim >= 1 && c->head_dim <= 256 && c->page_size >= 1 && c->n_pages >= 1 &&
+           c->n_pages <= INT32_MAX / c->page_size && c->page_stride >= 0 && c->tok_stride >= 0 &&
+           c->head_stride >= 0 && aligned_to(c->k, 2) && aligned_to(c->v, 2);
+}
+
+bool good_rotation(const cbq::Rotation &r, int dim) {
+    return r.pos && r.turns && aligned_to(r.pos, 4) && aligned_to(r.turns, 8) && r.rot >= 2 && r.rot % 2 == 0 &&
+           r.off >= 0 && r.off <= dim - r.rot && (r.layout == CBQ_ROPE_HALF || r.layout == CBQ_ROPE_PAIRS) &&
+           std::isfinite(r.mscale);
+}
+
+}  // namespace
+
+int cbq_rope_turns(int rot_dim, double base, int scaling, double factor, double orig_len, double low, double high,
+                   double *turns_host) {
+    if (!turns_host || rot_dim < 2 || rot_dim % 2 || rot_dim > CBQ_ROPE_MAX_DIM || !(base > 1.0) ||
+        !std::isfinite(base) || scaling < CBQ_ROPE_NONE || scaling > CBQ_ROPE_BY_INDEX)
+        return CBQ_EINVAL;
+    if (scaling != CBQ_ROPE_NONE && !(factor > 0.0 && std::isfinite(factor))) return CBQ_EINVAL;
+    const bool mixed = scaling == CBQ_ROPE_BY_TURNS || scaling == CBQ_ROPE_BY_INDEX;
+    if (mixed && !(orig_len > 0.0 && std::isfinite(orig_len) && low > 0.0 && high > low && std::isfinite(high)))
+        return CBQ_EINVAL;
+    constexpr double kTwoPi = 6.283185307179586476925;
+    const int half = rot_dim / 2;
+    double first = 0.0, last = 0.0;  // BY_INDEX: the part that stays falls from 1 to 0 between these indices
+    if (scaling == CBQ_ROPE_BY_INDEX) {
+        const double step = std::log(base) / half;  // ln of the ratio of neighbouring frequencies
+        first = std::max(std::floor(std::log(orig_len / (high * kTwoPi)) / step), 0.0);
+        last = std::min(std::ceil(std::log(orig_len / (low * kTwoPi)) / step), half - 1.0);
+    }
+    for (int i = 0; i < half; ++i) {
+        const double t = std::pow(base, -(double)i / half) / kTwoPi;
+        double keep = scaling == CBQ_ROPE_NONE ? 1.0 : 0.0;
+        if (scaling == CBQ_ROPE_BY_TURNS) keep = (t * orig_len - low) / (high - low);
+        if (scaling == CBQ_ROPE_BY_INDEX) keep = 1.0 - (i - first) / std::max(last - first, 1e-3);
+        keep = std::min(std::max(keep, 0.0), 1.0);
+        turns_host[i] = scaling == CBQ_ROPE_NONE ? t : t * keep + t / factor * (1.0 - keep);
+    }
+    return CBQ_OK;
+}
+
+int cbq_rope(const void *x_dev, int dtype, int64_t n_tok, int heads, int head_dim, int64_t x_tok_stride,
+             int64_t x_head_stride, const int32_t *pos_dev, const double *turns_dev, int rot_dim, int rot_off,
+             int layout, float mscale, void *out_dev, int64_t out_tok_stride, int64_t out_head_stride, void *stream) {
+    const cbq::Rotation r = {pos_dev, turns_dev, rot_dim, rot_off, layout, mscale};
+    if (!x_dev || !out_dev || !known_dtype(dtype) || n_tok < 1 || n_tok > (1 << 24) || heads < 1 || heads > 65535 ||
+        head_dim < 1 || head_dim > CBQ_ROPE_MAX_DIM || x_tok_stride < 0 || x_head_stride < 0 || out_tok_stride < 0 ||
+        out_head_stride < 0 || !good_rotation(r, head_dim) || !aligned_to(x_dev, dtype_bytes(dtype)) ||
+        !aligned_to(out_dev, dtype_bytes(dtype)))
+        return CBQ_EINVAL;
+    if (x_dev == out_dev && (x_tok_stride != out_tok_stride || x_head_stride != out_head_stride)) return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    CBQ_CUDA(cbq::launch_rope({const_cast<void *>(x_dev), x_tok_stride, x_head_stride},
+                              {out_dev, out_tok_stride, out_head_stride}, dtype, n_tok, heads, head_dim, r,
+                              as_stream(stream)));
+    return CBQ_OK;
+}
+
+int cbq_rope_append(const void *q_dev, const void *k_dev, const void *v_dev, int dtype, int64_t n_tok, int q_heads,
+                    int64_t q_tok_stride, int64_t q_head_stride, int64_t kv_tok_stride, int64_t kv_head_stride,
+                    const int32_t *pos_dev, const int64_t *slots_dev, const double *turns_dev, int rot_dim,
+                    int rot_off, int layout, float mscale, const cbq_kv_cache *cache, void *qout_dev,
+                    unsigned int *err_dev, void *stream) {
+    const cbq::Rotation r = {pos_dev, turns_dev, rot_dim, rot_off, layout, mscale};
+    if (!good_cache(cache) || !q_dev || !k_dev || !v_dev || !slots_dev || !qout_dev || !known_dtype(dtype) ||
+        n_tok < 1 || n_tok > (1 << 24) || q_heads < 1 || q_heads > 65535 || q_tok_stride < 0 || q_head_stride < 0 ||
+        kv_tok_stride < 0 || kv_head_stride < 0 || !good_rotation(r, cache->head_dim) || !aligned_to(slots_dev, 8) ||
+        !aligned_to(q_dev, dtype_bytes(dtype)) || !aligned_to(k_dev, dtype_bytes(dtype)) ||
+        !aligned_to(v_dev, dtype_bytes(dtype)) || !aligned_to(qout_dev, 2) || !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const int64_t dim = cache->head_dim;
+    CBQ_CUDA(cbq::launch_rope_append({const_cast<void *>(q_dev), q_tok_stride, q_head_stride},
+                                     {const_cast<void *>(k_dev), kv_tok_stride, kv_head_stride},
+                                     {const_cast<void *>(v_dev), kv_tok_stride, kv_head_stride},
+                                     {qout_dev, q_heads * dim, dim}, dtype, n_tok, q_heads, slots_dev, *cache, r,
+                                     err_dev, as_stream(stream)));
+    return CBQ_OK;
+}
+
+namespace {
+
+bool good_tree_limits(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
+                      int head_dim) {
+    return n_seq >= 1 && n_seq <= 65535 && total_tok >= 1 && total_tok <= (1 << 24) && max_tok >= 1 &&
+           max_tok <= CBQ_TREE_MAX && max_len >= 1 && max_len <= INT32_MAX && kv_heads >= 1 && kv_heads <= 256 &&
+           q_heads >= kv_heads && q_heads <= 1024 && q_heads % kv_heads == 0 && head_dim >= 1 && head_dim <= 256;
+}
+
+}  // namespace
+
+int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads,
+                                 int kv_heads, int head_dim, int64_t *bytes) {
+    if (!bytes || !good_tree_limits(n_seq, total_tok, max_tok, max_len, q_heads, kv_heads, head_dim))
+        return CBQ_EINVAL;
+    *bytes = (int64_t)cbq::tree_attention_workspace(n_seq, total_tok, max_tok, max_len, q_heads, kv_heads, head_dim);
+    return CBQ_OK;
+}
+
+int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
+                       const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
+                       const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,
+                       int64_t max_len, float scale, void *out_dev, int out_dtype, float *lse_dev, void *ws_dev,
+                       int64_t ws_bytes, unsigned int *err_dev, void *stream) {
+    if (!good_cache(cache) ||
+        !good_tree_limits(n_seq, total_tok, max_tok, max_len, q_heads, cache->kv_heads, cache->head_dim))
+        return CBQ_EINVAL;
+    const size_t need = cbq::tree_attention_workspace(n_seq, total_tok, max_tok, max_len, q_heads, cache->kv_heads,
+                                                      cache->head_dim);
+    if (!q_dev || !table_dev || !ctx_dev || !start_dev || !mask_dev || !out_dev || !ws_dev || q_tok_stride < 0 ||
+        q_head_stride < 0 || table_width < 1 || !std::isfinite(scale) ||
+        (out_dtype != cache->dtype && out_dtype != CBQ_F32) || !aligned16(ws_dev) || ws_bytes < (int64_t)need ||
+        !aligned_to(q_dev, 2) || !aligned_to(out_dev, dtype_bytes(out_dtype)) || !aligned_to(table_dev, 4) ||
+        !aligned_to(ctx_dev, 4) || !aligned_to(start_dev, 4) || !aligned_to(mask_dev, 8) || !aligned_to(lse_dev, 4) ||
+        !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    cbq::TreeAttention a = {};
+    a.q = q_dev;
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.q_heads = q_heads;
+    a.total_tok = total_tok;
+    a.c = *cache;
+    a.table = table_dev;
+    a.table_width = table_width;
+    a.n_seq = n_seq;
+    a.ctx = ctx_dev;
+    a.start = start_dev;
+    a.mask = mask_dev;
+    a.max_tok = max_tok;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.out = out_dev;
+    a.out_f32 = out_dtype == CBQ_F32;
+    a.lse = lse_dev;
+    a.ws = ws_dev;
+    a.err = err_dev;
+    CBQ_CUDA(cbq::launch_tree_attention(a, as_stream(stream)));
+    return CBQ_OK;
+}
+
+int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
+               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+               int32_t *ids_dev, float *probs_dev, void *stream) {
+    if (!logits_dev || !u_dev || !ids_dev || !known_dtype(dtype) || n < 1 || n > 65535 || V < 1 ||
+        V > CBQ_SAMPLE_MAX_V || row_stride < 0 || (n > 1 && row_stride < V) ||
+        !aligned_to(logits_dev, dtype_bytes(dtype)) || !aligned_to(temperature_dev, 4) || !aligned_to(top_k_dev, 4) ||
+        !aligned_to(top_p_dev, 4) || !aligned_to(min_p_dev, 4) || !aligned_to(u_dev, 4) || !aligned_to(ids_dev, 4) ||
+        !aligned_to(probs_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const cbq::Sample a = {logits_dev, dtype,     n,         V,     row_stride, temperature_dev,
+                           top_k_dev,  top_p_dev, min_p_dev, u_dev, ids_dev,    probs_dev};
+    CBQ_CUDA(cbq::launch_sample(a, as_stream(stream)));
     return CBQ_OK;
 }
 
