@@ -458,7 +458,8 @@ int cbq_rope_append(const void *q_dev, const void *k_dev, const void *v_dev, int
                     int rot_off, int layout, float mscale, const cbq_kv_cache *cache, void *qout_dev,
                     unsigned int *err_dev, void *stream);
 
-#define CBQ_TREE_MAX 64 /* drafted tokens of one sequence per call (bits of a mask) */
+#define CBQ_TREE_MAX 64             /* drafted tokens of one sequence per call (bits of a mask) */
+#define CBQ_TREE_MAX_LEN (1 << 30)  /* largest max_len */
 
 /* Bytes of workspace cbq_tree_attention needs for these limits (at least 16;
  * the same for every content of the device arrays).  Errors: EINVAL (null or
@@ -490,8 +491,8 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
  * is split.  ws_dev: 16-byte aligned, ws_bytes at least what
  * cbq_tree_attention_workspace says, one call at a time.
  * Errors: EINVAL (null; n_seq < 1 or > 65535; total_tok < 1 or > 2^24;
- * max_tok outside 1..CBQ_TREE_MAX; max_len < 1 or >= 2^31; kv_heads < 1, > 256
- * or no divisor of q_heads; q_heads > 1024; table_width < 1; scale not finite; a bad
+ * max_tok outside 1..CBQ_TREE_MAX; max_len outside 1..CBQ_TREE_MAX_LEN;
+ * kv_heads < 1, > 256 or no divisor of q_heads; q_heads > 1024; table_width < 1; scale not finite; a bad
  * cache; a workspace too small or misaligned), ECUDA, EDEVICE. */
 int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
                        const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,

@@ -63,7 +63,7 @@ def test_tree_attention_refusals(lib):
                 max_tok=3, max_len=8, scale=1.0, out=P(0x20000), out_dtype=1, lse=None, ws=A, ws_bytes=1 << 40,
                 err=None, stream=None)
     limits = [dict(heads=0), dict(heads=3), dict(heads=1026), dict(total=0), dict(total=(1 << 24) + 1), dict(n_seq=0),
-              dict(n_seq=65536), dict(max_tok=0), dict(max_tok=65), dict(max_len=0), dict(max_len=1 << 31)]
+              dict(n_seq=65536), dict(max_tok=0), dict(max_tok=65), dict(max_len=0), dict(max_len=(1 << 30) + 1)]
     _refused(lib.cbq_tree_attention, good, limits + [
         dict(q=None), dict(table=None), dict(ctx=None), dict(start=None), dict(mask=None), dict(out=None),
         dict(ws=None), dict(cache=None), dict(qt=-1), dict(qh=-1), dict(width=0), dict(scale=math.inf),

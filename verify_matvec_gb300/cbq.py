@@ -39,6 +39,7 @@ CBQ_ROPE_NONE, CBQ_ROPE_LINEAR, CBQ_ROPE_BY_TURNS, CBQ_ROPE_BY_INDEX = 0, 1, 2, 
 CBQ_ROPE_HALF, CBQ_ROPE_PAIRS = 0, 1
 CBQ_ROPE_MAX_DIM = 1024
 CBQ_TREE_MAX = 64
+CBQ_TREE_MAX_LEN = 1 << 30
 CBQ_SAMPLE_MAX_V = 1 << 18
 
 _P = ctypes.c_void_p

@@ -816,7 +816,7 @@ namespace {
 bool good_tree_limits(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
                       int head_dim) {
     return n_seq >= 1 && n_seq <= 65535 && total_tok >= 1 && total_tok <= (1 << 24) && max_tok >= 1 &&
-           max_tok <= CBQ_TREE_MAX && max_len >= 1 && max_len <= INT32_MAX && kv_heads >= 1 && kv_heads <= 256 &&
+           max_tok <= CBQ_TREE_MAX && max_len >= 1 && max_len <= CBQ_TREE_MAX_LEN && kv_heads >= 1 && kv_heads <= 256 &&
            q_heads >= kv_heads && q_heads <= 1024 && q_heads % kv_heads == 0 && head_dim >= 1 && head_dim <= 256;
 }
 

@@ -1,4 +1,16 @@
 // cbq_attn.cu -- attention of a tree of drafted tokens over a paged cache.
+//
+// For each sequence and kv head the rows are its drafted tokens times the
+// query heads of the group, R = n G of them, and all of them read the same
+// keys: one pass over K and V serves every row,
+//   o = sum_p 2^(x_p - m) v_p / sum_p 2^(x_p - m),  x = scale log2(e) q.k,
+// with the running maximum m and the running sum kept per row while the keys
+// stream by (each new maximum scales what was summed before).  The keys are
+// cut into chunks, a block each, so that a few sequences fill the GPU; a
+// second kernel joins the chunks' (m, sum, o) of a row.
+#include <algorithm>
+#include <type_traits>
+
 #include "cbq_device.cuh"
 #include "step/cbq_step.h"
 #include "step/cbq_types.cuh"
@@ -8,32 +20,48 @@ namespace cbq {
 namespace {
 
 constexpr int kMaxDim = 256;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
-// One warp per (token, head): the lanes hold the head's values, a key at a
-// time, the running maximum and sum of the softmax beside the weighted sum.
-// grid (q_heads, max_tok, n_seq).
-template <typename T>
-__global__ void __launch_bounds__(32) k_tree_attention(TreeAttention a) {
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x, h = blockIdx.x, i = blockIdx.y, s = blockIdx.z, D = a.c.head_dim;
+// What a block needs to know of a sequence, with everything out of range cut.
+struct Seq {
+    int64_t row0;  // its first row of q
+    int n, ctx, len;
+};
+
+__device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool report) {
     const int64_t room = (int64_t)a.table_width * a.c.page_size;
     const int64_t b0 = a.start[s], b1 = a.start[s + 1];
     const int64_t most = a.max_len < room ? a.max_len : room;
     int64_t n = b1 - b0, ctx = a.ctx[s];
-    bool cut = b0 < 0 || b1 > a.total_tok || n < 0 || n > a.max_tok || ctx < 0;
-    if (b0 < 0 || b1 > a.total_tok || n < 0) n = 0;
+    bool cut = n > a.max_tok || ctx < 0;
+    if (b0 < 0 || b1 > a.total_tok || n < 0) {
+        n = 0;
+        cut = true;
+    }
     if (n > a.max_tok) n = a.max_tok;
     if (ctx < 0) ctx = 0;
-    int64_t len = ctx + n;
-    if (len > most) {
-        cut = true;
-        len = most;
-    }
-    if (cut && a.err && lane == 0) atomicOr(a.err, CBQ_DEVERR_BAD_LENGTH);
-    if (i >= n) return;
-    const int64_t row = b0 + i;
-    const uint64_t mask = (uint64_t)a.mask[row];
+    cut |= ctx + n > most;
+    if (cut && report && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_LENGTH);
+    return Seq{b0, (int)n, (int)(ctx < most ? ctx : most), (int)(ctx + n < most ? ctx + n : most)};
+}
+
+// Bits of the drafts that row's token sees, none beyond the sequence's own.
+__device__ __forceinline__ uint64_t seen_drafts(const TreeAttention &a, const Seq &q, int64_t row) {
+    const int k = q.len - q.ctx;
+    return (uint64_t)a.mask[row] & (k >= 64 ? ~0ull : (1ull << k) - 1);
+}
+
+// Any head size and any strides: one warp per (token, head), the lanes hold
+// the head's values, a key at a time.  grid (q_heads, max_tok, n_seq).
+template <typename T>
+__global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x, h = blockIdx.x, i = blockIdx.y, s = blockIdx.z, D = a.c.head_dim;
+    const Seq sq = sequence(a, s, lane == 0 && h == 0 && i == 0);
+    if (i >= sq.n) return;
+    const int64_t row = sq.row0 + i;
+    const uint64_t mask = seen_drafts(a, sq, row);
     const T *q = static_cast<const T *>(a.q) + row * a.q_tok + h * a.q_head;
     const int g = h / (a.q_heads / a.c.kv_heads);
     float qv[kMaxDim / 32], acc[kMaxDim / 32];
@@ -43,8 +71,8 @@ __global__ void __launch_bounds__(32) k_tree_attention(TreeAttention a) {
         qv[j] = j * 32 + lane < D ? to_f32(q[j * 32 + lane]) : 0.0f;
     }
     float top = -INFINITY, sum = 0.0f;
-    for (int64_t p = 0; p < len; ++p) {
-        if (p >= ctx && !(mask >> (p - ctx) & 1)) continue;
+    for (int p = 0; p < sq.len; ++p) {
+        if (p >= sq.ctx && !(mask >> (p - sq.ctx) & 1)) continue;
         const int64_t page = a.table[s * (int64_t)a.table_width + p / a.c.page_size];
         if (page < 0 || page >= a.c.n_pages) {
             if (a.err && lane == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
@@ -80,22 +108,509 @@ __global__ void __launch_bounds__(32) k_tree_attention(TreeAttention a) {
     if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = sum > 0.0f ? top + logf(sum) : (sum == 0.0f ? -INFINITY : sum);
 }
 
-}  // namespace
+// ------------------------------------------------- the tensor-core kernel --
 
-size_t tree_attention_workspace(int, int64_t, int, int64_t, int, int, int) { return 16; }
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes to shared memory, or 16 zero bytes where put is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool put) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(put ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-cudaError_t launch_tree_attention(const TreeAttention &a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq);
-    cfg.blockDim = dim3(32);
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+__device__ __forceinline__ float pow2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Sizes of the kernel for head size D and 16 * WR rows a block.  Four warps:
+// WR of them share out the rows, and 4 / WR the keys of a tile.  Rows of a
+// tile are padded by 16 bytes, which puts the eight rows of an ldmatrix into
+// different banks.
+template <int D, int WR>
+struct Shape {
+    static constexpr int kRows = 16 * WR, kParts = 4 / WR;
+    static constexpr int kTile = D > 128 && WR > 1 ? 32 : 64;  // keys of a tile
+    static constexpr int kKeys = kTile / kParts;               // of them, a warp's
+    static constexpr int kCopied = kTile / 4;                  // rows that a warp copies
+    static constexpr int kStages = 3;
+    static constexpr int kPitch = 2 * D + 16;                  // bytes of a row
+    static constexpr int kTileBytes = kTile * kPitch;
+    static constexpr bool kHoldQ = D <= 128;                   // q's fragments stay in registers
+    static constexpr int kRing = kStages * 2 * kTileBytes;
+    // q (read again for every tile where it is not held) and the parts' results; the latter two may lie in the ring
+    static constexpr int kSmem = kRing + (kHoldQ ? 0 : kRows * kPitch);
+    static constexpr int kResult = kParts * kRows * D * 4;
+    static_assert(kResult <= kRing && kRows * kPitch <= 2 * kTileBytes, "what lies in the ring fits it");
+    static_assert(kKeys % 16 == 0, "16 keys a product");
+};
+
+// Chunk c of one (sequence, kv head, row tile): see the top of the file.
+// Scores and sums are fp32; the weights 2^(x-m) are rounded to the cache's 16
+// bits for the product with v (the tensor cores take no mixed types), so a
+// weight is off by half a step, and the sum they are divided by is not
+// rounded.  For fp16, whose weights below 2^-14 lose bits, m is kept 10 lower
+// than the maximum: weights reach 2^10 and keep all bits down to 2^-24.
+// What a row does not see: a key's score becomes -inf (weight 0), keys
+// outside the sequence are not read and are zero in shared memory, and the
+// drafts' values, which some rows see and others do not, are looked over for
+// NaN and infinities first (they would make 0 * v NaN): such a value row is
+// zeroed and added by hand to the rows that see it.
+template <typename T, int D, int WR>
+__global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
+    k_tree_attention(TreeAttention a, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml) {
+    using S = Shape<D, WR>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t valid[S::kStages][4];
+    __shared__ uint64_t drafts[S::kRows];
+    __shared__ float2 ml[S::kParts][S::kRows];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
+    const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
+    const int group = a.q_heads / a.c.kv_heads;
+    const Seq sq = sequence(a, s, tid == 0 && blockIdx.x == 0 && c == 0);
+    const int rows = min(sq.n * group - r0, S::kRows);
+    const int begin = c * chunk, end = min(sq.len, begin + chunk);
+    // a row that has no keys at all is written by its first block
+    if (rows <= 0 || (begin >= end && c > 0)) return;
+    const int chunks = max(1, (sq.len + chunk - 1) / chunk);  // of this sequence
+
+    // q of the block's rows (row r: token r / group, head r % group of the group), the sign of the scale with it
+    const float sc = fabsf(a.scale) * kLog2e;
+    const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    uint8_t *qs = S::kHoldQ ? smem + (S::kStages - 1) * 2 * S::kTileBytes : smem + S::kRing;
+    for (int i = tid; i < S::kRows * (D / 8); i += 128) {
+        const int r = i / (D / 8), d = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+            const int tok = (r0 + r) / group, h = kvh * group + (r0 + r) % group;
+            const T *from = static_cast<const T *>(a.q) + (sq.row0 + tok) * a.q_tok + h * a.q_head + d * 8;
+            if (q_whole) {
+                v = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                __align__(16) T y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = from[e];
+                v = *reinterpret_cast<const uint4 *>(y);
+            }
+        }
+        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+        *reinterpret_cast<uint4 *>(qs + r * S::kPitch + d * 16) = v;
+    }
+    if (tid < S::kRows) drafts[tid] = tid < rows ? seen_drafts(a, sq, sq.row0 + (r0 + tid) / group) : 0;
+
+    // copies: each warp brings kCopied rows of a tile; lane l < kCopied keeps the place of row l
+    const int tiles = (end - begin + S::kTile - 1) / S::kTile;
+    const int32_t *table = a.table + (int64_t)s * a.table_width;
+    const int64_t head = kvh * a.c.head_stride;
+    auto page_of = [&](int t) {  // the page of this lane's row of tile t, -1 past the end
+        const int p = begin + t * S::kTile + warp * S::kCopied + lane;
+        return lane < S::kCopied && p < end ? table[(uint32_t)p / (uint32_t)a.c.page_size] : -1;
+    };
+    auto fetch = [&](int t, int page) {
+        const int slot = t % S::kStages;
+        const uint32_t p = begin + t * S::kTile + warp * S::kCopied + lane;
+        const bool in = lane < S::kCopied && p < (uint32_t)end, good = in && page >= 0 && page < a.c.n_pages;
+        if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+        const int64_t at = good ? page * a.c.page_stride + (int64_t)(p % (uint32_t)a.c.page_size) * a.c.tok_stride + head : -1;
+        const uint32_t bits = __ballot_sync(~0u, good);
+        if (lane == 0) valid[slot][warp] = bits;
+        const uint32_t ks = smem_addr(smem) + slot * 2 * S::kTileBytes + warp * S::kCopied * S::kPitch;
+#pragma unroll
+        for (int i = 0; i < S::kCopied * (D / 8) / 32; ++i) {
+            const int x = i * 32 + lane, r = x / (D / 8), d = x % (D / 8);
+            const int64_t from = __shfl_sync(~0u, at, r);
+            const int64_t off = from < 0 ? 0 : from + d * 8;
+            copy16(ks + r * S::kPitch + d * 16, static_cast<const T *>(a.c.k) + off, from >= 0);
+            copy16(ks + S::kTileBytes + r * S::kPitch + d * 16, static_cast<const T *>(a.c.v) + off, from >= 0);
+        }
+    };
+    static_assert(S::kCopied * (D / 8) % 32 == 0, "whole warps of copies");
+#pragma unroll
+    for (int t = 0; t < S::kStages - 1; ++t) {
+        if (t < tiles) fetch(t, page_of(t));
+        copy_commit();
+    }
+    int page = S::kStages - 1 < tiles ? page_of(S::kStages - 1) : -1;
+    __syncthreads();
+    const uint32_t q_at = smem_addr(qs) + (wr * 16 + lane % 16) * S::kPitch + lane / 16 * 16;
+    uint32_t qf[S::kHoldQ ? D / 16 : 1][4];
+    if constexpr (S::kHoldQ) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], q_at + k * 32);
+    }
+
+    constexpr float kLower = std::is_same_v<T, __half> ? 10.0f : 0.0f;
+    float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    const int ra = wr * 16 + lane / 4;  // this lane's rows are ra and ra + 8
+    for (int t = 0; t < tiles; ++t) {
+        copy_wait<S::kStages - 2>();
+        __syncthreads();
+        if (t + S::kStages - 1 < tiles) {
+            fetch(t + S::kStages - 1, page);
+            if (t + S::kStages < tiles) page = page_of(t + S::kStages);
+        }
+        copy_commit();
+        const int slot = t % S::kStages, key0 = begin + t * S::kTile;
+        uint8_t *kt = smem + slot * 2 * S::kTileBytes, *vt = kt + S::kTileBytes;
+
+        // scores of this warp's keys
+        float x[S::kKeys / 8][4] = {};
+        const uint32_t k_at = smem_addr(kt) + (wk * S::kKeys + lane % 8 + lane / 16 * 8) * S::kPitch + lane / 8 % 2 * 16;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t qk[4];
+            if constexpr (!S::kHoldQ) ldsm4(qk, q_at + k * 32);
+#pragma unroll
+            for (int j = 0; j < S::kKeys / 16; ++j) {
+                uint32_t b[4];
+                ldsm4(b, k_at + j * 16 * S::kPitch + k * 32);
+                if constexpr (S::kHoldQ) {
+                    mma<T>(x[2 * j], qf[k], b[0], b[1]);
+                    mma<T>(x[2 * j + 1], qf[k], b[2], b[3]);
+                } else {
+                    mma<T>(x[2 * j], qk, b[0], b[1]);
+                    mma<T>(x[2 * j + 1], qk, b[2], b[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < S::kKeys / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][e] *= sc;
+
+        // tiles with drafts, a ragged end or missing pages: the keys each row sees, bit by bit
+        uint64_t there = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) there |= (uint64_t)valid[slot][w] << (w * S::kCopied);
+        const bool special = key0 + S::kTile > sq.ctx || there != (S::kTile == 64 ? ~0ull : (1ull << S::kTile) - 1);
+        uint64_t odd = 0;  // keys whose values are not all finite
+        if (special) {
+            const int known = min(max(sq.ctx - key0, 0), 64);  // committed keys of the tile
+            const uint64_t old = known == 64 ? ~0ull : (1ull << known) - 1;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t tree = drafts[ra + half * 8];
+                const int gone = key0 - sq.ctx;  // drafts before this tile
+                const uint64_t sees = (old | (known == 64 ? 0 : gone > 0 ? (gone < 64 ? tree >> gone : 0) : tree << known)) & there;
+                const uint32_t mine = (uint32_t)(sees >> (wk * S::kKeys + lane % 4 * 2));
+                const uint32_t more = S::kKeys > 32 ? (uint32_t)(sees >> (wk * S::kKeys + lane % 4 * 2 + 32)) : 0;
+#pragma unroll
+                for (int j = 0; j < S::kKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!((j < 4 ? mine >> (j * 8 + e) : more >> (j * 8 - 32 + e)) & 1)) x[j][half * 2 + e] = -INFINITY;
+            }
+            if (key0 + S::kTile > sq.ctx) {
+                // exponent bits all ones in any 16-bit half: NaN or infinity
+                constexpr uint32_t kExp = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+                __shared__ unsigned long long found;
+                if (tid == 0) found = 0;
+                __syncthreads();
+                for (int i = tid; i < S::kTile * (D / 8); i += 128) {
+                    const int r = i / (D / 8);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vt + r * S::kPitch + i % (D / 8) * 16);
+                    bool bad = false;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t y = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+                        bad |= (y & kExp) == kExp || (y >> 16 & kExp) == kExp;
+                    }
+                    if (bad && key0 + r >= sq.ctx) atomicOr(&found, 1ull << r);
+                }
+                __syncthreads();
+                odd = found;
+                if (odd) {
+                    for (int i = tid; i < S::kTile * (D / 8); i += 128)
+                        if (odd >> (i / (D / 8)) & 1)
+                            *reinterpret_cast<uint4 *>(vt + i / (D / 8) * S::kPitch + i % (D / 8) * 16) = make_uint4(0, 0, 0, 0);
+                    __syncthreads();
+                }
+            }
+        }
+
+        // the running maximum of each row over its four lanes, and what it scales
+        float shift[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < S::kKeys / 8; ++j) top = fmaxf(top, fmaxf(x[j][half * 2], x[j][half * 2 + 1]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const float now = fmaxf(m[half], top - kLower);
+            shift[half] = now == -INFINITY ? 0.0f : now;  // nothing seen yet: every weight stays 0
+            const float keep = pow2(m[half] - shift[half]);
+            m[half] = now;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S::kKeys / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[j][half * 2 + e] = pow2(x[j][half * 2 + e] - shift[half]);
+                    sum += x[j][half * 2 + e];
+                }
+            l[half] = l[half] * keep + sum;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                o[d][half * 2] *= keep;
+                o[d][half * 2 + 1] *= keep;
+            }
+        }
+        const uint32_t v_at = smem_addr(vt) + (wk * S::kKeys + lane % 16) * S::kPitch + lane / 16 * 16;
+#pragma unroll
+        for (int j = 0; j < S::kKeys / 16; ++j) {
+            const uint32_t p[4] = {pack2<T>(x[2 * j][0], x[2 * j][1]), pack2<T>(x[2 * j][2], x[2 * j][3]),
+                                   pack2<T>(x[2 * j + 1][0], x[2 * j + 1][1]), pack2<T>(x[2 * j + 1][2], x[2 * j + 1][3])};
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t b[4];
+                ldsm4t(b, v_at + j * 16 * S::kPitch + d * 32);
+                mma<T>(o[2 * d], p, b[0], b[1]);
+                mma<T>(o[2 * d + 1], p, b[2], b[3]);
+            }
+        }
+        if (odd) {  // value rows taken out above: by hand, for the rows that see them
+            for (int key = wk * S::kKeys; key < (wk + 1) * S::kKeys; ++key) {
+                if (!(odd >> key & 1)) continue;
+                const uint32_t p = key0 + key;
+                const int64_t at = table[p / (uint32_t)a.c.page_size] * a.c.page_stride +
+                                   (int64_t)(p % (uint32_t)a.c.page_size) * a.c.tok_stride + head;
+                const int local = key - wk * S::kKeys;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float w = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < S::kKeys / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (j * 8 + e == (local & ~7) + (local & 1)) w = x[j][half * 2 + e];
+                    w = __shfl_sync(~0u, w, (lane & ~3) | (local & 7) >> 1);
+                    if (!(drafts[ra + half * 8] >> (p - sq.ctx) & 1)) continue;
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            o[d][half * 2 + e] += w * to_f32(static_cast<const T *>(a.c.v)[at + d * 8 + lane % 4 * 2 + e]);
+                }
+            }
+        }
+    }
+    copy_wait<0>();
+
+    // join the warps that shared out the keys, then one division
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        l[half] += __shfl_xor_sync(~0u, l[half], 1);
+        l[half] += __shfl_xor_sync(~0u, l[half], 2);
+        if (lane % 4 == 0) ml[wk][ra + half * 8] = make_float2(m[half], l[half]);
+    }
+    __syncthreads();
+    float *res = reinterpret_cast<float *>(smem);  // [part][row][D]
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = ra + half * 8;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < S::kParts; ++w) top = fmaxf(top, ml[w][r].x);
+        const float f = top == -INFINITY ? 1.0f : pow2(m[half] - top);
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+            *reinterpret_cast<float2 *>(res + (wk * S::kRows + r) * D + d * 8 + lane % 4 * 2) =
+                make_float2(o[d][half * 2] * f, o[d][half * 2 + 1] * f);
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 4); i += 128) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < S::kParts; ++w) top = fmaxf(top, ml[w][r].x);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < S::kParts; ++w) {
+            if (top != -INFINITY) sum += ml[w][r].y * pow2(ml[w][r].x - top);
+            const float4 y = *reinterpret_cast<const float4 *>(res + (w * S::kRows + r) * D + d);
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        const int64_t row = (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group;
+        if (chunks > 1) {
+            const int64_t at = (int64_t)c * a.total_tok * a.q_heads + row;
+            *reinterpret_cast<float4 *>(part_o + at * D + d) = v;
+            if (d == 0) part_ml[at] = make_float2(top, sum);
+            continue;
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (a.out_f32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        } else {
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * D + d) =
+                make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+        }
+        if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+}
+
+// The chunks of a row joined: one warp per (token, head).  grid
+// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, const float *part_o, const float2 *part_ml) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, h = blockIdx.x * 4 + threadIdx.x / 32, i = blockIdx.y;
+    const Seq sq = sequence(a, blockIdx.z, false);
+    const int chunks = (sq.len + chunk - 1) / chunk;
+    if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;
+    const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
+    float top = -INFINITY;
+    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[c * step + row].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    constexpr int kEach = D / 32;
+    float v[kEach] = {}, sum = 0.0f;
+    if (top != -INFINITY) {
+#pragma unroll 4
+        for (int c = 0; c < chunks; ++c) {
+            const float2 p = part_ml[c * step + row];
+            const float f = pow2(p.x - top);
+            sum += p.y * f;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(c * step + row) * D + j * 32 + lane];
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        if (a.out_f32) static_cast<float *>(a.out)[row * D + j * 32 + lane] = v[j] * inv;
+        else static_cast<T *>(a.out)[row * D + j * 32 + lane] = from_f32<T>(v[j] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// How a call is cut: rows of a block (16 * wr), tiles of them, and the chunk
+// of keys a block takes.
+struct Plan {
+    int wr, row_tiles, chunk, n_chunks;
+};
+
+Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads) {
+    Plan p;
+    const int rows = max_tok * (q_heads / kv_heads);
+    p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.row_tiles = (rows + 16 * p.wr - 1) / (16 * p.wr);
+    // two blocks for each of 152 SMs; with several sequences, whose lengths may differ, at most 2048 keys each
+    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
+    int64_t n = (304 + blocks - 1) / blocks;
+    if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
+    n = std::min<int64_t>(n, 65535);  // of the grid's second axis
+    int64_t chunk = (max_len + n - 1) / n;
+    chunk = std::max<int64_t>((chunk + 63) / 64 * 64, 128);
+    p.chunk = (int)chunk;
+    p.n_chunks = (int)((max_len + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+bool tiled_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+template <typename K>
+cudaError_t start(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchConfig_t &cfg,
+                  cudaLaunchAttribute *at) {
+    cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return a.c.dtype == CBQ_BF16 ? cudaLaunchKernelEx(&cfg, k_tree_attention<__nv_bfloat16>, a)
-                                 : cudaLaunchKernelEx(&cfg, k_tree_attention<__half>, a);
+    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                            : cudaSuccess;
+}
+
+template <typename T, int D, int WR>
+cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at[1];
+    const size_t rows = (size_t)a.total_tok * a.q_heads;
+    float2 *part_ml = static_cast<float2 *>(a.ws);
+    float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
+    cudaError_t e = start(k_tree_attention<T, D, WR>, dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                          128, Shape<D, WR>::kSmem, s, cfg, at);
+    if (e == cudaSuccess)
+        e = cudaLaunchKernelEx(&cfg, k_tree_attention<T, D, WR>, a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml);
+    if (e != cudaSuccess || p.n_chunks == 1) return e;
+    e = start(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s, cfg, at);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_tree_join<T, D>, a, p.chunk, (const float *)part_o, (const float2 *)part_ml);
+    return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_dim(const TreeAttention &a, const Plan &p, cudaStream_t s) {
+    return p.wr == 1 ? launch_tiled<T, D, 1>(a, p, s) : p.wr == 2 ? launch_tiled<T, D, 2>(a, p, s) : launch_tiled<T, D, 4>(a, p, s);
+}
+
+template <typename T>
+cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
+    // 16-byte copies want every row of k and v on a 16-byte boundary, 16-byte stores every row of out
+    const uintptr_t ends = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | reinterpret_cast<uintptr_t>(a.out);
+    if (tiled_dim(a.c.head_dim) && ends % 16 == 0 && (a.c.page_stride | a.c.tok_stride | a.c.head_stride) % 8 == 0) {
+        const Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads);
+        if (a.c.head_dim == 64) return launch_dim<T, 64>(a, p, s);
+        if (a.c.head_dim == 128) return launch_dim<T, 128>(a, p, s);
+        return launch_dim<T, 256>(a, p, s);
+    }
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at[1];
+    cudaError_t e = start(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, cfg, at);
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, k_tree_general<T>, a) : e;
+}
+
+}  // namespace
+
+size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
+                                int head_dim) {
+    if (!tiled_dim(head_dim)) return 16;
+    const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads);
+    if (p.n_chunks == 1) return 16;
+    const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
+    return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
+}
+
+cudaError_t launch_tree_attention(const TreeAttention &a, cudaStream_t s) {
+    return a.c.dtype == CBQ_BF16 ? launch_type<__nv_bfloat16>(a, s) : launch_type<__half>(a, s);
 }
 
 }  // namespace cbq
