@@ -8,6 +8,7 @@ computing anything another way.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -529,48 +530,77 @@ def cbq_debug_mmq_block_dots(W: Weights, qx, stream=None):
 
 
 # ------------------------------------- positions, attention, sampling --
+#
+# A small call of these takes the GPU about as long as Python takes to make
+# it, so the marshalling looks each tensor property up once and calls into
+# torch only where it has to.
 
 _SCALINGS = {"none": CBQ_ROPE_NONE, "linear": CBQ_ROPE_LINEAR, "turns": CBQ_ROPE_BY_TURNS, "index": CBQ_ROPE_BY_INDEX}
 _LAYOUTS = {"half": CBQ_ROPE_HALF, "pairs": CBQ_ROPE_PAIRS}
 
 
-def _dtype(t, name):
+@functools.cache
+def _codes():
     torch = _torch()
-    code = {torch.float32: CBQ_F32, torch.bfloat16: CBQ_BF16, torch.float16: CBQ_F16}.get(t.dtype)
+    return {torch.float32: CBQ_F32, torch.bfloat16: CBQ_BF16, torch.float16: CBQ_F16}
+
+
+def _dtype(t, name):
+    code = _codes().get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     return code
 
 
-def _heads_ptr(t, name):
-    """Pointer of a CUDA tensor (tokens, heads, dim) whose last axis is contiguous."""
+def _raw_stream(stream, t):
+    """The cudaStream_t of `stream`, or of torch's current one on t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _layout(layout):
+    code = _LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+    return code
+
+
+def _heads(t, name):
+    """(pointer, token stride, head stride) of a CUDA tensor (tokens, heads,
+    dim) whose last axis is contiguous."""
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and t.shape[2] != 1):
         raise ValueError(f"{name} must be (tokens, heads, dim) with a contiguous last axis")
-    return t.data_ptr()
+    return t.data_ptr(), st[0], st[1]
 
 
 def _cache(kc, vc):
     """cbq_kv_cache of two CUDA tensors (pages, page_size, kv_heads, dim)."""
     if not kc.is_cuda or not vc.is_cuda or kc.dtype != vc.dtype:
         raise TypeError("kc and vc must be CUDA tensors of one dtype")
-    if kc.dim() != 4 or kc.shape != vc.shape or kc.stride() != vc.stride():
+    shape, st = kc.shape, kc.stride()
+    if len(shape) != 4 or shape != vc.shape or st != vc.stride():
         raise ValueError("kc and vc must be (pages, page_size, kv_heads, dim) of one shape and strides")
-    pages, page, heads, dim = kc.shape
-    sp, st, sh, sd = kc.stride()
-    if sd != 1 and dim != 1:
+    pages, page, heads, dim = shape
+    if st[3] != 1 and dim != 1:
         raise ValueError("the cache's last axis must be contiguous")
-    return cbq_kv_cache(kc.data_ptr(), vc.data_ptr(), _dtype(kc, "kc"), heads, dim, page, pages, sp, st, sh)
+    return cbq_kv_cache(kc.data_ptr(), vc.data_ptr(), _dtype(kc, "kc"), heads, dim, page, pages, st[0], st[1], st[2])
 
 
-def _opt_ptr(t, dtype, n, name):
-    """Pointer of an optional contiguous CUDA tensor of n values (None: null)."""
-    if t is None:
-        return None
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} values")
-    return _dev_ptr(t, dtype, name)
+def _vec(t, dtype, n, name):
+    """Pointer of a contiguous CUDA tensor of n values of dtype (n < 0: any number)."""
+    if t.dtype is not dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if not t.is_contiguous() or (n >= 0 and t.numel() != n):
+        raise ValueError(f"{name} must be contiguous" + (f" with {n} values" if n >= 0 else ""))
+    return t.data_ptr()
+
+
+def _opt_vec(t, dtype, n, name):
+    return None if t is None else _vec(t, dtype, n, name)
 
 
 def cbq_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -595,14 +625,13 @@ def cbq_rope(x, pos, turns, rot_off: int = 0, layout: str = "half", mscale: floa
     n, heads, dim = x.shape
     if out is None:
         out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and dtype of x")
-    if layout not in _LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
-    _check(load().cbq_rope(_heads_ptr(x, "x"), _dtype(x, "x"), n, heads, dim, x.stride(0), x.stride(1),
-                           _opt_ptr(pos, torch.int32, n, "pos"), _dev_ptr(turns, torch.float64, "turns"),
-                           2 * turns.numel(), rot_off, _LAYOUTS[layout], mscale, _heads_ptr(out, "out"),
-                           out.stride(0), out.stride(1), _stream(stream)), "cbq_rope")
+    xp, xt, xh = _heads(x, "x")
+    op, ot, oh = _heads(out, "out")
+    _check(load().cbq_rope(xp, _dtype(x, "x"), n, heads, dim, xt, xh, _vec(pos, torch.int32, n, "pos"),
+                           _vec(turns, torch.float64, -1, "turns"), 2 * turns.numel(), rot_off, _layout(layout),
+                           mscale, op, ot, oh, _raw_stream(stream, x)), "cbq_rope")
     return out
 
 
@@ -613,27 +642,27 @@ def cbq_rope_append(q, k, v, pos, slots, turns, kc, vc, rot_off: int = 0, layout
     page_size, kv_heads, dim) at slots (tokens) int64 (negative: not written).
     err: an optional int32 tensor of one value for the CBQ_DEVERR_* bits."""
     torch = _torch()
-    n, heads, dim = q.shape
+    shape = q.shape
+    n, heads, dim = shape
     c = _cache(kc, vc)
     if k.shape != (n, c.kv_heads, dim) or v.shape != k.shape or dim != c.head_dim:
         raise ValueError("k and v must be (tokens, kv_heads, dim) as the cache, dim as q")
-    if k.stride() != v.stride() or k.dtype != q.dtype or v.dtype != q.dtype:
+    qp, qt, qh = _heads(q, "q")
+    kp, kt, kh = _heads(k, "k")
+    vp, vt, vh = _heads(v, "v")
+    if kt != vt or kh != vh or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype, and k and v one set of strides")
-    if layout not in _LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=kc.dtype, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    _check(load().cbq_rope_append(_heads_ptr(q, "q"), _heads_ptr(k, "k"), _heads_ptr(v, "v"), _dtype(q, "q"), n, heads,
-                                  q.stride(0), q.stride(1), k.stride(0), k.stride(1),
-                                  _opt_ptr(pos, torch.int32, n, "pos"), _opt_ptr(slots, torch.int64, n, "slots"),
-                                  _dev_ptr(turns, torch.float64, "turns"), 2 * turns.numel(), rot_off,
-                                  _LAYOUTS[layout], mscale, ctypes.byref(c), _dev_ptr(out, kc.dtype, "out"),
-                                  _opt_ptr(err, torch.int32, 1, "err"), _stream(stream)), "cbq_rope_append")
+        out = torch.empty(shape, dtype=kc.dtype, device=q.device)
+    _check(load().cbq_rope_append(qp, kp, vp, _dtype(q, "q"), n, heads, qt, qh, kt, kh,
+                                  _vec(pos, torch.int32, n, "pos"), _vec(slots, torch.int64, n, "slots"),
+                                  _vec(turns, torch.float64, -1, "turns"), 2 * turns.numel(), rot_off,
+                                  _layout(layout), mscale, c, _vec(out, kc.dtype, n * heads * dim, "out"),
+                                  _opt_vec(err, torch.int32, 1, "err"), _raw_stream(stream, q)), "cbq_rope_append")
     return out
 
 
+@functools.lru_cache(1024)
 def cbq_tree_attention_workspace(n_seq: int, total_tok: int, max_tok: int, max_len: int, q_heads: int, kv_heads: int,
                                  head_dim: int) -> int:
     """Bytes of workspace of cbq_tree_attention for these limits."""
@@ -653,28 +682,29 @@ def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len
     (out, lse) with with_lse.  workspace: a uint8 tensor of
     cbq_tree_attention_workspace bytes (allocated when None)."""
     torch = _torch()
-    n, heads, dim = q.shape
+    shape, dev, i32 = q.shape, q.device, torch.int32
+    n, heads, dim = shape
     c = _cache(kc, vc)
     if q.dtype != kc.dtype or dim != c.head_dim:
         raise ValueError("q must have the cache's dtype and dim")
     n_seq, width = table.shape
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError("out must be a contiguous CUDA tensor of the shape of q")
-    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if with_lse else None
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    elif out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if with_lse else None
     if workspace is None:
-        workspace = torch.empty(cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim),
-                                dtype=torch.uint8, device=q.device)
-    _check(load().cbq_tree_attention(_heads_ptr(q, "q"), q.stride(0), q.stride(1), heads, n, ctypes.byref(c),
-                                     _dev_ptr(table, torch.int32, "table"), width, n_seq,
-                                     _opt_ptr(ctx, torch.int32, n_seq, "ctx"),
-                                     _opt_ptr(start, torch.int32, n_seq + 1, "start"),
-                                     _opt_ptr(mask, torch.int64, n, "mask"), max_tok, max_len,
-                                     dim ** -0.5 if scale is None else scale, out.data_ptr(), _dtype(out, "out"),
+        need = cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    qp, qt, qh = _heads(q, "q")
+    _check(load().cbq_tree_attention(qp, qt, qh, heads, n, c, _vec(table, i32, -1, "table"), width, n_seq,
+                                     _vec(ctx, i32, n_seq, "ctx"), _vec(start, i32, n_seq + 1, "start"),
+                                     _vec(mask, torch.int64, n, "mask"), max_tok, max_len,
+                                     dim ** -0.5 if scale is None else scale,
+                                     _vec(out, out.dtype, n * heads * dim, "out"), _dtype(out, "out"),
                                      None if lse is None else lse.data_ptr(),
-                                     _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                     _opt_ptr(err, torch.int32, 1, "err"), _stream(stream)), "cbq_tree_attention")
+                                     _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel(),
+                                     _opt_vec(err, i32, 1, "err"), _raw_stream(stream, q)), "cbq_tree_attention")
     return (out, lse) if with_lse else out
 
 
@@ -684,20 +714,19 @@ def cbq_sample(logits, temperature, top_k, top_p, min_p, u, ids=None, probs=None
     ids int32 and the drawn tokens' probabilities among the kept ones."""
     torch = _torch()
     n, V = logits.shape
+    st = logits.stride()
     if not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
-    if logits.stride(1) != 1 and V != 1:
+    if st[1] != 1 and V != 1:
         raise ValueError("logits must have a contiguous last axis")
-    if u is None:
-        raise ValueError("u must be given")
+    f, i32 = torch.float32, torch.int32
     if ids is None:
-        ids = torch.empty(n, dtype=torch.int32, device=logits.device)
+        ids = torch.empty(n, dtype=i32, device=logits.device)
     if probs is None:
-        probs = torch.empty(n, dtype=torch.float32, device=logits.device)
-    f = torch.float32
-    _check(load().cbq_sample(logits.data_ptr(), _dtype(logits, "logits"), n, V, logits.stride(0),
-                             _opt_ptr(temperature, f, n, "temperature"), _opt_ptr(top_k, torch.int32, n, "top_k"),
-                             _opt_ptr(top_p, f, n, "top_p"), _opt_ptr(min_p, f, n, "min_p"), _opt_ptr(u, f, n, "u"),
-                             _opt_ptr(ids, torch.int32, n, "ids"), _opt_ptr(probs, f, n, "probs"), _stream(stream)),
+        probs = torch.empty(n, dtype=f, device=logits.device)
+    _check(load().cbq_sample(logits.data_ptr(), _dtype(logits, "logits"), n, V, st[0],
+                             _opt_vec(temperature, f, n, "temperature"), _opt_vec(top_k, i32, n, "top_k"),
+                             _opt_vec(top_p, f, n, "top_p"), _opt_vec(min_p, f, n, "min_p"), _vec(u, f, n, "u"),
+                             _vec(ids, i32, n, "ids"), _vec(probs, f, n, "probs"), _raw_stream(stream, logits)),
            "cbq_sample")
     return ids, probs

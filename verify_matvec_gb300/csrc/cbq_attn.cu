@@ -544,37 +544,37 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads) {
 
 bool tiled_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
-template <typename K>
-cudaError_t start(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchConfig_t &cfg,
-                  cudaLaunchAttribute *at) {
-    cfg = {};
+// Launches kernel<<<grid, threads, smem>>> as a programmatic dependent of the
+// work ahead.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
+    cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                            : cudaSuccess;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, (P)args...);
 }
 
 template <typename T, int D, int WR>
 cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) {
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute at[1];
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
     float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
-    cudaError_t e = start(k_tree_attention<T, D, WR>, dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
-                          128, Shape<D, WR>::kSmem, s, cfg, at);
-    if (e == cudaSuccess)
-        e = cudaLaunchKernelEx(&cfg, k_tree_attention<T, D, WR>, a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml);
+    const cudaError_t e = launch(k_tree_attention<T, D, WR>, dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                                 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1) return e;
-    e = start(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s, cfg, at);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_tree_join<T, D>, a, p.chunk, (const float *)part_o, (const float2 *)part_ml);
-    return e;
+    return launch(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s,
+                  a, p.chunk, part_o, part_ml);
 }
 
 template <typename T, int D>
@@ -592,10 +592,7 @@ cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
         if (a.c.head_dim == 128) return launch_dim<T, 128>(a, p, s);
         return launch_dim<T, 256>(a, p, s);
     }
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute at[1];
-    cudaError_t e = start(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, cfg, at);
-    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, k_tree_general<T>, a) : e;
+    return launch(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, a);
 }
 
 }  // namespace
