@@ -1,12 +1,13 @@
 // cbq_sample.cu -- one token from each row of logits: temperature, top-k,
 // top-p and min-p, drawn by a given uniform number.
 //
-// A cluster of up to eight blocks takes a row: each brings its part of the
-// logits into shared memory once, as integers in the logits' order, and every
-// later step reads them there.  Nothing is sorted: what top-k and top-p keep
-// is all above a border in the order and the first few equal to it, and the
-// border is found by histograms (of counts for top-k, of weights for top-p)
-// whose bins narrow down to one value.  Weights are whole numbers of 2^-45, so
+// A cluster of up to sixteen blocks takes a row; every thread reads its few
+// logits once.  Nothing is sorted: what top-k and top-p keep is all above a
+// border in the order and the first few equal to it.  A histogram over the
+// row (of counts for top-k, of weights for top-p) finds the bin of the border;
+// what lies in that bin, some hundred logits, every block gets from all
+// others, and finds the border in it by itself.  Only what can still be kept
+// is listed and looked at after that.  Weights are whole numbers of 2^-45, so
 // that their sums do not depend on the order of atomics and a choice is the
 // same on every run.
 #include "cbq_device.cuh"
@@ -17,14 +18,15 @@ namespace cbq {
 
 namespace {
 
-constexpr int kSampleThreads = 512, kNumWarps = kSampleThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kMaxBlocks = 8;             // of a cluster
+constexpr int kSampleThreads = 1024, kNumWarps = kSampleThreads / 32;
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;
+constexpr int kGather = 2048;             // logits of a border's bin, from all blocks
+constexpr int kMaxBlocks = 16;            // of a cluster
 constexpr int kTable = 256;               // steps of 2^(1/256) of the weights' table
 constexpr uint64_t kOne = 1ull << 45;     // the weight 1
 constexpr uint32_t kNone = 0x007FFFFFu;   // order of -inf: what is not above has no weight
 
-// 2^(i/256) in units of 2^-45, from the eight square roots 2^(1/2) .. 2^(1/256).
+// 2^(i/256) in units of 2^-46, from the eight square roots 2^(1/2) .. 2^(1/256).
 struct PowTable {
     uint64_t v[kTable];
 };
@@ -45,18 +47,16 @@ constexpr PowTable make_table() {
         double p = 1.0;
         for (int j = 0; j < 8; ++j)
             if (i >> (7 - j) & 1) p *= roots[j];
-        t.v[i] = (uint64_t)(p * (double)kOne + 0.5);
+        t.v[i] = (uint64_t)(p * 2.0 * (double)kOne + 0.5);
     }
     return t;
 }
 __device__ const PowTable kPow = make_table();
 
-// Unsigned numbers in the order of the logits; NaN below all (0).  Adding
-// zero makes -0 and +0 one value, as the order wants.
+// Unsigned numbers in the order of the logits (no NaN, no -0 among them).
 __device__ __forceinline__ uint32_t order_of(float l) {
-    const uint32_t b = __float_as_uint(l + 0.0f);
-    if (l != l) return 0u;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t b = __float_as_uint(l);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float logit_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
@@ -68,32 +68,32 @@ __device__ __forceinline__ float logit_of(uint32_t o) {
 // round(256 y) and t = (y - n/256) ln 2, |t| <= 2^-9.5: the weight is
 // table[n mod 256] * (1 + (t + t^2/2 + t^3/6)) >> -floor(n/256); 1 + .. is a
 // 2^-40 fixed-point number, whose rounding (2^-41) is the largest error.
+// Rounding to a whole number by adding 1.5 * 2^23 keeps the conversion units,
+// a quarter as wide as the others, out of it but for one conversion.
 struct Scale {
     float top, hi, lo;  // hi + lo = log2(e) / T
 };
 __device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64_t *table) {
-    if (l == s.top) return kOne;  // +inf at the top too
+    constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236017e-9f;
+    constexpr float k40 = 1099511627776.0f, kRound = 12582912.0f;
+    constexpr int kRoundBits = 0x4B400000;
     const float d = l - s.top;
-    const float y = d * s.hi;
-    if (!(y > -47.0f)) return 0;
+    const float y = fmaxf(d * s.hi, -50.0f);            // NaN (both infinite) becomes -50 too
     const float back = d + s.top;                       // two-sum: d + e is the exact difference
     const float e = (l - back) + ((back - d) - s.top);
     const float yl = __fmaf_rn(d, s.hi, -y) + __fmaf_rn(d, s.lo, e * s.hi);
-    const float n = rintf(y * kTable);
-    const float r = __fmaf_rn(n, -1.0f / kTable, y);  // exact: y and n/256 agree in their leading bits
-    constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236017e-9f;
+    const float nr = __fmaf_rn(y, (float)kTable, kRound);
+    const float r = __fmaf_rn(nr - kRound, -1.0f / kTable, y);  // exact: y and n/256 agree in their leading bits
+    const int ni = __float_as_int(nr) - kRoundBits;
     const float th = r * kLn2Hi;
     const float tl = __fmaf_rn(r, kLn2Hi, -th) + __fmaf_rn(r, kLn2Lo, yl * kLn2Hi);
     const float t = th + tl;
     const float quad = __fmaf_rn(t * t, __fmaf_rn(t, 1.0f / 6.0f, 0.5f), tl);
-    constexpr float k40 = 1099511627776.0f;
-    const int p = __float2int_rn(th * k40) + __float2int_rn(quad * k40);
-    const int ni = (int)n;
+    const int p = __float2int_rn(th * k40) + (__float_as_int(__fmaf_rn(quad, k40, kRound)) - kRoundBits);
     const uint64_t w = table[ni & (kTable - 1)];
-    const int64_t more = (int64_t)(int32_t)(w >> 15) * p >> 25;
-    const uint64_t full = w + (uint64_t)more;
-    const int sh = -(ni >> 8);
-    return sh > 46 ? 0 : (full + ((1ull << sh) >> 1)) >> sh;
+    const uint64_t full = w + (uint64_t)((int64_t)(int32_t)(w >> 16) * p >> 24);
+    const uint64_t v = ((full >> (-(ni >> 8))) + 1) >> 1;
+    return l == s.top ? kOne : y > -47.0f ? v : 0;      // +inf at the top too
 }
 
 // ------------------------------------------------------------- clusters ----
@@ -115,17 +115,21 @@ __device__ __forceinline__ uint32_t peer(const void *p, uint32_t r) {
 __device__ __forceinline__ void peer_store(uint32_t a, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint2 peer_load2(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+__device__ __forceinline__ void peer_store(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t peer_load(uint32_t a) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
 
-// A histogram: counts in part[0], or weights in their three 16-bit parts (a
-// block adds fewer than 2^16 of them, so 32 bits hold each part's sum; 64-bit
-// atomics on shared memory are loops).
+// Sums by bin.  Weights are added in three 16-bit parts (a block adds fewer
+// than 2^16 of them, so 32 bits hold each part's sum; 64-bit atomics on shared
+// memory are loops), counts in part[0]; all[] is the whole.
 struct Hist {
     uint32_t part[3][kBins];
+    uint64_t all[kBins];
 };
 
 struct alignas(16) Shared {
@@ -133,16 +137,32 @@ struct alignas(16) Shared {
     Hist hist[2];
     uint64_t swap[2][kMaxBlocks][2];  // what the blocks of the cluster tell one another
     uint64_t warp[kNumWarps];
-    uint32_t key[kNumWarps], at[kNumWarps];
+    uint32_t key[kNumWarps], at[kNumWarps], listed[kNumWarps];
+    uint32_t mine[kGather];           // the border's bin: this block's, and everyone's
+    uint32_t gather[kGather];
     uint64_t above, inside;
     int bin, index;
+    uint32_t count;
 };
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    return v;
+// f * n, rounded down or up to a whole number, exactly; f in [0, 1].  (64-bit
+// floating point is a sixty-fourth as wide as 32-bit on this GPU.)
+__device__ __forceinline__ uint64_t share(uint64_t n, float f, bool up) {
+    const uint32_t b = __float_as_uint(f);
+    const uint64_t m = (b & 0x7FFFFFu) | (b >> 23 ? 0x800000u : 0u);
+    const int s = 150 - max((int)(b >> 23), 1);  // f = m 2^-s, 23 <= s <= 149
+    const uint64_t lo = n * m, hi = __umul64hi(n, m);
+    uint64_t whole, rest;
+    if (s < 64) {
+        whole = hi << (64 - s) | lo >> s;
+        rest = lo << (64 - s);
+    } else {
+        whole = s < 128 ? hi >> (s - 64) : 0;
+        rest = lo | (s < 128 ? hi & ((1ull << (s - 64)) - 1) : hi);
+    }
+    return whole + (up && rest ? 1 : 0);
 }
+
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -152,24 +172,20 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
     return v;
 }
 
-// One block's part of a row and its place in the cluster.
+// One block's part of a row and its place in the cluster.  Warp w has the
+// stretch of 32 N logits from first + 32 N w on; those that may be kept are
+// listed, in order, with their place in the stretch.
+template <int N>
 struct Part {
     Shared &s;
-    const uint32_t *x;  // the order of the logits first .. first + len
-    int first, len, blocks, rank;
+    float *list;        // 32 N a warp
+    uint16_t *place;
+    int first, blocks, rank, warp, lane;
+    int listed = 0;         // of this warp
     int turn = 0, use = 0;  // which of the two swap buffers and histograms is next
 
-    // f(index in the part, order), a warp to a contiguous stretch
-    template <typename F>
-    __device__ void each(F f) const {
-        const int per = (len + kNumWarps - 1) / kNumWarps, w = threadIdx.x / 32;
-        const int end = min(len, (w + 1) * per);
-#pragma unroll 4
-        for (int i = w * per + threadIdx.x % 32; i < end; i += 32) f(i, x[i]);
-    }
-
-    // Every block gives two numbers (of its thread 0) and gets all blocks'.
-    // A buffer is written again two calls later: all blocks have read it by then.
+    // Every block gives two numbers (the same in all its threads) and gets all
+    // blocks'.  A buffer is written again two calls later: all have read it by then.
     __device__ const uint64_t (*tell(uint64_t a, uint64_t b))[2] {
         uint64_t(*to)[2] = s.swap[turn];
         turn ^= 1;
@@ -181,132 +197,164 @@ struct Part {
         return to;
     }
 
-    // The block's sum of v, in every thread.
-    __device__ uint64_t block_sum(uint64_t v) {
-        v = warp_sum(v);
+    // The inclusive sum of v over the threads before and this one; *total: over
+    // all; s.warp[]: the warps' inclusive sums.
+    __device__ uint64_t block_scan(uint64_t v, uint64_t *total) {
+        v = warp_scan(v, lane);
         __syncthreads();
-        if (threadIdx.x % 32 == 0) s.warp[threadIdx.x / 32] = v;
+        if (lane == 31) s.warp[warp] = v;
         __syncthreads();
-        v = 0;
-#pragma unroll
-        for (int i = 0; i < kNumWarps; ++i) v += s.warp[i];
-        return v;
+        const uint64_t sums = warp_scan(s.warp[lane], lane);
+        *total = __shfl_sync(~0u, sums, 31);
+        const uint64_t before = __shfl_sync(~0u, sums, (warp + 31) % 32);
+        return v + (warp ? before : 0);
     }
 
-    // One step of a descent: bin_of(order) in [0, kBins), or -1 for what does
-    // not take part, ascending as the order descends; value(order) is counted
-    // (kWeights false: at most 1) or summed.  need(total): how much to take.
-    // Finds the first bin with which that is reached: s.bin (-1: never),
-    // s.above before it, s.inside in it.
-    template <bool kWeights, typename B, typename V, typename N>
-    __device__ void step(B bin_of, V value, N need) {
-        Hist &h = s.hist[use];  // last read two steps ago: a cluster barrier lies between
+    // A step of a descent: fill(add) calls add(bin, value) for what takes part,
+    // bins ascending as the order descends; kWide: over all blocks of the
+    // cluster, otherwise this block's.  need(total): how much to take.  Finds
+    // the first bin with which that is reached: s.bin (-1: never), s.above
+    // before it, s.inside in it.
+    template <bool kWeights, bool kWide, typename F, typename G>
+    __device__ void step(F fill, G need) {
+        static_assert(kNumWarps == 32 && kBins <= kSampleThreads, "a bin a thread, a warp a lane");
+        Hist &h = s.hist[use];  // last read two steps ago: a barrier lies between
         use ^= 1;
-        constexpr int kParts = kWeights ? 3 : 1;
         __syncthreads();  // s.bin of the step before has been read
-        for (int i = threadIdx.x; i < kParts * kBins; i += kSampleThreads) h.part[0][i] = 0;
+        if (threadIdx.x < kBins) {
+#pragma unroll
+            for (int p = 0; p < (kWeights ? 3 : 1); ++p) h.part[p][threadIdx.x] = 0;
+        }
         if (threadIdx.x == 0) s.bin = -1;
         __syncthreads();
-        each([&](int, uint32_t o) {
-            const int b = bin_of(o);
-            if (b < 0) return;
+        fill([&](int b, uint64_t v) {
             if constexpr (kWeights) {
-                const uint64_t v = value(o);
-                if (!v) return;
                 atomicAdd(&h.part[0][b], (uint32_t)v & 0xFFFFu);
                 atomicAdd(&h.part[1][b], (uint32_t)(v >> 16) & 0xFFFFu);
                 atomicAdd(&h.part[2][b], (uint32_t)(v >> 32));
             } else {
-                atomicAdd(&h.part[0][b], 1u);
+                atomicAdd(&h.part[0][b], (uint32_t)v);
             }
         });
-        cluster_sync();
-        // every block adds up all blocks' bins (the same in each), two a thread
-        uint64_t v0 = 0, v1 = 0;
-        for (int r = 0; r < blocks; ++r)
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                const uint2 u = peer_load2(peer(&h.part[p][2 * threadIdx.x], r));
-                v0 += (uint64_t)u.x << (16 * p);
-                v1 += (uint64_t)u.y << (16 * p);
-            }
-        const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-        uint64_t sum = warp_scan(v0 + v1, lane);
-        if (lane == 31) s.warp[w] = sum;
         __syncthreads();
-        uint64_t total = 0, before = 0;
-#pragma unroll
-        for (int i = 0; i < kNumWarps; ++i) {
-            if (i < w) before += s.warp[i];
-            total += s.warp[i];
+        uint64_t sum = 0;
+        if (threadIdx.x < kBins) {
+            sum = h.part[0][threadIdx.x];
+            if constexpr (kWeights)
+                sum += ((uint64_t)h.part[1][threadIdx.x] << 16) + ((uint64_t)h.part[2][threadIdx.x] << 32);
+            if constexpr (kWide) h.all[threadIdx.x] = sum;
         }
-        sum += before;
-        const uint64_t want = need(total), b0 = sum - v0 - v1, b1 = sum - v1;
-        if (b0 < want && sum >= want) {
-            const bool second = b1 < want;
-            s.bin = 2 * threadIdx.x + (second ? 1 : 0);
-            s.above = second ? b1 : b0;
-            s.inside = second ? v1 : v0;
+        if constexpr (kWide) {
+            cluster_sync();
+            if (threadIdx.x < kBins) {
+                sum = 0;
+                for (int r0 = 0; r0 < blocks; r0 += 8) {
+                    uint64_t u[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        u[r] = r0 + r < blocks ? peer_load(peer(&h.all[threadIdx.x], r0 + r)) : 0;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) sum += u[r];
+                }
+            }
+        }
+        uint64_t total;
+        const uint64_t upto = block_scan(sum, &total), want = need(total);
+        if (upto - sum < want && upto >= want) {
+            s.bin = threadIdx.x;
+            s.above = upto - sum;
+            s.inside = sum;
         }
         __syncthreads();
     }
 
-    // The border of the row: the order's value at which `value` over what
-    // takes(order) accepts, summed from the top, reaches need(total).  t_of
-    // cuts the row into bins for a start (kept monotone by fp32's rounding);
-    // then the bins are stretches of the integers, until one is left.
-    // Returns false if it is never reached.  *above: the sum above the border
-    // value; *inside: at it; *want: need(total).
-    template <bool kWeights, typename A, typename V, typename N, typename B>
-    __device__ bool border(A takes, V value, N need, B t_of, uint32_t *tau, uint64_t *above, uint64_t *inside,
-                           uint64_t *want) {
-        step<kWeights>([&](uint32_t o) { return takes(o) ? t_of(o) : -1; }, value,
-                       [&](uint64_t total) { return *want = need(total); });
-        const int first_bin = s.bin;
-        if (first_bin < 0) return false;
-        uint64_t up = s.above;
-        *inside = s.inside;
-        // the least and the greatest of the bin
+    // The border in one bin of a wide step: the logit at which the counts or
+    // weights of what is listed and in_bin(logit), summed from the top after
+    // `up`, reach goal.  *above: the sum above it; *inside: at it.
+    template <bool kWeights, typename B, typename V>
+    __device__ float border(B in_bin, V value, uint64_t goal, uint64_t up, uint64_t *above, uint64_t *inside) {
+        if (threadIdx.x == 0) s.count = 0;
+        __syncthreads();
         uint32_t lo = ~0u, hi = 0;
-        each([&](int, uint32_t o) {
-            if (takes(o) && t_of(o) == first_bin) lo = min(lo, o), hi = max(hi, o);
-        });
+        for (int i = lane; i < listed; i += 32) {
+            const float l = list[i];
+            if (!in_bin(l)) continue;
+            const uint32_t o = order_of(l), n = atomicAdd(&s.count, 1u);
+            if (n < kGather) s.mine[n] = o;
+            lo = min(lo, o), hi = max(hi, o);
+        }
         lo = __reduce_min_sync(~0u, lo);
         hi = __reduce_max_sync(~0u, hi);
-        if (threadIdx.x % 32 == 0) s.key[threadIdx.x / 32] = lo, s.at[threadIdx.x / 32] = hi;
+        if (lane == 0) s.key[warp] = lo, s.at[warp] = hi;
         __syncthreads();
+        lo = __reduce_min_sync(~0u, s.key[lane]);
+        hi = __reduce_max_sync(~0u, s.at[lane]);
+        const int count = s.count, room = kGather / blocks;
+        for (int i = threadIdx.x; i < min(count, room) * blocks; i += kSampleThreads)
+            peer_store(peer(&s.gather[rank * room + i / blocks], i % blocks), s.mine[i / blocks]);
+        const uint64_t(*all)[2] = tell((uint64_t)hi << 32 | lo, count);
+        bool fits = true;
+        for (int r = 0; r < blocks; ++r) {
+            lo = min(lo, (uint32_t)all[r][0]), hi = max(hi, (uint32_t)(all[r][0] >> 32));
+            fits &= (int)all[r][1] <= room;
+        }
+        constexpr int kEach = kGather / kSampleThreads;
+        uint32_t o[kEach];
+        uint64_t v[kEach];
 #pragma unroll
-        for (int i = 0; i < kNumWarps; ++i) lo = min(lo, s.key[i]), hi = max(hi, s.at[i]);
-        const uint64_t(*all)[2] = tell(lo, hi);
-        for (int r = 0; r < blocks; ++r) lo = min(lo, (uint32_t)all[r][0]), hi = max(hi, (uint32_t)all[r][1]);
-        const uint64_t goal = *want;
+        for (int j = 0; j < kEach; ++j) {
+            const int i = threadIdx.x + j * kSampleThreads;
+            const bool there = fits && i / room < blocks && i % room < (int)all[min(i / room, blocks - 1)][1];
+            o[j] = there ? s.gather[i] : 0;
+            v[j] = there ? value(logit_of(o[j])) : 0;
+        }
+        *inside = 0;
+        if (lo == hi) {  // equal ones alone: nothing to look for, but what they come to
+            uint64_t n = 0;
+            for (int r = 0; r < blocks; ++r) n += all[r][1];
+            *inside = n * value(logit_of(lo));
+        }
         while (lo < hi) {
-            const int sh = max(0, 32 - __clz(hi - lo) - 10);  // (hi - lo) >> sh is below kBins
-            step<kWeights>([&](uint32_t o) { return takes(o) && o >= lo && o <= hi ? (int)((hi - o) >> sh) : -1; }, value,
-                           [&](uint64_t) { return goal - up; });
+            const int sh = max(0, 32 - __clz(hi - lo) - kBinBits);  // (hi - lo) >> sh is below kBins
+            auto need = [&](uint64_t) { return goal - up; };
+            if (fits) {
+                step<kWeights, false>([&](auto add) {
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j)
+                        if (hi - o[j] <= hi - lo && v[j]) add((int)((hi - o[j]) >> sh), v[j]);
+                }, need);
+            } else {  // very many equal or near ones: the lists themselves, over all blocks
+                step<kWeights, true>([&](auto add) {
+                    for (int i = lane; i < listed; i += 32) {
+                        const uint32_t k = hi - order_of(list[i]);
+                        if (k > hi - lo || !in_bin(list[i])) continue;
+                        const uint64_t x = value(list[i]);
+                        if (x) add((int)(k >> sh), x);
+                    }
+                }, need);
+            }
             const uint32_t top = hi - ((uint32_t)s.bin << sh);
-            const uint32_t low = top - lo < (1u << sh) ? lo : top - ((1u << sh) - 1);
+            lo = top - lo < (1u << sh) ? lo : top - ((1u << sh) - 1);
             hi = top;
-            lo = low;
             up += s.above;
             *inside = s.inside;
         }
-        *tau = lo;
         *above = up;
-        return true;
+        return logit_of(lo);
     }
 
-    // The place in the part where `what`, summed in the order of the indices
-    // over the whole row, reaches need; -1 in the blocks that do not hold it.
-    // *total: the row's sum.  need(total) is asked once it is known.
-    template <typename W, typename N>
-    __device__ int walk(W what, N need, uint64_t *total) {
-        const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    // The index where what(index, logit) of what is listed, summed in the order
+    // of the indices over the whole row, reaches need(sum); -1 in the blocks
+    // that do not hold it.  *total: the row's sum; *value: what() there.
+    template <typename W, typename G>
+    __device__ int walk(W what, G need, uint64_t *total, uint64_t *value) {
         uint64_t mine = 0;
-        each([&](int i, uint32_t o) { mine += what(i, o); });
-        mine = warp_sum(mine);
-        const uint64_t block = block_sum(lane == 0 ? mine : 0);
-        if (threadIdx.x == 0) s.index = -1;
+        const int start = first + warp * N * 32;
+#pragma unroll 4
+        for (int i = lane; i < listed; i += 32) mine += what(start + place[i], list[i]);
+        uint64_t block;
+        block_scan(mine, &block);
+        if (lane == 0) s.listed[warp] = listed;
         const uint64_t(*all)[2] = tell(block, 0);
         uint64_t before = 0, sum = 0;
         for (int r = 0; r < blocks; ++r) {
@@ -315,176 +363,206 @@ struct Part {
         }
         *total = sum;
         const uint64_t goal = need(sum);
-        for (int i = 0; i < w; ++i) before += s.warp[i];
-        if (before < goal && before + mine >= goal) {
-            const int per = (len + kNumWarps - 1) / kNumWarps, end = min(len, (w + 1) * per);
-            for (int i0 = w * per; i0 < end; i0 += 32) {
-                const int i = i0 + lane;
-                const uint64_t v = warp_scan(i < end ? what(i, x[i]) : 0, lane);
-                const unsigned hit = __ballot_sync(~0u, before + v >= goal);
-                if (hit) {
-                    if (lane == 0) s.index = i0 + __ffs(hit) - 1;
-                    break;
-                }
-                before += __shfl_sync(~0u, v, 31);
-            }
+        if (!(before < goal && before + block >= goal)) return -1;
+        // this block: its threads share out the list of the warp that holds it
+        const uint64_t sums = warp_scan(s.warp[lane], lane);
+        const int owner = __ffs(__ballot_sync(~0u, before + sums >= goal)) - 1;
+        const uint64_t upto = __shfl_sync(~0u, sums, (owner + 31) % 32);
+        before += owner ? upto : 0;
+        constexpr int kEach = (N * 32 + kSampleThreads - 1) / kSampleThreads;
+        static_assert(kEach == 1, "a thread a place");
+        const int to = owner - warp, n = s.listed[owner], i = threadIdx.x;
+        const int where = first + owner * N * 32 + (i < n ? place[to * N * 32 + i] : 0);
+        const uint64_t v = i < n ? what(where, list[to * N * 32 + i]) : 0;
+        uint64_t rest;
+        const uint64_t at = before + block_scan(v, &rest);
+        if (at - v < goal && at >= goal) {
+            s.index = where;
+            s.inside = v;
         }
         __syncthreads();
+        *value = s.inside;
         return s.index;
     }
 };
 
-// Values of type T from p on, n of them, as orders into to[]: 16 bytes a load
-// where p is aligned, else one by one.
-template <typename T>
-__device__ __forceinline__ void bring(const T *p, int n, uint32_t *to) {
-    constexpr int kVec = 16 / sizeof(T);
-    int done = 0;
-    if (reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-        done = n / kVec * kVec;
-#pragma unroll 4
-        for (int i = threadIdx.x * kVec; i < done; i += kSampleThreads * kVec) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
-            const T *e = reinterpret_cast<const T *>(&v);
-#pragma unroll
-            for (int j = 0; j < kVec; j += 4)
-                *reinterpret_cast<uint4 *>(to + i + j) = make_uint4(order_of(to_f32(e[j])), order_of(to_f32(e[j + 1])),
-                                                                    order_of(to_f32(e[j + 2])), order_of(to_f32(e[j + 3])));
-        }
-    }
-#pragma unroll 8
-    for (int i = done + threadIdx.x; i < n; i += kSampleThreads) to[i] = order_of(to_f32(p[i]));
-}
-
-// grid (blocks of the cluster, rows); part: how many logits a block takes.
-template <typename T>
-__global__ void __launch_bounds__(kSampleThreads, 2) k_sample(Sample a, int part) {
+// grid (blocks of the cluster, rows).
+template <typename T, int N>
+__global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    uint32_t *x = reinterpret_cast<uint32_t *>(smem + sizeof(Shared));
     pdl_trigger();
-    for (int i = threadIdx.x; i < kTable; i += kSampleThreads) s.table[i] = kPow.v[i];
+    const int c = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x < kTable) s.table[threadIdx.x] = kPow.v[threadIdx.x];
+    float *lists = reinterpret_cast<float *>(smem + sizeof(Shared));
+    uint16_t *places = reinterpret_cast<uint16_t *>(lists + N * kSampleThreads);
+    Part<N> row = {s, lists + warp * N * 32, places + warp * N * 32, (int)blockIdx.x * N * kSampleThreads, (int)gridDim.x,
+                   (int)cluster_rank(), warp, lane};
     pdl_wait();
-    const int c = blockIdx.y, lane = threadIdx.x % 32, w = threadIdx.x / 32;
-    const int first = blockIdx.x * part, len = max(0, min(part, a.V - first));
-    Part row = {s, x, first, len, (int)gridDim.x, (int)cluster_rank()};
     const float temp = a.temperature ? a.temperature[c] : 1.0f, p = a.top_p ? a.top_p[c] : 1.0f;
     const float least = a.min_p ? a.min_p[c] : 0.0f, u = a.u[c];
     const int k = a.top_k ? a.top_k[c] : 0;
-    bring(static_cast<const T *>(a.logits) + c * a.row_stride + first, len, x);
-    cluster_sync();  // and every block of the cluster runs: its shared memory may be written
-
-    // the first of the order
-    uint32_t best = 0, at = 0;
-    row.each([&](int i, uint32_t o) {
-        if (o > best) best = o, at = (uint32_t)i;
-    });
-    const uint32_t warp_best = __reduce_max_sync(~0u, best);
-    at = __reduce_min_sync(~0u, best == warp_best ? at : ~0u);
-    if (lane == 0) s.key[w] = warp_best, s.at[w] = at;
-    __syncthreads();
-    best = 0, at = 0;
+    const T *logits = static_cast<const T *>(a.logits) + c * a.row_stride;
+    const int start = row.first + warp * N * 32 + lane;
+    float x[N];
 #pragma unroll
-    for (int i = 0; i < kNumWarps; ++i)
-        if (s.key[i] > best) best = s.key[i], at = s.at[i];
-    {
-        const uint64_t(*all)[2] = row.tell(best, (uint64_t)(first + at));
-        best = 0, at = 0;
-        for (int r = 0; r < row.blocks; ++r)
-            if ((uint32_t)all[r][0] > best) best = (uint32_t)all[r][0], at = (uint32_t)all[r][1];
+    for (int j = 0; j < N; ++j) x[j] = start + j * 32 < a.V ? to_f32(logits[start + j * 32]) : -INFINITY;
+
+    // the first of the order; NaN becomes -inf, and -0 becomes +0
+    float best = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        x[j] = x[j] == x[j] ? x[j] + 0.0f : -INFINITY;
+        best = fmaxf(best, x[j]);
     }
-    if (best <= kNone || !(temp > 0.0f)) {
+    uint32_t at = ~0u;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j)
+        if (x[j] == best) at = (uint32_t)(start + j * 32);
+    uint32_t top = __reduce_max_sync(~0u, order_of(best));
+    at = __reduce_min_sync(~0u, order_of(best) == top ? at : ~0u);
+    if (lane == 0) s.key[warp] = top, s.at[warp] = at;
+    cluster_sync();  // and every block of the cluster runs: its shared memory may be written
+    top = __reduce_max_sync(~0u, s.key[lane]);
+    at = __reduce_min_sync(~0u, s.key[lane] == top ? s.at[lane] : ~0u);
+    {
+        const uint64_t(*all)[2] = row.tell(top, at);
+        top = 0;
+        for (int r = 0; r < row.blocks; ++r)
+            if ((uint32_t)all[r][0] > top) top = (uint32_t)all[r][0], at = (uint32_t)all[r][1];
+    }
+    if (top <= kNone || !(temp > 0.0f)) {
         if (threadIdx.x == 0 && row.rank == 0) {
-            a.ids[c] = best <= kNone ? -1 : (int)at;
-            if (a.probs) a.probs[c] = best <= kNone ? 0.0f : 1.0f;
+            a.ids[c] = top <= kNone ? -1 : (int)at;
+            if (a.probs) a.probs[c] = top <= kNone ? 0.0f : 1.0f;
         }
         return;
     }
     const int top_at = (int)at;
-    const double per = fmin(1.4426950408889634 / (double)temp, 1e30);
+    constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500011e-8f;
     Scale sc;
-    sc.top = logit_of(best);
-    sc.hi = (float)per;
-    sc.lo = (float)(per - (double)sc.hi);
+    sc.top = logit_of(top);
+    sc.hi = fminf(kLog2eHi / temp, 1e30f);
+    sc.lo = sc.hi < 1e30f && temp < INFINITY ? (__fmaf_rn(-sc.hi, temp, kLog2eHi) + kLog2eLo) / temp : 0.0f;
 
-    // bins of 1/21 of a power of two of the weight; the last takes the rest
-    const float cut = sc.hi * 21.0f;
-    auto t_of = [&](uint32_t o) {
-        return o == best ? 0 : min(__float2int_rz((sc.top - logit_of(o)) * cut), kBins - 1);
-    };
-    auto mass = [&](uint32_t o) { return weight(logit_of(o), sc, s.table); };
-    uint32_t tau = kNone + 1;  // kept: above tau, and the first `ties` at it (all, if ~0)
-    uint64_t ties = ~0ull, above, inside, want;
-    if (k > 0 && k < a.V) {
-        uint32_t to;
-        if (row.border<false>([](uint32_t o) { return o > kNone; }, [](uint32_t) { return (uint64_t)1; },
-                              [&](uint64_t) { return (uint64_t)k; }, t_of, &to, &above, &inside, &want)) {
-            tau = to;
-            ties = (uint64_t)k - above < inside ? (uint64_t)k - above : ~0ull;
-        }
+    // bins of 1/10.5 of a power of two of the weight; the last takes the rest
+    const float cut = sc.hi * (kBins / 48.6f);
+    auto t_of = [&](float l) { return l == sc.top ? 0 : min(__float2int_rz((sc.top - l) * cut), kBins - 1); };
+    auto mass = [&](float l) { return weight(l, sc, s.table); };
+    auto one = [](float) { return (uint64_t)1; };
+    // the least weight that min-p keeps, and a logit surely below it (or below any mass), which is not weighed
+    const uint64_t floor_w = least > 0.0f ? (least < 1.0f ? share(kOne, least, true) : least > 1.0f ? ~0ull : kOne) : 0;
+    const float floor_y = least > 0.0f ? log2f(least) - 0.01f : -47.0f;
+    auto heavy = [&](float l) { return (l - sc.top) * sc.hi >= floor_y || l == sc.top; };
+
+    // a histogram of the whole row, by counts for top-k or else by weights for top-p, and the bin of the border
+    bool by_k = k > 0 && k < a.V;
+    const bool by_p = p < 1.0f, weighed = by_p && !by_k;  // (weights first only where top-k cuts nothing)
+    int bin = kBins - 1;
+    uint64_t want = 0, above = 0, inside = 0;
+    auto goal = [&](uint64_t mass_of) { return max(share(mass_of, fmaxf(p, 0.0f), true), (uint64_t)1); };
+    if (by_k) {
+        row.template step<false, true>([&](auto add) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (x[j] > -INFINITY) add(t_of(x[j]), 1);
+        }, [&](uint64_t) { return (uint64_t)k; });
+        by_k = s.bin >= 0;
+        if (by_k) bin = s.bin, above = s.above;
+    } else if (weighed) {
+        row.template step<true, true>([&](auto add) {
+#pragma unroll
+            for (int j0 = 0; j0 < N; j0 += 4) {  // four chains of arithmetic at a time
+                uint64_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = mass(x[j0 + j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (v[j]) add(t_of(x[j0 + j]), v[j]);
+            }
+        }, [&](uint64_t total) { return want = goal(total); });
+        bin = s.bin;
+        above = s.above;
     }
-    if (p < 1.0f) {
+
+    // the list of what may still be kept
+    const bool all_of = by_k || by_p;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const bool in = x[j] > -INFINITY && (all_of ? t_of(x[j]) <= bin : heavy(x[j]));
+        const unsigned who = __ballot_sync(~0u, in);
+        const int to = row.listed + __popc(who & ((1u << lane) - 1));
+        if (in) row.list[to] = x[j], row.place[to] = (uint16_t)(j * 32 + lane);
+        row.listed += __popc(who);
+    }
+    __syncwarp();
+
+    float tau = -INFINITY;  // kept: above tau, and the first `ties` at it (all, if ~0)
+    uint64_t ties = ~0ull;
+    if (by_k) {
+        tau = row.template border<false>([&](float l) { return t_of(l) == bin; }, one, (uint64_t)k, above, &above, &inside);
+        ties = (uint64_t)k - above < inside ? (uint64_t)k - above : ~0ull;
+    }
+    if (by_p) {
         // with a cut among the equals at tau, those weigh `ties` times one of them: the border is looked for above them
         const bool part_of = ties != ~0ull;
-        const uint64_t rest = part_of ? ties * mass(tau) : 0;
-        const uint32_t from = part_of ? tau + 1 : tau;
-        uint64_t all = 0;  // the mass from there on
-        auto goal = [&](uint64_t total) {
-            all = total;
-            const double g = ceil(fmax((double)p, 0.0) * (double)(total + rest));
-            return g < 1.0 ? (uint64_t)1 : (uint64_t)g;
-        };
-        uint32_t to;
-        if (row.border<true>([&](uint32_t o) { return o >= from; }, mass, goal, t_of, &to, &above, &inside, &want)) {
-            const uint64_t one = mass(to);
-            tau = to;
-            ties = (want - above + one - 1) / one;
-            if (ties * one >= inside) ties = ~0ull;
+        auto takes = [&](float l) { return l > tau || (l == tau && !part_of); };
+        uint64_t all = 0;  // the mass of what is looked at
+        if (!weighed) {
+            const uint64_t rest = part_of ? ties * mass(tau) : 0;
+            row.template step<true, true>([&](auto add) {
+                for (int i = lane; i < row.listed; i += 32) {
+                    const uint64_t v = takes(row.list[i]) ? mass(row.list[i]) : 0;
+                    if (v) add(t_of(row.list[i]), v);
+                }
+            }, [&](uint64_t total) {
+                all = total;
+                return want = goal(total + rest);
+            });
+            bin = s.bin;
+            above = s.above;
+        }
+        if (bin >= 0) {
+            tau = row.template border<true>([&](float l) { return takes(l) && t_of(l) == bin; }, mass, want, above, &above, &inside);
+            const uint64_t each = mass(tau);
+            ties = (want - above + each - 1) / each;
+            if (ties * each >= inside) ties = ~0ull;
         } else {  // among the equals
-            const uint64_t one = mass(tau);
-            ties = min(ties, (want - all + one - 1) / one);
+            const uint64_t each = mass(tau);
+            ties = min(ties, (want - all + each - 1) / each);
         }
     }
     int last = a.V;  // the index of the last kept one at tau
+    uint64_t total, value;
     if (ties != ~0ull) {
-        uint64_t total;
-        const int i = row.walk([&](int, uint32_t o) { return (uint64_t)(o == tau); }, [&](uint64_t) { return ties; }, &total);
-        const uint64_t(*all)[2] = row.tell(i < 0 ? 0 : (uint64_t)(first + i) + 1, 0);
+        const int i = row.walk([&](int, float l) { return (uint64_t)(l == tau); }, [&](uint64_t) { return ties; }, &total, &value);
+        const uint64_t(*all)[2] = row.tell((uint64_t)(i + 1), 0);
         uint64_t got = 0;
         for (int r = 0; r < row.blocks; ++r) got = max(got, all[r][0]);
         last = (int)got - 1;
     }
-    const double floor_w = (double)least * (double)kOne;
-    const float floor_y = least > 0.0f ? log2f(least) - 0.01f : -INFINITY;  // surely below: not weighed
-    auto kept = [&](int i, uint32_t o) -> uint64_t {
-        if (o < tau || (o == tau && first + i > last)) return 0;
-        if ((logit_of(o) - sc.top) * sc.hi < floor_y && o != best) return 0;
-        const uint64_t v = mass(o);
-        return (double)v >= floor_w || !(floor_w > 0.0) || first + i == top_at ? v : 0;
-    };
-    uint64_t total;
-    const int i = row.walk(kept, [&](uint64_t sum) {
-        const uint64_t g = (uint64_t)(fmin(fmax((double)u, 0.0), 1.0) * (double)sum) + 1;
-        return g < sum ? g : sum;
-    }, &total);
+    const int i = row.walk([&](int at, float l) -> uint64_t {
+        if (!(l > tau || (l == tau && at <= last)) || !heavy(l)) return 0;
+        const uint64_t v = mass(l);
+        return v >= floor_w || at == top_at ? v : 0;
+    }, [&](uint64_t sum) { return min(share(sum, fminf(fmaxf(u, 0.0f), 1.0f), false) + 1, sum); }, &total, &value);
     if (i >= 0 && threadIdx.x == 0) {
-        a.ids[c] = first + i;
-        if (a.probs) a.probs[c] = (float)((double)kept(i, x[i]) / (double)total);
+        a.ids[c] = i;
+        if (a.probs) a.probs[c] = (float)((double)value / (double)total);
     }
 }
 
-template <typename T>
-cudaError_t launch(const Sample &a, cudaStream_t s) {
-    // blocks of a row: more of them for a longer row, up to the portable eight
-    const int blocks = a.V <= 4096 ? 1 : a.V <= 16384 ? 2 : a.V <= 49152 ? 4 : 8;
-    const int part = ((a.V + blocks - 1) / blocks + 7) / 8 * 8;  // whole vectors, so each part is aligned as the row is
-    const size_t smem = sizeof(Shared) + (size_t)part * sizeof(uint32_t);
-    cudaError_t e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, int N>
+cudaError_t launch_part(const Sample &a, int blocks, cudaStream_t s) {
+    constexpr int kSmem = sizeof(Shared) + N * kSampleThreads * (sizeof(float) + sizeof(uint16_t));
+    cudaError_t e = cudaFuncSetAttribute(k_sample<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess && blocks > 8)
+        e = cudaFuncSetAttribute(k_sample<T, N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.n);
     cfg.blockDim = dim3(kSampleThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -494,8 +572,20 @@ cudaError_t launch(const Sample &a, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sample<T>, a, part);
+    return cudaLaunchKernelEx(&cfg, k_sample<T, N>, a);
 }
+
+template <typename T>
+cudaError_t launch(const Sample &a, cudaStream_t s) {
+    // Sixteen logits a thread where there are rows enough to fill the GPU, else eight in twice the blocks
+    const int most = a.n <= 8 ? 16 : 8;
+    int blocks = 1;
+    while (blocks < most && blocks * 8 * kSampleThreads < a.V) blocks *= 2;
+    if (blocks * 8 * kSampleThreads >= a.V) return launch_part<T, 8>(a, blocks, s);
+    while (blocks * 16 * kSampleThreads < a.V) blocks *= 2;
+    return launch_part<T, 16>(a, blocks, s);
+}
+static_assert(CBQ_SAMPLE_MAX_V <= kMaxBlocks * 16 * kSampleThreads, "the longest row fits a cluster");
 
 }  // namespace
 
