@@ -126,10 +126,14 @@ __device__ __forceinline__ uint64_t peer_load(uint32_t a) {
 
 // Sums by bin.  Weights are added in three 16-bit parts (a block adds fewer
 // than 2^16 of them, so 32 bits hold each part's sum; 64-bit atomics on shared
-// memory are loops), counts in part[0]; all[] is the whole.
+// memory are loops), counts in part[0]; mine[] is the block's whole, all[] the
+// cluster's.
 struct Hist {
-    uint32_t part[3][kBins];
-    uint64_t all[kBins];
+    union {
+        uint32_t part[3][kBins];
+        uint64_t all[kBins];
+    };
+    uint64_t mine[kBins];
 };
 
 struct alignas(16) Shared {
@@ -184,9 +188,10 @@ struct Part {
     int listed = 0;         // of this warp
     int turn = 0, use = 0;  // which of the two swap buffers and histograms is next
 
-    // Every block gives two numbers (the same in all its threads) and gets all
-    // blocks'.  A buffer is written again two calls later: all have read it by then.
-    __device__ const uint64_t (*tell(uint64_t a, uint64_t b))[2] {
+    // Every block gives two numbers (the same in all its threads); lane r of
+    // each warp gets block r's, {0, 0} past the last.  A buffer is written again
+    // two calls later: all have read it by then.
+    __device__ ulonglong2 tell(uint64_t a, uint64_t b) {
         uint64_t(*to)[2] = s.swap[turn];
         turn ^= 1;
         if (threadIdx.x < (unsigned)blocks) {
@@ -194,7 +199,7 @@ struct Part {
             peer_store(peer(&to[rank][1], threadIdx.x), b);
         }
         cluster_sync();
-        return to;
+        return lane < blocks ? make_ulonglong2(to[lane][0], to[lane][1]) : make_ulonglong2(0, 0);
     }
 
     // The inclusive sum of v over the threads before and this one; *total: over
@@ -242,21 +247,20 @@ struct Part {
             sum = h.part[0][threadIdx.x];
             if constexpr (kWeights)
                 sum += ((uint64_t)h.part[1][threadIdx.x] << 16) + ((uint64_t)h.part[2][threadIdx.x] << 32);
-            if constexpr (kWide) h.all[threadIdx.x] = sum;
+            if constexpr (kWide) h.mine[threadIdx.x] = sum;
         }
         if constexpr (kWide) {
+            // each block adds up a share of the bins over all blocks and hands the sums out: a load and a store a
+            // thread (all bins of all blocks read by each block took twice as long: 14 bytes a clock come from others)
             cluster_sync();
+            const int r = threadIdx.x & (blocks - 1), b = (rank * kBins + (int)threadIdx.x) / blocks;
             if (threadIdx.x < kBins) {
-                sum = 0;
-                for (int r0 = 0; r0 < blocks; r0 += 8) {
-                    uint64_t u[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        u[r] = r0 + r < blocks ? peer_load(peer(&h.all[threadIdx.x], r0 + r)) : 0;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) sum += u[r];
-                }
+                sum = peer_load(peer(&h.mine[b], r));
+                for (int o = blocks / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                peer_store(peer(&h.all[b], r), sum);
             }
+            cluster_sync();
+            sum = threadIdx.x < kBins ? h.all[threadIdx.x] : 0;
         }
         uint64_t total;
         const uint64_t upto = block_scan(sum, &total), want = need(total);
@@ -292,27 +296,24 @@ struct Part {
         const int count = s.count, room = kGather / blocks;
         for (int i = threadIdx.x; i < min(count, room) * blocks; i += kSampleThreads)
             peer_store(peer(&s.gather[rank * room + i / blocks], i % blocks), s.mine[i / blocks]);
-        const uint64_t(*all)[2] = tell((uint64_t)hi << 32 | lo, count);
-        bool fits = true;
-        for (int r = 0; r < blocks; ++r) {
-            lo = min(lo, (uint32_t)all[r][0]), hi = max(hi, (uint32_t)(all[r][0] >> 32));
-            fits &= (int)all[r][1] <= room;
-        }
+        const ulonglong2 all = tell((uint64_t)hi << 32 | lo, count);
+        lo = __reduce_min_sync(~0u, lane < blocks ? (uint32_t)all.x : ~0u);
+        hi = __reduce_max_sync(~0u, (uint32_t)(all.x >> 32));
+        const bool fits = __all_sync(~0u, (int)all.y <= room);
         constexpr int kEach = kGather / kSampleThreads;
         uint32_t o[kEach];
         uint64_t v[kEach];
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             const int i = threadIdx.x + j * kSampleThreads;
-            const bool there = fits && i / room < blocks && i % room < (int)all[min(i / room, blocks - 1)][1];
+            // (32 threads in a row look at one block's room, which is a multiple of that)
+            const bool there = fits && i % room < (int)__shfl_sync(~0u, (uint32_t)all.y, i / room);
             o[j] = there ? s.gather[i] : 0;
             v[j] = there ? value(logit_of(o[j])) : 0;
         }
         *inside = 0;
         if (lo == hi) {  // equal ones alone: nothing to look for, but what they come to
-            uint64_t n = 0;
-            for (int r = 0; r < blocks; ++r) n += all[r][1];
-            *inside = n * value(logit_of(lo));
+            *inside = __reduce_add_sync(~0u, (uint32_t)all.y) * value(logit_of(lo));
         }
         while (lo < hi) {
             const int sh = max(0, 32 - __clz(hi - lo) - kBinBits);  // (hi - lo) >> sh is below kBins
@@ -355,12 +356,8 @@ struct Part {
         uint64_t block;
         block_scan(mine, &block);
         if (lane == 0) s.listed[warp] = listed;
-        const uint64_t(*all)[2] = tell(block, 0);
-        uint64_t before = 0, sum = 0;
-        for (int r = 0; r < blocks; ++r) {
-            if (r < rank) before += all[r][0];
-            sum += all[r][0];
-        }
+        const uint64_t upto_block = warp_scan(tell(block, 0).x, lane), sum = __shfl_sync(~0u, upto_block, 31);
+        uint64_t before = __shfl_sync(~0u, upto_block, rank) - block;
         *total = sum;
         const uint64_t goal = need(sum);
         if (!(before < goal && before + block >= goal)) return -1;
@@ -426,10 +423,9 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     top = __reduce_max_sync(~0u, s.key[lane]);
     at = __reduce_min_sync(~0u, s.key[lane] == top ? s.at[lane] : ~0u);
     {
-        const uint64_t(*all)[2] = row.tell(top, at);
-        top = 0;
-        for (int r = 0; r < row.blocks; ++r)
-            if ((uint32_t)all[r][0] > top) top = (uint32_t)all[r][0], at = (uint32_t)all[r][1];
+        const ulonglong2 all = row.tell(top, at);
+        top = __reduce_max_sync(~0u, (uint32_t)all.x);
+        at = __reduce_min_sync(~0u, (uint32_t)all.x == top ? (uint32_t)all.y : ~0u);
     }
     if (top <= kNone || !(temp > 0.0f)) {
         if (threadIdx.x == 0 && row.rank == 0) {
@@ -536,10 +532,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     uint64_t total, value;
     if (ties != ~0ull) {
         const int i = row.walk([&](int, float l) { return (uint64_t)(l == tau); }, [&](uint64_t) { return ties; }, &total, &value);
-        const uint64_t(*all)[2] = row.tell((uint64_t)(i + 1), 0);
-        uint64_t got = 0;
-        for (int r = 0; r < row.blocks; ++r) got = max(got, all[r][0]);
-        last = (int)got - 1;
+        last = (int)__reduce_max_sync(~0u, (uint32_t)row.tell((uint64_t)(i + 1), 0).x) - 1;
     }
     const int i = row.walk([&](int at, float l) -> uint64_t {
         if (!(l > tau || (l == tau && at <= last)) || !heavy(l)) return 0;
