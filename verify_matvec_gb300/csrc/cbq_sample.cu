@@ -103,8 +103,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The address of p, a place in this block's shared memory, in block r of the cluster.
 __device__ __forceinline__ uint32_t peer(const void *p, uint32_t r) {
@@ -140,11 +143,11 @@ struct alignas(16) Shared {
     uint64_t table[kTable];
     Hist hist[2];
     uint64_t swap[2][kMaxBlocks][2];  // what the blocks of the cluster tell one another
-    uint64_t warp[kNumWarps];
+    uint64_t warp[kNumWarps], upto[kNumWarps];  // sums of the warps, and inclusive sums of those
     uint32_t key[kNumWarps], at[kNumWarps], listed[kNumWarps];
     uint32_t mine[kGather];           // the border's bin: this block's, and everyone's
     uint32_t gather[kGather];
-    uint64_t above, inside;
+    uint64_t above, inside, goal;
     int bin, index;
     uint32_t count;
 };
@@ -202,17 +205,22 @@ struct Part {
         return lane < blocks ? make_ulonglong2(to[lane][0], to[lane][1]) : make_ulonglong2(0, 0);
     }
 
-    // The inclusive sum of v over the threads before and this one; *total: over
-    // all; s.warp[]: the warps' inclusive sums.
-    __device__ uint64_t block_scan(uint64_t v, uint64_t *total) {
-        v = warp_scan(v, lane);
+    // s.upto from a sum a warp (shuffles of 64 bits are dear: one warp does them).
+    __device__ void sum_warps(uint64_t v) {
         __syncthreads();
         if (lane == 31) s.warp[warp] = v;
         __syncthreads();
-        const uint64_t sums = warp_scan(s.warp[lane], lane);
-        *total = __shfl_sync(~0u, sums, 31);
-        const uint64_t before = __shfl_sync(~0u, sums, (warp + 31) % 32);
-        return v + (warp ? before : 0);
+        if (warp == 0) s.upto[lane] = warp_scan(s.warp[lane], lane);
+        __syncthreads();
+    }
+
+    // The inclusive sum of v over the threads before and this one; *total: over
+    // all.  Only the first `warps` warps have any.
+    __device__ uint64_t block_scan(uint64_t v, int warps, uint64_t *total) {
+        v = warp < warps ? warp_scan(v, lane) : 0;
+        sum_warps(v);
+        *total = s.upto[31];
+        return v + (warp ? s.upto[warp - 1] : 0);
     }
 
     // A step of a descent: fill(add) calls add(bin, value) for what takes part,
@@ -263,7 +271,7 @@ struct Part {
             sum = threadIdx.x < kBins ? h.all[threadIdx.x] : 0;
         }
         uint64_t total;
-        const uint64_t upto = block_scan(sum, &total), want = need(total);
+        const uint64_t upto = block_scan(sum, kBins / 32, &total), want = need(total);
         if (upto - sum < want && upto >= want) {
             s.bin = threadIdx.x;
             s.above = upto - sum;
@@ -349,30 +357,42 @@ struct Part {
     // that do not hold it.  *total: the row's sum; *value: what() there.
     template <typename W, typename G>
     __device__ int walk(W what, G need, uint64_t *total, uint64_t *value) {
-        uint64_t mine = 0;
         const int start = first + warp * N * 32;
-#pragma unroll 4
-        for (int i = lane; i < listed; i += 32) mine += what(start + place[i], list[i]);
-        uint64_t block;
-        block_scan(mine, &block);
+        uint64_t mine = 0;
+        for (int i0 = 0; i0 < listed; i0 += 128) {  // four chains of arithmetic at a time
+            uint64_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * 32 + lane;
+                v[j] = i < listed ? what(start + place[i], list[i]) : 0;
+            }
+            mine += v[0] + v[1] + v[2] + v[3];
+        }
+        // at most 2^50 a lane: the sum of a warp in two halves
+        sum_warps((uint64_t)__reduce_add_sync(~0u, (uint32_t)mine & 0xFFFFFFu) +
+                  ((uint64_t)__reduce_add_sync(~0u, (uint32_t)(mine >> 24)) << 24));
         if (lane == 0) s.listed[warp] = listed;
-        const uint64_t upto_block = warp_scan(tell(block, 0).x, lane), sum = __shfl_sync(~0u, upto_block, 31);
-        uint64_t before = __shfl_sync(~0u, upto_block, rank) - block;
-        *total = sum;
-        const uint64_t goal = need(sum);
+        const uint64_t block = s.upto[31], other = tell(block, 0).x;
+        if (warp == 0) {
+            const uint64_t upto = warp_scan(other, lane), sum = __shfl_sync(~0u, upto, 31);
+            const uint64_t before = __shfl_sync(~0u, upto, rank) - block, goal = need(sum);
+            if (lane == 0) s.above = before, s.inside = sum, s.goal = goal;
+        }
+        __syncthreads();
+        uint64_t before = s.above;
+        const uint64_t goal = s.goal;
+        *total = s.inside;
         if (!(before < goal && before + block >= goal)) return -1;
         // this block: its threads share out the list of the warp that holds it
-        const uint64_t sums = warp_scan(s.warp[lane], lane);
-        const int owner = __ffs(__ballot_sync(~0u, before + sums >= goal)) - 1;
-        const uint64_t upto = __shfl_sync(~0u, sums, (owner + 31) % 32);
-        before += owner ? upto : 0;
+        const int owner = __ffs(__ballot_sync(~0u, before + s.upto[lane] >= goal)) - 1;
+        before += owner ? s.upto[owner - 1] : 0;
         constexpr int kEach = (N * 32 + kSampleThreads - 1) / kSampleThreads;
         static_assert(kEach == 1, "a thread a place");
         const int to = owner - warp, n = s.listed[owner], i = threadIdx.x;
         const int where = first + owner * N * 32 + (i < n ? place[to * N * 32 + i] : 0);
         const uint64_t v = i < n ? what(where, list[to * N * 32 + i]) : 0;
         uint64_t rest;
-        const uint64_t at = before + block_scan(v, &rest);
+        const uint64_t at = before + block_scan(v, N, &rest);
         if (at - v < goal && at >= goal) {
             s.index = where;
             s.inside = v;
@@ -388,6 +408,7 @@ template <typename T, int N>
 __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
+    cluster_arrive();
     pdl_trigger();
     const int c = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (threadIdx.x < kTable) s.table[threadIdx.x] = kPow.v[threadIdx.x];
@@ -419,7 +440,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     uint32_t top = __reduce_max_sync(~0u, order_of(best));
     at = __reduce_min_sync(~0u, order_of(best) == top ? at : ~0u);
     if (lane == 0) s.key[warp] = top, s.at[warp] = at;
-    cluster_sync();  // and every block of the cluster runs: its shared memory may be written
+    __syncthreads();
+    cluster_wait();  // every block of the cluster runs: its shared memory may be written
     top = __reduce_max_sync(~0u, s.key[lane]);
     at = __reduce_min_sync(~0u, s.key[lane] == top ? s.at[lane] : ~0u);
     {
@@ -535,9 +557,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         last = (int)__reduce_max_sync(~0u, (uint32_t)row.tell((uint64_t)(i + 1), 0).x) - 1;
     }
     const int i = row.walk([&](int at, float l) -> uint64_t {
-        if (!(l > tau || (l == tau && at <= last)) || !heavy(l)) return 0;
         const uint64_t v = mass(l);
-        return v >= floor_w || at == top_at ? v : 0;
+        return (l > tau || (l == tau && at <= last)) && (v >= floor_w || at == top_at) ? v : 0;
     }, [&](uint64_t sum) { return min(share(sum, fminf(fmaxf(u, 0.0f), 1.0f), false) + 1, sum); }, &total, &value);
     if (i >= 0 && threadIdx.x == 0) {
         a.ids[c] = i;
