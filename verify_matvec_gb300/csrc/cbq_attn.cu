@@ -9,47 +9,13 @@
 // cut into chunks, a block each, so that a few sequences fill the GPU; a
 // second kernel joins the chunks' (m, sum, o) of a row.
 #include <algorithm>
-#include <type_traits>
 
-#include "cbq_device.cuh"
-#include "step/cbq_step.h"
-#include "step/cbq_types.cuh"
+#include "cbq_pipe.cuh"
+#include "step/cbq_attn.cuh"
 
 namespace cbq {
 
 namespace {
-
-constexpr int kMaxDim = 256;
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-
-// What a block needs to know of a sequence, with everything out of range cut.
-struct Seq {
-    int64_t row0;  // its first row of q
-    int n, ctx, len;
-};
-
-__device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool report) {
-    const int64_t room = (int64_t)a.table_width * a.c.page_size;
-    const int64_t b0 = a.start[s], b1 = a.start[s + 1];
-    const int64_t most = a.max_len < room ? a.max_len : room;
-    int64_t n = b1 - b0, ctx = a.ctx[s];
-    bool cut = n > a.max_tok || ctx < 0;
-    if (b0 < 0 || b1 > a.total_tok || n < 0) {
-        n = 0;
-        cut = true;
-    }
-    if (n > a.max_tok) n = a.max_tok;
-    if (ctx < 0) ctx = 0;
-    cut |= ctx + n > most;
-    if (cut && report && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_LENGTH);
-    return Seq{b0, (int)n, (int)(ctx < most ? ctx : most), (int)(ctx + n < most ? ctx + n : most)};
-}
-
-// Bits of the drafts that row's token sees, none beyond the sequence's own.
-__device__ __forceinline__ uint64_t seen_drafts(const TreeAttention &a, const Seq &q, int64_t row) {
-    const int k = q.len - q.ctx;
-    return (uint64_t)a.mask[row] & (k >= 64 ? ~0ull : (1ull << k) - 1);
-}
 
 // Any head size and any strides: one warp per (token, head), the lanes hold
 // the head's values, a key at a time.  grid (q_heads, max_tok, n_seq).
@@ -110,15 +76,6 @@ __global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
 
 // ------------------------------------------------- the tensor-core kernel --
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16 bytes to shared memory, or 16 zero bytes where put is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool put) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(put ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -138,22 +95,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-}
-__device__ __forceinline__ float pow2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // Sizes of the kernel for head size D and 16 * WR rows a block.  Four warps:
 // WR of them share out the rows, and 4 / WR the keys of a tile.  Rows of a
 // tile are padded by 16 bytes, which puts the eight rows of an ldmatrix into
@@ -176,7 +117,8 @@ struct Shape {
     static_assert(kKeys % 16 == 0, "16 keys a product");
 };
 
-// Chunk c of one (sequence, kv head, row tile): see the top of the file.
+// Chunk c of one (sequence, kv head, row tile): see the top of the file.  With
+// tail >= 0 the drafts alone, into slot `tail` of the parts.
 // Scores and sums are fp32; the weights 2^(x-m) are rounded to the cache's 16
 // bits for the product with v (the tensor cores take no mixed types), so a
 // weight is off by half a step, and the sum they are divided by is not
@@ -189,23 +131,25 @@ struct Shape {
 // zeroed and added by hand to the rows that see it.
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
-    k_tree_attention(TreeAttention a, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml) {
+    k_tree_attention(TreeAttention a, int chunk, int tail, int row_tiles, float *part_o, float2 *part_ml) {
     using S = Shape<D, WR>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t valid[S::kStages][4];
     __shared__ uint64_t drafts[S::kRows];
     __shared__ float2 ml[S::kParts][S::kRows];
-    pdl_trigger();
+    if (tail < 0) pdl_trigger();
     pdl_wait();
+    if (tail >= 0) pdl_trigger();  // not before: the wide kernel behind this one reads its inputs without a wait of its own
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
+    const bool whole = tail < 0;
     const int group = a.q_heads / a.c.kv_heads;
     const Seq sq = sequence(a, s, tid == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, S::kRows);
-    const int begin = c * chunk, end = min(sq.len, begin + chunk);
+    const int begin = whole ? c * chunk : sq.ctx, end = whole ? min(sq.len, begin + chunk) : sq.len;
     // a row that has no keys at all is written by its first block
     if (rows <= 0 || (begin >= end && c > 0)) return;
-    const int chunks = max(1, (sq.len + chunk - 1) / chunk);  // of this sequence
+    const bool alone = whole && sq.len <= chunk;  // the only chunk of this sequence
 
     // q of the block's rows (row r: token r / group, head r % group of the group), the sign of the scale with it
     const float sc = fabsf(a.scale) * kLog2e;
@@ -466,8 +410,8 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
         const int64_t row = (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group;
-        if (chunks > 1) {
-            const int64_t at = (int64_t)c * a.total_tok * a.q_heads + row;
+        if (!alone) {
+            const int64_t at = (int64_t)(whole ? c : tail) * a.total_tok * a.q_heads + row;
             *reinterpret_cast<float4 *>(part_o + at * D + d) = v;
             if (d == 0) part_ml[at] = make_float2(top, sum);
             continue;
@@ -484,18 +428,20 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
 }
 
 // The chunks of a row joined: one warp per (token, head).  grid
-// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.
+// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.  With tail >= 0 the chunks hold
+// the committed keys, and slot `tail` the drafts.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, const float *part_o, const float2 *part_ml) {
+__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, int tail, const float *part_o, const float2 *part_ml) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, h = blockIdx.x * 4 + threadIdx.x / 32, i = blockIdx.y;
     const Seq sq = sequence(a, blockIdx.z, false);
-    const int chunks = (sq.len + chunk - 1) / chunk;
-    if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;
+    const int own = ((tail < 0 ? sq.len : sq.ctx) + chunk - 1) / chunk, chunks = own + (tail < 0 ? 0 : 1);
+    if (i >= sq.n || h >= a.q_heads || (tail < 0 && chunks <= 1)) return;
+    auto slot = [&](int c) { return c < own ? c : tail; };
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
     float top = -INFINITY;
-    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[c * step + row].x);
+    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[slot(c) * step + row].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     constexpr int kEach = D / 32;
@@ -503,11 +449,11 @@ __global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, c
     if (top != -INFINITY) {
 #pragma unroll 4
         for (int c = 0; c < chunks; ++c) {
-            const float2 p = part_ml[c * step + row];
+            const float2 p = part_ml[slot(c) * step + row];
             const float f = pow2(p.x - top);
             sum += p.y * f;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(c * step + row) * D + j * 32 + lane];
+            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(slot(c) * step + row) * D + j * 32 + lane];
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -520,20 +466,39 @@ __global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, c
 }
 
 // How a call is cut: rows of a block (16 * wr), tiles of them, and the chunk
-// of keys a block takes.
+// of keys a block takes.  wide: the committed keys by the wide kernel (256 rows
+// a block), the drafts by this one.
 struct Plan {
     int wr, row_tiles, chunk, n_chunks;
+    bool wide;
+    int wide_tiles;
+    int slots() const { return wide ? n_chunks + 1 : n_chunks; }
 };
 
-Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads) {
-    Plan p;
+constexpr int kSms = 152;
+
+Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, int head_dim) {
+    Plan p = {};
     const int rows = max_tok * (q_heads / kv_heads);
     p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.row_tiles = (rows + 16 * p.wr - 1) / (16 * p.wr);
-    // two blocks for each of 152 SMs; with several sequences, whose lengths may differ, at most 2048 keys each
-    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
-    int64_t n = (304 + blocks - 1) / blocks;
-    if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
+    p.wide = rows > 64 && head_dim <= 128 && max_len >= 1024;
+    int64_t n = 1;
+    if (p.wide) {
+        p.wide_tiles = (rows + kWideRows - 1) / kWideRows;
+        // a chunk costs a block about 10 ns a key and 6 us for its results: the n with the least time over all waves
+        const int64_t blocks = (int64_t)n_seq * kv_heads * p.wide_tiles;
+        double least = 0.0;
+        for (int64_t m = 1; m <= 64; ++m) {
+            const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)max_len / m * 0.01 + 6.0);
+            if (m == 1 || t < least) least = t, n = m;
+        }
+    } else {
+        // two blocks for each SM; with several sequences, whose lengths may differ, at most 2048 keys each
+        const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
+        n = (2 * kSms + blocks - 1) / blocks;
+        if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
+    }
     n = std::min<int64_t>(n, 65535);  // of the grid's second axis
     int64_t chunk = (max_len + n - 1) / n;
     chunk = std::max<int64_t>((chunk + 63) / 64 * 64, 128);
@@ -544,37 +509,19 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads) {
 
 bool tiled_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
-// Launches kernel<<<grid, threads, smem>>> as a programmatic dependent of the
-// work ahead.
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, (P)args...);
-}
-
 template <typename T, int D, int WR>
 cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) {
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
-    float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
-    const cudaError_t e = launch(k_tree_attention<T, D, WR>, dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
-                                 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml);
+    float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.slots() * sizeof(float2) + 15) / 16 * 16);
+    const int tail = p.wide ? p.n_chunks : -1;
+    cudaError_t e = launch_dependent(k_tree_attention<T, D, WR>,
+                                     dim3((unsigned)(a.c.kv_heads * p.row_tiles), p.wide ? 1u : (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                                     128, Shape<D, WR>::kSmem, s, a, p.chunk, tail, p.row_tiles, part_o, part_ml);
+    if (e == cudaSuccess && p.wide) e = launch_tree_wide(a, p.chunk, p.n_chunks, p.wide_tiles, part_o, part_ml, s);
     if (e != cudaSuccess || p.n_chunks == 1) return e;
-    return launch(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s,
-                  a, p.chunk, part_o, part_ml);
+    return launch_dependent(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s,
+                            a, p.chunk, tail, part_o, part_ml);
 }
 
 template <typename T, int D>
@@ -587,12 +534,13 @@ cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
     // 16-byte copies want every row of k and v on a 16-byte boundary, 16-byte stores every row of out
     const uintptr_t ends = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | reinterpret_cast<uintptr_t>(a.out);
     if (tiled_dim(a.c.head_dim) && ends % 16 == 0 && (a.c.page_stride | a.c.tok_stride | a.c.head_stride) % 8 == 0) {
-        const Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads);
+        Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads, a.c.head_dim);
+        if (a.scale == 0.0f) p.wide = false;  // its masked scores are -inf before the scaling
         if (a.c.head_dim == 64) return launch_dim<T, 64>(a, p, s);
         if (a.c.head_dim == 128) return launch_dim<T, 128>(a, p, s);
         return launch_dim<T, 256>(a, p, s);
     }
-    return launch(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, a);
+    return launch_dependent(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, a);
 }
 
 }  // namespace
@@ -600,9 +548,9 @@ cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
 size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
                                 int head_dim) {
     if (!tiled_dim(head_dim)) return 16;
-    const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads);
-    if (p.n_chunks == 1) return 16;
-    const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
+    const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads, head_dim);
+    if (p.slots() == 1) return 16;
+    const size_t rows = (size_t)total_tok * q_heads * p.slots();
     return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
 }
 
