@@ -117,8 +117,7 @@ struct Shape {
     static_assert(kKeys % 16 == 0, "16 keys a product");
 };
 
-// Chunk c of one (sequence, kv head, row tile): see the top of the file.  With
-// tail >= 0 the drafts alone, into slot `tail` of the parts.
+// Chunk c of one (sequence, kv head, row tile): see the top of the file.
 // Scores and sums are fp32; the weights 2^(x-m) are rounded to the cache's 16
 // bits for the product with v (the tensor cores take no mixed types), so a
 // weight is off by half a step, and the sum they are divided by is not
@@ -131,25 +130,23 @@ struct Shape {
 // zeroed and added by hand to the rows that see it.
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
-    k_tree_attention(TreeAttention a, int chunk, int tail, int row_tiles, float *part_o, float2 *part_ml) {
+    k_tree_attention(TreeAttention a, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
     using S = Shape<D, WR>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t valid[S::kStages][4];
     __shared__ uint64_t drafts[S::kRows];
     __shared__ float2 ml[S::kParts][S::kRows];
-    if (tail < 0) pdl_trigger();
+    pdl_trigger();
     pdl_wait();
-    if (tail >= 0) pdl_trigger();  // not before: the wide kernel behind this one reads its inputs without a wait of its own
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
-    const bool whole = tail < 0;
     const int group = a.q_heads / a.c.kv_heads;
     const Seq sq = sequence(a, s, tid == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, S::kRows);
-    const int begin = whole ? c * chunk : sq.ctx, end = whole ? min(sq.len, begin + chunk) : sq.len;
+    const int begin = c * chunk, end = min(sq.len, begin + chunk);
     // a row that has no keys at all is written by its first block
     if (rows <= 0 || (begin >= end && c > 0)) return;
-    const bool alone = whole && sq.len <= chunk;  // the only chunk of this sequence
+    const bool alone = sq.len <= chunk;  // the only chunk of this sequence
 
     // q of the block's rows (row r: token r / group, head r % group of the group), the sign of the scale with it
     const float sc = fabsf(a.scale) * kLog2e;
@@ -411,7 +408,7 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
         }
         const int64_t row = (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group;
         if (!alone) {
-            const int64_t at = (int64_t)(whole ? c : tail) * a.total_tok * a.q_heads + row;
+            const int64_t at = (int64_t)c * a.total_tok * a.q_heads + row;
             *reinterpret_cast<float4 *>(part_o + at * D + d) = v;
             if (d == 0) part_ml[at] = make_float2(top, sum);
             continue;
@@ -428,20 +425,19 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
 }
 
 // The chunks of a row joined: one warp per (token, head).  grid
-// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.  With tail >= 0 the chunks hold
-// the committed keys, and slot `tail` the drafts.
+// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.  The wide kernel cuts the
+// committed keys alone (and takes the drafts with the last chunk).
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, int tail, const float *part_o, const float2 *part_ml) {
+__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, h = blockIdx.x * 4 + threadIdx.x / 32, i = blockIdx.y;
     const Seq sq = sequence(a, blockIdx.z, false);
-    const int own = ((tail < 0 ? sq.len : sq.ctx) + chunk - 1) / chunk, chunks = own + (tail < 0 ? 0 : 1);
-    if (i >= sq.n || h >= a.q_heads || (tail < 0 && chunks <= 1)) return;
-    auto slot = [&](int c) { return c < own ? c : tail; };
+    const int chunks = ((wide ? sq.ctx : sq.len) + chunk - 1) / chunk;
+    if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
     float top = -INFINITY;
-    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[slot(c) * step + row].x);
+    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[c * step + row].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     constexpr int kEach = D / 32;
@@ -449,11 +445,11 @@ __global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, i
     if (top != -INFINITY) {
 #pragma unroll 4
         for (int c = 0; c < chunks; ++c) {
-            const float2 p = part_ml[slot(c) * step + row];
+            const float2 p = part_ml[c * step + row];
             const float f = pow2(p.x - top);
             sum += p.y * f;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(slot(c) * step + row) * D + j * 32 + lane];
+            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(c * step + row) * D + j * 32 + lane];
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -465,14 +461,11 @@ __global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, i
     if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-// How a call is cut: rows of a block (16 * wr), tiles of them, and the chunk
-// of keys a block takes.  wide: the committed keys by the wide kernel (256 rows
-// a block), the drafts by this one.
+// How a call is cut: rows of a block (16 * wr, or the wide kernel's 256), tiles
+// of them, and the chunk of keys a block takes.
 struct Plan {
-    int wr, row_tiles, chunk, n_chunks;
     bool wide;
-    int wide_tiles;
-    int slots() const { return wide ? n_chunks + 1 : n_chunks; }
+    int wr, row_tiles, chunk, n_chunks;
 };
 
 constexpr int kSms = 152;
@@ -480,14 +473,14 @@ constexpr int kSms = 152;
 Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, int head_dim) {
     Plan p = {};
     const int rows = max_tok * (q_heads / kv_heads);
-    p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.row_tiles = (rows + 16 * p.wr - 1) / (16 * p.wr);
     p.wide = rows > 64 && head_dim <= 128 && max_len >= 1024;
     int64_t n = 1;
+    p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    const int block_rows = p.wide ? kWideRows : 16 * p.wr;
+    p.row_tiles = (rows + block_rows - 1) / block_rows;
+    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
     if (p.wide) {
-        p.wide_tiles = (rows + kWideRows - 1) / kWideRows;
         // a chunk costs a block about 10 ns a key and 6 us for its results: the n with the least time over all waves
-        const int64_t blocks = (int64_t)n_seq * kv_heads * p.wide_tiles;
         double least = 0.0;
         for (int64_t m = 1; m <= 64; ++m) {
             const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)max_len / m * 0.01 + 6.0);
@@ -495,7 +488,6 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
         }
     } else {
         // two blocks for each SM; with several sequences, whose lengths may differ, at most 2048 keys each
-        const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
         n = (2 * kSms + blocks - 1) / blocks;
         if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
     }
@@ -513,15 +505,14 @@ template <typename T, int D, int WR>
 cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) {
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
-    float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.slots() * sizeof(float2) + 15) / 16 * 16);
-    const int tail = p.wide ? p.n_chunks : -1;
-    cudaError_t e = launch_dependent(k_tree_attention<T, D, WR>,
-                                     dim3((unsigned)(a.c.kv_heads * p.row_tiles), p.wide ? 1u : (unsigned)p.n_chunks, (unsigned)a.n_seq),
-                                     128, Shape<D, WR>::kSmem, s, a, p.chunk, tail, p.row_tiles, part_o, part_ml);
-    if (e == cudaSuccess && p.wide) e = launch_tree_wide(a, p.chunk, p.n_chunks, p.wide_tiles, part_o, part_ml, s);
+    float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
+    const cudaError_t e = p.wide ? launch_tree_wide(a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
+                                 : launch_dependent(k_tree_attention<T, D, WR>,
+                                                    dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                                                    128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1) return e;
     return launch_dependent(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s,
-                            a, p.chunk, tail, part_o, part_ml);
+                            a, p.chunk, p.wide, part_o, part_ml);
 }
 
 template <typename T, int D>
@@ -534,8 +525,7 @@ cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
     // 16-byte copies want every row of k and v on a 16-byte boundary, 16-byte stores every row of out
     const uintptr_t ends = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | reinterpret_cast<uintptr_t>(a.out);
     if (tiled_dim(a.c.head_dim) && ends % 16 == 0 && (a.c.page_stride | a.c.tok_stride | a.c.head_stride) % 8 == 0) {
-        Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads, a.c.head_dim);
-        if (a.scale == 0.0f) p.wide = false;  // its masked scores are -inf before the scaling
+        const Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads, a.c.head_dim);
         if (a.c.head_dim == 64) return launch_dim<T, 64>(a, p, s);
         if (a.c.head_dim == 128) return launch_dim<T, 128>(a, p, s);
         return launch_dim<T, 256>(a, p, s);
@@ -549,8 +539,8 @@ size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64
                                 int head_dim) {
     if (!tiled_dim(head_dim)) return 16;
     const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads, head_dim);
-    if (p.slots() == 1) return 16;
-    const size_t rows = (size_t)total_tok * q_heads * p.slots();
+    if (p.n_chunks == 1) return 16;
+    const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
     return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
 }
 

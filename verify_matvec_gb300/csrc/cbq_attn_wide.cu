@@ -1,7 +1,6 @@
-// cbq_attn_wide.cu -- the tree attention's committed keys for many rows: more
-// than 64 rows a kv head are bound by the matrix products, which run here on
-// the 5th-generation tensor cores (tcgen05) with scores, weights and results
-// in tensor memory.
+// cbq_attn_wide.cu -- the tree attention for many rows: more than 64 rows a kv
+// head are bound by the matrix products, which run here on the 5th-generation
+// tensor cores (tcgen05) with scores, weights and results in tensor memory.
 //
 // A block takes 256 rows of one kv head as two groups of 128 (or, where there
 // are no more than 128, the even and the odd key tiles for the same rows) and
@@ -13,9 +12,13 @@
 //   O += P V (128 x D, tensor memory x shared memory).
 // O is scaled down only when a row's maximum has grown by 2^8 (fp16: 2^5):
 // until then the weights are just larger, and the last division takes it out.
-// Roles: warps 0..3 and 4..7 the two groups, 8 and 9 the copies, 10 and 11 the
-// products of a group each (waiting, issuing and committing takes a warp longer
-// than the products themselves: one warp for both groups was the bound).
+// The drafts are a tile of their own, the last of a sequence: a row's weights
+// follow its mask there, and a value row with NaN or infinities, which some
+// rows may not see (0 * v would be NaN), is zeroed in shared memory by the
+// copying warp and added by hand to the rows that see it.
+// Roles: warps 0..3 and 4..7 the two groups, 8 and 9 the copies, 10 the scores'
+// products and 11 the sums' (waiting, issuing and committing takes a warp as
+// long as the products themselves: one warp for both was the bound).
 // Tiles lie in shared memory as 8 x 16-byte core matrices (row / 8, column /
 // 16 bytes): eight rows' 16 bytes are 128 bytes in a row, so the copies of
 // eight keys fill them without bank conflicts, and the same tile serves as K
@@ -30,23 +33,25 @@ namespace {
 constexpr int kGroup = 128;                   // rows of a group
 constexpr int kTile = 64;                     // keys of a tile
 constexpr int kStages = 5;
-constexpr int kCopyWarp = 8, kMmaWarp = 10, kWideThreads = 12 * 32;  // (more warps would leave 128 registers a thread)
+constexpr int kCopyWarp = 8, kScoreWarp = 10, kSumWarp = 11, kWideThreads = 12 * 32;  // (more warps would leave 128 registers a thread)
 constexpr int kTmemCols = 512;
 
-// Columns of tensor memory: scores, weights, results of a group.
+// Columns of tensor memory: a group's scores, two items' (the weights of an
+// item take the place of its scores), and its results.
 template <int D>
 struct Cols {
-    static constexpr uint32_t s(int g) { return g * kTile; }
-    static constexpr uint32_t p(int g) { return 2 * kTile + g * (kTile / 2); }
-    static constexpr uint32_t o(int g) { return 3 * kTile + g * D; }
+    static constexpr uint32_t s(int g, int b) { return (2 * g + b) * kTile; }
+    static constexpr uint32_t o(int g) { return 4 * kTile + g * D; }
     static_assert(o(2) <= kTmemCols, "the tensor memory holds both groups");
 };
 
 struct WideShared {
     uint64_t full[kStages], empty[kStages];   // a tile's copies have landed; its products are done
-    uint64_t scored[2], taken[2], weighed[2], summed[2];  // of a group's item: S is there, S is read, P is there, O has it
+    // of a group's item: S is there; P is there; O has it (even and odd items apart where the next may come first)
+    uint64_t scored[2][2], weighed[2], summed[2][2];
     uint64_t done[2];
     uint32_t valid[kStages][2];               // keys of a tile that exist, 32 a copying warp
+    uint32_t odd[2];                          // drafts whose values are not all finite
     uint32_t tmem_slot;
     int abort;
     float2 ml[kGroup];
@@ -106,8 +111,19 @@ __device__ __forceinline__ void tm_st(uint32_t at, const uint32_t (&v)[32]) {
 }
 #undef CBQ_R8
 #undef CBQ_I8
+// One column, there on return.
+__device__ __forceinline__ uint32_t tm_ld1(uint32_t at) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // The eight warps of the two groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -143,46 +159,48 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    k_tree_wide(const __grid_constant__ TreeAttention a, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml) {
+    k_tree_wide(const __grid_constant__ TreeAttention a, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
     constexpr uint32_t kCol = 128, kRow = D / 8 * 128;       // bytes between core matrices along a row, and to the next eight rows
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WideShared sh;
     pdl_trigger();
+    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kWideRows, c = blockIdx.y, s = blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;
-    const Seq sq = sequence(a, s, false);  // (the drafts' kernel has reported)
+    const Seq sq = sequence(a, s, threadIdx.x == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, kWideRows);
     const int begin = c * chunk, end = min(sq.ctx, begin + chunk);
-    if (rows <= 0 || (begin >= end && n_chunks > 1)) {
-        pdl_wait();  // what follows this kernel counts on the drafts' kernel being done
-        return;
-    }
+    if (rows <= 0 || (begin >= end && c > 0)) return;
+    const bool last = end == sq.ctx, alone = last && c == 0;  // with the drafts; the only chunk
     const bool split = rows <= kGroup;  // the groups share out the key tiles
-    const int tiles = max(0, (end - begin + kTile - 1) / kTile), items = split ? tiles : 2 * tiles;
-    if (warp == kMmaWarp) {
+    const int old_tiles = (end - begin + kTile - 1) / kTile, tiles = old_tiles + (last ? 1 : 0);
+    const int items = split ? tiles : 2 * tiles;
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem_slot)), "n"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 64 + 2);  // the copying threads' copies, and their warps' word on valid[]
-            mbar_init(smem_addr(&sh.empty[i]), split ? 1 : 2);
+            mbar_init(smem_addr(&sh.empty[i]), 1);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(smem_addr(&sh.scored[g]), 1);
-            mbar_init(smem_addr(&sh.taken[g]), 4);
+            mbar_init(smem_addr(&sh.scored[g][0]), 2);  // the products, and the word of their warp, which has seen the tile's valid[]
+            mbar_init(smem_addr(&sh.scored[g][1]), 2);
             mbar_init(smem_addr(&sh.weighed[g]), 4);
-            mbar_init(smem_addr(&sh.summed[g]), 1);
+            mbar_init(smem_addr(&sh.summed[g][0]), 1);
+            mbar_init(smem_addr(&sh.summed[g][1]), 1);
         }
         mbar_init(smem_addr(&sh.done[0]), 1);
         mbar_init(smem_addr(&sh.done[1]), 1);
         sh.abort = 0;
+        sh.odd[0] = sh.odd[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // q of the rows, the sign of the scale with it; absent rows are zero
-    const float sc = fabsf(a.scale) * kLog2e;
+    const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1e-45f);  // (not zero: -inf times that would be NaN)
     const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     for (int i = tid; i < (split ? 1 : 2) * kGroup * (D / 8); i += kWideThreads) {
@@ -209,114 +227,168 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     fence_after();
     const uint32_t tmem = sh.tmem_slot;
     const uint32_t q_at = smem_addr(smem), ring = q_at + 2 * kQBytes;
+    const int32_t *table = a.table + (int64_t)s * a.table_width;
 
-    if (warp >= kCopyWarp && warp < kMmaWarp) {
+    if (warp >= kCopyWarp && warp < kScoreWarp) {
         // copies: a warp brings 32 keys of each tile; lane l keeps the place of key l
         const int cw = warp - kCopyWarp;
-        const int32_t *table = a.table + (int64_t)s * a.table_width;
         const int64_t head = kvh * a.c.head_stride;
+        // the place of this lane's key of tile t, -1 where there is none
+        auto place = [&](int t) {
+            const int p = (t < old_tiles ? begin + t * kTile : sq.ctx) + cw * 32 + lane;
+            return t < tiles && p < (t < old_tiles ? end : sq.len) ? p : -1;
+        };
         auto page_of = [&](int t) {
-            const int p = begin + t * kTile + cw * 32 + lane;
-            return t < tiles && p < end ? table[(uint32_t)p / (uint32_t)a.c.page_size] : -1;
+            const int p = place(t);
+            return p >= 0 ? table[(uint32_t)p / (uint32_t)a.c.page_size] : -1;
         };
         Place put;
         // lane l copies 16 bytes of key l % 8 of every eight, at columns l / 8, l / 8 + 4, ..: whole sectors are read
         const char *from0 = static_cast<const char *>(a.c.k) + lane / 8 * 16;
         const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k);
         const uint32_t to0 = ring + cw * 4 * kRow + lane / 8 * kCol + lane % 8 * 16;
-        int page = page_of(0);
-        for (int t = 0; t < tiles; ++t, put.step(1)) {
-            if (t >= kStages && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
-            const uint32_t p = begin + t * kTile + cw * 32 + lane;
-            const bool in = p < (uint32_t)end, good = in && page >= 0 && page < a.c.n_pages;
-            if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-            const int64_t at = good ? (page * a.c.page_stride + (int64_t)(p % (uint32_t)a.c.page_size) * a.c.tok_stride + head) * 2 : -1;
-            const uint32_t bits = __ballot_sync(~0u, good);
-            page = page_of(t + 1);
-            const uint32_t to = to0 + put.slot * 2 * kTileBytes;
+        // Page ids are loaded four tiles ahead: a load returns behind the copies issued before it.
+        int pages[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int64_t off = __shfl_sync(~0u, at, h * 8 + lane % 8);
-                const char *from = from0 + max(off, (int64_t)0);
+        for (int j = 0; j < 4; ++j) pages[j] = page_of(j);
+        bool ok = true;
+        for (int t0 = 0; t0 < tiles && ok; t0 += 4) {
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    copy16(to + h * kRow + d * 4 * kCol, from + d * 64, off >= 0);
-                    copy16(to + kTileBytes + h * kRow + d * 4 * kCol, from + to_v + d * 64, off >= 0);
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + j, page = pages[j];
+                if (t >= tiles || !ok) break;
+                if (t >= kStages) ok = warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err);
+                if (!ok) break;
+                const int p = place(t);
+                const bool in = p >= 0, good = in && page >= 0 && page < a.c.n_pages;
+                if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+                const int64_t at = good ? (page * a.c.page_stride + (int64_t)((uint32_t)p % (uint32_t)a.c.page_size) * a.c.tok_stride + head) * 2 : -1;
+                const uint32_t bits = __ballot_sync(~0u, good);
+                pages[j] = page_of(t + 4);
+                const uint32_t to = to0 + put.slot * 2 * kTileBytes;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int64_t off = __shfl_sync(~0u, at, h * 8 + lane % 8);
+                    const char *from = from0 + max(off, (int64_t)0);
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d) {
+                        copy16(to + h * kRow + d * 4 * kCol, from + d * 64, off >= 0);
+                        copy16(to + kTileBytes + h * kRow + d * 4 * kCol, from + to_v + d * 64, off >= 0);
+                    }
                 }
-            }
-            // arrives when this thread's copies have landed.  (Their writes are handed to the tensor cores by the fence of
-            // the warp that issues the products; a fence here would wait for every copy under way.)
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.full[put.slot])) : "memory");
-            if (lane == 0) {
-                sh.valid[put.slot][cw] = bits;
-                mbar_arrive(smem_addr(&sh.full[put.slot]));
+                if (t >= old_tiles) {  // the drafts: a value row with NaN or infinities is taken out
+                    copy_commit();
+                    copy_wait<0>();
+                    __syncwarp();
+                    constexpr uint32_t kExp = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;  // all ones: not finite
+                    uint8_t *v = smem + 2 * kQBytes + (put.slot * 2 + 1) * kTileBytes + (cw * 4 + lane / 8) * kRow + lane % 8 * 16;
+                    bool odd = false;
+#pragma unroll 4
+                    for (int d = 0; d < D / 8; ++d) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(v + d * kCol);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t z = w == 0 ? y.x : w == 1 ? y.y : w == 2 ? y.z : y.w;
+                            odd |= (z & kExp) == kExp || (z >> 16 & kExp) == kExp;
+                        }
+                    }
+                    const uint32_t odds = __ballot_sync(~0u, odd);
+                    if (odds) {
+                        if (lane == 0) sh.odd[cw] = odds;
+                        if (odd)
+                            for (int d = 0; d < D / 8; ++d) *reinterpret_cast<uint4 *>(v + d * kCol) = make_uint4(0, 0, 0, 0);
+                        proxy_fence();
+                        __syncwarp();
+                    }
+                }
+                // arrives when this thread's copies have landed.  (Their writes are handed to the tensor cores by the fence
+                // of the warp that issues the products; a fence here would wait for every copy under way.)
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.full[put.slot])) : "memory");
+                if (lane == 0) {
+                    sh.valid[put.slot][cw] = bits;
+                    mbar_arrive(smem_addr(&sh.full[put.slot]));
+                }
+                put.step(1);
             }
         }
         copy_commit();
         copy_wait<0>();
-    } else if (warp >= kMmaWarp) {
-        const int g = warp - kMmaWarp, by = split ? 2 : 1, last = (items - g + 1) / 2;  // items of this group
-        const uint32_t at = q_at + (split ? 0 : g) * kQBytes, s_at = tmem + Cols<D>::s(g), p_at = tmem + Cols<D>::p(g);
-        Place k, v;  // of the tiles of the next scores and of the next sums
-        if (split && g) k.step(1), v.step(1);
-        auto score = [&]() {  // the next S
-            if (!warp_wait(sh, sh.full[k.slot], k.round & 1, a.err)) return false;
-            proxy_fence();
-            fence_after();
-            const uint32_t k_at = ring + k.slot * 2 * kTileBytes;
+    } else if (warp >= kScoreWarp) {
+        // item i: group i % 2, tile i (keys shared out) or i / 2
+        bool ok = true;
+        Place at;
+        if (warp == kScoreWarp) {
+            for (int i = 0; i < items; ++i) {
+                const int g = i & 1, n = i >> 1, b = n & 1;
+                if (split || g == 0) {
+                    ok = warp_wait(sh, sh.full[at.slot], at.round & 1, a.err);
+                    if (!ok) break;
+                    proxy_fence();
+                }
+                // into the place of the weights two items back, once they are in O
+                if (n >= 2) ok = warp_wait(sh, sh.summed[g][b], (n >> 1 & 1) ^ 1, a.err);
+                if (!ok) break;
+                fence_after();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.scored[g][b]));
+                const uint32_t q = q_at + (split ? 0 : g) * kQBytes, k_at = ring + at.slot * 2 * kTileBytes;
+                const uint32_t s_at = tmem + Cols<D>::s(g, b);
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-                mma_ss(s_at, tile_desc(at + j * 2 * kCol, kCol, kRow), tile_desc(k_at + j * 2 * kCol, kCol, kRow),
-                       wide_idesc<T, kTile, false>(), j > 0);
-            commit(sh.scored[g]);
-            k.step(by);
-            return true;
-        };
-        bool ok = last == 0 || score();
-        for (int n = 0; n < last && ok; ++n) {
-            // the group's next scores as soon as these have been read: they are there when its weights are done
-            ok = n + 1 >= last || (warp_wait(sh, sh.taken[g], n & 1, a.err) && score());
-            ok = ok && warp_wait(sh, sh.weighed[g], n & 1, a.err);
-            if (!ok) break;
-            fence_after();
-            const uint32_t v_at = ring + (v.slot * 2 + 1) * kTileBytes;
+                for (int j = 0; j < D / 16; ++j)
+                    mma_ss(s_at, tile_desc(q + j * 2 * kCol, kCol, kRow), tile_desc(k_at + j * 2 * kCol, kCol, kRow),
+                           wide_idesc<T, kTile, false>(), j > 0);
+                commit(sh.scored[g][b]);
+                if (split || g == 1) at.step(1);
+            }
+        } else {
+            for (int i = 0; i < items; ++i) {
+                const int g = i & 1, n = i >> 1;
+                ok = warp_wait(sh, sh.weighed[g], n & 1, a.err);
+                if (!ok) break;
+                fence_after();
+                const uint32_t v_at = ring + (at.slot * 2 + 1) * kTileBytes, p_at = tmem + Cols<D>::s(g, n & 1);
 #pragma unroll
-            for (int j = 0; j < kTile / 16; ++j)
-                mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2 * kRow, kRow, kCol), wide_idesc<T, D, true>(), n > 0 || j > 0);
-            commit(sh.summed[g]);
-            commit(sh.empty[v.slot]);
-            v.step(by);
+                for (int j = 0; j < kTile / 16; ++j)
+                    mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2 * kRow, kRow, kCol), wide_idesc<T, D, true>(),
+                           n > 0 || j > 0);
+                commit(sh.summed[g][n & 1]);
+                if (split || g == 1) {
+                    commit(sh.empty[at.slot]);
+                    at.step(1);
+                }
+            }
         }
         // every product is done before the tensor memory is freed
-        commit(sh.done[g]);
+        uint64_t &done = sh.done[warp - kScoreWarp];
+        commit(done);
         const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(smem_addr(&sh.done[g]), 0u) && global_ns() - t0 < kWaitLimitNs) {}
+        while (!mbar_try_wait(smem_addr(&done), 0u) && global_ns() - t0 < kWaitLimitNs) {}
     } else {
         // weights: thread = row of its group
         const int g = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
         constexpr float kLower = std::is_same_v<T, __half> ? 10.0f : 0.0f, kGrow = std::is_same_v<T, __half> ? 5.0f : 8.0f;
         float m = -INFINITY, l = 0.0f;  // weights are 2^(x - m): m is the maximum less kLower, or up to kGrow below that
+        const int row_in = (split ? 0 : g * kGroup) + r;
+        const bool live = row_in < rows;
+        const int64_t tok = sq.row0 + (r0 + (live ? row_in : 0)) / group;
+        const uint64_t sees = live ? seen_drafts(a, sq, tok) : 0;
         bool ok = true;
         int n = 0;  // items of this group so far
         Place at;
         if (split && g) at.step(1);
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
-            ok = warp_wait(sh, sh.scored[g], n & 1, a.err);
+            ok = warp_wait(sh, sh.scored[g][n & 1], n >> 1 & 1, a.err);
             if (!ok) break;
             fence_after();
             uint32_t x[2][32];
-            tm_ld(lanes + Cols<D>::s(g), x[0]);
-            tm_ld(lanes + Cols<D>::s(g) + 32, x[1]);
-            // which keys there are (for the copies' writes to be seen, the wait is theirs too)
-            ok = warp_wait(sh, sh.full[slot], at.round & 1, a.err);
-            const uint32_t there[2] = {sh.valid[slot][0], sh.valid[slot][1]};
+            const uint32_t s_at = lanes + Cols<D>::s(g, 0) + (n & 1) * kTile;
+            tm_ld(s_at, x[0]);
+            tm_ld(s_at + 32, x[1]);
+            uint32_t there[2] = {sh.valid[slot][0], sh.valid[slot][1]};
+            if ((split ? i : i >> 1) >= old_tiles) there[0] &= (uint32_t)sees, there[1] &= (uint32_t)(sees >> 32);
             tm_wait_ld();
             if (!ok) break;
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.taken[g]));
             if ((there[0] & there[1]) != ~0u) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -326,48 +398,71 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j >> 5][j & 31]));
+            for (int j = 0; j < 64; j += 2)
+                top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1]));
             const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc - kLower;
             const bool grown = now > m + kGrow || (m == -INFINITY && now > -INFINITY);
             const float keep = grown ? pow2(m - now) : 1.0f;
             if (grown) m = now, l *= keep;
-            if (n > 0) {
-                // the products with the weights before are done: O may be scaled, and P written
-                ok = warp_wait(sh, sh.summed[g], (n - 1) & 1, a.err);
+            if (n > 0 && __any_sync(~0u, grown)) {
+                // O is scaled, once the products before are in it
+                ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
                 if (!ok) break;
                 fence_after();
-                if (__any_sync(~0u, grown)) {
 #pragma unroll
-                    for (int d = 0; d < D; d += 32) {
-                        uint32_t o[32];
-                        tm_ld(lanes + Cols<D>::o(g) + d, o);
-                        tm_wait_ld();
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    tm_ld(lanes + Cols<D>::o(g) + d, o);
+                    tm_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                        tm_st(lanes + Cols<D>::o(g) + d, o);
-                    }
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                    tm_st(lanes + Cols<D>::o(g) + d, o);
                 }
             }
             const float less = m == -INFINITY ? 0.0f : -m;
-            float sum[4] = {};
+            const float2 sc2 = make_float2(sc, sc), less2 = make_float2(less, less);
+            float2 sum[2] = {};
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                const float w0 = pow2(__fmaf_rn(__uint_as_float(x[j >> 4][2 * j & 31]), sc, less));
-                const float w1 = pow2(__fmaf_rn(__uint_as_float(x[j >> 4][2 * j + 1 & 31]), sc, less));
-                sum[j & 1] += w0;
-                sum[2 + (j & 1)] += w1;
-                p[j] = pack2<T>(w0, w1);
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), sc2, less2);
+                const float2 w = make_float2(pow2(y.x), pow2(y.y));
+                sum[j & 1] = __fadd2_rn(sum[j & 1], w);
+                p[j] = pack2<T>(w.x, w.y);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tm_st(lanes + Cols<D>::p(g), p);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tm_st(s_at, p);
             tm_wait_st();
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.weighed[g]));
         }
-        if (ok && n > 0) ok = warp_wait(sh, sh.summed[g], (n - 1) & 1, a.err);
+        if (ok && n > 0) ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
         fence_after();
+        // The value rows taken out above, to the rows that see them: the weight of draft j is still in its place.
+        if (ok && n > 0 && last && (split ? (tiles - 1) % 2 == g : true)) {
+            for (uint64_t odd = (uint64_t)sh.odd[1] << 32 | sh.odd[0]; odd; odd &= odd - 1) {
+                const int j = __ffsll((long long)odd) - 1;
+                const uint32_t p = sq.ctx + j;
+                const T *v = static_cast<const T *>(a.c.v) + table[p / (uint32_t)a.c.page_size] * a.c.page_stride +
+                             (int64_t)(p % (uint32_t)a.c.page_size) * a.c.tok_stride + kvh * a.c.head_stride;
+                const uint32_t two = tm_ld1(lanes + Cols<D>::s(g, 0) + ((n - 1) & 1) * kTile + j / 2);
+                uint16_t half = (uint16_t)(j & 1 ? two >> 16 : two);
+                const float w = to_f32(*reinterpret_cast<const T *>(&half));
+#pragma unroll
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    tm_ld(lanes + Cols<D>::o(g) + d, o);
+                    tm_wait_ld();
+                    if (sees >> j & 1)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + w * to_f32(v[d + e]));
+                    __syncwarp();
+                    tm_st(lanes + Cols<D>::o(g) + d, o);
+                    tm_wait_st();
+                }
+            }
+        }
         // Where the groups shared out the keys, group 1's part goes to group 0 through the ring.
         float *pass = reinterpret_cast<float *>(smem + 2 * kQBytes) + r * (D + 4);
         groups_sync();  // all products of both are done: the ring is free
@@ -384,22 +479,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
         groups_sync();
-        const int row_in = (split ? 0 : g * kGroup) + r;
         if (!(split && g == 1)) {
-            const bool live = row_in < rows;
-            const int64_t row = live ? (sq.row0 + (r0 + row_in) / group) * a.q_heads + kvh * group + (r0 + row_in) % group : 0;
-            const int64_t step = a.total_tok * a.q_heads;
-            // up to three parts of the row: this group's, the other group's, and the drafts' where this is the only chunk
-            float2 other = make_float2(-INFINITY, 0.0f), draft = make_float2(-INFINITY, 0.0f);
+            const int64_t row = tok * a.q_heads + kvh * group + (r0 + (live ? row_in : 0)) % group;
+            float2 other = make_float2(-INFINITY, 0.0f);  // the other group's part of the row
             if (split && items > 1) other = sh.ml[r];
-            pdl_wait();
-            const bool last = n_chunks == 1;
-            if (last && live) draft = part_ml[step + row];
-            const float top = fmaxf(fmaxf(m, other.x), draft.x);
-            const float f0 = n == 0 || top == -INFINITY ? 0.0f : pow2(m - top);
-            const float f1 = top == -INFINITY ? 0.0f : pow2(other.x - top), f2 = top == -INFINITY ? 0.0f : pow2(draft.x - top);
-            const float sum = l * f0 + other.y * f1 + draft.y * f2;
-            const float inv = !last ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float top = fmaxf(m, other.x);
+            const float f0 = n == 0 || top == -INFINITY ? 0.0f : pow2(m - top), f1 = top == -INFINITY ? 0.0f : pow2(other.x - top);
+            const float sum = l * f0 + other.y * f1;
+            const float inv = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int64_t part = (int64_t)c * a.total_tok * a.q_heads + row;
 #pragma unroll
             for (int d = 0; d < D; d += 32) {
                 uint32_t o[32];
@@ -407,30 +495,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tm_wait_ld();
                 if (live && ok) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    float v[4];
-                    const float4 y = split && items > 1 ? *reinterpret_cast<const float4 *>(pass + d + j) : make_float4(0, 0, 0, 0);
-                    const float4 z = last ? *reinterpret_cast<const float4 *>(part_o + (step + row) * D + d + j) : make_float4(0, 0, 0, 0);
+                    for (int j = 0; j < 32; j += 8) {
+                        float v[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float ye = e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w, ze = e == 0 ? z.x : e == 1 ? z.y : e == 2 ? z.z : z.w;
-                        // (what was never written may hold anything: it is not multiplied)
-                        const float own = n == 0 ? 0.0f : __uint_as_float(o[j + e]) * f0;
-                        v[e] = (own + ye * f1 + ze * f2) * inv;
+                        for (int e = 0; e < 8; ++e)  // (what was never written may hold anything: it is not multiplied)
+                            v[e] = n == 0 ? 0.0f : __uint_as_float(o[j + e]) * f0;
+                        if (split && items > 1) {
+                            const float4 y0 = *reinterpret_cast<const float4 *>(pass + d + j), y1 = *reinterpret_cast<const float4 *>(pass + d + j + 4);
+                            v[0] += y0.x * f1, v[1] += y0.y * f1, v[2] += y0.z * f1, v[3] += y0.w * f1;
+                            v[4] += y1.x * f1, v[5] += y1.y * f1, v[6] += y1.z * f1, v[7] += y1.w * f1;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] *= inv;
+                        if (alone && !a.out_f32) {
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + d + j) =
+                                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+                        } else {
+                            float4 *to = reinterpret_cast<float4 *>(alone ? static_cast<float *>(a.out) + row * D + d + j : part_o + part * D + d + j);
+                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
                     }
-                    if (!last) {
-                        *reinterpret_cast<float4 *>(part_o + (c * step + row) * D + d + j) = make_float4(v[0], v[1], v[2], v[3]);
-                    } else if (a.out_f32) {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d + j) = make_float4(v[0], v[1], v[2], v[3]);
-                    } else {
-                        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * D + d + j) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-                    }
-                }
                 }
                 __syncwarp();
             }
             if (live && ok) {
-                if (!last) part_ml[c * step + row] = make_float2(top, sum);
+                if (!alone) part_ml[part] = make_float2(top, sum);
                 else if (a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
         }
@@ -439,7 +529,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kScoreWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
 }
 
@@ -448,7 +538,7 @@ cudaError_t launch_wide(const TreeAttention &a, int chunk, int n_chunks, int row
     constexpr size_t kSmem = 2 * kGroup * D * 2 + kStages * 2 * kTile * D * 2;
     static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
     return launch_dependent(k_tree_wide<T, D>, dim3((unsigned)(a.c.kv_heads * row_tiles), (unsigned)n_chunks, (unsigned)a.n_seq),
-                            kWideThreads, kSmem, s, a, chunk, n_chunks, row_tiles, part_o, part_ml);
+                            kWideThreads, kSmem, s, a, chunk, row_tiles, part_o, part_ml);
 }
 
 }  // namespace

@@ -87,9 +87,8 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
 }
 
 // The wide kernel (cbq_attn_wide.cu; head sizes 64 and 128): 256 rows of a kv
-// head a block, the committed keys from c * chunk on in block c.  The drafts'
-// part lies in slot n_chunks of part_o and part_ml.  With one chunk it writes
-// the results, with more its parts.
+// head a block, the committed keys from c * chunk on in block c, and the drafts
+// in the sequence's last.
 constexpr int kWideRows = 256;
 cudaError_t launch_tree_wide(const TreeAttention &a, int chunk, int n_chunks, int row_tiles, float *part_o,
                              float2 *part_ml, cudaStream_t s);
