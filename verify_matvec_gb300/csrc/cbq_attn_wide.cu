@@ -19,10 +19,12 @@
 // Roles: warps 0..3 and 4..7 the two groups, 8 and 9 the copies, 10 the scores'
 // products and 11 the sums' (waiting, issuing and committing takes a warp as
 // long as the products themselves: one warp for both was the bound).
-// Tiles lie in shared memory as 8 x 16-byte core matrices (row / 8, column /
-// 16 bytes): eight rows' 16 bytes are 128 bytes in a row, so the copies of
-// eight keys fill them without bank conflicts, and the same tile serves as K
-// (columns are the summed axis) and as V (rows are).
+// Tiles lie in shared memory in halves of 64 columns, 128 bytes a row, the 16-
+// byte pieces of a row permuted by the row (128-byte swizzle): a copy takes
+// whole 128-byte lines of four keys and meets no bank conflict, and the same
+// tile serves as K (columns are the summed axis) and as V (rows are).  (With
+// eight keys' 64 bytes a copy, as unpermuted core matrices want them, the
+// copies were the bound: 2,100 clocks a tile for 1,700.)
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
@@ -57,11 +59,12 @@ struct WideShared {
     float2 ml[kGroup];
 };
 
-// Descriptor of a tile in shared memory: 16-byte units; `lead` between core
-// matrices along the summed axis for rows-are-outputs operands.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t at, uint32_t lead, uint32_t stride) {
-    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+// Descriptor of a tile in shared memory with 128-byte rows, swizzled: eight
+// rows are 1024 bytes; `lead` bytes to the next 64 columns where rows are the
+// summed axis.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t at, uint32_t lead) {
+    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
 }
 
 // Instruction descriptor: fp32 sums, 16-bit operands of T, 128 x N, the second
@@ -160,7 +163,7 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
 template <typename T, int D>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_tree_wide(const __grid_constant__ TreeAttention a, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
-    constexpr uint32_t kCol = 128, kRow = D / 8 * 128;       // bytes between core matrices along a row, and to the next eight rows
+    constexpr uint32_t kQHalf = kGroup * 128, kHalf = kTile * 128;  // bytes of 64 columns
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WideShared sh;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
         v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-        *reinterpret_cast<uint4 *>(smem + r / 8 * kRow + d * kCol + r % 8 * 16) = v;
+        *reinterpret_cast<uint4 *>(smem + r / kGroup * kQBytes + d / 8 * kQHalf + r % kGroup * 128 + ((d ^ r) & 7) * 16) = v;
     }
     proxy_fence();
     fence_before();
@@ -243,10 +246,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             return p >= 0 ? table[(uint32_t)p / (uint32_t)a.c.page_size] : -1;
         };
         Place put;
-        // lane l copies 16 bytes of key l % 8 of every eight, at columns l / 8, l / 8 + 4, ..: whole sectors are read
-        const char *from0 = static_cast<const char *>(a.c.k) + lane / 8 * 16;
+        // lane l copies piece l % 8 of the 128 bytes of keys l / 8, l / 8 + 4, ..
+        const char *from0 = static_cast<const char *>(a.c.k) + lane % 8 * 16;
         const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k);
-        const uint32_t to0 = ring + cw * 4 * kRow + lane / 8 * kCol + lane % 8 * 16;
+        const uint32_t to0 = ring + (cw * 32 + lane / 8) * 128;
         // Page ids are loaded four tiles ahead: a load returns behind the copies issued before it.
         int pages[4];
 #pragma unroll
@@ -267,13 +270,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 pages[j] = page_of(t + 4);
                 const uint32_t to = to0 + put.slot * 2 * kTileBytes;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int64_t off = __shfl_sync(~0u, at, h * 8 + lane % 8);
+                for (int h = 0; h < 8; ++h) {
+                    const int64_t off = __shfl_sync(~0u, at, h * 4 + lane / 8);
                     const char *from = from0 + max(off, (int64_t)0);
+                    const uint32_t dst = to + h * 512 + ((lane ^ (h * 4 + lane / 8)) & 7) * 16;
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d) {
-                        copy16(to + h * kRow + d * 4 * kCol, from + d * 64, off >= 0);
-                        copy16(to + kTileBytes + h * kRow + d * 4 * kCol, from + to_v + d * 64, off >= 0);
+                    for (int d = 0; d < D / 64; ++d) {
+                        copy16(dst + d * kHalf, from + d * 128, off >= 0);
+                        copy16(dst + kTileBytes + d * kHalf, from + to_v + d * 128, off >= 0);
                     }
                 }
                 if (t >= old_tiles) {  // the drafts: a value row with NaN or infinities is taken out
@@ -281,11 +285,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     copy_wait<0>();
                     __syncwarp();
                     constexpr uint32_t kExp = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;  // all ones: not finite
-                    uint8_t *v = smem + 2 * kQBytes + (put.slot * 2 + 1) * kTileBytes + (cw * 4 + lane / 8) * kRow + lane % 8 * 16;
+                    uint8_t *v = smem + 2 * kQBytes + (put.slot * 2 + 1) * kTileBytes + (cw * 32 + lane) * 128;
                     bool odd = false;
 #pragma unroll 4
                     for (int d = 0; d < D / 8; ++d) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(v + d * kCol);
+                        const uint4 y = *reinterpret_cast<const uint4 *>(v + d / 8 * kHalf + d % 8 * 16);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             const uint32_t z = w == 0 ? y.x : w == 1 ? y.y : w == 2 ? y.z : y.w;
@@ -296,7 +300,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (odds) {
                         if (lane == 0) sh.odd[cw] = odds;
                         if (odd)
-                            for (int d = 0; d < D / 8; ++d) *reinterpret_cast<uint4 *>(v + d * kCol) = make_uint4(0, 0, 0, 0);
+                            for (int d = 0; d < D / 8; ++d)
+                                *reinterpret_cast<uint4 *>(v + d / 8 * kHalf + d % 8 * 16) = make_uint4(0, 0, 0, 0);
                         proxy_fence();
                         __syncwarp();
                     }
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint32_t s_at = tmem + Cols<D>::s(g, b);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
-                    mma_ss(s_at, tile_desc(q + j * 2 * kCol, kCol, kRow), tile_desc(k_at + j * 2 * kCol, kCol, kRow),
+                    mma_ss(s_at, tile_desc(q + j / 4 * kQHalf + j % 4 * 32, 16), tile_desc(k_at + j / 4 * kHalf + j % 4 * 32, 16),
                            wide_idesc<T, kTile, false>(), j > 0);
                 commit(sh.scored[g][b]);
                 if (split || g == 1) at.step(1);
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint32_t v_at = ring + (at.slot * 2 + 1) * kTileBytes, p_at = tmem + Cols<D>::s(g, n & 1);
 #pragma unroll
                 for (int j = 0; j < kTile / 16; ++j)
-                    mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2 * kRow, kRow, kCol), wide_idesc<T, D, true>(),
+                    mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2048, kHalf), wide_idesc<T, D, true>(),
                            n > 0 || j > 0);
                 commit(sh.summed[g][n & 1]);
                 if (split || g == 1) {
