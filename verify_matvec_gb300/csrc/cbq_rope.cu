@@ -51,99 +51,105 @@ struct alignas(V * sizeof(T)) Vec {
 // A token's values are taken V at a time (16 bytes of input): an item is two
 // such pieces whose values form pairs (half layout), one piece (pairs of
 // neighbours), or one piece that is copied.  V = 1 takes any alignment: an item
-// is a pair or a value.  grid (tokens, parts of a token's items): few tokens
-// are spread over blocks.  Each block turns its token's rot/2 angles into sines
-// and cosines once, behind the loads of its first items.
-template <typename Tin, typename Tout, int V, bool kHalfLayout>
+// is a pair or a value.  A thread takes one item of kTok tokens: it works out
+// the place once and has all their loads under way together.  grid (blocks of
+// kTok tokens, parts of a token's items).  Each block turns its tokens' angles
+// into sines and cosines once, behind the loads of its first items.
+template <typename Tin, typename Tout, int V, bool kHalfLayout, int kTok>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs a) {
-    constexpr int kItems = 2;                          // of a thread at a time
     constexpr int kPiece = !kHalfLayout && V == 1 ? 2 : V;  // values of a rotated piece
-    constexpr int kTwo = kHalfLayout ? 2 : 1;
-    __shared__ float2 cs[CBQ_ROPE_MAX_DIM / 2];
+    constexpr bool kTwo = kHalfLayout || V == 1;            // a rotated item is two loads
+    constexpr int kPairs = V == 1 ? 1 : kHalfLayout ? V : V / 2;  // of a rotated item
+    // kTok x rot/2 sines and cosines, two pairs of every item side by side, then the next two: lanes with items in a row
+    // read them without bank conflicts
+    extern __shared__ __align__(16) float2 cs[];
+    __shared__ int64_t place[kTok];
     pdl_trigger();
     pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int half = a.r.rot / 2, turning = a.r.rot / (kPiece * kTwo);  // rotated items of a head
-    int64_t slot_at = -1;
+    const int64_t t0 = (int64_t)blockIdx.x * kTok;
+    const int half = a.r.rot / 2, turning = a.r.rot / (kPiece * (kHalfLayout ? 2 : 1));  // rotated items of a head
+    const int tokens = a.n_tok - t0 < kTok ? (int)(a.n_tok - t0) : kTok;
     if (a.slots) {
-        const int64_t slot = a.slots[t];
-        if (slot >= 0 && slot < a.n_slots) slot_at = slot / a.page_size * a.page_stride + slot % a.page_size * a.tok_stride;
-        else if (slot >= 0 && a.err && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+        if (threadIdx.x < tokens) {
+            const int64_t slot = a.slots[t0 + threadIdx.x];
+            const bool good = slot >= 0 && slot < a.n_slots;
+            if (slot >= a.n_slots && a.err && blockIdx.y == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+            place[threadIdx.x] = good ? slot / a.page_size * a.page_stride + slot % a.page_size * a.tok_stride : -1;
+        }
+        __syncthreads();
     }
-    const double pos = (double)a.r.pos[t];
-    const int step = kItems * kRopeThreads;
     const int end = a.first[a.n_groups];
     bool known = false;
-    for (int x0 = blockIdx.y * step; x0 < end; x0 += gridDim.y * step) {
-        Vec<Tin, V> va[kItems], vb[kItems];
-        Tout *to[kItems];
-        int pair[kItems];  // the first pair of a rotated piece; -1: copied; -2: nothing
+    for (int x0 = blockIdx.y * kRopeThreads; x0 < end; x0 += gridDim.y * kRopeThreads) {
+        const int x = x0 + threadIdx.x;
+        const bool some = x < end;
+        const int n = x >= a.first[1] ? (x >= a.first[2] ? 2 : 1) : 0;
+        const Group &g = a.g[some ? n : 0];
+        const unsigned each = a.per_head[some ? n : 0], in = some ? x - a.first[n] : 0, h = in / each, i = in - h * each;
+        const bool turns = g.rotate && i < (unsigned)turning;
+        int d = turns ? a.r.off + i * kPiece : (i - (g.rotate ? turning : 0)) * V;
+        if (!turns && g.rotate && d >= a.r.off) d += a.r.rot;
+        const int second = kHalfLayout ? half : 1;
+        const Tin *from = static_cast<const Tin *>(g.src) + t0 * g.src_tok + h * g.src_head + d;
+        Tout *to = static_cast<Tout *>(g.dst) + (g.cached ? 0 : t0 * g.dst_tok) + h * g.dst_head + d;
+        Vec<Tin, V> va[kTok], vb[kTok];
 #pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int x = x0 + u * kRopeThreads + threadIdx.x;
-            pair[u] = -2;
-            to[u] = nullptr;
-            if (x >= end) continue;
-            const int n = x >= a.first[1] ? (x >= a.first[2] ? 2 : 1) : 0;
-            const Group &g = a.g[n];
-            if (g.cached && slot_at < 0) continue;
-            const unsigned in = x - a.first[n], h = in / (unsigned)a.per_head[n], i = in - h * a.per_head[n];
-            const Tin *from = static_cast<const Tin *>(g.src) + t * g.src_tok + h * g.src_head;
-            Tout *dst = static_cast<Tout *>(g.dst) + (g.cached ? slot_at : t * g.dst_tok) + h * g.dst_head;
-            if (g.rotate && i < (unsigned)turning) {
-                const int d = a.r.off + i * kPiece;
-                va[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + d);
-                if constexpr (kHalfLayout) vb[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + d + half);
-                else if constexpr (V == 1) vb[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + d + 1);
-                to[u] = dst + d;
-                pair[u] = kHalfLayout ? i * V : i * (kPiece / 2);
-            } else {
-                int d = (i - (g.rotate ? turning : 0)) * V;
-                if (g.rotate && d >= a.r.off) d += a.r.rot;
-                va[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + d);
-                to[u] = dst + d;
-                pair[u] = -1;
-            }
+        for (int u = 0; u < kTok; ++u) {
+            if (!some || u >= tokens) continue;
+            va[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + u * g.src_tok);
+            if (kTwo && turns) vb[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + u * g.src_tok + second);
         }
         if (!known) {
             known = true;
-            for (int i = threadIdx.x; i < half; i += kRopeThreads) {
-                double turn = pos * a.r.turns[i];
+            for (int j = threadIdx.x; j < tokens * half; j += kRopeThreads) {
+                const int u = j / half;
+                double turn = (double)a.r.pos[t0 + u] * a.r.turns[j - u * half];
                 turn -= rint(turn);
                 float s, c;
                 sincospif(2.0f * (float)turn, &s, &c);
-                cs[i] = make_float2(c * a.r.mscale, s * a.r.mscale);
+                const int p = j - u * half, i = p / kPairs, q = p % kPairs;
+                cs[u * half + (kPairs == 1 ? p : (q / 2 * turning + i) * 2 + q % 2)] = make_float2(c * a.r.mscale, s * a.r.mscale);
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            if (pair[u] == -2) continue;
+        for (int u = 0; u < kTok; ++u) {
+            if (!some || u >= tokens) continue;
+            const int64_t at = g.cached ? place[u] : u * g.dst_tok;
+            if (at < 0) continue;
             Vec<Tout, V> oa, ob;
-            if (pair[u] == -1) {
+            float2 c[kPairs];
+            if (turns) {
+                if constexpr (kPairs == 1) {
+                    c[0] = cs[u * half + i];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kPairs; q += 2) {
+                        const float4 y = *reinterpret_cast<const float4 *>(cs + u * half + (q / 2 * turning + i) * 2);
+                        c[q] = make_float2(y.x, y.y), c[q + 1] = make_float2(y.z, y.w);
+                    }
+                }
+            }
+            if (!turns) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) oa.v[e] = from_f32<Tout>(to_f32(va[u].v[e]));
-                *reinterpret_cast<Vec<Tout, V> *>(to[u]) = oa;
-            } else if constexpr (kHalfLayout || V == 1) {
+            } else if constexpr (kTwo) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float2 c = cs[pair[u] + e];
                     const float x = to_f32(va[u].v[e]), y = to_f32(vb[u].v[e]);
-                    oa.v[e] = from_f32<Tout>(x * c.x - y * c.y);
-                    ob.v[e] = from_f32<Tout>(x * c.y + y * c.x);
+                    oa.v[e] = from_f32<Tout>(x * c[e].x - y * c[e].y);
+                    ob.v[e] = from_f32<Tout>(x * c[e].y + y * c[e].x);
                 }
-                *reinterpret_cast<Vec<Tout, V> *>(to[u]) = oa;
-                *reinterpret_cast<Vec<Tout, V> *>(to[u] + (kHalfLayout ? half : 1)) = ob;
+                *reinterpret_cast<Vec<Tout, V> *>(to + at + second) = ob;
             } else {
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
-                    const float2 c = cs[pair[u] + e / 2];
                     const float x = to_f32(va[u].v[e]), y = to_f32(va[u].v[e + 1]);
-                    oa.v[e] = from_f32<Tout>(x * c.x - y * c.y);
-                    oa.v[e + 1] = from_f32<Tout>(x * c.y + y * c.x);
+                    oa.v[e] = from_f32<Tout>(x * c[e / 2].x - y * c[e / 2].y);
+                    oa.v[e + 1] = from_f32<Tout>(x * c[e / 2].y + y * c[e / 2].x);
                 }
-                *reinterpret_cast<Vec<Tout, V> *>(to[u]) = oa;
             }
+            *reinterpret_cast<Vec<Tout, V> *>(to + at) = oa;
         }
     }
 }
@@ -161,18 +167,22 @@ cudaError_t launch_pieces(RopeArgs a, cudaStream_t s) {
     }
     a.first[a.n_groups] = end;
     for (int n = a.n_groups + 1; n < 4; ++n) a.first[n] = end;
-    // a block a token where there are enough of them, else as many as its items fill
-    const int parts = (end + 2 * kRopeThreads - 1) / (2 * kRopeThreads);
+    const int parts = (end + kRopeThreads - 1) / kRopeThreads;
+    // some tokens a block where that leaves two blocks for each of 152 SMs
+    constexpr int kTok = kHalfLayout ? 2 : 4;
+    const bool many = a.n_tok >= kTok * 304;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.n_tok, (unsigned)(a.n_tok >= 608 ? 1 : parts < 64 ? parts : 64));
+    cfg.gridDim = dim3((unsigned)(many ? (a.n_tok + kTok - 1) / kTok : a.n_tok), (unsigned)(parts < 64 ? parts : 64));
     cfg.blockDim = dim3(kRopeThreads);
+    cfg.dynamicSmemBytes = (many ? kTok : 1) * (a.r.rot / 2) * sizeof(float2);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout>, a);
+    return many ? cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout, kTok>, a)
+                : cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout, 1>, a);
 }
 
 // Whether all rows, heads and parts begin on V values (of 16 bytes of input).
