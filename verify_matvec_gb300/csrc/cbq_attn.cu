@@ -424,39 +424,66 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
     }
 }
 
-// The chunks of a row joined: one warp per (token, head).  grid
-// (ceil(q_heads / 4), max_tok, n_seq), 4 warps.  The wide kernel cuts the
-// committed keys alone (and takes the drafts with the last chunk).
-template <typename T, int D>
-__global__ void __launch_bounds__(128) k_tree_join(TreeAttention a, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
+// The chunks of a row (token, head) joined by W warps: with many chunks the
+// eight warps of a block share out those of one row (one warp going through 32
+// chunks took 18 us of a 33 us call), with few each takes a row of its own.  The
+// wide kernel cuts the committed keys alone (and takes the drafts with the last
+// chunk).  grid (ceil(q_heads * W / 8), max_tok, n_seq).
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
+    constexpr int kEach = D / 32;  // values of a lane, side by side
+    struct alignas(kEach * 4 < 16 ? kEach * 4 : 16) Values {
+        float v[kEach];
+    };
+    __shared__ float tops[8], sums[8];
+    __shared__ Values vals[W > 1 ? W - 1 : 1][32];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, h = blockIdx.x * 4 + threadIdx.x / 32, i = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, w = warp % W, h = blockIdx.x * (8 / W) + warp / W, i = blockIdx.y;
     const Seq sq = sequence(a, blockIdx.z, false);
     const int chunks = ((wide ? sq.ctx : sq.len) + chunk - 1) / chunk;
-    if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;
+    if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;  // (all warps of a row alike)
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
     float top = -INFINITY;
-    for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part_ml[c * step + row].x);
+    for (int c = w * 32 + lane; c < chunks; c += 32 * W) top = fmaxf(top, part_ml[c * step + row].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    constexpr int kEach = D / 32;
-    float v[kEach] = {}, sum = 0.0f;
+    if constexpr (W > 1) {
+        if (lane == 0) tops[w] = top;
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < W; ++o) top = fmaxf(top, tops[o]);
+    }
+    Values v = {};
+    float sum = 0.0f;
     if (top != -INFINITY) {
-#pragma unroll 4
-        for (int c = 0; c < chunks; ++c) {
+#pragma unroll 8
+        for (int c = w; c < chunks; c += W) {
             const float2 p = part_ml[c * step + row];
+            const Values y = reinterpret_cast<const Values *>(part_o + (c * step + row) * D)[lane];
             const float f = pow2(p.x - top);
             sum += p.y * f;
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v[j] += f * part_o[(c * step + row) * D + j * 32 + lane];
+            for (int j = 0; j < kEach; ++j) v.v[j] += f * y.v[j];
+        }
+    }
+    if constexpr (W > 1) {
+        if (lane == 0) sums[w] = sum;
+        if (w > 0) vals[w - 1][lane] = v;
+        __syncthreads();
+        if (w > 0) return;
+        for (int o = 1; o < W; ++o) {
+            sum += sums[o];
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) v.v[j] += vals[o - 1][lane].v[j];
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        if (a.out_f32) static_cast<float *>(a.out)[row * D + j * 32 + lane] = v[j] * inv;
-        else static_cast<T *>(a.out)[row * D + j * 32 + lane] = from_f32<T>(v[j] * inv);
+        const int64_t at = row * D + lane * kEach + j;
+        if (a.out_f32) static_cast<float *>(a.out)[at] = v.v[j] * inv;
+        else static_cast<T *>(a.out)[at] = from_f32<T>(v.v[j] * inv);
     }
     if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
@@ -511,8 +538,10 @@ cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) 
                                                     dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
                                                     128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1) return e;
-    return launch_dependent(k_tree_join<T, D>, dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.max_tok, (unsigned)a.n_seq), 128, 0, s,
-                            a, p.chunk, p.wide, part_o, part_ml);
+    const unsigned heads = (unsigned)a.q_heads, toks = (unsigned)a.max_tok, seqs = (unsigned)a.n_seq;
+    return p.n_chunks > 8 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
+                          : launch_dependent(k_tree_join<T, D, 1>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, p.chunk, p.wide,
+                                             part_o, part_ml);
 }
 
 template <typename T, int D>
