@@ -148,31 +148,6 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
     if (rows <= 0 || (begin >= end && c > 0)) return;
     const bool alone = sq.len <= chunk;  // the only chunk of this sequence
 
-    // q of the block's rows (row r: token r / group, head r % group of the group), the sign of the scale with it
-    const float sc = fabsf(a.scale) * kLog2e;
-    const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-    uint8_t *qs = S::kHoldQ ? smem + (S::kStages - 1) * 2 * S::kTileBytes : smem + S::kRing;
-    for (int i = tid; i < S::kRows * (D / 8); i += 128) {
-        const int r = i / (D / 8), d = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-            const int tok = (r0 + r) / group, h = kvh * group + (r0 + r) % group;
-            const T *from = static_cast<const T *>(a.q) + (sq.row0 + tok) * a.q_tok + h * a.q_head + d * 8;
-            if (q_whole) {
-                v = *reinterpret_cast<const uint4 *>(from);
-            } else {
-                __align__(16) T y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = from[e];
-                v = *reinterpret_cast<const uint4 *>(y);
-            }
-        }
-        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-        *reinterpret_cast<uint4 *>(qs + r * S::kPitch + d * 16) = v;
-    }
-    if (tid < S::kRows) drafts[tid] = tid < rows ? seen_drafts(a, sq, sq.row0 + (r0 + tid) / group) : 0;
-
     // copies: each warp brings kCopied rows of a tile; lane l < kCopied keeps the place of row l
     const int tiles = (end - begin + S::kTile - 1) / S::kTile;
     const int32_t *table = a.table + (int64_t)s * a.table_width;
@@ -200,12 +175,46 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
         }
     };
     static_assert(S::kCopied * (D / 8) % 32 == 0, "whole warps of copies");
+    // What the first tiles and the rows need from memory is asked for together: their pages, q (row r: token r / group,
+    // head r % group of the group) and the masks.
+    int pages[S::kStages];
+#pragma unroll
+    for (int t = 0; t < S::kStages; ++t) pages[t] = t < tiles ? page_of(t) : -1;
+    const float sc = fabsf(a.scale) * kLog2e;
+    const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // (the sign of the scale goes with q)
+    uint4 qv[S::kRows * (D / 8) / 128];
+#pragma unroll
+    for (int x = 0; x < S::kRows * (D / 8) / 128; ++x) {
+        const int r = (x * 128 + tid) / (D / 8), d = (x * 128 + tid) % (D / 8);
+        qv[x] = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+            const int tok = (r0 + r) / group, h = kvh * group + (r0 + r) % group;
+            const T *from = static_cast<const T *>(a.q) + (sq.row0 + tok) * a.q_tok + h * a.q_head + d * 8;
+            if (q_whole) {
+                qv[x] = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                __align__(16) T y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = from[e];
+                qv[x] = *reinterpret_cast<const uint4 *>(y);
+            }
+        }
+    }
+    const uint64_t tree = tid < rows ? seen_drafts(a, sq, sq.row0 + (r0 + tid) / group) : 0;
 #pragma unroll
     for (int t = 0; t < S::kStages - 1; ++t) {
-        if (t < tiles) fetch(t, page_of(t));
+        if (t < tiles) fetch(t, pages[t]);
         copy_commit();
     }
-    int page = S::kStages - 1 < tiles ? page_of(S::kStages - 1) : -1;
+    int page = pages[S::kStages - 1];
+    uint8_t *qs = S::kHoldQ ? smem + (S::kStages - 1) * 2 * S::kTileBytes : smem + S::kRing;
+#pragma unroll
+    for (int x = 0; x < S::kRows * (D / 8) / 128; ++x) {
+        const int r = (x * 128 + tid) / (D / 8), d = (x * 128 + tid) % (D / 8);
+        *reinterpret_cast<uint4 *>(qs + r * S::kPitch + d * 16) = make_uint4(qv[x].x ^ flip, qv[x].y ^ flip, qv[x].z ^ flip, qv[x].w ^ flip);
+    }
+    if (tid < S::kRows) drafts[tid] = tree;
     __syncthreads();
     const uint32_t q_at = smem_addr(qs) + (wr * 16 + lane % 16) * S::kPitch + lane / 16 * 16;
     uint32_t qf[S::kHoldQ ? D / 16 : 1][4];
@@ -513,6 +522,9 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
             const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)max_len / m * 0.01 + 6.0);
             if (m == 1 || t < least) least = t, n = m;
         }
+        // several sequences may differ in length: no block takes much longer than others, as long as the parts' bytes stay
+        // small beside the keys'
+        if (n_seq > 1) n = std::max(n, max_len / std::max(2048, 32 * rows));
     } else {
         // two blocks for each SM; with several sequences, whose lengths may differ, at most 2048 keys each
         n = (2 * kSms + blocks - 1) / blocks;

@@ -202,29 +202,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         sh.odd[0] = sh.odd[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // q of the rows, the sign of the scale with it; absent rows are zero
     const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1e-45f);  // (not zero: -inf times that would be NaN)
-    const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-    for (int i = tid; i < (split ? 1 : 2) * kGroup * (D / 8); i += kWideThreads) {
-        const int r = i / (D / 8), d = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-            const int tok = (r0 + r) / group, h = kvh * group + (r0 + r) % group;
-            const T *from = static_cast<const T *>(a.q) + (sq.row0 + tok) * a.q_tok + h * a.q_head + d * 8;
-            if (q_whole) {
-                v = *reinterpret_cast<const uint4 *>(from);
-            } else {
-                __align__(16) T y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = from[e];
-                v = *reinterpret_cast<const uint4 *>(y);
-            }
-        }
-        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-        *reinterpret_cast<uint4 *>(smem + r / kGroup * kQBytes + d / 8 * kQHalf + r % kGroup * 128 + ((d ^ r) & 7) * 16) = v;
-    }
-    proxy_fence();
     fence_before();
     __syncthreads();
     fence_after();
@@ -232,18 +210,63 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t q_at = smem_addr(smem), ring = q_at + 2 * kQBytes;
     const int32_t *table = a.table + (int64_t)s * a.table_width;
 
-    if (warp >= kCopyWarp && warp < kScoreWarp) {
+    const bool copies = warp >= kCopyWarp && warp < kScoreWarp;
+    if (!copies) {
+        // q of the rows, the sign of the scale with it; absent rows are zero
+        const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        constexpr int kOthers = kWideThreads - 64, kAtOnce = 6;
+        const int me = warp < kCopyWarp ? tid : tid - 64, pieces = (split ? 1 : 2) * kGroup * (D / 8);
+        for (int i0 = me; i0 < pieces; i0 += kAtOnce * kOthers) {
+            uint4 v[kAtOnce];
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const int r = (i0 + x * kOthers) / (D / 8), d = (i0 + x * kOthers) % (D / 8), at = r < rows ? r0 + r : r0;
+                const T *from = static_cast<const T *>(a.q) + (sq.row0 + at / group) * a.q_tok + (kvh * group + at % group) * a.q_head + d * 8;
+                if (q_whole) {
+                    v[x] = *reinterpret_cast<const uint4 *>(from);
+                } else {
+                    __align__(16) T y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = from[e];
+                    v[x] = *reinterpret_cast<const uint4 *>(y);
+                }
+                if (r >= rows) v[x] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const int i = i0 + x * kOthers, r = i / (D / 8), d = i % (D / 8);
+                if (i >= pieces) break;
+                *reinterpret_cast<uint4 *>(smem + r / kGroup * kQBytes + d / 8 * kQHalf + r % kGroup * 128 + ((d ^ r) & 7) * 16) =
+                    make_uint4(v[x].x ^ flip, v[x].y ^ flip, v[x].z ^ flip, v[x].w ^ flip);
+            }
+        }
+        proxy_fence();
+        asm volatile("bar.sync 2, %0;" ::"n"(kOthers) : "memory");
+    }
+
+    if (copies) {
         // copies: a warp brings 32 keys of each tile; lane l keeps the place of key l
         const int cw = warp - kCopyWarp;
         const int64_t head = kvh * a.c.head_stride;
-        // the place of this lane's key of tile t, -1 where there is none
-        auto place = [&](int t) {
-            const int p = (t < old_tiles ? begin + t * kTile : sq.ctx) + cw * 32 + lane;
-            return t < tiles && p < (t < old_tiles ? end : sq.len) ? p : -1;
-        };
-        auto page_of = [&](int t) {
-            const int p = place(t);
-            return p >= 0 ? table[(uint32_t)p / (uint32_t)a.c.page_size] : -1;
+        // Keys are looked up in order: the page of the next tile's key is some pages and tokens on (no divisions).
+        const uint32_t size = a.c.page_size, pages_on = kTile / size, tokens_on = kTile % size;
+        uint32_t entry = 0, token = 0;  // of this lane's key of the tile looked up next
+        int p = begin + cw * 32 + lane;
+        // the id of its page, and the token within (-1 where there is no such key)
+        auto look = [&](int t, int &page, int &within) {
+            if (t == 0 || t == old_tiles) {  // the drafts begin anywhere
+                if (t == old_tiles) p = sq.ctx + cw * 32 + lane;
+                entry = (uint32_t)p / size;
+                token = (uint32_t)p % size;
+            }
+            const bool key = t < tiles && p < (t < old_tiles ? end : sq.len);
+            page = key ? table[entry] : -1;
+            within = key ? (int)token : -1;
+            p += kTile;
+            entry += pages_on;
+            token += tokens_on;
+            if (token >= size) token -= size, ++entry;
         };
         Place put;
         // lane l copies piece l % 8 of the 128 bytes of keys l / 8, l / 8 + 4, ..
@@ -251,23 +274,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k);
         const uint32_t to0 = ring + (cw * 32 + lane / 8) * 128;
         // Page ids are loaded four tiles ahead: a load returns behind the copies issued before it.
-        int pages[4];
+        int pages[4], withins[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pages[j] = page_of(j);
+        for (int j = 0; j < 4; ++j) look(j, pages[j], withins[j]);
         bool ok = true;
         for (int t0 = 0; t0 < tiles && ok; t0 += 4) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int t = t0 + j, page = pages[j];
+                const int t = t0 + j, page = pages[j], within = withins[j];
                 if (t >= tiles || !ok) break;
                 if (t >= kStages) ok = warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err);
                 if (!ok) break;
-                const int p = place(t);
-                const bool in = p >= 0, good = in && page >= 0 && page < a.c.n_pages;
-                if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-                const int64_t at = good ? (page * a.c.page_stride + (int64_t)((uint32_t)p % (uint32_t)a.c.page_size) * a.c.tok_stride + head) * 2 : -1;
+                const bool good = within >= 0 && page >= 0 && page < a.c.n_pages;
+                if (within >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+                const int64_t at = good ? (page * a.c.page_stride + within * a.c.tok_stride + head) * 2 : -1;
                 const uint32_t bits = __ballot_sync(~0u, good);
-                pages[j] = page_of(t + 4);
+                look(t + 4, pages[j], withins[j]);
                 const uint32_t to = to0 + put.slot * 2 * kTileBytes;
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
