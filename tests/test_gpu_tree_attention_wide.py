@@ -145,3 +145,17 @@ def test_strides_output_type_repeats_and_graph(torch):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(into, whole)
+
+
+@pytest.mark.parametrize("drafts", [16, 32])
+def test_rows_that_scale_alone(torch, drafts):
+    """Along these keys the maxima of one warp's 32 rows grow at every tile, so
+    that warp rescales its results each time while the others never do."""
+    s = Setup(torch, [6000], [drafts], 8, 1, 128, 64, seed=3)
+    s.q[4:] *= 0.001
+    s.q[:4] = s.q[:4].abs() * 2
+    order = torch.from_numpy(s.table[0].astype(np.int64)).cuda()
+    s.kc[order] = (s.kc[order].abs().float() * torch.linspace(0.01, 3.0, len(order), device="cuda")[:, None, None, None]).to(s.dt)
+    want = s.want(128 ** -0.5)
+    for _ in range(5):
+        s.check(*s.run(), want=want)

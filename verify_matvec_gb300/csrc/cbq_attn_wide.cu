@@ -49,8 +49,9 @@ struct Cols {
 
 struct WideShared {
     uint64_t full[kStages], empty[kStages];   // a tile's copies have landed; its products are done
-    // of a group's item: S is there; P is there; O has it (even and odd items apart where the next may come first)
-    uint64_t scored[2][2], weighed[2], summed[2][2];
+    // of a group's item: S is there; P is there; O has it.  Even and odd items apart: scores run two items ahead, so one
+    // warp of a group may be at the next item while another is still at this one.
+    uint64_t scored[2][2], weighed[2][2], summed[2][2];
     uint64_t done[2];
     uint32_t valid[kStages][2];               // keys of a tile that exist, 32 a copying warp
     uint32_t odd[2];                          // drafts whose values are not all finite
@@ -190,11 +191,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_init(smem_addr(&sh.empty[i]), 1);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(smem_addr(&sh.scored[g][0]), 2);  // the products, and the word of their warp, which has seen the tile's valid[]
-            mbar_init(smem_addr(&sh.scored[g][1]), 2);
-            mbar_init(smem_addr(&sh.weighed[g]), 4);
-            mbar_init(smem_addr(&sh.summed[g][0]), 1);
-            mbar_init(smem_addr(&sh.summed[g][1]), 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_addr(&sh.scored[g][b]), 2);  // the products, and the word of their warp, which has seen the tile's valid[]
+                mbar_init(smem_addr(&sh.weighed[g][b]), 4);
+                mbar_init(smem_addr(&sh.summed[g][b]), 1);
+            }
         }
         mbar_init(smem_addr(&sh.done[0]), 1);
         mbar_init(smem_addr(&sh.done[1]), 1);
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         } else {
             for (int i = 0; i < items; ++i) {
                 const int g = i & 1, n = i >> 1;
-                ok = warp_wait(sh, sh.weighed[g], n & 1, a.err);
+                ok = warp_wait(sh, sh.weighed[g][n & 1], n >> 1 & 1, a.err);
                 if (!ok) break;
                 fence_after();
                 const uint32_t v_at = ring + (at.slot * 2 + 1) * kTileBytes, p_at = tmem + Cols<D>::s(g, n & 1);
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tm_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.weighed[g]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.weighed[g][n & 1]));
         }
         if (ok && n > 0) ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
         fence_after();
