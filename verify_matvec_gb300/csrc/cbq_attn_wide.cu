@@ -53,7 +53,7 @@ struct WideShared {
     // warp of a group may be at the next item while another is still at this one.
     uint64_t scored[2][2], weighed[2][2], summed[2][2];
     uint64_t done[2];
-    uint32_t valid[kStages][2];               // keys of a tile that exist, 32 a copying warp
+    uint32_t valid[kStages][2];               // keys of a tile that exist
     uint32_t odd[2];                          // drafts whose values are not all finite
     uint32_t tmem_slot;
     int abort;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), 64 + 2);  // the copying threads' copies, and their warps' word on valid[]
+            mbar_init(smem_addr(&sh.full[i]), 32 + 1);  // the copying warp's copies, and its word on valid[]
             mbar_init(smem_addr(&sh.empty[i]), 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -247,60 +247,79 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
 
     if (copies) {
-        // copies: a warp brings 32 keys of each tile; lane l keeps the place of key l
+        // copies: the two warps take tiles in turn (what a tile costs a warp is mostly waits and look-ups); lane l keeps
+        // the places of keys l and l + 32
         const int cw = warp - kCopyWarp;
         const int64_t head = kvh * a.c.head_stride;
         // Keys are looked up in order: the page of the next tile's key is some pages and tokens on (no divisions).
-        const uint32_t size = a.c.page_size, pages_on = kTile / size, tokens_on = kTile % size;
-        uint32_t entry = 0, token = 0;  // of this lane's key of the tile looked up next
-        int p = begin + cw * 32 + lane;
-        // the id of its page, and the token within (-1 where there is no such key)
-        auto look = [&](int t, int &page, int &within) {
-            if (t == 0 || t == old_tiles) {  // the drafts begin anywhere
-                if (t == old_tiles) p = sq.ctx + cw * 32 + lane;
-                entry = (uint32_t)p / size;
-                token = (uint32_t)p % size;
+        const uint32_t size = a.c.page_size, pages_on = 2 * kTile / size, tokens_on = 2 * kTile % size;
+        uint32_t entry[2], token[2];  // of this lane's keys of the tile looked up next
+        int p = begin + cw * kTile + lane;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) entry[e] = (uint32_t)(p + 32 * e) / size, token[e] = (uint32_t)(p + 32 * e) % size;
+        struct Look {
+            int page[2], within[2];  // the id of a key's page, and the token within (-1 where there is no such key)
+        };
+        auto look = [&](int t) {
+            Look l;
+            if (t == old_tiles) {  // the drafts begin anywhere
+                p = sq.ctx + lane;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) entry[e] = (uint32_t)(p + 32 * e) / size, token[e] = (uint32_t)(p + 32 * e) % size;
             }
-            const bool key = t < tiles && p < (t < old_tiles ? end : sq.len);
-            page = key ? table[entry] : -1;
-            within = key ? (int)token : -1;
-            p += kTile;
-            entry += pages_on;
-            token += tokens_on;
-            if (token >= size) token -= size, ++entry;
+            const int stop = t >= tiles ? 0 : t < old_tiles ? end : sq.len;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool key = p + 32 * e < stop;
+                l.page[e] = key ? table[entry[e]] : -1;
+                l.within[e] = key ? (int)token[e] : -1;
+                entry[e] += pages_on;
+                token[e] += tokens_on;
+                if (token[e] >= size) token[e] -= size, ++entry[e];
+            }
+            p += 2 * kTile;
+            return l;
         };
         Place put;
+        if (cw) put.step(1);
         // lane l copies piece l % 8 of the 128 bytes of keys l / 8, l / 8 + 4, ..
         const char *from0 = static_cast<const char *>(a.c.k) + lane % 8 * 16;
         const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k);
-        const uint32_t to0 = ring + (cw * 32 + lane / 8) * 128;
+        const uint32_t to0 = ring + lane / 8 * 128;
         // Page ids are loaded four tiles ahead: a load returns behind the copies issued before it.
-        int pages[4], withins[4];
+        Look next[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) look(j, pages[j], withins[j]);
+        for (int j = 0; j < 2; ++j) next[j] = look(cw + 2 * j);
         bool ok = true;
-        for (int t0 = 0; t0 < tiles && ok; t0 += 4) {
+        for (int t0 = cw; t0 < tiles && ok; t0 += 4) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + j, page = pages[j], within = withins[j];
-                if (t >= tiles || !ok) break;
+            for (int j = 0; j < 2; ++j) {
+                const int t = t0 + 2 * j;
+                if (t >= tiles) break;
+                const Look now = next[j];
+                next[j] = look(t + 4);
+                int64_t at[2];
+                uint32_t bits[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool good = now.within[e] >= 0 && now.page[e] >= 0 && now.page[e] < a.c.n_pages;
+                    if (now.within[e] >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+                    at[e] = good ? (now.page[e] * a.c.page_stride + now.within[e] * a.c.tok_stride + head) * 2 : 0;
+                    bits[e] = __ballot_sync(~0u, good);
+                }
                 if (t >= kStages) ok = warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err);
                 if (!ok) break;
-                const bool good = within >= 0 && page >= 0 && page < a.c.n_pages;
-                if (within >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-                const int64_t at = good ? (page * a.c.page_stride + within * a.c.tok_stride + head) * 2 : -1;
-                const uint32_t bits = __ballot_sync(~0u, good);
-                look(t + 4, pages[j], withins[j]);
                 const uint32_t to = to0 + put.slot * 2 * kTileBytes;
 #pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const int64_t off = __shfl_sync(~0u, at, h * 4 + lane / 8);
-                    const char *from = from0 + max(off, (int64_t)0);
+                for (int h = 0; h < 16; ++h) {
+                    const int64_t off = __shfl_sync(~0u, at[h / 8], h % 8 * 4 + lane / 8);
+                    const bool good = bits[h / 8] >> (h % 8 * 4 + lane / 8) & 1;
+                    const char *from = from0 + off;
                     const uint32_t dst = to + h * 512 + ((lane ^ (h * 4 + lane / 8)) & 7) * 16;
 #pragma unroll
                     for (int d = 0; d < D / 64; ++d) {
-                        copy16(dst + d * kHalf, from + d * 128, off >= 0);
-                        copy16(dst + kTileBytes + d * kHalf, from + to_v + d * 128, off >= 0);
+                        copy16(dst + d * kHalf, from + d * 128, good);
+                        copy16(dst + kTileBytes + d * kHalf, from + to_v + d * 128, good);
                     }
                 }
                 if (t >= old_tiles) {  // the drafts: a value row with NaN or infinities is taken out
@@ -308,35 +327,39 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     copy_wait<0>();
                     __syncwarp();
                     constexpr uint32_t kExp = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;  // all ones: not finite
-                    uint8_t *v = smem + 2 * kQBytes + (put.slot * 2 + 1) * kTileBytes + (cw * 32 + lane) * 128;
-                    bool odd = false;
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        uint8_t *v = smem + 2 * kQBytes + (put.slot * 2 + 1) * kTileBytes + (e * 32 + lane) * 128;
+                        bool odd = false;
 #pragma unroll 4
-                    for (int d = 0; d < D / 8; ++d) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(v + d / 8 * kHalf + d % 8 * 16);
+                        for (int d = 0; d < D / 8; ++d) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(v + d / 8 * kHalf + d % 8 * 16);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t z = w == 0 ? y.x : w == 1 ? y.y : w == 2 ? y.z : y.w;
-                            odd |= (z & kExp) == kExp || (z >> 16 & kExp) == kExp;
+                            for (int w = 0; w < 4; ++w) {
+                                const uint32_t z = w == 0 ? y.x : w == 1 ? y.y : w == 2 ? y.z : y.w;
+                                odd |= (z & kExp) == kExp || (z >> 16 & kExp) == kExp;
+                            }
                         }
-                    }
-                    const uint32_t odds = __ballot_sync(~0u, odd);
-                    if (odds) {
-                        if (lane == 0) sh.odd[cw] = odds;
-                        if (odd)
-                            for (int d = 0; d < D / 8; ++d)
-                                *reinterpret_cast<uint4 *>(v + d / 8 * kHalf + d % 8 * 16) = make_uint4(0, 0, 0, 0);
-                        proxy_fence();
-                        __syncwarp();
+                        const uint32_t odds = __ballot_sync(~0u, odd);
+                        if (odds) {
+                            if (lane == 0) sh.odd[e] = odds;
+                            if (odd)
+                                for (int d = 0; d < D / 8; ++d)
+                                    *reinterpret_cast<uint4 *>(v + d / 8 * kHalf + d % 8 * 16) = make_uint4(0, 0, 0, 0);
+                            proxy_fence();
+                            __syncwarp();
+                        }
                     }
                 }
                 // arrives when this thread's copies have landed.  (Their writes are handed to the tensor cores by the fence
                 // of the warp that issues the products; a fence here would wait for every copy under way.)
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.full[put.slot])) : "memory");
                 if (lane == 0) {
-                    sh.valid[put.slot][cw] = bits;
+                    sh.valid[put.slot][0] = bits[0];
+                    sh.valid[put.slot][1] = bits[1];
                     mbar_arrive(smem_addr(&sh.full[put.slot]));
                 }
-                put.step(1);
+                put.step(2);
             }
         }
         copy_commit();
