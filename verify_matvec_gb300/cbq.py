@@ -672,6 +672,12 @@ def cbq_tree_attention_workspace(n_seq: int, total_tok: int, max_tok: int, max_l
     return b.value
 
 
+@functools.cache
+def _least_workspace(dev):
+    """What calls that need no workspace pass for one (nothing is written there)."""
+    return _torch().empty(16, dtype=_torch().uint8, device=dev)
+
+
 def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len: int, scale: float | None = None,
                        out=None, with_lse: bool = False, workspace=None, err=None, stream=None):
     """Attention of each sequence's drafted tokens, packed in q (tokens,
@@ -695,7 +701,7 @@ def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len
     lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if with_lse else None
     if workspace is None:
         need = cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _least_workspace(dev) if need <= 16 else torch.empty(need, dtype=torch.uint8, device=dev)
     qp, qt, qh = _heads(q, "q")
     _check(load().cbq_tree_attention(qp, qt, qh, heads, n, c, _vec(table, i32, -1, "table"), width, n_seq,
                                      _vec(ctx, i32, n_seq, "ctx"), _vec(start, i32, n_seq + 1, "start"),

@@ -6,8 +6,11 @@
 //   o = sum_p 2^(x_p - m) v_p / sum_p 2^(x_p - m),  x = scale log2(e) q.k,
 // with the running maximum m and the running sum kept per row while the keys
 // stream by (each new maximum scales what was summed before).  The keys are
-// cut into chunks, a block each, so that a few sequences fill the GPU; a
-// second kernel joins the chunks' (m, sum, o) of a row.
+// cut into chunks, a block each, so that a few sequences fill the GPU; the
+// chunks' (m, sum, o) of a row are joined by a second kernel, or, where there
+// are at most sixteen, by the blocks themselves, which are a cluster then and
+// read one another's shared memory (one launch, no workspace: what short calls
+// need).
 #include <algorithm>
 
 #include "cbq_pipe.cuh"
@@ -95,6 +98,26 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of p, a place in this block's shared memory, in block r of the cluster.
+__device__ __forceinline__ uint32_t peer(const void *p, uint32_t r) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(r));
+    return a;
+}
+__device__ __forceinline__ float2 peer_load2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 // Sizes of the kernel for head size D and 16 * WR rows a block.  Four warps:
 // WR of them share out the rows, and 4 / WR the keys of a tile.  Rows of a
 // tile are padded by 16 bytes, which puts the eight rows of an ldmatrix into
@@ -130,12 +153,12 @@ struct Shape {
 // zeroed and added by hand to the rows that see it.
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
-    k_tree_attention(TreeAttention a, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
+    k_tree_attention(TreeAttention a, int chunk, int row_tiles, bool cluster, float *part_o, float2 *part_ml) {
     using S = Shape<D, WR>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t valid[S::kStages][4];
     __shared__ uint64_t drafts[S::kRows];
-    __shared__ float2 ml[S::kParts][S::kRows];
+    __shared__ float2 ml[S::kParts][S::kRows], joined[S::kRows];
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
@@ -403,6 +426,15 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
                 make_float2(o[d][half * 2] * f, o[d][half * 2 + 1] * f);
     }
     __syncthreads();
+    auto row_of = [&](int r) { return (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group; };
+    auto put = [&](int64_t row, int d, float4 v, float top, float sum) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (a.out_f32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * D + d) = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+        if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    };
     for (int i = tid; i < rows * (D / 4); i += 128) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float top = -INFINITY, sum = 0.0f;
@@ -415,22 +447,45 @@ __global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
             const float4 y = *reinterpret_cast<const float4 *>(res + (w * S::kRows + r) * D + d);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
-        const int64_t row = (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group;
+        if (!alone && cluster) {
+            *reinterpret_cast<float4 *>(res + r * D + d) = v;  // (only this thread has read it)
+            if (d == 0) joined[r] = make_float2(top, sum);
+            continue;
+        }
+        const int64_t row = row_of(r);
         if (!alone) {
             const int64_t at = (int64_t)c * a.total_tok * a.q_heads + row;
             *reinterpret_cast<float4 *>(part_o + at * D + d) = v;
             if (d == 0) part_ml[at] = make_float2(top, sum);
             continue;
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (a.out_f32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-        } else {
-            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * D + d) =
-                make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-        }
-        if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        put(row, d, v, top, sum);
     }
+    if (alone || !cluster) return;
+    // the blocks of the sequence's chunks share out its values: each takes its part from all of them
+    const int chunks = (sq.len + chunk - 1) / chunk;
+    cluster_sync();
+    for (int i = c * 128 + tid; i < rows * (D / 4); i += chunks * 128) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float2 m_of[16];
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int o = 0; o < 16; ++o) {
+            m_of[o] = o < chunks ? peer_load2(peer(&joined[r], o)) : make_float2(-INFINITY, 0.0f);
+            top = fmaxf(top, m_of[o].x);
+        }
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int o = 0; o < 16; ++o) {
+            if (o >= chunks) continue;
+            const float4 y = peer_load4(peer(res + r * D + d, o));
+            const float f = top == -INFINITY ? 0.0f : pow2(m_of[o].x - top);
+            sum += m_of[o].y * f;
+            v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+        }
+        put(row_of(r), d, v, top, sum);
+    }
+    cluster_sync();  // no block leaves while another reads its shared memory
 }
 
 // The chunks of a row (token, head) joined by W warps: with many chunks the
@@ -500,11 +555,11 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, b
 // How a call is cut: rows of a block (16 * wr, or the wide kernel's 256), tiles
 // of them, and the chunk of keys a block takes.
 struct Plan {
-    bool wide;
+    bool wide, cluster;  // the wide kernel; the chunks' blocks join one another
     int wr, row_tiles, chunk, n_chunks;
 };
 
-constexpr int kSms = 152;
+constexpr int kSms = 152, kMaxCluster = 16;
 
 Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, int head_dim) {
     Plan p = {};
@@ -529,12 +584,17 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
         // two blocks for each SM; with several sequences, whose lengths may differ, at most 2048 keys each
         n = (2 * kSms + blocks - 1) / blocks;
         if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
+        // Up to 256 keys a block the blocks join one another: 300 keys 6.4 us against 6.9 with a second kernel.  Beyond, more
+        // blocks and that kernel are faster: 8,191 keys in 16 blocks a head 22.7 us, in 32 with the kernel 16.5.
+        p.cluster = max_len <= kMaxCluster * 256;
+        if (p.cluster) n = std::min<int64_t>(n, kMaxCluster);
     }
     n = std::min<int64_t>(n, 65535);  // of the grid's second axis
     int64_t chunk = (max_len + n - 1) / n;
-    chunk = std::max<int64_t>((chunk + 63) / 64 * 64, 128);
+    chunk = (chunk + 63) / 64 * 64;
     p.chunk = (int)chunk;
     p.n_chunks = (int)((max_len + p.chunk - 1) / p.chunk);
+    p.cluster = p.cluster && p.n_chunks > 1;
     return p;
 }
 
@@ -546,10 +606,11 @@ cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) 
     float2 *part_ml = static_cast<float2 *>(a.ws);
     float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
     const cudaError_t e = p.wide ? launch_tree_wide(a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
-                                 : launch_dependent(k_tree_attention<T, D, WR>,
-                                                    dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
-                                                    128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles, part_o, part_ml);
-    if (e != cudaSuccess || p.n_chunks == 1) return e;
+                                 : launch_clusters(k_tree_attention<T, D, WR>,
+                                                   dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                                                   p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles,
+                                                   p.cluster, part_o, part_ml);
+    if (e != cudaSuccess || p.n_chunks == 1 || p.cluster) return e;
     const unsigned heads = (unsigned)a.q_heads, toks = (unsigned)a.max_tok, seqs = (unsigned)a.n_seq;
     return p.n_chunks > 8 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
                           : launch_dependent(k_tree_join<T, D, 1>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, p.chunk, p.wide,
@@ -580,7 +641,7 @@ size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64
                                 int head_dim) {
     if (!tiled_dim(head_dim)) return 16;
     const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads, head_dim);
-    if (p.n_chunks == 1) return 16;
+    if (p.n_chunks == 1 || p.cluster) return 16;
     const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
     return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
 }
