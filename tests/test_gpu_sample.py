@@ -178,3 +178,39 @@ def test_repeat_stream_graph_and_refusals(torch):
         cbq.cbq_sample(x.double(), t, k, p, None, u)
     with pytest.raises(cbq.CbqError):
         cbq.cbq_sample(torch.zeros((1, cbq.CBQ_SAMPLE_MAX_V + 1), device="cuda"), None, None, None, None, u[:1])
+
+
+@pytest.mark.parametrize("V,dtype", [(1, "float32"), (33, "bfloat16"), (1001, "float32"), (4097, "float16"), (50257, "float32"), (129280, "bfloat16"),
+                                     (262144, "float32")])
+def test_many_rows(torch, V, dtype):
+    """Enough rows that each is a block's own: every kind of setting, short and long rows, kept sets from one to all."""
+    n = 60
+    rng = np.random.default_rng(V)
+    x = _logits(torch, n, V, V + 1, dtype)
+    kinds = np.arange(n) % 6
+    _go(torch, x, t=[0.0 if k == 5 else float(v) for k, v in zip(kinds, rng.uniform(0.3, 2.0, n))],
+        k=[int(v) if k in (1, 4) else 0 for k, v in zip(kinds, np.exp(rng.uniform(0, np.log(V + 1), n)))],
+        p=[float(v) if k in (2, 4) else 1.0 for k, v in zip(kinds, rng.uniform(0.05, 0.9999, n))],
+        m=[float(v) if k in (3, 4) else 0.0 for k, v in zip(kinds, np.exp(rng.uniform(-12, 0.5, n)))])
+
+
+def test_many_rows_strange(torch):
+    """Ties, masks, odd strides and the odd values, a block a row."""
+    inf, nan = float("inf"), float("nan")
+    n, V = 64, 60001
+    rng = np.random.default_rng(4)
+    wide = torch.round(_logits(torch, n, V + 7, 9) * 2) / 2
+    x = wide[:, 3:V + 3]
+    x[0], x[1], x[2] = -inf, nan, 1.5
+    x[3, ::2], x[4, 5::3], x[5, [7, 9000]] = -inf, nan, inf
+    x[6] = -0.0
+    x[6, 11::2] = 0.0
+    x[7] = torch.finfo(torch.float32).min
+    for how in (dict(), dict(k=[int(v) for v in rng.integers(1, V, n)]), dict(p=list(rng.uniform(0.01, 0.999, n))),
+                dict(k=[int(v) for v in rng.integers(1, 50, n)], p=list(rng.uniform(0.1, 0.99, n)), m=list(rng.uniform(0, 0.3, n))),
+                dict(t=[1e-3] * n, k=[40] * n), dict(t=[1e30] * n, p=[0.5] * n), dict(t=[inf] * n), dict(t=[0.0] * n)):
+        ids, probs = _go(torch, x, **how)
+        assert ids[0] == ids[1] == -1 and probs[0] == 0
+    again = _go(torch, x, k=[100] * n, p=[0.9] * n)
+    once = _go(torch, x, k=[100] * n, p=[0.9] * n)
+    assert np.array_equal(again[0], once[0]) and np.array_equal(again[1], once[1])

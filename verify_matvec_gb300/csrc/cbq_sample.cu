@@ -2,7 +2,8 @@
 // top-p and min-p, drawn by a given uniform number.
 //
 // A cluster of up to sixteen blocks takes a row; every thread reads its few
-// logits once.  Nothing is sorted: what top-k and top-p keep is all above a
+// logits once (with many rows fewer blocks a row and more logits a thread, kept
+// in shared memory: less waiting for one another).  Nothing is sorted: what top-k and top-p keep is all above a
 // border in the order and the first few equal to it.  A histogram over the
 // row (of counts for top-k, of weights for top-p) finds the bin of the border;
 // what lies in that bin, some hundred logits, every block gets from all
@@ -78,7 +79,7 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64
     constexpr float k40 = 1099511627776.0f, kRound = 12582912.0f;
     constexpr int kRoundBits = 0x4B400000;
     const float d = l - s.top;
-    const float y = fmaxf(d * s.hi, -50.0f);            // NaN (both infinite) becomes -50 too
+    const float y = fmaxf(d * s.hi, -50.0f);            // (NaN, which no scale times -inf would give, becomes -50 too)
     const float back = d + s.top;                       // two-sum: d + e is the exact difference
     const float e = (l - back) + ((back - d) - s.top);
     const float yl = __fmaf_rn(d, s.hi, -y) + __fmaf_rn(d, s.lo, e * s.hi);
@@ -93,7 +94,7 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64
     const uint64_t w = table[ni & (kTable - 1)];
     const uint64_t full = w + (uint64_t)((int64_t)(int32_t)(w >> 16) * p >> 24);
     const uint64_t v = ((full >> (-(ni >> 8))) + 1) >> 1;
-    return l == s.top ? kOne : y > -47.0f ? v : 0;      // +inf at the top too
+    return y > -47.0f ? v : 0;
 }
 
 // ------------------------------------------------------------- clusters ----
@@ -145,8 +146,7 @@ struct alignas(16) Shared {
     uint64_t swap[2][kMaxBlocks][2];  // what the blocks of the cluster tell one another
     uint64_t warp[kNumWarps], upto[kNumWarps];  // sums of the warps, and inclusive sums of those
     uint32_t key[kNumWarps], at[kNumWarps], listed[kNumWarps];
-    uint32_t mine[kGather];           // the border's bin: this block's, and everyone's
-    uint32_t gather[kGather];
+    uint32_t gather[kGather];         // the border's bin, of all blocks
     uint64_t above, inside, goal;
     int bin, index;
     uint32_t count;
@@ -189,6 +189,7 @@ struct Part {
     uint16_t *place;
     int first, blocks, rank, warp, lane;
     int listed = 0;         // of this warp
+    bool whole = false;     // all of the stretch, each in its place
     int turn = 0, use = 0;  // which of the two swap buffers and histograms is next
 
     // Every block gives two numbers (the same in all its threads); lane r of
@@ -285,6 +286,8 @@ struct Part {
     // `up`, reach goal.  *above: the sum above it; *inside: at it.
     template <bool kWeights, typename B, typename V>
     __device__ float border(B in_bin, V value, uint64_t goal, uint64_t up, uint64_t *above, uint64_t *inside) {
+        uint32_t *own = reinterpret_cast<uint32_t *>(&s.hist[use]);  // this block's part (the next step's histogram, not yet used)
+        static_assert(sizeof(Hist) >= kGather * sizeof(uint32_t), "which has the room");
         if (threadIdx.x == 0) s.count = 0;
         __syncthreads();
         uint32_t lo = ~0u, hi = 0;
@@ -292,7 +295,7 @@ struct Part {
             const float l = list[i];
             if (!in_bin(l)) continue;
             const uint32_t o = order_of(l), n = atomicAdd(&s.count, 1u);
-            if (n < kGather) s.mine[n] = o;
+            if (n < kGather) own[n] = o;
             lo = min(lo, o), hi = max(hi, o);
         }
         lo = __reduce_min_sync(~0u, lo);
@@ -303,7 +306,7 @@ struct Part {
         hi = __reduce_max_sync(~0u, s.at[lane]);
         const int count = s.count, room = kGather / blocks;
         for (int i = threadIdx.x; i < min(count, room) * blocks; i += kSampleThreads)
-            peer_store(peer(&s.gather[rank * room + i / blocks], i % blocks), s.mine[i / blocks]);
+            peer_store(peer(&s.gather[rank * room + i / blocks], i % blocks), own[i / blocks]);
         const ulonglong2 all = tell((uint64_t)hi << 32 | lo, count);
         lo = __reduce_min_sync(~0u, lane < blocks ? (uint32_t)all.x : ~0u);
         hi = __reduce_max_sync(~0u, (uint32_t)(all.x >> 32));
@@ -364,7 +367,7 @@ struct Part {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = i0 + j * 32 + lane;
-                v[j] = i < listed ? what(start + place[i], list[i]) : 0;
+                v[j] = i < listed ? what(start + (whole ? i : (int)place[i]), list[i]) : 0;
             }
             mine += v[0] + v[1] + v[2] + v[3];
         }
@@ -389,7 +392,7 @@ struct Part {
         constexpr int kEach = (N * 32 + kSampleThreads - 1) / kSampleThreads;
         static_assert(kEach == 1, "a thread a place");
         const int to = owner - warp, n = s.listed[owner], i = threadIdx.x;
-        const int where = first + owner * N * 32 + (i < n ? place[to * N * 32 + i] : 0);
+        const int where = first + owner * N * 32 + (i < n ? (whole ? i : (int)place[to * N * 32 + i]) : 0);
         const uint64_t v = i < n ? what(where, list[to * N * 32 + i]) : 0;
         uint64_t rest;
         const uint64_t at = before + block_scan(v, N, &rest);
@@ -422,41 +425,65 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     const int k = a.top_k ? a.top_k[c] : 0;
     const T *logits = static_cast<const T *>(a.logits) + c * a.row_stride;
     const int start = row.first + warp * N * 32 + lane;
-    float x[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = start + j * 32 < a.V ? to_f32(logits[start + j * 32]) : -INFINITY;
-
-    // the first of the order; NaN becomes -inf, and -0 becomes +0
+    // The logits: in registers, or (32 a thread) in shared memory where the list will be, a thread reading its own.
+    // NaN becomes -inf, and -0 becomes +0.
+    constexpr bool kShared = N > 16;
+    constexpr int kSome = N < 16 ? N : 16;  // loads under way at a time
+    float held[kShared ? 1 : N];
     float best = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        x[j] = x[j] == x[j] ? x[j] + 0.0f : -INFINITY;
-        best = fmaxf(best, x[j]);
-    }
-    uint32_t at = ~0u;
+    for (int j0 = 0; j0 < N; j0 += kSome) {
+        T y[kSome];
 #pragma unroll
-    for (int j = N - 1; j >= 0; --j)
-        if (x[j] == best) at = (uint32_t)(start + j * 32);
+        for (int j = 0; j < kSome; ++j) y[j] = logits[min(start + (j0 + j) * 32, a.V - 1)];
+#pragma unroll
+        for (int j = 0; j < kSome; ++j) {
+            float l = to_f32(y[j]);
+            l = start + (j0 + j) * 32 < a.V && l == l ? l + 0.0f : -INFINITY;
+            best = fmaxf(best, l);
+            if constexpr (kShared) row.list[(j0 + j) * 32 + lane] = l;
+            else held[j0 + j] = l;
+        }
+    }
+    auto x = [&](int j) {
+        if constexpr (kShared) return row.list[j * 32 + lane];
+        else return held[j];
+    };
+
+    // the top of the order
     uint32_t top = __reduce_max_sync(~0u, order_of(best));
-    at = __reduce_min_sync(~0u, order_of(best) == top ? at : ~0u);
-    if (lane == 0) s.key[warp] = top, s.at[warp] = at;
+    if (lane == 0) s.key[warp] = top;
     __syncthreads();
     cluster_wait();  // every block of the cluster runs: its shared memory may be written
     top = __reduce_max_sync(~0u, s.key[lane]);
-    at = __reduce_min_sync(~0u, s.key[lane] == top ? s.at[lane] : ~0u);
-    {
-        const ulonglong2 all = row.tell(top, at);
-        top = __reduce_max_sync(~0u, (uint32_t)all.x);
-        at = __reduce_min_sync(~0u, (uint32_t)all.x == top ? (uint32_t)all.y : ~0u);
-    }
-    if (top <= kNone || !(temp > 0.0f)) {
+    top = __reduce_max_sync(~0u, (uint32_t)row.tell(top, 0).x);
+    if (top <= kNone || !(temp > 0.0f) || least > 1.0f) {
+        // no temperature, or a min-p that the first alone meets: the first it is (if there is any)
+        uint32_t at = ~0u;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j)
+            if (x(j) == logit_of(top)) at = (uint32_t)(start + j * 32);
+        at = __reduce_min_sync(~0u, at);
+        if (lane == 0) s.at[warp] = at;
+        __syncthreads();
+        at = __reduce_min_sync(~0u, s.at[lane]);
+        const ulonglong2 all = row.tell(at, 0);  // (by all lanes: a barrier of the cluster)
+        at = __reduce_min_sync(~0u, lane < row.blocks ? (uint32_t)all.x : ~0u);
         if (threadIdx.x == 0 && row.rank == 0) {
             a.ids[c] = top <= kNone ? -1 : (int)at;
             if (a.probs) a.probs[c] = top <= kNone ? 0.0f : 1.0f;
         }
         return;
     }
-    const int top_at = (int)at;
+    if (logit_of(top) == INFINITY) {  // only what is infinite has weight: as 0 among -inf
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float l = x(j) == INFINITY ? 0.0f : -INFINITY;
+            if constexpr (kShared) row.list[j * 32 + lane] = l;
+            else held[j] = l;
+        }
+        top = order_of(0.0f);
+    }
     constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500011e-8f;
     Scale sc;
     sc.top = logit_of(top);
@@ -469,7 +496,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     auto mass = [&](float l) { return weight(l, sc, s.table); };
     auto one = [](float) { return (uint64_t)1; };
     // the least weight that min-p keeps, and a logit surely below it (or below any mass), which is not weighed
-    const uint64_t floor_w = least > 0.0f ? (least < 1.0f ? share(kOne, least, true) : least > 1.0f ? ~0ull : kOne) : 0;
+    const uint64_t floor_w = least > 0.0f ? share(kOne, least, true) : 0;
     const float floor_y = least > 0.0f ? log2f(least) - 0.01f : -47.0f;
     auto heavy = [&](float l) { return (l - sc.top) * sc.hi >= floor_y || l == sc.top; };
 
@@ -483,35 +510,46 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         row.template step<false, true>([&](auto add) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (x[j] > -INFINITY) add(t_of(x[j]), 1);
+                if (x(j) > -INFINITY) add(t_of(x(j)), 1);
         }, [&](uint64_t) { return (uint64_t)k; });
         by_k = s.bin >= 0;
         if (by_k) bin = s.bin, above = s.above;
     } else if (weighed) {
         row.template step<true, true>([&](auto add) {
-#pragma unroll
+#pragma unroll (kShared ? 1 : N / 4)
             for (int j0 = 0; j0 < N; j0 += 4) {  // four chains of arithmetic at a time
+                float l[4];
                 uint64_t v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = mass(x[j0 + j]);
+                for (int j = 0; j < 4; ++j) l[j] = x(j0 + j), v[j] = mass(l[j]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (v[j]) add(t_of(x[j0 + j]), v[j]);
+                    if (v[j]) add(t_of(l[j]), v[j]);
             }
         }, [&](uint64_t total) { return want = goal(total); });
         bin = s.bin;
         above = s.above;
     }
 
-    // the list of what may still be kept
+    // the list of what may still be kept (where the logits lie in its place, it closes up behind what has been read)
     const bool all_of = by_k || by_p;
+    if (!all_of && !(least > 0.0f)) {
+        row.whole = true;
+        row.listed = N * 32;
+        if constexpr (!kShared) {
 #pragma unroll
+            for (int j = 0; j < N; ++j) row.list[j * 32 + lane] = held[j];
+        }
+    } else
+#pragma unroll (kShared ? 4 : N)
     for (int j = 0; j < N; ++j) {
-        const bool in = x[j] > -INFINITY && (all_of ? t_of(x[j]) <= bin : heavy(x[j]));
+        const float l = x(j);
+        const bool in = l > -INFINITY && (all_of ? t_of(l) <= bin : heavy(l));
         const unsigned who = __ballot_sync(~0u, in);
         const int to = row.listed + __popc(who & ((1u << lane) - 1));
-        if (in) row.list[to] = x[j], row.place[to] = (uint16_t)(j * 32 + lane);
+        if (in) row.list[to] = l, row.place[to] = (uint16_t)(j * 32 + lane);
         row.listed += __popc(who);
+        __syncwarp();
     }
     __syncwarp();
 
@@ -558,7 +596,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     }
     const int i = row.walk([&](int at, float l) -> uint64_t {
         const uint64_t v = mass(l);
-        return (l > tau || (l == tau && at <= last)) && (v >= floor_w || at == top_at) ? v : 0;
+        return (l > tau || (l == tau && at <= last)) && v >= floor_w ? v : 0;
     }, [&](uint64_t sum) { return min(share(sum, fminf(fmaxf(u, 0.0f), 1.0f), false) + 1, sum); }, &total, &value);
     if (i >= 0 && threadIdx.x == 0) {
         a.ids[c] = i;
@@ -591,15 +629,17 @@ cudaError_t launch_part(const Sample &a, int blocks, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch(const Sample &a, cudaStream_t s) {
-    // Sixteen logits a thread where there are rows enough to fill the GPU, else eight in twice the blocks
-    const int most = a.n <= 8 ? 16 : 8;
-    int blocks = 1;
-    while (blocks < most && blocks * 8 * kSampleThreads < a.V) blocks *= 2;
-    if (blocks * 8 * kSampleThreads >= a.V) return launch_part<T, 8>(a, blocks, s);
-    while (blocks * 16 * kSampleThreads < a.V) blocks *= 2;
-    return launch_part<T, 16>(a, blocks, s);
+    // Few rows: many blocks each, for the shortest call.  Many: few blocks each, as those of a row wait for one another
+    // (256 rows of 129,280 logits of all kinds: eight blocks a row 215 us, four 149).
+    const int least = a.n <= 8 ? 8 : a.n <= 24 ? 16 : 32;  // logits a thread, where a row is long enough
+    int n = 8, blocks = 1;
+    while (n * blocks * kSampleThreads < a.V) {
+        if (n < least || blocks == kMaxBlocks) n *= 2;
+        else blocks *= 2;
+    }
+    return n == 8 ? launch_part<T, 8>(a, blocks, s) : n == 16 ? launch_part<T, 16>(a, blocks, s) : launch_part<T, 32>(a, blocks, s);
 }
-static_assert(CBQ_SAMPLE_MAX_V <= kMaxBlocks * 16 * kSampleThreads, "the longest row fits a cluster");
+static_assert(CBQ_SAMPLE_MAX_V <= kMaxBlocks * 32 * kSampleThreads, "the longest row fits a cluster");
 
 }  // namespace
 
