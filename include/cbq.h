@@ -487,13 +487,17 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
  * launch; a sequence beyond them, or beyond its table, is cut to them and
  * sets CBQ_DEVERR_BAD_LENGTH; a page id outside the cache is not seen and
  * sets CBQ_DEVERR_BAD_SLOT.  The result does not depend on timing (no
- * atomics on it) but a row's last bits depend on max_len, by which the work
- * is split.  ws_dev: 16-byte aligned, ws_bytes at least what
- * cbq_tree_attention_workspace says, one call at a time.
+ * atomics on it) but a row's last bits depend on the call's limits (n_seq,
+ * max_tok, max_len and the heads), by which the work is split.  Every wait in
+ * the kernels is bounded; one that runs out (1 s) sets
+ * CBQ_DEVERR_PIPE_TIMEOUT and leaves its rows undefined.  ws_dev: 16-byte
+ * aligned, ws_bytes at least what cbq_tree_attention_workspace says, one call
+ * at a time.
  * Errors: EINVAL (null; n_seq < 1 or > 65535; total_tok < 1 or > 2^24;
  * max_tok outside 1..CBQ_TREE_MAX; max_len outside 1..CBQ_TREE_MAX_LEN;
- * kv_heads < 1, > 256 or no divisor of q_heads; q_heads > 1024; table_width < 1; scale not finite; a bad
- * cache; a workspace too small or misaligned), ECUDA, EDEVICE. */
+ * kv_heads < 1, > 256 or no divisor of q_heads; q_heads > 1024; table_width
+ * < 1; scale not finite; a bad cache; a workspace too small or misaligned),
+ * ECUDA, EDEVICE. */
 int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
                        const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
                        const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,

@@ -214,3 +214,32 @@ def test_many_rows_strange(torch):
     again = _go(torch, x, k=[100] * n, p=[0.9] * n)
     once = _go(torch, x, k=[100] * n, p=[0.9] * n)
     assert np.array_equal(again[0], once[0]) and np.array_equal(again[1], once[1])
+
+
+def test_many_rows_dense_and_thin_stretches(torch):
+    """What is kept fills some stretches of a row and leaves few or none in others."""
+    n, V = 40, 70001
+    rng = np.random.default_rng(11)
+    x = _logits(torch, n, V, 17, scale=0.3)
+    x[:, 1500:9000] += 6
+    x[:, 40000:40300] += 6
+    x[::2, 60000:60001] += 5
+    for how in (dict(p=list(rng.uniform(0.3, 0.97, n))), dict(k=[int(v) for v in rng.integers(1, 9000, n)]), dict(m=[0.2] * n),
+                dict(k=[7000] * n, p=list(rng.uniform(0.3, 0.99, n)), m=[0.02] * n)):
+        _go(torch, x, u=rng.random(n, dtype=np.float32), **how)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_top_k_of_clustered_logits(torch, n):
+    """The largest logits next to one another, a thread's own or a block's own; fewer of any weight than top-k takes."""
+    V = 129280
+    rng = np.random.default_rng(12)
+    x = _logits(torch, n, V, 18, scale=0.5)
+    x[:, 32 * 7::32][:, :200] += 9      # one lane's
+    x[::3, 70000:70600] += 9.5          # one block's
+    x[1] = -float("inf")
+    x[1, 5:45] = torch.arange(40, device="cuda") / 8
+    x[2, 100:130] = float("inf")
+    for k in (1, 29, 30, 31, 39, 40, 41, 199, 511, 512, 513, 700):
+        _go(torch, x, k=[k] * n, u=rng.random(n, dtype=np.float32))
+    _go(torch, x, k=[int(v) for v in rng.integers(1, 800, n)], p=list(rng.uniform(0.3, 0.99, n)), u=rng.random(n, dtype=np.float32))

@@ -3,14 +3,25 @@
 //
 // A cluster of up to sixteen blocks takes a row; every thread reads its few
 // logits once (with many rows fewer blocks a row and more logits a thread, kept
-// in shared memory: less waiting for one another).  Nothing is sorted: what top-k and top-p keep is all above a
-// border in the order and the first few equal to it.  A histogram over the
-// row (of counts for top-k, of weights for top-p) finds the bin of the border;
-// what lies in that bin, some hundred logits, every block gets from all
-// others, and finds the border in it by itself.  Only what can still be kept
-// is listed and looked at after that.  Weights are whole numbers of 2^-45, so
-// that their sums do not depend on the order of atomics and a choice is the
+// in shared memory: less waiting for one another).  Nothing is sorted: what
+// top-k and top-p keep is all above a border in the order and the first few
+// equal to it.  A histogram over the row (of counts for top-k, of weights for
+// top-p) finds the bin of the border, and only what can still be kept is
+// listed.  Up to 256 of those one block compares with one another, each with
+// all, and is done.  With more, what lies in the border's bin every block gets
+// from all others and finds the border in it by itself, and the lists are
+// summed up in the order of the indices.  Weights are whole numbers of 2^-45,
+// so that their sums do not depend on the order of atomics and a choice is the
 // same on every run.
+//
+// Bound by the arithmetic of the weights where a whole row is weighed (no cut,
+// or top-p alone: some 50 instructions a logit, 11 of a row's 18 us in a block
+// with 32 logits a thread) and otherwise by its phases' latency: a cluster's
+// wait for all its blocks takes 0.5 to 0.9 us, a histogram of a row with its
+// sums 3.  129,280 fp32 logits: five rows with all cuts 14.3 us (the general
+// way, without one block that settles few: 20.9), 256 rows of all kinds 124.
+#include <cfloat>
+
 #include "cbq_device.cuh"
 #include "step/cbq_step.h"
 #include "step/cbq_types.cuh"
@@ -23,6 +34,8 @@ constexpr int kSampleThreads = 1024, kNumWarps = kSampleThreads / 32;
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 constexpr int kGather = 2048;             // logits of a border's bin, from all blocks
 constexpr int kMaxBlocks = 16;            // of a cluster
+constexpr int kFew = kGather / 4;         // a top-k whose list will mostly fit there
+constexpr int kSettle = kSampleThreads / 4;  // listed ones that one block settles, four threads each
 constexpr int kTable = 256;               // steps of 2^(1/256) of the weights' table
 constexpr uint64_t kOne = 1ull << 45;     // the weight 1
 constexpr uint32_t kNone = 0x007FFFFFu;   // order of -inf: what is not above has no weight
@@ -93,8 +106,7 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64
     const int p = __float2int_rn(th * k40) + (__float_as_int(__fmaf_rn(quad, k40, kRound)) - kRoundBits);
     const uint64_t w = table[ni & (kTable - 1)];
     const uint64_t full = w + (uint64_t)((int64_t)(int32_t)(w >> 16) * p >> 24);
-    const uint64_t v = ((full >> (-(ni >> 8))) + 1) >> 1;
-    return y > -47.0f ? v : 0;
+    return ((full >> (-(ni >> 8))) + 1) >> 1;  // (full is below 2^48: nothing from y = -50, whatever p is there)
 }
 
 // ------------------------------------------------------------- clusters ----
@@ -146,7 +158,7 @@ struct alignas(16) Shared {
     uint64_t swap[2][kMaxBlocks][2];  // what the blocks of the cluster tell one another
     uint64_t warp[kNumWarps], upto[kNumWarps];  // sums of the warps, and inclusive sums of those
     uint32_t key[kNumWarps], at[kNumWarps], listed[kNumWarps];
-    uint32_t gather[kGather];         // the border's bin, of all blocks
+    alignas(8) uint32_t gather[kGather];  // the border's bin, of all blocks
     uint64_t above, inside, goal;
     int bin, index;
     uint32_t count;
@@ -170,6 +182,19 @@ __device__ __forceinline__ uint64_t share(uint64_t n, float f, bool up) {
     return whole + (up && rest ? 1 : 0);
 }
 
+// Of a mass, how much has to be reached for the number u.
+__device__ __forceinline__ uint64_t taken(uint64_t mass, float u) {
+    return min(share(mass, fminf(fmaxf(u, 0.0f), 1.0f), false) + 1, mass);
+}
+
+__device__ __forceinline__ int warp_scan32(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -287,7 +312,7 @@ struct Part {
     template <bool kWeights, typename B, typename V>
     __device__ float border(B in_bin, V value, uint64_t goal, uint64_t up, uint64_t *above, uint64_t *inside) {
         uint32_t *own = reinterpret_cast<uint32_t *>(&s.hist[use]);  // this block's part (the next step's histogram, not yet used)
-        static_assert(sizeof(Hist) >= kGather * sizeof(uint32_t), "which has the room");
+        static_assert(sizeof(Hist) >= kGather * sizeof(uint32_t) && kBins >= kSettle, "which has the room");
         if (threadIdx.x == 0) s.count = 0;
         __syncthreads();
         uint32_t lo = ~0u, hi = 0;
@@ -327,6 +352,44 @@ struct Part {
             *inside = __reduce_add_sync(~0u, (uint32_t)all.y) * value(logit_of(lo));
         }
         while (lo < hi) {
+            if (fits) {  // few: each with all (a step of a descent takes 1.4 us, and there would be three)
+                uint64_t *w = s.hist[use].mine;
+                if (threadIdx.x == 0) s.count = 0;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    if (hi - o[j] > hi - lo || !v[j]) continue;
+                    const uint32_t n = atomicAdd(&s.count, 1u);
+                    if (n < kSettle) own[n] = o[j], w[n] = v[j];
+                }
+                __syncthreads();
+                const int n = s.count, e = threadIdx.x / 4, some = warp * 8 < n ? n : 0;
+                if (n <= kSettle) {
+                    const uint32_t mine = e < n ? own[e] : ~0u;
+                    uint64_t before = 0, equal = 0;
+#pragma unroll 4
+                    for (int f = threadIdx.x % 4; f < some; f += 4) {
+                        const uint32_t other = own[f];
+                        const uint64_t x = w[f];
+                        before += other > mine ? x : 0;
+                        equal += other == mine ? x : 0;
+                    }
+#pragma unroll
+                    for (int i = 1; i < 4; i *= 2) {
+                        before += __shfl_xor_sync(~0u, before, i);
+                        equal += __shfl_xor_sync(~0u, equal, i);
+                    }
+                    if (e < n && up + before < goal && up + before + equal >= goal) {  // (equal ones: all of them)
+                        s.above = up + before;
+                        s.inside = equal;
+                        s.index = (int)mine;
+                    }
+                    __syncthreads();
+                    *above = s.above;
+                    *inside = s.inside;
+                    return logit_of((uint32_t)s.index);
+                }
+            }
             const int sh = max(0, 32 - __clz(hi - lo) - kBinBits);  // (hi - lo) >> sh is below kBins
             auto need = [&](uint64_t) { return goal - up; };
             if (fits) {
@@ -403,6 +466,70 @@ struct Part {
         __syncthreads();
         *value = s.inside;
         return s.index;
+    }
+
+    // What is listed, of all blocks, into the first block's gather, if it is no more than kSettle: order and index in
+    // one number that is larger the earlier in the order.  The number of all, in every thread.
+    __device__ int collect() {
+        if (lane == 0) s.listed[warp] = listed;
+        __syncthreads();
+        const int upto = warp_scan32(s.listed[lane], lane), block = __shfl_sync(~0u, upto, 31);
+        const int others = warp_scan32((int)tell(block, 0).x, lane), n = __shfl_sync(~0u, others, 31);
+        const int to = __shfl_sync(~0u, others, rank) - block + __shfl_sync(~0u, upto, warp) - listed;
+        if (n <= kSettle) {
+            const uint64_t *all = reinterpret_cast<const uint64_t *>(s.gather);
+            for (int i = lane; i < listed; i += 32)
+                peer_store(peer(all + to + i, 0), (uint64_t)order_of(list[i]) << 32 | ~(uint32_t)(first + warp * N * 32 + place[i]));
+        }
+        cluster_sync();
+        return n;
+    }
+
+    // The rest for those n in one block, without another word from the others: for each, what comes before it in the
+    // order, and, of what is kept, before it by index.  want(mass of the first k): what top-p's must reach.
+    template <typename F, typename G>
+    __device__ void settle(int n, int k, F mass, G want, uint64_t least, float u, int32_t *id, float *prob) {
+        uint64_t *key = reinterpret_cast<uint64_t *>(s.gather), *w = key + kSettle, *kept = w + kSettle;
+        static_assert(sizeof(s.gather) >= 3 * kSettle * sizeof(uint64_t), "three numbers each");
+        if (threadIdx.x < (unsigned)n) w[threadIdx.x] = mass(logit_of((uint32_t)(key[threadIdx.x] >> 32)));
+        __syncthreads();
+        const int e = threadIdx.x / 4, q = threadIdx.x % 4, some = warp * 8 < n ? n : 0;
+        const uint64_t mine = e < n ? key[e] : ~0ull, own = e < n ? w[e] : 0;
+        int place_of = 0;
+        uint64_t before = 0;
+#pragma unroll 4
+        for (int f = q; f < some; f += 4) {
+            const uint64_t other = key[f], x = w[f];
+            place_of += other > mine;
+            before += other > mine ? x : 0;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+            place_of += __shfl_xor_sync(~0u, place_of, o);
+            before += __shfl_xor_sync(~0u, before, o);
+        }
+        if (e < n && place_of == min(k, n) - 1) s.goal = before + own;
+        __syncthreads();
+        const bool stays = e < n && place_of < k && before < want(s.goal) && own >= least;
+        if (e < n && q == 0) kept[e] = stays ? own : 0;
+        __syncthreads();
+        uint64_t upto = 0, total = 0;
+#pragma unroll 4
+        for (int f = q; f < some; f += 4) {
+            const uint64_t x = kept[f];
+            total += x;
+            upto += (uint32_t)key[f] >= (uint32_t)mine ? x : 0;  // (the complement of the index)
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+            upto += __shfl_xor_sync(~0u, upto, o);
+            total += __shfl_xor_sync(~0u, total, o);
+        }
+        const uint64_t goal = taken(total, u);
+        if (stays && q == 0 && upto - own < goal && upto >= goal) {
+            *id = (int32_t)~(uint32_t)mine;
+            if (prob) *prob = (float)((double)own / (double)total);
+        }
     }
 };
 
@@ -482,6 +609,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
             if constexpr (kShared) row.list[j * 32 + lane] = l;
             else held[j] = l;
         }
+        best = best == INFINITY ? 0.0f : -INFINITY;
         top = order_of(0.0f);
     }
     constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500011e-8f;
@@ -495,18 +623,26 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     auto t_of = [&](float l) { return l == sc.top ? 0 : min(__float2int_rz((sc.top - l) * cut), kBins - 1); };
     auto mass = [&](float l) { return weight(l, sc, s.table); };
     auto one = [](float) { return (uint64_t)1; };
-    // the least weight that min-p keeps, and a logit surely below it (or below any mass), which is not weighed
-    const uint64_t floor_w = least > 0.0f ? share(kOne, least, true) : 0;
-    const float floor_y = least > 0.0f ? log2f(least) - 0.01f : -47.0f;
-    auto heavy = [&](float l) { return (l - sc.top) * sc.hi >= floor_y || l == sc.top; };
+    const uint64_t floor_w = least > 0.0f ? share(kOne, least, true) : 0;  // the least weight that min-p keeps
 
     // a histogram of the whole row, by counts for top-k or else by weights for top-p, and the bin of the border
     bool by_k = k > 0 && k < a.V;
     const bool by_p = p < 1.0f, weighed = by_p && !by_k;  // (weights first only where top-k cuts nothing)
+    // For the few of a small top-k the largest logit of each thread is enough: as many of those as top-k takes lie at or
+    // above a bin, so its border does, and all that is listed may be the border's (256 rows of 129,280 logits, top-k 100:
+    // 153 us with every logit counted, 148 so, and then 92 as one block settles what is listed).
+    bool few = by_k && k <= kFew;
     int bin = kBins - 1;
     uint64_t want = 0, above = 0, inside = 0;
     auto goal = [&](uint64_t mass_of) { return max(share(mass_of, fmaxf(p, 0.0f), true), (uint64_t)1); };
-    if (by_k) {
+    if (few) {
+        row.template step<false, true>([&](auto add) {
+            if (best > -INFINITY) add(t_of(best), 1);
+        }, [&](uint64_t) { return (uint64_t)k; });
+        few = s.bin >= 0;
+        if (few) bin = s.bin;
+    }
+    if (by_k && !few) {
         row.template step<false, true>([&](auto add) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -531,7 +667,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         above = s.above;
     }
 
-    // the list of what may still be kept (where the logits lie in its place, it closes up behind what has been read)
+    // The list of what may still be kept (where the logits lie in its place, it closes up behind what has been read):
+    // all down to a logit that lies a little below the border's bin, or below what min-p keeps.
     const bool all_of = by_k || by_p;
     if (!all_of && !(least > 0.0f)) {
         row.whole = true;
@@ -540,23 +677,33 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
 #pragma unroll
             for (int j = 0; j < N; ++j) row.list[j * 32 + lane] = held[j];
         }
-    } else
-#pragma unroll (kShared ? 4 : N)
-    for (int j = 0; j < N; ++j) {
-        const float l = x(j);
-        const bool in = l > -INFINITY && (all_of ? t_of(l) <= bin : heavy(l));
-        const unsigned who = __ballot_sync(~0u, in);
-        const int to = row.listed + __popc(who & ((1u << lane) - 1));
-        if (in) row.list[to] = l, row.place[to] = (uint16_t)(j * 32 + lane);
-        row.listed += __popc(who);
         __syncwarp();
+    } else {
+        const float down = !all_of ? (0.01f - log2f(least)) / sc.hi : bin < kBins - 1 ? (bin + 1) / cut : INFINITY;
+        const float lim = fmaxf(__fsub_rd(sc.top, down * 1.00001f), -FLT_MAX);
+#pragma unroll (kShared ? 8 : N)
+        for (int j = 0; j < N; ++j) {
+            const float l = x(j);
+            const unsigned who = __ballot_sync(~0u, l >= lim);
+            if (!who) continue;
+            const int to = row.listed + __popc(who & ((1u << lane) - 1));
+            if (l >= lim) row.list[to] = l, row.place[to] = (uint16_t)(j * 32 + lane);
+            row.listed += __popc(who);
+        }
+        __syncwarp();
+        const int n = row.collect();
+        if (n <= kSettle) {
+            if (row.rank == 0)
+                row.settle(n, by_k ? k : a.V, mass, [&](uint64_t m) { return !by_p ? ~0ull : weighed ? want : goal(m); }, floor_w, u,
+                           a.ids + c, a.probs ? a.probs + c : nullptr);
+            return;
+        }
     }
-    __syncwarp();
 
     float tau = -INFINITY;  // kept: above tau, and the first `ties` at it (all, if ~0)
     uint64_t ties = ~0ull;
     if (by_k) {
-        tau = row.template border<false>([&](float l) { return t_of(l) == bin; }, one, (uint64_t)k, above, &above, &inside);
+        tau = row.template border<false>([&](float l) { return few || t_of(l) == bin; }, one, (uint64_t)k, above, &above, &inside);
         ties = (uint64_t)k - above < inside ? (uint64_t)k - above : ~0ull;
     }
     if (by_p) {
@@ -581,7 +728,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         if (bin >= 0) {
             tau = row.template border<true>([&](float l) { return takes(l) && t_of(l) == bin; }, mass, want, above, &above, &inside);
             const uint64_t each = mass(tau);
-            ties = (want - above + each - 1) / each;
+            ties = 1;
+            if (inside > each) ties = (want - above + each - 1) / each;  // (dear: not where there are no equal ones)
             if (ties * each >= inside) ties = ~0ull;
         } else {  // among the equals
             const uint64_t each = mass(tau);
@@ -597,7 +745,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     const int i = row.walk([&](int at, float l) -> uint64_t {
         const uint64_t v = mass(l);
         return (l > tau || (l == tau && at <= last)) && v >= floor_w ? v : 0;
-    }, [&](uint64_t sum) { return min(share(sum, fminf(fmaxf(u, 0.0f), 1.0f), false) + 1, sum); }, &total, &value);
+    }, [&](uint64_t sum) { return taken(sum, u); }, &total, &value);
     if (i >= 0 && threadIdx.x == 0) {
         a.ids[c] = i;
         if (a.probs) a.probs[c] = (float)((double)value / (double)total);
@@ -630,7 +778,8 @@ cudaError_t launch_part(const Sample &a, int blocks, cudaStream_t s) {
 template <typename T>
 cudaError_t launch(const Sample &a, cudaStream_t s) {
     // Few rows: many blocks each, for the shortest call.  Many: few blocks each, as those of a row wait for one another
-    // (256 rows of 129,280 logits of all kinds: eight blocks a row 215 us, four 149).
+    // (256 rows of 129,280 logits of all kinds: eight blocks a row 215 us, four 149, before few
+    // were settled by one block; two blocks of 512 threads an SM, eight a row, were no faster than four).
     const int least = a.n <= 8 ? 8 : a.n <= 24 ? 16 : 32;  // logits a thread, where a row is long enough
     int n = 8, blocks = 1;
     while (n * blocks * kSampleThreads < a.V) {
