@@ -8,9 +8,8 @@
 // stream by (each new maximum scales what was summed before).  The keys are
 // cut into chunks, a block each, so that a few sequences fill the GPU; the
 // chunks' (m, sum, o) of a row are joined by a second kernel, or, where there
-// are at most sixteen, by the blocks themselves, which are a cluster then and
-// read one another's shared memory (one launch, no workspace: what short calls
-// need).
+// are few, by the blocks themselves, which are a cluster then and read one
+// another's shared memory (one launch, no workspace: what short calls need).
 #include <algorithm>
 
 #include "cbq_pipe.cuh"
@@ -118,6 +117,9 @@ __device__ __forceinline__ float4 peer_load4(uint32_t a) {
     return v;
 }
 
+// Blocks of k_tree_attention that run on an SM together, for its shared memory.
+constexpr int blocks_an_sm(int head_dim) { return head_dim <= 64 ? 3 : head_dim <= 128 ? 2 : 1; }
+
 // Sizes of the kernel for head size D and 16 * WR rows a block.  Four warps:
 // WR of them share out the rows, and 4 / WR the keys of a tile.  Rows of a
 // tile are padded by 16 bytes, which puts the eight rows of an ldmatrix into
@@ -152,7 +154,7 @@ struct Shape {
 // NaN and infinities first (they would make 0 * v NaN): such a value row is
 // zeroed and added by hand to the rows that see it.
 template <typename T, int D, int WR>
-__global__ void __launch_bounds__(128, D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(128, blocks_an_sm(D))
     k_tree_attention(TreeAttention a, int chunk, int row_tiles, bool cluster, float *part_o, float2 *part_ml) {
     using S = Shape<D, WR>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -559,12 +561,22 @@ struct Plan {
     int wr, row_tiles, chunk, n_chunks;
 };
 
-constexpr int kSms = 152, kMaxCluster = 16;
+constexpr int kSms = 152, kMaxCluster = 8;
+
+// Many rows are the wide kernel's.  us by tiles of 64 rows / by the wide kernel, D = 128, 8 kv heads, one sequence: 40 rows
+// at 200 keys 10.4 / 11.5, at 1,000 12.2 / 12.4, at 8,000 19.4 / 16.8; 256 rows 15.0 / 18.7, 28.5 / 23.3, 54.5 / 29.3.
+// 24 sequences: 40 rows 29 / 20, 53 / 36, 204 / 154.  D = 64, 5 kv heads: 78 rows at 200 keys 8.1 / 9.8, at 8,000 15.4 /
+// 14.3; 8 sequences of 384 rows 25 / 11, 152 / 85; 24 sequences of 40 rows, 8 kv heads, 12 / 16, 116 / 113.
+bool wide_rows(int n_seq, int rows, int64_t max_len, int kv_heads, int head_dim) {
+    if (head_dim > 128) return false;
+    const bool full = (int64_t)n_seq * kv_heads * ((rows + 63) / 64) >= kSms;  // tiles of 64 rows would fill the GPU
+    return head_dim > 64 ? rows > 32 && (full || max_len >= 512) : rows > 64 && (full || max_len >= 1024);
+}
 
 Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, int head_dim) {
     Plan p = {};
     const int rows = max_tok * (q_heads / kv_heads);
-    p.wide = rows > 64 && head_dim <= 128 && max_len >= 1024;
+    p.wide = wide_rows(n_seq, rows, max_len, kv_heads, head_dim);
     int64_t n = 1;
     p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     const int block_rows = p.wide ? kWideRows : 16 * p.wr;
@@ -581,13 +593,25 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
         // small beside the keys'
         if (n_seq > 1) n = std::max(n, max_len / std::max(2048, 32 * rows));
     } else {
-        // two blocks for each SM; with several sequences, whose lengths may differ, at most 2048 keys each
-        n = (2 * kSms + blocks - 1) / blocks;
-        if (n_seq > 1) n = std::max(n, (max_len + 2047) / 2048);
-        // Up to 256 keys a block the blocks join one another: 300 keys 6.4 us against 6.9 with a second kernel.  Beyond, more
-        // blocks and that kernel are faster: 8,191 keys in 16 blocks a head 22.7 us, in 32 with the kernel 16.5.
-        p.cluster = max_len <= kMaxCluster * 256;
-        if (p.cluster) n = std::min<int64_t>(n, kMaxCluster);
+        // A block takes 24 ns a key, and 1.6 us and 0.17 a row for the rest; a join by a second kernel costs 2.5 us and one
+        // inside clusters 1.5.  Looked at are the most chunks that fill one wave of blocks, two, three and four: 24
+        // sequences of 2,000 keys (8 kv heads, D = 128) take 47 us in 192 blocks, 53 in 384, 43 in 576 (two waves), 48 in
+        // 768.  Several sequences may differ in length: half the time with half of the chunks empty counts beside the time
+        // with none.  Clusters of more than eight blocks, or beyond one wave, were slower than the second kernel.
+        const int64_t slots = kSms * blocks_an_sm(head_dim), most = (max_len + 63) / 64;
+        const double rest = 1.6 + 0.17 * std::min(rows, block_rows);
+        double least = 0.0;
+        for (int64_t w = 0; w <= 4; ++w) {
+            const int64_t cut = w ? std::min(most, w * slots / blocks) : 1;
+            if (w && cut <= 1) continue;
+            const int64_t keys = ((max_len + cut - 1) / cut + 63) / 64 * 64, m = (max_len + keys - 1) / keys;
+            const bool cluster = m > 1 && m <= kMaxCluster && blocks * m <= slots;
+            const double each = (double)keys * 0.024 + rest;
+            double t = (double)((blocks * m + slots - 1) / slots) * each;
+            if (n_seq > 1) t += 0.5 * (double)((blocks * m / 2 + slots - 1) / slots) * each;
+            t += m == 1 ? 0.0 : cluster ? 1.5 : 2.5;
+            if (w == 0 || t < least) least = t, n = m, p.cluster = cluster;
+        }
     }
     n = std::min<int64_t>(n, 65535);  // of the grid's second axis
     int64_t chunk = (max_len + n - 1) / n;
