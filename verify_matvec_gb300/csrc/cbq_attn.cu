@@ -583,10 +583,13 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
     p.row_tiles = (rows + block_rows - 1) / block_rows;
     const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
     if (p.wide) {
-        // a chunk costs a block about 10 ns a key and 6 us for its results: the n with the least time over all waves
+        // A chunk costs a block about 10 ns a key and 6 us for its results; the join 3 us and the way of the parts to memory
+        // and back (5 TB/s): the n with the least time over all waves.  8 sequences of 256 rows x 500 keys: one chunk 20
+        // us, two 26; one sequence of 128 rows x 8,000: one 75, eight 21, sixteen 19, 24 30.
+        const double part_us = (double)n_seq * kv_heads * rows * head_dim * 8.0 / 5e6;
         double least = 0.0;
         for (int64_t m = 1; m <= 64; ++m) {
-            const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)max_len / m * 0.01 + 6.0);
+            const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)max_len / m * 0.01 + 6.0) + (m > 1 ? 3.0 + part_us * m : 0.0);
             if (m == 1 || t < least) least = t, n = m;
         }
         // several sequences may differ in length: no block takes much longer than others, as long as the parts' bytes stay
