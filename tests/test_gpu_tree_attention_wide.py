@@ -159,3 +159,21 @@ def test_rows_that_scale_alone(torch, drafts):
     want = s.want(128 ** -0.5)
     for _ in range(5):
         s.check(*s.run(), want=want)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("dim,drafts", [(128, 9), (128, 16), (64, 17)])
+def test_many_short_sequences(torch, dim, drafts, dtype):
+    """Sequences enough to fill the GPU with few keys each: none, one, part of a tile, a tile and one more."""
+    rng = np.random.default_rng(drafts)
+    ctx = [0, 1, 63, 64, 65, 128, 200] + [int(v) for v in rng.integers(0, 150, 33)]
+    count = [drafts, 1, 0, drafts] + [int(v) for v in rng.integers(0, drafts + 1, 36)]
+    _go(torch, ctx, count, 16, 4, dim, 16, dtype=dtype, seed=drafts)
+
+
+@pytest.mark.parametrize("ctx", [470, 503, 600, 2100])
+@pytest.mark.parametrize("drafts", [9, 15, 16])
+def test_rows_of_half_a_group(torch, ctx, drafts):
+    """33 to 64 rows a kv head, one sequence and a few."""
+    _go(torch, [ctx], [drafts], 8, 2, 128, 32, seed=ctx)
+    _go(torch, [ctx, 3, 900], [drafts, 9, 2], 4, 1, 128, 48, seed=ctx)
