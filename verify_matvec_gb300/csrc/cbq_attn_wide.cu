@@ -28,10 +28,10 @@
 // copies were the bound: 2,100 clocks a tile for 1,700.)
 //
 // 8 sequences of 64 drafts x 8 heads a kv head over 16,000 keys (270 GFLOP, 543
-// MB) take 263 us, 1,023 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
-// SM 1,050 clocks, of which the products take 594 (S 8 x 46, both operands from
+// MB) take 253 us, 1,064 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
+// SM 1,020 clocks, of which the products take 594 (S 8 x 46, both operands from
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
-// MB) take 65 us: 12 us a block beside its keys, and lengths that differ.
+// MB) take 65 us: some 5 us a block beside its keys, and lengths that differ.
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
@@ -223,31 +223,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // q of the rows, the sign of the scale with it; absent rows are zero
         const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-        constexpr int kOthers = kWideThreads - 64, kAtOnce = 6;
+        // (all loads under way at once: a second round would wait behind the copies of five tiles, some 3 us)
+        constexpr int kOthers = kWideThreads - 64, kAtOnce = (2 * kGroup * (D / 8) + kOthers - 1) / kOthers;
         const int me = warp < kCopyWarp ? tid : tid - 64, pieces = (split ? 1 : 2) * kGroup * (D / 8);
-        for (int i0 = me; i0 < pieces; i0 += kAtOnce * kOthers) {
-            uint4 v[kAtOnce];
+        uint4 v[kAtOnce];
 #pragma unroll
-            for (int x = 0; x < kAtOnce; ++x) {
-                const int r = (i0 + x * kOthers) / (D / 8), d = (i0 + x * kOthers) % (D / 8), at = r < rows ? r0 + r : r0;
-                const T *from = static_cast<const T *>(a.q) + (sq.row0 + at / group) * a.q_tok + (kvh * group + at % group) * a.q_head + d * 8;
-                if (q_whole) {
-                    v[x] = *reinterpret_cast<const uint4 *>(from);
-                } else {
-                    __align__(16) T y[8];
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int r = (me + x * kOthers) / (D / 8), d = (me + x * kOthers) % (D / 8);
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (r >= rows) continue;
+            const T *from = static_cast<const T *>(a.q) + (sq.row0 + (r0 + r) / group) * a.q_tok + (kvh * group + (r0 + r) % group) * a.q_head + d * 8;
+            if (q_whole) {
+                v[x] = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                __align__(16) T y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = from[e];
-                    v[x] = *reinterpret_cast<const uint4 *>(y);
-                }
-                if (r >= rows) v[x] = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 8; ++e) y[e] = from[e];
+                v[x] = *reinterpret_cast<const uint4 *>(y);
             }
+        }
 #pragma unroll
-            for (int x = 0; x < kAtOnce; ++x) {
-                const int i = i0 + x * kOthers, r = i / (D / 8), d = i % (D / 8);
-                if (i >= pieces) break;
-                *reinterpret_cast<uint4 *>(smem + r / kGroup * kQBytes + d / 8 * kQHalf + r % kGroup * 128 + ((d ^ r) & 7) * 16) =
-                    make_uint4(v[x].x ^ flip, v[x].y ^ flip, v[x].z ^ flip, v[x].w ^ flip);
-            }
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int i = me + x * kOthers, r = i / (D / 8), d = i % (D / 8);
+            if (i >= pieces) break;
+            *reinterpret_cast<uint4 *>(smem + r / kGroup * kQBytes + d / 8 * kQHalf + r % kGroup * 128 + ((d ^ r) & 7) * 16) =
+                make_uint4(v[x].x ^ flip, v[x].y ^ flip, v[x].z ^ flip, v[x].w ^ flip);
         }
         proxy_fence();
         asm volatile("bar.sync 2, %0;" ::"n"(kOthers) : "memory");
