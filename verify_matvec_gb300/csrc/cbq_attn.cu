@@ -497,9 +497,10 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     cluster_sync();  // no block leaves while another reads its shared memory
 }
 
-// The chunks of a row (token, head) joined by W warps: with many chunks the
-// eight warps of a block share out those of one row (one warp going through 32
-// chunks took 18 us of a 33 us call), with few each takes a row of its own.  The
+// The chunks of a row (token, head) joined by W warps: with many chunks and few
+// rows the eight warps of a block share out those of one row (one warp going
+// through 32 chunks took 18 us of a 33 us call), otherwise each takes a row of
+// its own.  The
 // wide kernel cuts the committed keys alone (and takes the drafts with the last
 // chunk).  grid (ceil(q_heads * W / 8), max_tok, n_seq).
 template <typename T, int D, int W>
@@ -645,8 +646,10 @@ cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) 
                                                    p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles,
                                                    p.cluster, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1 || p.cluster) return e;
+    // (a warp for each of 1,024 rows of 19 chunks: 21.3 us a call, eight warps 20.4; of 2,048: 28.0 and 30.2; a ragged batch
+    // of 5,000 rows of up to 12: 62 and 65)
     const unsigned heads = (unsigned)a.q_heads, toks = (unsigned)a.max_tok, seqs = (unsigned)a.n_seq;
-    return p.n_chunks > 8 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
+    return p.n_chunks > 8 && rows < 2048 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
                           : launch_dependent(k_tree_join<T, D, 1>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, p.chunk, p.wide,
                                              part_o, part_ml);
 }

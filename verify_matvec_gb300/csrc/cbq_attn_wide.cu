@@ -31,7 +31,7 @@
 // MB) take 253 us, 1,064 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
 // SM 1,020 clocks, of which the products take 594 (S 8 x 46, both operands from
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
-// MB) take 65 us: some 5 us a block beside its keys, and lengths that differ.
+// MB) take 62 us: some 5 us a block beside its keys, and lengths that differ.
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
