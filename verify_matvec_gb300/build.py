@@ -1,7 +1,11 @@
 """Build libcbq.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-The translation units compiled in parallel, linked with the static CUDA
-runtime.  `python -m verify_matvec_gb300.build` or `build()`; the result sits
+The translation units compiled in parallel, linked with the toolkit's shared
+CUDA runtime: a process that has it already (PyTorch brings the same) then runs
+one runtime's code and not two, which is worth 3 us a call from Python where
+tensor operations and the library's calls take turns (an allocation and a
+launch 9.4 us with a static runtime of the library's own, 6.1 with the shared
+one).  `python -m verify_matvec_gb300.build` or `build()`; the result sits
 next to this file and is what the binding loads.
 """
 from __future__ import annotations
@@ -62,7 +66,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(log)
     tmp = OUT + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+    libs = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "lib64")
+    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared", "-Xlinker", "-rpath," + libs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
