@@ -15,11 +15,11 @@
 // same on every run.
 //
 // Bound by the arithmetic of the weights where a whole row is weighed (no cut,
-// or top-p alone: some 50 instructions a logit, 11 of a row's 18 us in a block
-// with 32 logits a thread) and otherwise by its phases' latency: a cluster's
+// or top-p alone: some 40 instructions a logit, packed ones for two at a time
+// among them, 10 of a row's 16 us in a block with 32 logits a thread) and otherwise by its phases' latency: a cluster's
 // wait for all its blocks takes 0.5 to 0.9 us, a histogram of a row with its
 // sums 3.  129,280 fp32 logits: five rows with all cuts 14.3 us (the general
-// way, without one block that settles few: 20.9), 256 rows of all kinds 124.
+// way, without one block that settles few: 20.9), 256 rows of all kinds 121.
 #include <cfloat>
 
 #include "cbq_device.cuh"
@@ -87,27 +87,37 @@ __device__ __forceinline__ float logit_of(uint32_t o) {
 struct Scale {
     float top, hi, lo;  // hi + lo = log2(e) / T
 };
-__device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64_t *table) {
+// Two logits at a time: a packed instruction does the arithmetic of both.
+struct Two {
+    uint64_t a, b;
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Two weigh(float la, float lb, const Scale &s, const uint64_t *table) {
     constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236017e-9f;
     constexpr float k40 = 1099511627776.0f, kRound = 12582912.0f;
     constexpr int kRoundBits = 0x4B400000;
-    const float d = l - s.top;
-    const float y = fmaxf(d * s.hi, -50.0f);            // (NaN, which no scale times -inf would give, becomes -50 too)
-    const float back = d + s.top;                       // two-sum: d + e is the exact difference
-    const float e = (l - back) + ((back - d) - s.top);
-    const float yl = __fmaf_rn(d, s.hi, -y) + __fmaf_rn(d, s.lo, e * s.hi);
-    const float nr = __fmaf_rn(y, (float)kTable, kRound);
-    const float r = __fmaf_rn(nr - kRound, -1.0f / kTable, y);  // exact: y and n/256 agree in their leading bits
-    const int ni = __float_as_int(nr) - kRoundBits;
-    const float th = r * kLn2Hi;
-    const float tl = __fmaf_rn(r, kLn2Hi, -th) + __fmaf_rn(r, kLn2Lo, yl * kLn2Hi);
-    const float t = th + tl;
-    const float quad = __fmaf_rn(t * t, __fmaf_rn(t, 1.0f / 6.0f, 0.5f), tl);
-    const int p = __float2int_rn(th * k40) + (__float_as_int(__fmaf_rn(quad, k40, kRound)) - kRoundBits);
-    const uint64_t w = table[ni & (kTable - 1)];
-    const uint64_t full = w + (uint64_t)((int64_t)(int32_t)(w >> 16) * p >> 24);
-    return ((full >> (-(ni >> 8))) + 1) >> 1;  // (full is below 2^48: nothing from y = -50, whatever p is there)
+    const float2 l = make_float2(la, lb), minus = both(-1.0f), hi = both(s.hi);
+    const float2 d = __fadd2_rn(l, both(-s.top)), w = __fmul2_rn(d, both(-s.hi));
+    const float2 z = make_float2(fminf(w.x, 50.0f), fminf(w.y, 50.0f));  // -y (NaN, which no scale times -inf would give, becomes 50 too)
+    const float2 back = __fadd2_rn(d, both(s.top));                      // two-sum: d + e is the exact difference
+    const float2 e = __fadd2_rn(__ffma2_rn(back, minus, l), __fadd2_rn(__ffma2_rn(d, minus, back), both(-s.top)));
+    const float2 yl = __fadd2_rn(__ffma2_rn(d, hi, z), __ffma2_rn(d, both(s.lo), __fmul2_rn(e, hi)));
+    const float2 nr = __ffma2_rn(z, both(-(float)kTable), both(kRound));
+    const float2 r = __ffma2_rn(__fadd2_rn(nr, both(-kRound)), both(1.0f / kTable), z);  // n/256 - y, exact: they agree in their leading bits
+    const float2 th = __fmul2_rn(r, both(kLn2Hi));                       // -t's larger part
+    const float2 tl = __fadd2_rn(__ffma2_rn(r, both(-kLn2Hi), th), __ffma2_rn(r, both(-kLn2Lo), __fmul2_rn(yl, both(kLn2Hi))));
+    const float2 t = __ffma2_rn(th, minus, tl);
+    const float2 quad = __ffma2_rn(__fmul2_rn(t, t), __ffma2_rn(t, both(1.0f / 6.0f), both(0.5f)), tl);
+    const float2 large = __fmul2_rn(th, both(-k40)), small = __ffma2_rn(quad, both(k40), both(kRound));
+    auto whole = [&](float n256, float x, float y) {
+        const int ni = __float_as_int(n256) - kRoundBits, p = __float2int_rn(x) + (__float_as_int(y) - kRoundBits);
+        const uint64_t v = table[ni & (kTable - 1)];
+        const uint64_t full = v + (uint64_t)((int64_t)(int32_t)(v >> 16) * p >> 24);
+        return ((full >> (-(ni >> 8))) + 1) >> 1;  // (full is below 2^48: nothing from y = -50, whatever p is there)
+    };
+    return Two{whole(nr.x, large.x, small.x), whole(nr.y, large.y, small.y)};
 }
+__device__ __forceinline__ uint64_t weight(float l, const Scale &s, const uint64_t *table) { return weigh(l, l, s, table).a; }
 
 // ------------------------------------------------------------- clusters ----
 
@@ -418,21 +428,23 @@ struct Part {
         return logit_of(lo);
     }
 
-    // The index where what(index, logit) of what is listed, summed in the order
-    // of the indices over the whole row, reaches need(sum); -1 in the blocks
-    // that do not hold it.  *total: the row's sum; *value: what() there.
-    template <typename W, typename G>
-    __device__ int walk(W what, G need, uint64_t *total, uint64_t *value) {
+    // The index where value(two logits) of what is listed and counts(index, logit,
+    // value), summed in the order of the indices over the whole row, reaches
+    // need(sum); -1 in the blocks that do not hold it.  *total: the row's sum;
+    // *at: the value there.
+    template <typename V, typename C, typename G>
+    __device__ int walk(V value, C counts, G need, uint64_t *total, uint64_t *at) {
         const int start = first + warp * N * 32;
         uint64_t mine = 0;
-        for (int i0 = 0; i0 < listed; i0 += 128) {  // four chains of arithmetic at a time
-            uint64_t v[4];
+        for (int i0 = 0; i0 < listed; i0 += 128) {  // two chains of arithmetic at a time (and within the stretch)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; j += 2) {
                 const int i = i0 + j * 32 + lane;
-                v[j] = i < listed ? what(start + (whole ? i : (int)place[i]), list[i]) : 0;
+                const float la = list[i], lb = list[i + 32];
+                const Two v = value(la, lb);
+                mine += i < listed && counts(start + (whole ? i : (int)place[i]), la, v.a) ? v.a : 0;
+                mine += i + 32 < listed && counts(start + (whole ? i + 32 : (int)place[i + 32]), lb, v.b) ? v.b : 0;
             }
-            mine += v[0] + v[1] + v[2] + v[3];
         }
         // at most 2^50 a lane: the sum of a warp in two halves
         sum_warps((uint64_t)__reduce_add_sync(~0u, (uint32_t)mine & 0xFFFFFFu) +
@@ -456,15 +468,20 @@ struct Part {
         static_assert(kEach == 1, "a thread a place");
         const int to = owner - warp, n = s.listed[owner], i = threadIdx.x;
         const int where = first + owner * N * 32 + (i < n ? (whole ? i : (int)place[to * N * 32 + i]) : 0);
-        const uint64_t v = i < n ? what(where, list[to * N * 32 + i]) : 0;
+        uint64_t v = 0;
+        if (i < n) {
+            const float l = list[to * N * 32 + i];
+            v = value(l, l).a;
+            v = counts(where, l, v) ? v : 0;
+        }
         uint64_t rest;
-        const uint64_t at = before + block_scan(v, N, &rest);
-        if (at - v < goal && at >= goal) {
+        const uint64_t upto = before + block_scan(v, N, &rest);
+        if (upto - v < goal && upto >= goal) {
             s.index = where;
             s.inside = v;
         }
         __syncthreads();
-        *value = s.inside;
+        *at = s.inside;
         return s.index;
     }
 
@@ -653,11 +670,15 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     } else if (weighed) {
         row.template step<true, true>([&](auto add) {
 #pragma unroll (kShared ? 1 : N / 4)
-            for (int j0 = 0; j0 < N; j0 += 4) {  // four chains of arithmetic at a time
+            for (int j0 = 0; j0 < N; j0 += 4) {  // two chains of arithmetic at a time
                 float l[4];
                 uint64_t v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) l[j] = x(j0 + j), v[j] = mass(l[j]);
+                for (int j = 0; j < 4; j += 2) {
+                    l[j] = x(j0 + j), l[j + 1] = x(j0 + j + 1);
+                    const Two w = weigh(l[j], l[j + 1], sc, s.table);
+                    v[j] = w.a, v[j + 1] = w.b;
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (v[j]) add(t_of(l[j]), v[j]);
@@ -739,12 +760,12 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     int last = a.V;  // the index of the last kept one at tau
     uint64_t total, value;
     if (ties != ~0ull) {
-        const int i = row.walk([&](int, float l) { return (uint64_t)(l == tau); }, [&](uint64_t) { return ties; }, &total, &value);
+        const int i = row.walk([](float, float) { return Two{1, 1}; }, [&](int, float l, uint64_t) { return l == tau; },
+                               [&](uint64_t) { return ties; }, &total, &value);
         last = (int)__reduce_max_sync(~0u, (uint32_t)row.tell((uint64_t)(i + 1), 0).x) - 1;
     }
-    const int i = row.walk([&](int at, float l) -> uint64_t {
-        const uint64_t v = mass(l);
-        return (l > tau || (l == tau && at <= last)) && v >= floor_w ? v : 0;
+    const int i = row.walk([&](float x, float y) { return weigh(x, y, sc, s.table); }, [&](int at, float l, uint64_t v) {
+        return (l > tau || (l == tau && at <= last)) && v >= floor_w;
     }, [&](uint64_t sum) { return taken(sum, u); }, &total, &value);
     if (i >= 0 && threadIdx.x == 0) {
         a.ids[c] = i;
