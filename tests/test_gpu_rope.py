@@ -174,3 +174,56 @@ def test_stream_graph_and_refusals(torch):
         cbq.cbq_rope(x, pos.long(), t)
     with pytest.raises(cbq.CbqError):
         cbq.cbq_rope(x, pos, t, rot_off=2)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("n,heads,dim,rot,off", [(4801, 3, 64, 64, 0), (5000, 2, 96, 32, 64), (1700, 40, 128, 64, 64), (420, 9, 1024, 1024, 0)])
+def test_many_tokens(torch, dtype, layout, n, heads, dim, rot, off):
+    """Blocks that go through several tokens: an odd number of them, several parts of a token, heads turned in part."""
+    test_rope(torch, dtype, layout, n, heads, dim, rot, off)
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_many_tokens_strides_and_in_place(torch, layout):
+    n = 4003
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").flip(0)
+    t = cbq.cbq_rope_turns(64)
+    for base in (_randn(torch, 2, n, 5, 136, dtype=torch.bfloat16)[:, 1:4, :128], _randn(torch, 4, 3, n, 128).transpose(0, 1)):
+        want, size = step_ref.rotate(base.double().cpu().numpy(), pos.cpu().numpy(), t.cpu().numpy(), 64, layout)
+        got = cbq.cbq_rope(base, pos, t, rot_off=64, layout=layout)
+        _check(torch, got, want, size, base.dtype)
+        assert cbq.cbq_rope(base, pos, t, rot_off=64, layout=layout, out=base) is base
+        assert torch.equal(base, got)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_append_many_tokens(torch, dtype):
+    """A prompt into a cache, with tokens that have no place in it."""
+    test_append(torch, dtype, "float16", 4100, 4, 2, 64, 64, 0, 16, True)
+    n, dt = 4100, getattr(torch, dtype)
+    q, k, v = (_randn(torch, i, n, h, 64, dtype=dt) for i, h in enumerate((3, 1, 1)))
+    kc, vc = (_randn(torch, 5 + i, 300, 16, 1, 64, dtype=torch.bfloat16) for i in range(2))
+    before = kc.clone(), vc.clone()
+    slots = torch.randperm(4800, device="cuda")[:n]
+    slots[::3] = -1
+    slots[4099] = 4800
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    t = cbq.cbq_rope_turns(32)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cbq.cbq_rope_append(q, k, v, pos, slots, t, kc, vc, err=err)
+    assert err.item() == cbq.CBQ_DEVERR_BAD_SLOT
+    good = torch.ones(n, dtype=torch.bool, device="cuda")
+    good[::3] = False
+    good[4099] = False
+    for c, b, x in ((kc, before[0], cbq.cbq_rope(k, pos, t)), (vc, before[1], v)):
+        b = b.view(4800, 1, 64)
+        b[slots[good]] = x[good].to(torch.bfloat16) if x is v else b[slots[good]]
+        if x is v:
+            assert torch.equal(c.view(4800, 1, 64), b)
+        else:
+            rest = torch.ones(4800, dtype=torch.bool, device="cuda")
+            rest[slots[good]] = False
+            assert torch.equal(c.view(4800, 1, 64)[rest], b[rest])
+            want, size = step_ref.rotate(k.double().cpu().numpy(), pos.cpu().numpy(), t.cpu().numpy(), 0, "half")
+            _check(torch, c.view(4800, 1, 64)[slots[good]], want[good.cpu().numpy()], size[good.cpu().numpy()], torch.bfloat16)

@@ -8,14 +8,16 @@
 // three digits of the part), then sine and cosine are fp32 (sincospif).
 //
 // Bound by memory: each value is read once and written once.  8,192 tokens x 32
-// heads x 128 bf16 (134 MB) take 29.3 us, 4.6 TB/s; 4,095 tokens x 48 heads into
-// a cache (101 MB) 22.9 us, 4.4 TB/s; a handful of tokens 2.1 to 2.4 us, a
-// launch.  Measured on the first: a value a thread 53.7 us, 16-byte pieces 39,
-// with the places worked out once for the tokens of a block and their loads
-// under way together 31, the sines and cosines laid out without bank conflicts
-// 29 (four tokens a block for pairs of neighbours; for halves, which need twice
-// the registers an item, two: four took 47).
-#include "cbq_device.cuh"
+// heads x 128 bf16 (134 MB) take 23.9 us, 5.6 TB/s; 4,095 tokens x 48 heads into
+// random places of a cache (101 MB) 22.2 us, 4.5 TB/s; a handful of tokens 2.1
+// to 2.2 us, a launch.  Measured on the first: a value a thread 53.7 us, 16-byte
+// pieces 39, loads of two tokens under way together and sines and cosines laid
+// out without bank conflicts 29, blocks that go through several tokens with the
+// next ones' pieces coming meanwhile 23.9.
+#include <algorithm>
+
+#include "cbq_pipe.cuh"
+#include "step/cbq_copy.cuh"
 #include "step/cbq_step.h"
 #include "step/cbq_types.cuh"
 
@@ -24,6 +26,8 @@ namespace cbq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kStreamTokens = 2;  // a block, from which on k_rope_stream goes through them (1,200 tokens x 8 heads of 128 bf16:
+                                  // 3.2 us, a token a block 3.9; 300 tokens, pairs: 2.7 and 2.3)
 
 // One group of heads of a token: rotated or copied, to plain strides or (cached) to the token's slot.
 struct Group {
@@ -60,106 +64,184 @@ struct alignas(V * sizeof(T)) Vec {
 // A token's values are taken V at a time (16 bytes of input): an item is two
 // such pieces whose values form pairs (half layout), one piece (pairs of
 // neighbours), or one piece that is copied.  V = 1 takes any alignment: an item
-// is a pair or a value.  A thread takes one item of kTok tokens: it works out
-// the place once and has all their loads under way together.  grid (blocks of
-// kTok tokens, parts of a token's items).  Each block turns its tokens' angles
-// into sines and cosines once, behind the loads of its first items.
-template <typename Tin, typename Tout, int V, bool kHalfLayout, int kTok>
+// is a pair or a value.
+template <typename Tin, typename Tout, int V, bool kHalfLayout>
+struct Item {
+    static constexpr int kPiece = !kHalfLayout && V == 1 ? 2 : V;  // values of a rotated piece
+    static constexpr bool kTwo = kHalfLayout || V == 1;            // a rotated item is two loads
+    static constexpr int kPairs = V == 1 ? 1 : kHalfLayout ? V : V / 2;  // of a rotated item
+    static constexpr int kStep = kTwo ? 2 : 4;                     // tokens of a step of k_rope_stream
+    const Group &g;
+    const Tin *from;  // of token 0
+    Tout *to;         // of token 0, or (cached) of place 0
+    int i, turning, half, second;
+    bool turns;
+
+    __device__ Item(const RopeArgs &a, int x, int n)
+        : g(a.g[n]), half(a.r.rot / 2), turning(a.r.rot / (kPiece * (kHalfLayout ? 2 : 1))), second(kHalfLayout ? half : 1) {
+        const unsigned each = a.per_head[n], in = x - a.first[n], h = in / each;
+        i = in - h * each;
+        turns = g.rotate && i < turning;
+        int d = turns ? a.r.off + i * kPiece : (i - (g.rotate ? turning : 0)) * V;
+        if (!turns && g.rotate && d >= a.r.off) d += a.r.rot;
+        from = static_cast<const Tin *>(g.src) + h * g.src_head + d;
+        to = static_cast<Tout *>(g.dst) + h * g.dst_head + d;
+    }
+    static __device__ int group(const RopeArgs &a, int x) { return x >= a.first[1] ? (x >= a.first[2] ? 2 : 1) : 0; }
+
+    // Where pair p of a head lies among a token's sines and cosines: two pairs of every item side by side, then the next
+    // two, so that lanes with items in a row read them without bank conflicts.
+    static __device__ int place_of(int p, int turning) {
+        const int i = p / kPairs, q = p % kPairs;
+        return kPairs == 1 ? p : (q / 2 * turning + i) * 2 + q % 2;
+    }
+
+    // The item turned (va and vb) or copied (va) to `at`.
+    __device__ void put(const Vec<Tin, V> &va, const Vec<Tin, V> &vb, const float2 *cs, Tout *at) const {
+        Vec<Tout, V> oa, ob;
+        if (!turns) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) oa.v[e] = from_f32<Tout>(to_f32(va.v[e]));
+            *reinterpret_cast<Vec<Tout, V> *>(at) = oa;
+            return;
+        }
+        float2 c[kPairs];
+        if constexpr (kPairs == 1) {
+            c[0] = cs[i];
+        } else {
+#pragma unroll
+            for (int q = 0; q < kPairs; q += 2) {
+                const float4 y = *reinterpret_cast<const float4 *>(cs + (q / 2 * turning + i) * 2);
+                c[q] = make_float2(y.x, y.y), c[q + 1] = make_float2(y.z, y.w);
+            }
+        }
+        if constexpr (kTwo) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float x = to_f32(va.v[e]), y = to_f32(vb.v[e]);
+                oa.v[e] = from_f32<Tout>(x * c[e].x - y * c[e].y);
+                ob.v[e] = from_f32<Tout>(x * c[e].y + y * c[e].x);
+            }
+            *reinterpret_cast<Vec<Tout, V> *>(at + second) = ob;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const float x = to_f32(va.v[e]), y = to_f32(va.v[e + 1]);
+                oa.v[e] = from_f32<Tout>(x * c[e / 2].x - y * c[e / 2].y);
+                oa.v[e + 1] = from_f32<Tout>(x * c[e / 2].y + y * c[e / 2].x);
+            }
+        }
+        *reinterpret_cast<Vec<Tout, V> *>(at) = oa;
+    }
+};
+
+// Sine and cosine of pair p at a position, times mscale.
+__device__ __forceinline__ float2 angle(const RopeArgs &a, int64_t token, int p) {
+    double turn = (double)a.r.pos[token] * a.r.turns[p];
+    turn -= rint(turn);
+    float s, c;
+    sincospif(2.0f * (float)turn, &s, &c);
+    return make_float2(c * a.r.mscale, s * a.r.mscale);
+}
+
+// Where a token's row of the cache begins, -1 if it has none.
+__device__ __forceinline__ int64_t cache_place(const RopeArgs &a, int64_t token, bool tell) {
+    const int64_t slot = a.slots[token];
+    if (slot >= a.n_slots && a.err && tell) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+    return slot >= 0 && slot < a.n_slots ? slot / a.page_size * a.page_stride + slot % a.page_size * a.tok_stride : -1;
+}
+
+// A token a block: grid (tokens, parts of a token's items).  The angles are
+// taken behind the loads of the first items.
+template <typename Tin, typename Tout, int V, bool kHalfLayout>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs a) {
-    constexpr int kPiece = !kHalfLayout && V == 1 ? 2 : V;  // values of a rotated piece
-    constexpr bool kTwo = kHalfLayout || V == 1;            // a rotated item is two loads
-    constexpr int kPairs = V == 1 ? 1 : kHalfLayout ? V : V / 2;  // of a rotated item
-    // kTok x rot/2 sines and cosines, two pairs of every item side by side, then the next two: lanes with items in a row
-    // read them without bank conflicts
+    using I = Item<Tin, Tout, V, kHalfLayout>;
     extern __shared__ __align__(16) float2 cs[];
-    __shared__ int64_t place[kTok];
+    __shared__ int64_t place;
     pdl_trigger();
     pdl_wait();
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    const int half = a.r.rot / 2, turning = a.r.rot / (kPiece * (kHalfLayout ? 2 : 1));  // rotated items of a head
-    const int tokens = a.n_tok - t0 < kTok ? (int)(a.n_tok - t0) : kTok;
-    if (a.slots) {
-        if (threadIdx.x < tokens) {
-            const int64_t slot = a.slots[t0 + threadIdx.x];
-            const bool good = slot >= 0 && slot < a.n_slots;
-            if (slot >= a.n_slots && a.err && blockIdx.y == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-            place[threadIdx.x] = good ? slot / a.page_size * a.page_stride + slot % a.page_size * a.tok_stride : -1;
-        }
-        __syncthreads();
-    }
+    const int64_t t = blockIdx.x;
+    if (a.slots && threadIdx.x == 0) place = cache_place(a, t, blockIdx.y == 0);
     const int end = a.first[a.n_groups];
     bool known = false;
     for (int x0 = blockIdx.y * kRopeThreads; x0 < end; x0 += gridDim.y * kRopeThreads) {
         const int x = x0 + threadIdx.x;
         const bool some = x < end;
-        const int n = x >= a.first[1] ? (x >= a.first[2] ? 2 : 1) : 0;
-        const Group &g = a.g[some ? n : 0];
-        const unsigned each = a.per_head[some ? n : 0], in = some ? x - a.first[n] : 0, h = in / each, i = in - h * each;
-        const bool turns = g.rotate && i < (unsigned)turning;
-        int d = turns ? a.r.off + i * kPiece : (i - (g.rotate ? turning : 0)) * V;
-        if (!turns && g.rotate && d >= a.r.off) d += a.r.rot;
-        const int second = kHalfLayout ? half : 1;
-        const Tin *from = static_cast<const Tin *>(g.src) + t0 * g.src_tok + h * g.src_head + d;
-        Tout *to = static_cast<Tout *>(g.dst) + (g.cached ? 0 : t0 * g.dst_tok) + h * g.dst_head + d;
-        Vec<Tin, V> va[kTok], vb[kTok];
-#pragma unroll
-        for (int u = 0; u < kTok; ++u) {
-            if (!some || u >= tokens) continue;
-            va[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + u * g.src_tok);
-            if (kTwo && turns) vb[u] = *reinterpret_cast<const Vec<Tin, V> *>(from + u * g.src_tok + second);
+        const I it(a, some ? x : x0, I::group(a, some ? x : x0));
+        Vec<Tin, V> va, vb;
+        if (some) {
+            va = *reinterpret_cast<const Vec<Tin, V> *>(it.from + t * it.g.src_tok);
+            if (I::kTwo && it.turns) vb = *reinterpret_cast<const Vec<Tin, V> *>(it.from + t * it.g.src_tok + it.second);
         }
         if (!known) {
             known = true;
-            for (int j = threadIdx.x; j < tokens * half; j += kRopeThreads) {
-                const int u = j / half;
-                double turn = (double)a.r.pos[t0 + u] * a.r.turns[j - u * half];
-                turn -= rint(turn);
-                float s, c;
-                sincospif(2.0f * (float)turn, &s, &c);
-                const int p = j - u * half, i = p / kPairs, q = p % kPairs;
-                cs[u * half + (kPairs == 1 ? p : (q / 2 * turning + i) * 2 + q % 2)] = make_float2(c * a.r.mscale, s * a.r.mscale);
-            }
+            for (int p = threadIdx.x; p < it.half; p += kRopeThreads) cs[I::place_of(p, it.turning)] = angle(a, t, p);
             __syncthreads();
         }
+        const int64_t at = !it.g.cached ? t * it.g.dst_tok : place;
+        if (some && at >= 0) it.put(va, vb, cs, it.to + at);
+    }
+}
+
+// Many tokens: a block goes through `each` of them in a row, kStep at a time,
+// for one item a thread.  The pieces come through shared memory, kRing - 1
+// steps ahead, every thread its own (it waits for its own copies and for nobody
+// else's); the next step's angles are taken while this one's results are
+// written.  grid (blocks of `each` tokens, parts of a token's items).
+constexpr int kRing = 3;
+template <typename Tin, typename Tout, int V, bool kHalfLayout>
+__global__ void __launch_bounds__(kRopeThreads, 4) k_rope_stream(const __grid_constant__ RopeArgs a, int each) {
+    using I = Item<Tin, Tout, V, kHalfLayout>;
+    using Piece = Vec<Tin, V>;
+    static_assert(sizeof(Piece) == 16, "16-byte copies");
+    constexpr int kPieces = I::kTwo ? 2 : 1, kStep = I::kStep;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Piece *ring = reinterpret_cast<Piece *>(smem) + threadIdx.x;  // [kRing][kStep][kPieces][threads]
+    float2 *cs = reinterpret_cast<float2 *>(smem + kRing * kStep * kPieces * kRopeThreads * 16);  // [2][kStep][rot/2]
+    __shared__ int64_t place[2][kStep];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t t0 = (int64_t)blockIdx.x * each;
+    const int tokens = a.n_tok - t0 < each ? (int)(a.n_tok - t0) : each, steps = (tokens + kStep - 1) / kStep;
+    const int end = a.first[a.n_groups], x = blockIdx.y * kRopeThreads + threadIdx.x;
+    const bool some = x < end;
+    const I it(a, some ? x : end - 1, I::group(a, some ? x : end - 1));
+    const Tin *from = it.from + t0 * it.g.src_tok;
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < kTok; ++u) {
-            if (!some || u >= tokens) continue;
-            const int64_t at = g.cached ? place[u] : u * g.dst_tok;
-            if (at < 0) continue;
-            Vec<Tout, V> oa, ob;
-            float2 c[kPairs];
-            if (turns) {
-                if constexpr (kPairs == 1) {
-                    c[0] = cs[u * half + i];
-                } else {
-#pragma unroll
-                    for (int q = 0; q < kPairs; q += 2) {
-                        const float4 y = *reinterpret_cast<const float4 *>(cs + u * half + (q / 2 * turning + i) * 2);
-                        c[q] = make_float2(y.x, y.y), c[q + 1] = make_float2(y.z, y.w);
-                    }
-                }
-            }
-            if (!turns) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) oa.v[e] = from_f32<Tout>(to_f32(va[u].v[e]));
-            } else if constexpr (kTwo) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float x = to_f32(va[u].v[e]), y = to_f32(vb[u].v[e]);
-                    oa.v[e] = from_f32<Tout>(x * c[e].x - y * c[e].y);
-                    ob.v[e] = from_f32<Tout>(x * c[e].y + y * c[e].x);
-                }
-                *reinterpret_cast<Vec<Tout, V> *>(to + at + second) = ob;
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; e += 2) {
-                    const float x = to_f32(va[u].v[e]), y = to_f32(va[u].v[e + 1]);
-                    oa.v[e] = from_f32<Tout>(x * c[e / 2].x - y * c[e / 2].y);
-                    oa.v[e + 1] = from_f32<Tout>(x * c[e / 2].y + y * c[e / 2].x);
-                }
-            }
-            *reinterpret_cast<Vec<Tout, V> *>(to + at) = oa;
+        for (int u = 0; u < kStep; ++u) {
+            if (i * kStep + u >= tokens || !some) continue;
+            Piece *to = ring + ((i % kRing) * kStep + u) * kPieces * kRopeThreads;
+            const Tin *x = from + (i * kStep + u) * it.g.src_tok;
+            copy16(smem_addr(to), x, true);
+            if (I::kTwo && it.turns) copy16(smem_addr(to + kRopeThreads), x + it.second, true);
         }
+        copy_commit();
+    };
+    auto angles = [&](int i) {
+        for (int j = threadIdx.x; j < kStep * it.half; j += kRopeThreads) {
+            const int u = j / it.half, p = j - u * it.half;
+            if (i * kStep + u < tokens) cs[((i & 1) * kStep + u) * it.half + I::place_of(p, it.turning)] = angle(a, t0 + i * kStep + u, p);
+        }
+        if (a.slots && threadIdx.x < kStep && i * kStep + threadIdx.x < tokens)
+            place[i & 1][threadIdx.x] = cache_place(a, t0 + i * kStep + threadIdx.x, blockIdx.y == 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
+    angles(0);
+    for (int i = 0; i < steps; ++i) {
+        copy_wait<kRing - 2>();
+        __syncthreads();  // this step's angles are there, and the step before has been read
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            if (i * kStep + u >= tokens || !some) continue;
+            const Piece *v = ring + ((i % kRing) * kStep + u) * kPieces * kRopeThreads;
+            const Piece va = v[0], vb = v[(kPieces - 1) * kRopeThreads];
+            const int64_t at = it.g.cached ? place[i & 1][u] : (t0 + i * kStep + u) * it.g.dst_tok;
+            if (at >= 0) it.put(va, vb, cs + ((i & 1) * kStep + u) * it.half, it.to + at);
+        }
+        fetch(i + kRing - 1);
+        if (i + 1 < steps) angles(i + 1);
     }
 }
 
@@ -177,21 +259,30 @@ cudaError_t launch_pieces(RopeArgs a, cudaStream_t s) {
     a.first[a.n_groups] = end;
     for (int n = a.n_groups + 1; n < 4; ++n) a.first[n] = end;
     const int parts = (end + kRopeThreads - 1) / kRopeThreads;
-    // some tokens a block where that leaves two blocks for each of 152 SMs
-    constexpr int kTok = kHalfLayout ? 2 : 4;
-    const bool many = a.n_tok >= kTok * 304;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(many ? (a.n_tok + kTok - 1) / kTok : a.n_tok), (unsigned)(parts < 64 ? parts : 64));
     cfg.blockDim = dim3(kRopeThreads);
-    cfg.dynamicSmemBytes = (many ? kTok : 1) * (a.r.rot / 2) * sizeof(float2);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout, kTok>, a)
-                : cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout, 1>, a);
+    if constexpr (V > 1) {
+        constexpr int kStep = Item<Tin, Tout, V, kHalfLayout>::kStep;
+        const int64_t room = std::max(1, 4 * 152 / parts), each = (a.n_tok + room - 1) / room;  // four blocks for each of 152 SMs
+        const size_t smem = kRing * kStep * (Item<Tin, Tout, V, kHalfLayout>::kTwo ? 2 : 1) * kRopeThreads * 16 +
+                            2 * kStep * (a.r.rot / 2) * sizeof(float2);
+        if (each >= kStreamTokens && parts <= 64) {
+            cfg.gridDim = dim3((unsigned)((a.n_tok + each - 1) / each), (unsigned)parts);
+            cfg.dynamicSmemBytes = smem;
+            const auto kernel = k_rope_stream<Tin, Tout, V, kHalfLayout>;
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a, (int)each);
+        }
+    }
+    cfg.gridDim = dim3((unsigned)a.n_tok, (unsigned)(parts < 64 ? parts : 64));
+    cfg.dynamicSmemBytes = (a.r.rot / 2) * sizeof(float2);
+    return cudaLaunchKernelEx(&cfg, k_rope<Tin, Tout, V, kHalfLayout>, a);
 }
 
 // Whether all rows, heads and parts begin on V values (of 16 bytes of input).

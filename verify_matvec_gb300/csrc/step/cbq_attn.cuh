@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "cbq_device.cuh"
+#include "step/cbq_copy.cuh"
 #include "step/cbq_step.h"
 #include "step/cbq_types.cuh"
 
@@ -40,14 +41,6 @@ __device__ __forceinline__ uint64_t seen_drafts(const TreeAttention &a, const Se
     const int k = q.len - q.ctx;
     return (uint64_t)a.mask[row] & (k >= 64 ? ~0ull : (1ull << k) - 1);
 }
-
-// 16 bytes to shared memory, or 16 zero bytes where put is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool put) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(put ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
