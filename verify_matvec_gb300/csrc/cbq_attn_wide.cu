@@ -546,36 +546,79 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const float sum = l * f0 + other.y * f1;
             const float inv = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t part = (int64_t)c * a.total_tok * a.q_heads + row;
+            const int64_t to_row = (alone ? row : part) * D;
+            if (split) {
 #pragma unroll
-            for (int d = 0; d < D; d += 32) {
-                uint32_t o[32];
-                tm_ld(lanes + Cols<D>::o(g) + d, o);
-                tm_wait_ld();
-                if (live && ok) {
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    tm_ld(lanes + Cols<D>::o(g) + d, o);
+                    tm_wait_ld();
+                    if (live && ok) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        float v[8];
+                        for (int j = 0; j < 32; j += 8) {
+                            float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)  // (what was never written may hold anything: it is not multiplied)
-                            v[e] = n == 0 ? 0.0f : __uint_as_float(o[j + e]) * f0;
-                        if (split && items > 1) {
-                            const float4 y0 = *reinterpret_cast<const float4 *>(pass + d + j), y1 = *reinterpret_cast<const float4 *>(pass + d + j + 4);
-                            v[0] += y0.x * f1, v[1] += y0.y * f1, v[2] += y0.z * f1, v[3] += y0.w * f1;
-                            v[4] += y1.x * f1, v[5] += y1.y * f1, v[6] += y1.z * f1, v[7] += y1.w * f1;
-                        }
+                            for (int e = 0; e < 8; ++e)  // (what was never written may hold anything: it is not multiplied)
+                                v[e] = n == 0 ? 0.0f : __uint_as_float(o[j + e]) * f0;
+                            if (items > 1) {
+                                const float4 y0 = *reinterpret_cast<const float4 *>(pass + d + j), y1 = *reinterpret_cast<const float4 *>(pass + d + j + 4);
+                                v[0] += y0.x * f1, v[1] += y0.y * f1, v[2] += y0.z * f1, v[3] += y0.w * f1;
+                                v[4] += y1.x * f1, v[5] += y1.y * f1, v[6] += y1.z * f1, v[7] += y1.w * f1;
+                            }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= inv;
-                        if (alone && !a.out_f32) {
-                            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + d + j) =
-                                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-                        } else {
-                            float4 *to = reinterpret_cast<float4 *>(alone ? static_cast<float *>(a.out) + row * D + d + j : part_o + part * D + d + j);
-                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            for (int e = 0; e < 8; ++e) v[e] *= inv;
+                            if (alone && !a.out_f32) {
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + d + j) =
+                                    make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+                            } else {
+                                float4 *to = reinterpret_cast<float4 *>(alone ? static_cast<float *>(a.out) + row * D + d + j : part_o + part * D + d + j);
+                                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            }
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
+            } else {
+                // 32 rows x 32 values at a time, turned in shared memory (q's place, 16-byte pieces permuted by the row) so
+                // that eight lanes write 128 bytes of a row: 12 sequences of 256 rows x 8,000 keys 116 us, each row by its
+                // own thread 123.  (Above, where four warps write and add the other group's part, that was slower.)
+                uint8_t *turn = smem + warp * 4096;
+                static_assert(8 * 4096 <= 2 * kQBytes, "which has the room");
+                const uint32_t lives = __ballot_sync(~0u, live && ok);
+                const float f = n == 0 ? 0.0f : f0 * inv;
+                int64_t at[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(~0u, to_row, i * 4 + lane / 8) + lane % 8 * 4;
+#pragma unroll
+                for (int d = 0; lives && d < D; d += 32) {
+                    uint32_t o[32];
+                    tm_ld(lanes + Cols<D>::o(g) + d, o);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (n > 0)
+                            v = make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f, __uint_as_float(o[j + 2]) * f,
+                                            __uint_as_float(o[j + 3]) * f);
+                        *reinterpret_cast<float4 *>(turn + lane * 128 + ((j / 4 ^ lane) & 7) * 16) = v;
+                    }
+                    __syncwarp();
+                    float4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = *reinterpret_cast<const float4 *>(turn + (i * 4 + lane / 8) * 128 + ((lane ^ (i * 4 + lane / 8)) & 7) * 16);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!(lives >> (i * 4 + lane / 8) & 1)) continue;
+                        if (alone && !a.out_f32)
+                            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + at[i] + d) =
+                                make_uint2(pack2<T>(v[i].x, v[i].y), pack2<T>(v[i].z, v[i].w));
+                        else
+                            *reinterpret_cast<float4 *>((alone ? static_cast<float *>(a.out) : part_o) + at[i] + d) = v[i];
+                    }
+                    __syncwarp();
+                }
             }
             if (live && ok) {
                 if (!alone) part_ml[part] = make_float2(top, sum);
