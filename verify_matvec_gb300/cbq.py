@@ -623,12 +623,14 @@ def cbq_rope(x, pos, turns, rot_off: int = 0, layout: str = "half", mscale: floa
     turns fp64 (cbq_rope_turns).  out may be x."""
     torch = _torch()
     n, heads, dim = x.shape
+    xp, xt, xh = _heads(x, "x")
     if out is None:
         out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have the shape and dtype of x")
-    xp, xt, xh = _heads(x, "x")
-    op, ot, oh = _heads(out, "out")
+        op, ot, oh = out.data_ptr(), heads * dim, dim
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have the shape and dtype of x")
+        op, ot, oh = _heads(out, "out")
     _check(load().cbq_rope(xp, _dtype(x, "x"), n, heads, dim, xt, xh, _vec(pos, torch.int32, n, "pos"),
                            _vec(turns, torch.float64, -1, "turns"), 2 * turns.numel(), rot_off, _layout(layout),
                            mscale, op, ot, oh, _raw_stream(stream, x)), "cbq_rope")
@@ -654,10 +656,13 @@ def cbq_rope_append(q, k, v, pos, slots, turns, kc, vc, rot_off: int = 0, layout
         raise ValueError("q, k and v must have one dtype, and k and v one set of strides")
     if out is None:
         out = torch.empty(shape, dtype=kc.dtype, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _vec(out, kc.dtype, n * heads * dim, "out")
     _check(load().cbq_rope_append(qp, kp, vp, _dtype(q, "q"), n, heads, qt, qh, kt, kh,
                                   _vec(pos, torch.int32, n, "pos"), _vec(slots, torch.int64, n, "slots"),
                                   _vec(turns, torch.float64, -1, "turns"), 2 * turns.numel(), rot_off,
-                                  _layout(layout), mscale, c, _vec(out, kc.dtype, n * heads * dim, "out"),
+                                  _layout(layout), mscale, c, op,
                                   _opt_vec(err, torch.int32, 1, "err"), _raw_stream(stream, q)), "cbq_rope_append")
     return out
 
@@ -696,20 +701,24 @@ def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len
     n_seq, width = table.shape
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=dev)
-    elif out.shape != shape:
-        raise ValueError("out must have the shape of q")
+        op, od = out.data_ptr(), c.dtype
+    else:
+        if out.shape != shape:
+            raise ValueError("out must have the shape of q")
+        op, od = _vec(out, out.dtype, n * heads * dim, "out"), _dtype(out, "out")
     lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if with_lse else None
     if workspace is None:
-        need = cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim)
-        workspace = _least_workspace(dev) if need <= 16 else torch.empty(need, dtype=torch.uint8, device=dev)
+        room = cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim)
+        workspace = _least_workspace(dev) if room <= 16 else torch.empty(room, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, room = _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel()
     qp, qt, qh = _heads(q, "q")
     _check(load().cbq_tree_attention(qp, qt, qh, heads, n, c, _vec(table, i32, -1, "table"), width, n_seq,
                                      _vec(ctx, i32, n_seq, "ctx"), _vec(start, i32, n_seq + 1, "start"),
                                      _vec(mask, torch.int64, n, "mask"), max_tok, max_len,
                                      dim ** -0.5 if scale is None else scale,
-                                     _vec(out, out.dtype, n * heads * dim, "out"), _dtype(out, "out"),
-                                     None if lse is None else lse.data_ptr(),
-                                     _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel(),
+                                     op, od, None if lse is None else lse.data_ptr(), wp, room,
                                      _opt_vec(err, i32, 1, "err"), _raw_stream(stream, q)), "cbq_tree_attention")
     return (out, lse) if with_lse else out
 
@@ -728,11 +737,17 @@ def cbq_sample(logits, temperature, top_k, top_p, min_p, u, ids=None, probs=None
     f, i32 = torch.float32, torch.int32
     if ids is None:
         ids = torch.empty(n, dtype=i32, device=logits.device)
+        ip = ids.data_ptr()
+    else:
+        ip = _vec(ids, i32, n, "ids")
     if probs is None:
         probs = torch.empty(n, dtype=f, device=logits.device)
+        pp = probs.data_ptr()
+    else:
+        pp = _vec(probs, f, n, "probs")
     _check(load().cbq_sample(logits.data_ptr(), _dtype(logits, "logits"), n, V, st[0],
                              _opt_vec(temperature, f, n, "temperature"), _opt_vec(top_k, i32, n, "top_k"),
                              _opt_vec(top_p, f, n, "top_p"), _opt_vec(min_p, f, n, "min_p"), _vec(u, f, n, "u"),
-                             _vec(ids, i32, n, "ids"), _vec(probs, f, n, "probs"), _raw_stream(stream, logits)),
+                             ip, pp, _raw_stream(stream, logits)),
            "cbq_sample")
     return ids, probs
