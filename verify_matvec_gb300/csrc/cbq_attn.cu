@@ -13,8 +13,8 @@
 //
 // Bound by memory where the contexts are long: two sequences of 131,000 keys
 // (1.07 GB, 16 rows a kv head) take 181 us, 5.9 TB/s.  8,191 keys of one
-// sequence (34 MB, 20 rows) take 17 us: a block's 256 keys, the two launches and
-// the join follow one another; 300 keys 6.4 us, latency throughout.  The
+// sequence (34 MB, 20 rows) take 14.6 us: a block's 256 keys, the two launches
+// and the join follow one another; 300 keys 6.4 us, latency throughout.  The
 // products run on mma.sync: a tile of K or V serves 64 rows at most here, and
 // the copies are the bound, not the products.
 #include <algorithm>
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     __shared__ uint32_t valid[S::kStages][4];
     __shared__ uint64_t drafts[S::kRows];
     __shared__ float2 ml[S::kParts][S::kRows], joined[S::kRows];
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;
@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
 // The chunks of a row (token, head) joined by W warps: with many chunks and few
 // rows the eight warps of a block share out those of one row (one warp going
 // through 32 chunks took 18 us of a 33 us call), otherwise each takes a row of
-// its own.  The
+// its own.  Eight parts' loads are under way together, each warp keeps its own
+// running maximum, and what the call was given is read while the parts' kernel
+// still runs (8,191 keys of one sequence 17.0 us before that, 14.6 with it).  The
 // wide kernel cuts the committed keys alone (and takes the drafts with the last
 // chunk).  grid (ceil(q_heads * W / 8), max_tok, n_seq).
 template <typename T, int D, int W>
@@ -509,47 +511,65 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, b
     struct alignas(kEach * 4 < 16 ? kEach * 4 : 16) Values {
         float v[kEach];
     };
-    __shared__ float tops[8], sums[8];
-    __shared__ Values vals[W > 1 ? W - 1 : 1][32];
+    __shared__ float tops[W], sums[W];
+    __shared__ Values vals[W][W > 1 ? 32 : 1];
     pdl_trigger();
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, w = warp % W, h = blockIdx.x * (8 / W) + warp / W, i = blockIdx.y;
+    // (the parts' kernel lets this one start when what the two are given is there: only the parts have to be waited for)
     const Seq sq = sequence(a, blockIdx.z, false);
+    pdl_wait();
     const int chunks = ((wide ? sq.ctx : sq.len) + chunk - 1) / chunk;
     if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;  // (all warps of a row alike)
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
-    float top = -INFINITY;
-    for (int c = w * 32 + lane; c < chunks; c += 32 * W) top = fmaxf(top, part_ml[c * step + row].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if constexpr (W > 1) {
-        if (lane == 0) tops[w] = top;
-        __syncthreads();
-#pragma unroll
-        for (int o = 0; o < W; ++o) top = fmaxf(top, tops[o]);
-    }
     Values v = {};
-    float sum = 0.0f;
-    if (top != -INFINITY) {
-#pragma unroll 8
-        for (int c = w; c < chunks; c += W) {
-            const float2 p = part_ml[c * step + row];
-            const Values y = reinterpret_cast<const Values *>(part_o + (c * step + row) * D)[lane];
-            const float f = pow2(p.x - top);
-            sum += p.y * f;
+    float top = -INFINITY, sum = 0.0f;
+    for (int c0 = w; c0 < chunks; c0 += 8 * W) {  // eight parts' loads at once
+        float2 p[8];
+        Values y[8];
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v.v[j] += f * y.v[j];
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * W;
+            p[j] = make_float2(-INFINITY, 0.0f);
+            y[j] = {};
+            if (c >= chunks) continue;
+            p[j] = part_ml[c * step + row];
+            y[j] = reinterpret_cast<const Values *>(part_o + (c * step + row) * D)[lane];
         }
+        float now = top;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) now = fmaxf(now, p[j].x);
+        if (now == -INFINITY) continue;
+        const float keep = pow2(top - now);
+        sum *= keep;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v.v[e] *= keep;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = pow2(p[j].x - now);
+            sum += p[j].y * f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v.v[e] += f * y[j].v[e];
+        }
+        top = now;
     }
     if constexpr (W > 1) {
-        if (lane == 0) sums[w] = sum;
-        if (w > 0) vals[w - 1][lane] = v;
+        if (lane == 0) tops[w] = top, sums[w] = sum;
+        vals[w][lane] = v;
         __syncthreads();
         if (w > 0) return;
-        for (int o = 1; o < W; ++o) {
-            sum += sums[o];
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) v.v[j] += vals[o - 1][lane].v[j];
+        for (int o = 1; o < W; ++o) top = fmaxf(top, tops[o]);
+        sum = 0.0f;
+        v = {};
+        if (top != -INFINITY) {
+#pragma unroll
+            for (int o = 0; o < W; ++o) {
+                const float f = pow2(tops[o] - top);
+                const Values y = vals[o][lane];
+                sum += f * sums[o];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) v.v[e] += f * y.v[e];
+            }
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -646,8 +666,8 @@ cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) 
                                                    p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles,
                                                    p.cluster, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1 || p.cluster) return e;
-    // (a warp for each of 1,024 rows of 19 chunks: 21.3 us a call, eight warps 20.4; of 2,048: 28.0 and 30.2; a ragged batch
-    // of 5,000 rows of up to 12: 62 and 65)
+    // (before its loads went together: a warp for each of 1,024 rows of 19 chunks 21.3 us a call, eight warps 20.4; of
+    // 2,048 rows 28.0 and 30.2; a ragged batch of 5,000 rows of up to 12 chunks 62 and 65)
     const unsigned heads = (unsigned)a.q_heads, toks = (unsigned)a.max_tok, seqs = (unsigned)a.n_seq;
     return p.n_chunks > 8 && rows < 2048 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
                           : launch_dependent(k_tree_join<T, D, 1>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, p.chunk, p.wide,

@@ -31,7 +31,7 @@
 // MB) take 253 us, 1,064 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
 // SM 1,020 clocks, of which the products take 594 (S 8 x 46, both operands from
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
-// MB) take 62 us: some 5 us a block beside its keys, and lengths that differ.
+// MB) take 60 us: some 5 us a block beside its keys, and lengths that differ.
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WideShared sh;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kWideRows, c = blockIdx.y, s = blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;

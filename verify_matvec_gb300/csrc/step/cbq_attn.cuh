@@ -21,9 +21,9 @@ struct Seq {
 
 __device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool report) {
     const int64_t room = (int64_t)a.table_width * a.c.page_size;
-    const int64_t b0 = a.start[s], b1 = a.start[s + 1];
+    const int64_t b0 = __ldcg(a.start + s), b1 = __ldcg(a.start + s + 1);  // (from L2: the join reads before it waits)
     const int64_t most = a.max_len < room ? a.max_len : room;
-    int64_t n = b1 - b0, ctx = a.ctx[s];
+    int64_t n = b1 - b0, ctx = __ldcg(a.ctx + s);
     bool cut = n > a.max_tok || ctx < 0;
     if (b0 < 0 || b1 > a.total_tok || n < 0) {
         n = 0;
