@@ -77,7 +77,6 @@ inline cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int cluster,
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, (P)args...) : e;
 }
 template <typename... P, typename... A>
