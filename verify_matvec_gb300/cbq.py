@@ -559,6 +559,24 @@ def _raw_stream(stream, t):
     return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _new(shape, dtype, device, stream, returned=True):
+    """A new tensor that kernels on `stream` (None: torch's current one) write.
+
+    Torch orders a block only with the stream it was taken for: one of the
+    current stream's may still be in use there when `stream` writes it, and one
+    that is dropped goes to the current stream's next allocation while `stream`
+    still works on it.  So it is taken for `stream`; what the caller gets is
+    marked as used on the current stream too, where the caller goes on with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _layout(layout):
     code = _LAYOUTS.get(layout)
     if code is None:
@@ -625,7 +643,7 @@ def cbq_rope(x, pos, turns, rot_off: int = 0, layout: str = "half", mscale: floa
     n, heads, dim = x.shape
     xp, xt, xh = _heads(x, "x")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+        out = _new((n, heads, dim), x.dtype, x.device, stream)
         op, ot, oh = out.data_ptr(), heads * dim, dim
     else:
         if out.shape != x.shape or out.dtype != x.dtype:
@@ -655,7 +673,7 @@ def cbq_rope_append(q, k, v, pos, slots, turns, kc, vc, rot_off: int = 0, layout
     if kt != vt or kh != vh or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype, and k and v one set of strides")
     if out is None:
-        out = torch.empty(shape, dtype=kc.dtype, device=q.device)
+        out = _new(shape, kc.dtype, q.device, stream)
         op = out.data_ptr()
     else:
         op = _vec(out, kc.dtype, n * heads * dim, "out")
@@ -700,16 +718,16 @@ def cbq_tree_attention(q, kc, vc, table, ctx, start, mask, max_tok: int, max_len
         raise ValueError("q must have the cache's dtype and dim")
     n_seq, width = table.shape
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        out = _new(shape, q.dtype, dev, stream)
         op, od = out.data_ptr(), c.dtype
     else:
         if out.shape != shape:
             raise ValueError("out must have the shape of q")
         op, od = _vec(out, out.dtype, n * heads * dim, "out"), _dtype(out, "out")
-    lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if with_lse else None
+    lse = _new((n, heads), torch.float32, dev, stream) if with_lse else None
     if workspace is None:
         room = cbq_tree_attention_workspace(n_seq, n, max_tok, max_len, heads, c.kv_heads, dim)
-        workspace = _least_workspace(dev) if room <= 16 else torch.empty(room, dtype=torch.uint8, device=dev)
+        workspace = _least_workspace(dev) if room <= 16 else _new((room,), torch.uint8, dev, stream, returned=False)
         wp = workspace.data_ptr()
     else:
         wp, room = _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel()
@@ -736,12 +754,12 @@ def cbq_sample(logits, temperature, top_k, top_p, min_p, u, ids=None, probs=None
         raise ValueError("logits must have a contiguous last axis")
     f, i32 = torch.float32, torch.int32
     if ids is None:
-        ids = torch.empty(n, dtype=i32, device=logits.device)
+        ids = _new((n,), i32, logits.device, stream)
         ip = ids.data_ptr()
     else:
         ip = _vec(ids, i32, n, "ids")
     if probs is None:
-        probs = torch.empty(n, dtype=f, device=logits.device)
+        probs = _new((n,), f, logits.device, stream)
         pp = probs.data_ptr()
     else:
         pp = _vec(probs, f, n, "probs")
