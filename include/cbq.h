@@ -478,7 +478,8 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
  *   out[i][h] = sum_p softmax_p(scale * q[i][h].k[p][g]) v[p][g],
  *   g = h / (q_heads / kv_heads);  lse[i][h] = ln sum_p exp(scale * q.k).
  * A row that sees nothing gives zeros and -inf.  What a row does not see,
- * NaN and infinities included, does not touch it.  q_dev: total_tok x q_heads
+ * NaN and infinities included, does not touch it; a NaN in its query or in a
+ * key that it sees makes out and lse NaN.  q_dev: total_tok x q_heads
  * x head_dim of the cache's dtype, with strides; out_dev: total_tok x q_heads
  * x head_dim, contiguous, out_dtype the cache's dtype or CBQ_F32; lse_dev:
  * total_tok x q_heads fp32 or NULL.  Scores, running maxima and sums are

@@ -159,7 +159,8 @@ struct Shape {
 // outside the sequence are not read and are zero in shared memory, and the
 // drafts' values, which some rows see and others do not, are looked over for
 // NaN and infinities first (they would make 0 * v NaN): such a value row is
-// zeroed and added by hand to the rows that see it.
+// zeroed and added by hand to the rows that see it.  A NaN that a row does see
+// makes its sum NaN, and so its results.
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(128, blocks_an_sm(D))
     k_tree_attention(TreeAttention a, int chunk, int row_tiles, bool cluster, float *part_o, float2 *part_ml) {
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     for (int half = 0; half < 2; ++half) {
         l[half] += __shfl_xor_sync(~0u, l[half], 1);
         l[half] += __shfl_xor_sync(~0u, l[half], 2);
+        if (l[half] != l[half]) m[half] = 0.0f;  // (no maximum keeps a NaN: what joins the parts must not take them for empty)
         if (lane % 4 == 0) ml[wk][ra + half * 8] = make_float2(m[half], l[half]);
     }
     __syncthreads();

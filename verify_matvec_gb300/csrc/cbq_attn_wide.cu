@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.weighed[g][n & 1]));
         }
+        if (l != l) m = 0.0f;  // (no maximum keeps a NaN: what joins the parts must not take them for empty)
         if (ok && n > 0) ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
         fence_after();
         // The value rows taken out above, to the rows that see them: the weight of draft j is still in its place.
