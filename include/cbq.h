@@ -414,9 +414,13 @@ typedef struct cbq_kv_cache {
  *             (high - low), 0, 1): pairs that make `high` turns or more over
  *             orig_len positions stay, those under `low` are divided;
  *   BY_INDEX  the same mix with g falling linearly in the index i, from 1 at
- *             floor(i(high)) to 0 at ceil(i(low)), where i(r) is the index
- *             whose pair makes r turns over orig_len (both ends clamped to
- *             the table).
+ *             max(floor(i(high)), 0) to 0 at min(ceil(i(low)), rot_dim - 1),
+ *             where i(r) = ln(orig_len / (2 pi r)) rot_dim / (2 ln base) is
+ *             the index whose pair makes r turns over orig_len (the end may
+ *             lie past the rot_dim/2 pairs: then none is divided whole).  The
+ *             method is YaRN's (Peng et al., 2023), with its beta_slow as
+ *             low, beta_fast as high, and 0.1 ln(factor) + 1 as cbq_rope's
+ *             mscale.
  * In fp64.  The unused parameters of a scaling are ignored.
  * Errors: EINVAL (null, rot_dim < 2, odd or > CBQ_ROPE_MAX_DIM, base <= 1 or
  * not finite, factor <= 0, orig_len <= 0, not 0 < low < high). */

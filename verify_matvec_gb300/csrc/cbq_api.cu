@@ -755,7 +755,7 @@ int cbq_rope_turns(int rot_dim, double base, int scaling, double factor, double 
     if (scaling == CBQ_ROPE_BY_INDEX) {
         const double step = std::log(base) / half;  // ln of the ratio of neighbouring frequencies
         first = std::max(std::floor(std::log(orig_len / (high * kTwoPi)) / step), 0.0);
-        last = std::min(std::ceil(std::log(orig_len / (low * kTwoPi)) / step), half - 1.0);
+        last = std::min(std::ceil(std::log(orig_len / (low * kTwoPi)) / step), rot_dim - 1.0);  // (may lie past the table)
     }
     for (int i = 0; i < half; ++i) {
         const double t = std::pow(base, -(double)i / half) / kTwoPi;
