@@ -15,6 +15,7 @@
 // out without bank conflicts 29, blocks that go through several tokens with the
 // next ones' pieces coming meanwhile 23.9.
 #include <algorithm>
+#include <mutex>
 
 #include "cbq_pipe.cuh"
 #include "step/cbq_copy.cuh"
@@ -245,6 +246,30 @@ __global__ void __launch_bounds__(kRopeThreads, 4) k_rope_stream(const __grid_co
     }
 }
 
+// Dynamic shared memory of k_rope_stream, of a token's `half` pairs.
+template <typename I>
+constexpr size_t stream_smem(int half) {
+    return (size_t)kRing * I::kStep * (I::kTwo ? 2 : 1) * kRopeThreads * 16 + 2 * I::kStep * half * sizeof(float2);
+}
+
+// Opts k_rope_stream in to the most that any rotation takes, once per device:
+// the limit is the kernel's, for the calls of all host threads.
+template <typename Tin, typename Tout, int V, bool kHalfLayout>
+cudaError_t raise_smem() {
+    static std::mutex mu;
+    static bool raised[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (raised[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(k_rope_stream<Tin, Tout, V, kHalfLayout>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)stream_smem<Item<Tin, Tout, V, kHalfLayout>>(CBQ_ROPE_MAX_DIM / 2));
+    raised[dev] = e == cudaSuccess;
+    return e;
+}
+
 template <typename Tin, typename Tout, int V, bool kHalfLayout>
 cudaError_t launch_pieces(RopeArgs a, cudaStream_t s) {
     const int piece = !kHalfLayout && V == 1 ? 2 : V, turning = a.r.rot / (piece * (kHalfLayout ? 2 : 1));
@@ -268,16 +293,12 @@ cudaError_t launch_pieces(RopeArgs a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if constexpr (V > 1) {
-        constexpr int kStep = Item<Tin, Tout, V, kHalfLayout>::kStep;
         const int64_t room = std::max(1, 4 * 152 / parts), each = (a.n_tok + room - 1) / room;  // four blocks for each of 152 SMs
-        const size_t smem = kRing * kStep * (Item<Tin, Tout, V, kHalfLayout>::kTwo ? 2 : 1) * kRopeThreads * 16 +
-                            2 * kStep * (a.r.rot / 2) * sizeof(float2);
         if (each >= kStreamTokens && parts <= 64) {
             cfg.gridDim = dim3((unsigned)((a.n_tok + each - 1) / each), (unsigned)parts);
-            cfg.dynamicSmemBytes = smem;
-            const auto kernel = k_rope_stream<Tin, Tout, V, kHalfLayout>;
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a, (int)each);
+            cfg.dynamicSmemBytes = stream_smem<Item<Tin, Tout, V, kHalfLayout>>(a.r.rot / 2);
+            const cudaError_t e = raise_smem<Tin, Tout, V, kHalfLayout>();
+            return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, k_rope_stream<Tin, Tout, V, kHalfLayout>, a, (int)each);
         }
     }
     cfg.gridDim = dim3((unsigned)a.n_tok, (unsigned)(parts < 64 ? parts : 64));
