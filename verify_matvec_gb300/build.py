@@ -1,12 +1,17 @@
 """Build libcbq.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-The translation units compiled in parallel, linked with the toolkit's shared
-CUDA runtime: a process that has it already (PyTorch brings the same) then runs
-one runtime's code and not two, which is worth 3 us a call from Python where
-tensor operations and the library's calls take turns (an allocation and a
-launch 9.4 us with a static runtime of the library's own, 6.1 with the shared
-one).  `python -m verify_matvec_gb300.build` or `build()`; the result sits
-next to this file and is what the binding loads.
+The translation units are compiled in parallel and linked twice, next to this
+file:
+  libcbq.so          with the CUDA runtime inside, for C programs: it needs
+                     the driver and nothing of the toolkit;
+  libcbq_binding.so  the same objects with the shared runtime, which the
+                     binding loads: PyTorch has brought it already, and one
+                     runtime's code and not two is worth 3 us a call where
+                     tensor operations and the library's calls take turns (an
+                     allocation and a launch 9.4 us with a runtime of the
+                     library's own, 6.1 so).
+`python -m verify_matvec_gb300.build` or `build()`, which returns the path of
+libcbq.so.
 """
 from __future__ import annotations
 
@@ -21,6 +26,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libcbq.so")
+OUT_BINDING = os.path.join(HERE, "libcbq_binding.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["cbq_kernels.cu", "cbq_mmq.cu", "cbq_hc.cu", "cbq_rope.cu", "cbq_attn.cu", "cbq_attn_wide.cu", "cbq_sample.cu", "cbq_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,12 +51,20 @@ def _compile(src: str) -> tuple[str, str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(OUT):
+    if not (os.path.exists(OUT) and os.path.exists(OUT_BINDING)):
         return True
-    t = os.path.getmtime(OUT)
+    t = min(os.path.getmtime(OUT), os.path.getmtime(OUT_BINDING))
     deps = [os.path.join(d, f) for d, _, files in os.walk(CSRC) for f in files]
     deps += [os.path.join(INCLUDE, "cbq.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _link(out: str, objs: list[str], *how: str):
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, *how], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -65,13 +79,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         f.write(log)
     if verbose:
         print(log)
-    tmp = OUT + f".tmp{os.getpid()}"
     libs = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "lib64")
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared", "-Xlinker", "-rpath," + libs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, OUT)
+    _link(OUT, objs, "-cudart", "static")
+    _link(OUT_BINDING, objs, "-cudart", "shared", "-Xlinker", "-rpath," + libs)
     return OUT
 
 

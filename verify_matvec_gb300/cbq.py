@@ -15,7 +15,7 @@ import re
 import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-LIB_PATH = os.path.join(HERE, "libcbq.so")
+LIB_PATH = os.path.join(HERE, "libcbq_binding.so")  # libcbq.so on the CUDA runtime that PyTorch has loaded
 HEADER = os.path.join(os.path.dirname(HERE), "include", "cbq.h")
 
 CBQ_OK, CBQ_EINVAL, CBQ_ECUDA, CBQ_ENOMEM, CBQ_EDEVICE = 0, -1, -2, -3, -4
@@ -119,7 +119,7 @@ def header_functions() -> list[str]:
 
 
 def load():
-    """Load libcbq.so; raises if it has not been built (no fallback exists)."""
+    """Load the library; raises if it has not been built (no fallback exists)."""
     global _lib
     if _lib is not None:
         return _lib
