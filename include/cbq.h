@@ -493,9 +493,11 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
  * sets CBQ_DEVERR_BAD_LENGTH; a page id outside the cache is not seen and
  * sets CBQ_DEVERR_BAD_SLOT.  The result does not depend on timing (no
  * atomics on it) but a row's last bits depend on the call's limits (n_seq,
- * max_tok, max_len and the heads), by which the work is split.  Every wait in
- * the kernels is bounded; one that runs out (1 s) sets
- * CBQ_DEVERR_PIPE_TIMEOUT and leaves its rows undefined.  ws_dev: 16-byte
+ * max_tok, max_len and the heads), by which the work is split.  The many-row
+ * kernel's roles wait for one another with a limit; a wait that runs out (1 s)
+ * sets CBQ_DEVERR_PIPE_TIMEOUT and leaves its block's rows undefined.  (The
+ * barriers of clusters and the allocation of tensor memory, which end as soon
+ * as the blocks beside them get on, have none.)  ws_dev: 16-byte
  * aligned, ws_bytes at least what cbq_tree_attention_workspace says, one call
  * at a time.
  * Errors: EINVAL (null; n_seq < 1 or > 65535; total_tok < 1 or > 2^24;
@@ -577,6 +579,16 @@ int cbq_moe_debug_stall(cbq_moe *L, int mode);
  * that bit, and leaves the handle usable: the next call is correct.
  * Errors: EINVAL (null handle, mode outside 0..1). */
 int cbq_debug_mmq_stall(cbq_weights *W, int mode);
+
+/* Give-up test mode of the calling thread's cbq_tree_attention calls (0 turns
+ * it off): with mode 1 the first block of the many-row kernel copies no tile,
+ * so its roles' bounded waits give up after 1 s (CBQ_DEVERR_PIPE_TIMEOUT in
+ * *err_dev), and it frees its tensor memory and ends.  Such a call returns
+ * after about a second, sets only that bit, leaves that block's rows (of the
+ * first sequence and kv head) undefined and the others as they would be; the
+ * next call is correct.  Calls that the other kernels take are not touched.
+ * Errors: EINVAL (mode outside 0..1). */
+int cbq_debug_tree_stall(int mode);
 
 /* Copy the intermediate of the last cbq_moe_matvec on this handle, for
  * slots p < nslots (at most CBQ_MAX_TOKENS * (CBQ_MAX_TOPK + 1)): routed

@@ -95,6 +95,7 @@ _SIGS = {
     "cbq_tree_attention_workspace": ([_I, _I64, _I, _I64, _I, _I, _I, ctypes.POINTER(_I64)], _I),
     "cbq_tree_attention": ([_P, _I64, _I64, _I, _I64, _KV, _P, _I, _I, _P, _P, _P, _I, _I64, _F, _P, _I, _P, _P, _I64,
                             _P, _P], _I),
+    "cbq_debug_tree_stall": ([_I], _I),
     "cbq_sample": ([_P, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "cbq_moe_debug_intermediate": ([_P, _I, _P, _P, _P, _P], _I),
 }
@@ -431,6 +432,12 @@ def cbq_debug_mmq_stall(W: Weights, mode: int):
     """Give-up test mode of the tensor-core path (0 off; 1 the first CTA
     copies nothing, so its waits run out)."""
     _check(load().cbq_debug_mmq_stall(W.handle, int(mode)), "cbq_debug_mmq_stall")
+
+
+def cbq_debug_tree_stall(mode: int):
+    """Give-up test mode of this thread's cbq_tree_attention calls (0 off; 1
+    the many-row kernel's first block copies nothing, so its waits run out)."""
+    _check(load().cbq_debug_tree_stall(int(mode)), "cbq_debug_tree_stall")
 
 
 def cbq_debug_block_dots(W: Weights, qx, s=None, stream=None):

@@ -830,6 +830,14 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
     return CBQ_OK;
 }
 
+static thread_local int t_tree_stall = 0;  // cbq_debug_tree_stall
+
+int cbq_debug_tree_stall(int mode) {
+    if (mode < 0 || mode > 1) return CBQ_EINVAL;
+    t_tree_stall = mode;
+    return CBQ_OK;
+}
+
 int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
                        const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
                        const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,
@@ -871,6 +879,7 @@ int cbq_tree_attention(const void *q_dev, int64_t q_tok_stride, int64_t q_head_s
     a.lse = lse_dev;
     a.ws = ws_dev;
     a.err = err_dev;
+    a.stall = t_tree_stall;
     CBQ_CUDA(cbq::launch_tree_attention(a, as_stream(stream)));
     return CBQ_OK;
 }

@@ -51,6 +51,7 @@ struct TreeAttention {
     float *lse;
     void *ws;
     unsigned *err;
+    int stall;  // give-up test mode: the many-row kernel's first block copies nothing
 };
 size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
                                 int head_dim);
