@@ -124,6 +124,8 @@ __device__ __forceinline__ float4 peer_load4(uint32_t a) {
     return v;
 }
 
+constexpr int kMaxCluster = 8;  // blocks that join one another's parts (plan())
+
 // Blocks of k_tree_attention that run on an SM together, for its shared memory.
 constexpr int blocks_an_sm(int head_dim) { return head_dim <= 64 ? 3 : head_dim <= 128 ? 2 : 1; }
 
@@ -478,16 +480,16 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     cluster_sync();
     for (int i = c * 128 + tid; i < rows * (D / 4); i += chunks * 128) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float2 m_of[16];
+        float2 m_of[kMaxCluster];
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int o = 0; o < 16; ++o) {
+        for (int o = 0; o < kMaxCluster; ++o) {
             m_of[o] = o < chunks ? peer_load2(peer(&joined[r], o)) : make_float2(-INFINITY, 0.0f);
             top = fmaxf(top, m_of[o].x);
         }
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int o = 0; o < 16; ++o) {
+        for (int o = 0; o < kMaxCluster; ++o) {
             if (o >= chunks) continue;
             const float4 y = peer_load4(peer(res + r * D + d, o));
             const float f = top == -INFINITY ? 0.0f : pow2(m_of[o].x - top);
@@ -591,7 +593,7 @@ struct Plan {
     int wr, row_tiles, chunk, n_chunks;
 };
 
-constexpr int kSms = 152, kMaxCluster = 8;
+constexpr int kSms = 152;
 
 // Many rows are the wide kernel's.  us by tiles of 64 rows / by the wide kernel, D = 128, 8 kv heads, one sequence: 40 rows
 // at 200 keys 10.4 / 11.5, at 1,000 12.2 / 12.4, at 8,000 19.4 / 16.8; 256 rows 15.0 / 18.7, 28.5 / 23.3, 54.5 / 29.3.
