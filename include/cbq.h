@@ -500,6 +500,10 @@ int cbq_tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int6
  * as the blocks beside them get on, have none.)  ws_dev: 16-byte
  * aligned, ws_bytes at least what cbq_tree_attention_workspace says, one call
  * at a time.
+ * Speed: heads of 64, 128 and 256 whose rows in the cache, and out_dev, begin
+ * on 16 bytes take the tensor cores with the keys shared out over the GPU.
+ * Every other size, stride or address is taken by a warp a row, one key after
+ * another: right, and slow (5 drafts over 8,191 keys 7 to 8 ms for 15 us).
  * Errors: EINVAL (null; n_seq < 1 or > 65535; total_tok < 1 or > 2^24;
  * max_tok outside 1..CBQ_TREE_MAX; max_len outside 1..CBQ_TREE_MAX_LEN;
  * kv_heads < 1, > 256 or no divisor of q_heads; q_heads > 1024; table_width

@@ -12,9 +12,9 @@
 // another's shared memory (one launch, no workspace: what short calls need).
 //
 // Bound by memory where the contexts are long: two sequences of 131,000 keys
-// (1.07 GB, 16 rows a kv head) take 181 us, 5.9 TB/s.  8,191 keys of one
-// sequence (34 MB, 20 rows) take 14.6 us: a block's 256 keys, the two launches
-// and the join follow one another; 300 keys 6.4 us, latency throughout.  The
+// (1.07 GB, 16 rows a kv head) take 169 to 179 us, 6.0 to 6.3 TB/s.  8,191 keys of one
+// sequence (34 MB, 20 rows) take 14.9 us: a block's 256 keys, the two launches
+// and the join follow one another; 300 keys 6.2 us, latency throughout.  The
 // products run on mma.sync: a tile of K or V serves 64 rows at most here, and
 // the copies are the bound, not the products.
 #include <algorithm>
@@ -27,7 +27,9 @@ namespace cbq {
 namespace {
 
 // Any head size and any strides: one warp per (token, head), the lanes hold
-// the head's values, a key at a time.  grid (q_heads, max_tok, n_seq).
+// the head's values, a key at a time.  Bound by that chain: each key's look-up,
+// row of k, five shuffles and row of v follow one another, some 0.9 us (5 drafts
+// over 8,191 keys 7.0 ms with heads of 96, 8.2 with 192).  grid (q_heads, max_tok, n_seq).
 template <typename T>
 __global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
     pdl_trigger();
@@ -593,7 +595,7 @@ struct Plan {
     int wr, row_tiles, chunk, n_chunks;
 };
 
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // of a GB300 (the size of a workspace is asked for without a device, too)
 
 // Many rows are the wide kernel's.  us by tiles of 64 rows / by the wide kernel, D = 128, 8 kv heads, one sequence: 40 rows
 // at 200 keys 10.4 / 11.5, at 1,000 12.2 / 12.4, at 8,000 19.4 / 16.8; 256 rows 15.0 / 18.7, 28.5 / 23.3, 54.5 / 29.3.

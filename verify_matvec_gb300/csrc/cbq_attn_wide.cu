@@ -28,10 +28,11 @@
 // copies were the bound: 2,100 clocks a tile for 1,700.)
 //
 // 8 sequences of 64 drafts x 8 heads a kv head over 16,000 keys (270 GFLOP, 543
-// MB) take 253 us, 1,064 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
+// MB) take 254 us, 1,060 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
 // SM 1,020 clocks, of which the products take 594 (S 8 x 46, both operands from
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
-// MB) take 60 us: some 5 us a block beside its keys, and lengths that differ.
+// MB) take 60 us: some 5 us a block beside its keys, an uneven last wave, and
+// 1,120 of 1,440 blocks without keys that take their turn on an SM all the same.
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 

@@ -5,7 +5,10 @@
 //   (a, b) -> mscale * (a cos r - b sin r, a sin r + b cos r).
 // pos * turns_i is taken in fp64 and reduced to its part of a turn there (a
 // position of 10^6 has turned 1.6 * 10^5 times in pair 0: fp32 would keep
-// three digits of the part), then sine and cosine are fp32 (sincospif).
+// three digits of the part), then the part, its sine and its cosine are fp32
+// (sincospif): the part's rounding is off by an angle of at most 2^-23, which is
+// what the sine and the products round by, too (against 64 bits 4.2e-8 of the
+// values' size for fp32 tensors, 3.0e-8 with angles in fp64).
 //
 // Bound by memory: each value is read once and written once.  8,192 tokens x 32
 // heads x 128 bf16 (134 MB) take 23.9 us, 5.6 TB/s; 4,095 tokens x 48 heads into

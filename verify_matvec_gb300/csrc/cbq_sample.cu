@@ -18,8 +18,12 @@
 // or top-p alone: some 40 instructions a logit, packed ones for two at a time
 // among them, 10 of a row's 16 us in a block with 32 logits a thread) and otherwise by its phases' latency: a cluster's
 // wait for all its blocks takes 0.5 to 0.9 us, a histogram of a row with its
-// sums 3.  129,280 fp32 logits: five rows with all cuts 14.3 us (the general
-// way, without one block that settles few: 20.9), 256 rows of all kinds 121.
+// sums 3.  Many rows: a block of 1,024 threads fills an SM, so a row's load waits
+// for the phases of the one before it (issue slots 61% busy while an SM has a
+// block, 38% over the launch).  129,280 fp32 logits: a row with top-p alone 11 us
+// where that keeps few, 19 with thousands, 29 with half of the row; five rows
+// with all cuts 14.4 us (the general way, without one block that settles few:
+// 20.9), 256 rows of all kinds 121.
 #include <cfloat>
 
 #include "cbq_device.cuh"
