@@ -2,7 +2,7 @@
 
 Argument marshalling only: torch tensors give device pointers and the current
 stream, numpy arrays give host pointers.  Every step of the path runs in the
-library's CUDA kernels; if libcbq.so is missing this module raises instead of
+library's CUDA kernels; if the library is missing this module raises instead of
 computing anything another way.
 """
 from __future__ import annotations
