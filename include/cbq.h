@@ -541,6 +541,137 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
                const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
                int32_t *ids_dev, float *probs_dev, void *stream);
 
+/* ---- behind the logits, and the cache -----------------------------------
+ *
+ * The end of a verify step: the distributions of the target and the drafter,
+ * the verification of the drafted trees against them, and what becomes of the
+ * cache: the accepted drafts move to the end of their context, pages that are
+ * full and old are kept in 8 bits, and the tree attention reads both kinds.
+ * No handles, as in the section before. */
+
+/* The distribution that cbq_sample draws from: out[c][i] = w_i / kept mass
+ * where i is kept by the row's temperature, top-k, top-p and min-p, else 0
+ * (the weights, the order and the cuts are cbq_sample's; a weight under 2^-46
+ * has no mass).  T <= 0 or NaN gives 1 to the first of the order; a row of
+ * nothing but -inf and NaN gives zeros.  out_dev: n x V fp32, row c at out_dev
+ * + c*out_stride, not overlapping the logits; each value is within 2^-23
+ * (relative) of its quotient, and that within 2^-38 of the formula's, both
+ * plus 2^-46 absolute.  u_dev and
+ * ids_dev, both or neither: one token a row is drawn too, the same that
+ * cbq_sample draws.  One launch.  Errors as cbq_sample, and EINVAL (out_dev
+ * null, out_stride < V with n > 1 or < 0, one of u_dev and ids_dev alone, an
+ * out_dev that overlaps the logits). */
+int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
+              const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+              float *out_dev, int64_t out_stride, int32_t *ids_dev, void *stream);
+
+/* Verification of each sequence's tree of drafted tokens by given random
+ * numbers, such that what comes out is distributed as the target's own tokens.
+ * Sequence s has n_s = start_dev[s+1] - start_dev[s] nodes, packed rows
+ * start_dev[s].. of the arrays.  Node 0 is the sequence's last token, which is
+ * settled already; node i > 0 is a drafted token tokens_dev[row], whose parent
+ * is the sequence's node parent_dev[row] < i.  Row r of probs_dev (V fp32 that
+ * sum to 1) is the target's distribution p of the token behind node r, and row
+ * r of draft_dev the distribution q from which the children of node r were
+ * drawn, each by itself.  The walk starts at node 0; at each node
+ *   c = 0, S = 1;  for its children i, tokens x, in the order of the indices:
+ *     u[i] * q(x) * S < p(x) - c * q(x):  i is accepted, the walk goes on there;
+ *     otherwise  c = c + S,  S = sum_x max(p(x) - c * q(x), 0);
+ *   where no child is accepted the walk ends with the token
+ *     next = the first x with  sum_{y <= x} r(y) > u_next[s] * sum_y r(y),
+ *     r(x) = max(p(x) - c * q(x), 0).
+ * (Rejection by several rounds: each child is a draw from q that is tried
+ * against what the ones before left over.)  draft_dev NULL: the children were
+ * chosen, not drawn, and q is 1 at the child's token: it is accepted if u[i] *
+ * S < r(x), otherwise x is taken out of r and S = S - r(x).  A token outside
+ * [0, V) is never accepted.  If nothing is left of r (the draft equals the
+ * target, and rounding refused it) the token is drawn from p; from a row of
+ * zeros next is -1.  NaN counts as 0.  c and S are fp64; the products and
+ * differences are carried as two fp32 numbers (within 2^-46 of their terms)
+ * and summed so, in an order that does not depend on timing.
+ * path_dev: n_seq x max_tok int32, the accepted nodes from node 0 on,
+ * ascending, then -1; count_dev[s]: how many; next_dev[s]: the token.  A
+ * sequence of no nodes gives 0 and -1.  One longer than max_tok is cut to it,
+ * one whose rows leave [0, total_tok) counts as empty, and both set
+ * CBQ_DEVERR_BAD_LENGTH; a node whose parent is not before it is never
+ * reached.  u_dev[row] (total_tok; node 0's is not used) and u_next_dev
+ * (n_seq) in [0, 1).  One launch; nothing but the rows of the nodes that the
+ * walk passes is read.
+ * Errors: EINVAL (null; V < 1 or > CBQ_SAMPLE_MAX_V; probs_stride or
+ * draft_stride < V with total_tok > 1, or < 0; total_tok < 1 or > 2^24; n_seq
+ * < 1 or > 65535; max_tok outside 1..CBQ_TREE_MAX; a pointer not aligned to
+ * its type), ECUDA, EDEVICE. */
+int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_dev, int64_t draft_stride, int V,
+               const int32_t *tokens_dev, const int32_t *parent_dev, int64_t total_tok, const int32_t *start_dev,
+               int n_seq, int max_tok, const float *u_dev, const float *u_next_dev, int32_t *path_dev,
+               int32_t *count_dev, int32_t *next_dev, unsigned int *err_dev, void *stream);
+
+/* The accepted drafts moved to the end of their context, in all layers' caches
+ * with one launch: for i < count_dev[s], the key and value at place ctx_dev[s]
+ * + path_dev[s*max_tok + i] go to place ctx_dev[s] + i (path and count as
+ * cbq_verify gives them), and ctx_out_dev[s] = ctx_dev[s] + count_dev[s].
+ * `cache` describes the first of `layers` caches of the same shape, the next
+ * one layer_stride elements on.  Places go through table_dev as in
+ * cbq_tree_attention.  A path that is not ascending, or leaves 0..max_tok-1,
+ * or places beyond the table or CBQ_TREE_MAX_LEN, end the sequence's moves there and set
+ * CBQ_DEVERR_BAD_LENGTH, as does a count outside 0..max_tok (which counts as
+ * the nearer end) or a negative ctx (nothing is moved); a page outside the
+ * cache is not read or written and sets CBQ_DEVERR_BAD_SLOT.  ctx_out_dev is
+ * written for every sequence: what counts there is how many entries of the
+ * path were good.  Pages that two of the call's sequences name must not lie
+ * behind their contexts.  ctx_out_dev may be NULL, and must not be ctx_dev.
+ * Errors: EINVAL (null; a bad cache; layers < 1 or > 65535; layer_stride < 0;
+ * table_width < 1; n_seq < 1 or > 65535; max_tok outside 1..CBQ_TREE_MAX;
+ * ctx_out_dev == ctx_dev; a pointer not aligned to its type), ECUDA, EDEVICE. */
+int cbq_kv_commit(const cbq_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table_dev,
+                  int table_width, int n_seq, const int32_t *ctx_dev, const int32_t *path_dev, int max_tok,
+                  const int32_t *count_dev, int32_t *ctx_out_dev, unsigned int *err_dev, void *stream);
+
+/* A paged cache in 8 bits: k and v hold e4m3 numbers (four exponent bits, three
+ * of the mantissa, no infinities, largest 448), value d of token t of page p of
+ * kv head h at p*page_stride + t*tok_stride + h*head_stride + d, and stand for
+ * that number times the fp32 scale at k_scale (v_scale) + p*scale_page_stride +
+ * (t / block)*scale_block_stride + h*scale_head_stride.  block <= 65536
+ * divides page_size; the other limits are those of cbq_kv_cache. */
+typedef struct cbq_kv_cache8 {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int kv_heads;
+    int head_dim;
+    int page_size;
+    int block;
+    int64_t n_pages;
+    int64_t page_stride;
+    int64_t tok_stride;
+    int64_t head_stride;
+    int64_t scale_page_stride;
+    int64_t scale_block_stride;
+    int64_t scale_head_stride;
+} cbq_kv_cache8;
+
+/* Pages of a 16-bit cache written into an 8-bit one: page src_dev[i] of `from`
+ * becomes page dst_dev[i] of `to`, i < n, in each of `layers` pairs of caches
+ * (the struct's, and those that the layer strides, in elements, lead to).  For
+ * each block of tokens and head, of k and of v:
+ *   scale = 2^e, the least with max |x| <= 448 * 2^e, -80 <= e <= 120 (1 where
+ *           all are zero), the maximum over the finite values;
+ *   number = x / scale, rounded to nearest even (nothing exceeds 448: that
+ *           would take a maximum above 448 * 2^120).
+ * A scale that is a power of two costs a floating-point number no precision,
+ * so the bytes do not depend on how the division rounds.  NaN and infinities
+ * become NaN.  A negative entry of src_dev or dst_dev skips its pair; one
+ * beyond the cache does too and sets CBQ_DEVERR_BAD_SLOT.  Two pairs with one
+ * dst page race.  One launch.
+ * Errors: EINVAL (null; a bad cache; heads, head_dim or page_size that differ;
+ * layers < 1 or > 65535; negative layer strides; n < 1 or > 2^24; n * kv_heads *
+ * page_size / block > 2^31 - 1; a pointer not aligned to its type), ECUDA,
+ * EDEVICE. */
+int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const int32_t *src_dev,
+                    const cbq_kv_cache8 *to, int64_t to_layer_stride, int64_t scale_layer_stride,
+                    const int32_t *dst_dev, int layers, int64_t n, unsigned int *err_dev, void *stream);
+
 /* ---- checking entry points (used by the parity tests) ---------------- */
 
 /* Per-block int32 dots s_dev[c][r][b] (n x M x K/32) of W with plain int8

@@ -28,7 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libcbq.so")
 OUT_BINDING = os.path.join(HERE, "libcbq_binding.so")
 OBJDIR = os.path.join(HERE, "_build")
-SOURCES = ["cbq_kernels.cu", "cbq_mmq.cu", "cbq_hc.cu", "cbq_rope.cu", "cbq_attn.cu", "cbq_attn_wide.cu", "cbq_sample.cu", "cbq_api.cu"]
+SOURCES = ["cbq_kernels.cu", "cbq_mmq.cu", "cbq_hc.cu", "cbq_rope.cu", "cbq_attn.cu", "cbq_attn_wide.cu", "cbq_sample.cu",
+           "cbq_verify.cu", "cbq_kv.cu", "cbq_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-Xptxas", "-v", "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -56,7 +56,16 @@ class cbq_kv_cache(ctypes.Structure):
                 ("n_pages", _I64), ("page_stride", _I64), ("tok_stride", _I64), ("head_stride", _I64)]
 
 
+class cbq_kv_cache8(ctypes.Structure):
+    """The C struct of the same name: a paged cache of keys and values in 8 bits."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("kv_heads", _I), ("head_dim", _I),
+                ("page_size", _I), ("block", _I), ("n_pages", _I64), ("page_stride", _I64), ("tok_stride", _I64),
+                ("head_stride", _I64), ("scale_page_stride", _I64), ("scale_block_stride", _I64),
+                ("scale_head_stride", _I64)]
+
+
 _KV = ctypes.POINTER(cbq_kv_cache)
+_KV8 = ctypes.POINTER(cbq_kv_cache8)
 _SIGS = {
     "cbq_status_string": ([_I], ctypes.c_char_p),
     "cbq_last_cuda_error": ([], ctypes.c_char_p),
@@ -97,6 +106,10 @@ _SIGS = {
                             _P, _P], _I),
     "cbq_debug_tree_stall": ([_I], _I),
     "cbq_sample": ([_P, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "cbq_probs": ([_P, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P], _I),
+    "cbq_verify": ([_P, _I64, _P, _I64, _I, _P, _P, _I64, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "cbq_kv_commit": ([_KV, _I, _I64, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P], _I),
+    "cbq_kv_quantize": ([_KV, _I64, _P, _KV8, _I64, _I64, _P, _I, _I64, _P, _P], _I),
     "cbq_moe_debug_intermediate": ([_P, _I, _P, _P, _P, _P], _I),
 }
 
@@ -776,3 +789,153 @@ def cbq_sample(logits, temperature, top_k, top_p, min_p, u, ids=None, probs=None
                              ip, pp, _raw_stream(stream, logits)),
            "cbq_sample")
     return ids, probs
+
+
+# --------------------------------------- behind the logits, and the cache --
+
+def cbq_probs(logits, temperature, top_k, top_p, min_p, u=None, out=None, ids=None, stream=None):
+    """The distribution (rows, V) fp32 that cbq_sample draws from: logits
+    (rows, V); temperature, top_p, min_p (rows) fp32 and top_k (rows) int32,
+    each may be None.  With u (rows) fp32 it returns (out, ids), ids (rows) int32
+    one token drawn from each row."""
+    torch = _torch()
+    n, V = logits.shape
+    st = logits.stride()
+    if not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if st[1] != 1 and V != 1:
+        raise ValueError("logits must have a contiguous last axis")
+    f, i32 = torch.float32, torch.int32
+    if out is None:
+        out = _new((n, V), f, logits.device, stream)
+        so = (V, 1)
+    else:
+        so = out.stride()
+        if out.shape != (n, V) or out.dtype != f or not out.is_cuda or (so[1] != 1 and V != 1):
+            raise ValueError("out must be a float32 CUDA tensor of the logits' shape with a contiguous last axis")
+    if u is None:
+        if ids is not None:
+            raise ValueError("ids are drawn by the numbers u")
+        ip = None
+    elif ids is None:
+        ids = _new((n,), i32, logits.device, stream)
+        ip = ids.data_ptr()
+    else:
+        ip = _vec(ids, i32, n, "ids")
+    _check(load().cbq_probs(logits.data_ptr(), _dtype(logits, "logits"), n, V, st[0],
+                            _opt_vec(temperature, f, n, "temperature"), _opt_vec(top_k, i32, n, "top_k"),
+                            _opt_vec(top_p, f, n, "top_p"), _opt_vec(min_p, f, n, "min_p"), _opt_vec(u, f, n, "u"),
+                            out.data_ptr(), so[0], ip, _raw_stream(stream, logits)), "cbq_probs")
+    return out if u is None else (out, ids)
+
+
+def _rows(t, name):
+    """(pointer, row stride) of an fp32 CUDA tensor (rows, V) with a contiguous last axis."""
+    st = t.stride()
+    if not t.is_cuda or t.dtype is not _torch().float32:
+        raise TypeError(f"{name} must be a CUDA tensor of torch.float32")
+    if len(st) != 2 or (st[1] != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be (rows, V) with a contiguous last axis")
+    return t.data_ptr(), st[0]
+
+
+def cbq_verify(probs, draft, tokens, parent, start, u, u_next, max_tok: int, path=None, count=None, next=None,
+               err=None, stream=None):
+    """Verification of each sequence's drafted tree: probs (nodes, V) fp32 the
+    target's distribution behind each node, draft (nodes, V) fp32 the one that
+    the node's children were drawn from (None: they were chosen), tokens and
+    parent (nodes) int32, start (sequences + 1) int32 first nodes, u (nodes) and
+    u_next (sequences) fp32 in [0, 1).  Returns path (sequences, max_tok) int32
+    (the accepted nodes, then -1), count and next (sequences) int32."""
+    torch = _torch()
+    f, i32, dev = torch.float32, torch.int32, probs.device
+    pp, ps = _rows(probs, "probs")
+    total, V = probs.shape
+    qp, qs = (None, 0) if draft is None else _rows(draft, "draft")
+    if draft is not None and draft.shape != probs.shape:
+        raise ValueError("draft must have the shape of probs")
+    n = start.numel() - 1
+    if path is None:
+        path = _new((n, max_tok), i32, dev, stream)
+    elif path.shape != (n, max_tok):
+        raise ValueError("path must be (sequences, max_tok)")
+    count = _new((n,), i32, dev, stream) if count is None else count
+    next = _new((n,), i32, dev, stream) if next is None else next
+    _check(load().cbq_verify(pp, ps, qp, qs, V, _vec(tokens, i32, total, "tokens"), _vec(parent, i32, total, "parent"),
+                             total, _vec(start, i32, n + 1, "start"), n, max_tok, _vec(u, f, total, "u"),
+                             _vec(u_next, f, n, "u_next"), _vec(path, i32, -1, "path"), _vec(count, i32, n, "count"),
+                             _vec(next, i32, n, "next"), _opt_vec(err, i32, 1, "err"), _raw_stream(stream, probs)),
+           "cbq_verify")
+    return path, count, next
+
+
+def _layers(kc, vc):
+    """(cbq_kv_cache, layers, layer stride) of two CUDA tensors (pages,
+    page_size, kv_heads, dim), or (layers, pages, page_size, kv_heads, dim)."""
+    if kc.dim() != 5:
+        return _cache(kc, vc), 1, 0
+    if kc.shape != vc.shape or kc.stride() != vc.stride():
+        raise ValueError("kc and vc must be of one shape and strides")
+    return _cache(kc[0], vc[0]), kc.shape[0], kc.stride(0)
+
+
+def cbq_kv_commit(kc, vc, table, ctx, path, count, out=None, err=None, stream=None):
+    """The accepted drafts of each sequence moved to the end of its context in
+    the paged cache kc, vc (pages, page_size, kv_heads, dim), or that of all
+    layers (layers, pages, ...): table (sequences, width) int32 page ids, ctx
+    (sequences) int32, path (sequences, max_tok) and count (sequences) int32 as
+    cbq_verify gives them.  Returns the new lengths (sequences) int32."""
+    i32 = _torch().int32
+    c, layers, stride = _layers(kc, vc)
+    n, width = table.shape
+    if path.dim() != 2 or path.shape[0] != n:
+        raise ValueError("path must be (sequences, max_tok)")
+    out = _new((n,), i32, kc.device, stream) if out is None else out
+    _check(load().cbq_kv_commit(c, layers, stride, _vec(table, i32, -1, "table"), width, n, _vec(ctx, i32, n, "ctx"),
+                                _vec(path, i32, -1, "path"), path.shape[1], _vec(count, i32, n, "count"),
+                                _vec(out, i32, n, "out"), _opt_vec(err, i32, 1, "err"), _raw_stream(stream, kc)),
+           "cbq_kv_commit")
+    return out
+
+
+def _cache8(k8, v8, ks, vs):
+    """(cbq_kv_cache8, layers, layer stride, scale layer stride) of CUDA tensors:
+    k8, v8 float8_e4m3fn ([layers,] pages, page_size, kv_heads, dim); ks, vs fp32
+    ([layers,] pages, page_size / block, kv_heads)."""
+    torch = _torch()
+    if any(t.dtype is not torch.float8_e4m3fn or not t.is_cuda for t in (k8, v8)):
+        raise TypeError("k8 and v8 must be CUDA tensors of torch.float8_e4m3fn")
+    if any(t.dtype is not torch.float32 or not t.is_cuda for t in (ks, vs)):
+        raise TypeError("ks and vs must be CUDA tensors of torch.float32")
+    shape, st, scales, sst = k8.shape, k8.stride(), ks.shape, ks.stride()
+    layers, stride, scale_stride = 1, 0, 0
+    if shape != v8.shape or st != v8.stride() or scales != vs.shape or sst != vs.stride():
+        raise ValueError("k8 and v8, and ks and vs, must be of one shape and strides")
+    if len(shape) == 5 and len(scales) == 4 and shape[0] == scales[0]:
+        layers, stride, scale_stride = shape[0], st[0], sst[0]
+        shape, st, scales, sst = shape[1:], st[1:], scales[1:], sst[1:]
+    if len(shape) != 4 or len(scales) != 3 or scales[0] != shape[0] or scales[2] != shape[2]:
+        raise ValueError("k8 and v8 must be (pages, page_size, kv_heads, dim), ks and vs (pages, blocks, kv_heads)")
+    pages, page, heads, dim = shape
+    if st[3] != 1 and dim != 1:
+        raise ValueError("the cache's last axis must be contiguous")
+    if scales[1] < 1 or page % scales[1]:
+        raise ValueError("a page must have a whole number of tokens to each of its scales")
+    return cbq_kv_cache8(k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(), heads, dim, page, page // scales[1],
+                         pages, *st[:3], *sst), layers, stride, scale_stride
+
+
+def cbq_kv_quantize(kc, vc, src, k8, v8, ks, vs, dst, err=None, stream=None):
+    """Pages src (n) int32 of the 16-bit cache kc, vc ([layers,] pages,
+    page_size, kv_heads, dim) written as pages dst (n) int32 of the 8-bit cache
+    k8, v8 (float8_e4m3fn, the same axes) with ks, vs ([layers,] pages,
+    page_size / block, kv_heads) fp32 scales.  A negative entry skips its pair."""
+    i32 = _torch().int32
+    c, layers, stride = _layers(kc, vc)
+    c8, layers8, stride8, scale_stride = _cache8(k8, v8, ks, vs)
+    if layers != layers8:
+        raise ValueError("both caches must have the same layers")
+    n = src.numel()
+    _check(load().cbq_kv_quantize(c, stride, _vec(src, i32, n, "src"), c8, stride8, scale_stride,
+                                  _vec(dst, i32, n, "dst"), layers, n, _opt_vec(err, i32, 1, "err"),
+                                  _raw_stream(stream, kc)), "cbq_kv_quantize")

@@ -896,9 +896,101 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
     int dev = 0;
     const int rc = check_device(&dev);
     if (rc != CBQ_OK) return rc;
-    const cbq::Sample a = {logits_dev, dtype,     n,         V,     row_stride, temperature_dev,
-                           top_k_dev,  top_p_dev, min_p_dev, u_dev, ids_dev,    probs_dev};
+    const cbq::Sample a = {logits_dev, dtype,     n,     V,       row_stride, temperature_dev, top_k_dev,
+                           top_p_dev,  min_p_dev, u_dev, ids_dev, probs_dev,  nullptr,         0};
     CBQ_CUDA(cbq::launch_sample(a, as_stream(stream)));
+    return CBQ_OK;
+}
+
+// ----------------------------------- behind the logits, and the cache ------
+
+int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
+              const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+              float *out_dev, int64_t out_stride, int32_t *ids_dev, void *stream) {
+    if (!logits_dev || !out_dev || !u_dev != !ids_dev || !known_dtype(dtype) || n < 1 || n > 65535 || V < 1 ||
+        V > CBQ_SAMPLE_MAX_V || row_stride < 0 || out_stride < 0 || (n > 1 && (row_stride < V || out_stride < V)) ||
+        !aligned_to(logits_dev, dtype_bytes(dtype)) || !aligned_to(temperature_dev, 4) || !aligned_to(top_k_dev, 4) ||
+        !aligned_to(top_p_dev, 4) || !aligned_to(min_p_dev, 4) || !aligned_to(u_dev, 4) || !aligned_to(ids_dev, 4) ||
+        !aligned_to(out_dev, 4))
+        return CBQ_EINVAL;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(logits_dev), y = reinterpret_cast<uintptr_t>(out_dev);
+    const uintptr_t x_bytes = ((uintptr_t)row_stride * (n - 1) + V) * dtype_bytes(dtype), y_bytes = ((uintptr_t)out_stride * (n - 1) + V) * 4;
+    if (x < y + y_bytes && y < x + x_bytes) return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const cbq::Sample a = {logits_dev, dtype,     n,     V,       row_stride, temperature_dev, top_k_dev,
+                           top_p_dev,  min_p_dev, u_dev, ids_dev, nullptr,    out_dev,         out_stride};
+    CBQ_CUDA(cbq::launch_sample(a, as_stream(stream)));
+    return CBQ_OK;
+}
+
+int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_dev, int64_t draft_stride, int V,
+               const int32_t *tokens_dev, const int32_t *parent_dev, int64_t total_tok, const int32_t *start_dev,
+               int n_seq, int max_tok, const float *u_dev, const float *u_next_dev, int32_t *path_dev,
+               int32_t *count_dev, int32_t *next_dev, unsigned int *err_dev, void *stream) {
+    if (!probs_dev || !tokens_dev || !parent_dev || !start_dev || !u_dev || !u_next_dev || !path_dev || !count_dev ||
+        !next_dev || V < 1 || V > CBQ_SAMPLE_MAX_V || total_tok < 1 || total_tok > (1 << 24) || n_seq < 1 ||
+        n_seq > 65535 || max_tok < 1 || max_tok > CBQ_TREE_MAX || probs_stride < 0 || draft_stride < 0 ||
+        (total_tok > 1 && (probs_stride < V || (draft_dev && draft_stride < V))))
+        return CBQ_EINVAL;
+    for (const void *p : {(const void *)probs_dev, (const void *)draft_dev, (const void *)tokens_dev,
+                          (const void *)parent_dev, (const void *)start_dev, (const void *)u_dev,
+                          (const void *)u_next_dev, (const void *)path_dev, (const void *)count_dev,
+                          (const void *)next_dev, (const void *)err_dev})
+        if (!aligned_to(p, 4)) return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const cbq::Verify a = {probs_dev, probs_stride, draft_dev, draft_stride, V,        tokens_dev, parent_dev, total_tok, start_dev,
+                           n_seq,     max_tok,      u_dev,     u_next_dev,   path_dev, count_dev,  next_dev,   err_dev};
+    CBQ_CUDA(cbq::launch_verify(a, as_stream(stream)));
+    return CBQ_OK;
+}
+
+int cbq_kv_commit(const cbq_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table_dev,
+                  int table_width, int n_seq, const int32_t *ctx_dev, const int32_t *path_dev, int max_tok,
+                  const int32_t *count_dev, int32_t *ctx_out_dev, unsigned int *err_dev, void *stream) {
+    if (!good_cache(cache) || layers < 1 || layers > 65535 || layer_stride < 0 || !table_dev || table_width < 1 ||
+        n_seq < 1 || n_seq > 65535 || !ctx_dev || !path_dev || max_tok < 1 || max_tok > CBQ_TREE_MAX || !count_dev ||
+        ctx_out_dev == ctx_dev || !aligned_to(table_dev, 4) || !aligned_to(ctx_dev, 4) || !aligned_to(path_dev, 4) ||
+        !aligned_to(count_dev, 4) || !aligned_to(ctx_out_dev, 4) || !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const cbq::KvCommit a = {*cache,  layers,  layer_stride, table_dev,   table_width, n_seq,
+                             ctx_dev, path_dev, max_tok,      count_dev, ctx_out_dev, err_dev};
+    CBQ_CUDA(cbq::launch_kv_commit(a, as_stream(stream)));
+    return CBQ_OK;
+}
+
+namespace {
+
+bool good_cache8(const cbq_kv_cache8 *c) {
+    return c && c->k && c->v && c->k_scale && c->v_scale && c->kv_heads >= 1 && c->kv_heads <= 256 && c->head_dim >= 1 &&
+           c->head_dim <= 256 && c->page_size >= 1 && c->block >= 1 && c->block <= 65536 && c->page_size % c->block == 0 &&
+           c->n_pages >= 1 && c->n_pages <= INT32_MAX / c->page_size && c->page_stride >= 0 && c->tok_stride >= 0 &&
+           c->head_stride >= 0 && c->scale_page_stride >= 0 && c->scale_block_stride >= 0 && c->scale_head_stride >= 0 &&
+           aligned_to(c->k_scale, 4) && aligned_to(c->v_scale, 4);
+}
+
+}  // namespace
+
+int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const int32_t *src_dev,
+                    const cbq_kv_cache8 *to, int64_t to_layer_stride, int64_t scale_layer_stride,
+                    const int32_t *dst_dev, int layers, int64_t n, unsigned int *err_dev, void *stream) {
+    if (!good_cache(from) || !good_cache8(to) || from->kv_heads != to->kv_heads || from->head_dim != to->head_dim ||
+        from->page_size != to->page_size || from_layer_stride < 0 || to_layer_stride < 0 || scale_layer_stride < 0 ||
+        !src_dev || !dst_dev || layers < 1 || layers > 65535 || n < 1 || n > (1 << 24) ||
+        n * to->kv_heads > INT32_MAX / (to->page_size / to->block) || !aligned_to(src_dev, 4) || !aligned_to(dst_dev, 4) ||
+        !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    const cbq::KvQuantize a = {*from, from_layer_stride, src_dev, *to, to_layer_stride, scale_layer_stride, dst_dev, layers, n, err_dev};
+    CBQ_CUDA(cbq::launch_kv_quantize(a, as_stream(stream)));
     return CBQ_OK;
 }
 

@@ -508,8 +508,8 @@ struct Part {
 
     // The rest for those n in one block, without another word from the others: for each, what comes before it in the
     // order, and, of what is kept, before it by index.  want(mass of the first k): what top-p's must reach.
-    template <typename F, typename G>
-    __device__ void settle(int n, int k, F mass, G want, uint64_t least, float u, int32_t *id, float *prob) {
+    template <typename F, typename G, typename H>
+    __device__ void settle(int n, int k, F mass, G want, uint64_t least, float u, int32_t *id, float *prob, H keeps) {
         uint64_t *key = reinterpret_cast<uint64_t *>(s.gather), *w = key + kSettle, *kept = w + kSettle;
         static_assert(sizeof(s.gather) >= 3 * kSettle * sizeof(uint64_t), "three numbers each");
         if (threadIdx.x < (unsigned)n) w[threadIdx.x] = mass(logit_of((uint32_t)(key[threadIdx.x] >> 32)));
@@ -547,15 +547,35 @@ struct Part {
             total += __shfl_xor_sync(~0u, total, o);
         }
         const uint64_t goal = taken(total, u);
-        if (stays && q == 0 && upto - own < goal && upto >= goal) {
+        if (stays && q == 0) keeps((int)~(uint32_t)mine, own, total);
+        if (id && stays && q == 0 && upto - own < goal && upto >= goal) {
             *id = (int32_t)~(uint32_t)mine;
             if (prob) *prob = (float)((double)own / (double)total);
         }
     }
 };
 
-// grid (blocks of the cluster, rows).
-template <typename T, int N>
+// A weight's part of a mass, within 2^-23 of itself; inv = 2^23 / mass as two
+// numbers.  The weight (at most 2^45) is split at bit 23: both halves are exact
+// in fp32, made by the bits of a number between 2^23 and 2^24.
+struct Inverse {
+    float hi, lo;
+};
+__device__ __forceinline__ Inverse inverse(uint64_t mass) {
+    const float m = (float)mass, rest = (float)(int64_t)(mass - (uint64_t)m);
+    const float hi = 8388608.0f / m;
+    return Inverse{hi, (__fmaf_rn(-hi, m, 8388608.0f) - hi * rest) / m};
+}
+__device__ __forceinline__ float part_of(uint64_t w, Inverse inv) {
+    const float h = __uint_as_float(0x4B000000u | (uint32_t)(w >> 23)) - 8388608.0f;
+    const float l = (__uint_as_float(0x4B000000u | ((uint32_t)w & 0x7FFFFFu)) - 8388608.0f) * 0x1p-23f;
+    return __fmaf_rn(h, inv.hi, __fmaf_rn(l, inv.hi, __fmaf_rn(l, inv.lo, h * inv.lo)));
+}
+
+// grid (blocks of the cluster, rows).  kDist: the whole distribution is written
+// too (cbq_probs), first zeros wherever some logits are cut, and what is kept
+// into those once it is known; a token is drawn if there is a number for it.
+template <typename T, int N, bool kDist>
 __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
@@ -569,7 +589,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
                    (int)cluster_rank(), warp, lane};
     pdl_wait();
     const float temp = a.temperature ? a.temperature[c] : 1.0f, p = a.top_p ? a.top_p[c] : 1.0f;
-    const float least = a.min_p ? a.min_p[c] : 0.0f, u = a.u[c];
+    const float least = a.min_p ? a.min_p[c] : 0.0f, u = !kDist || a.u ? a.u[c] : 0.0f;
+    float *dist = kDist ? a.dist + c * a.dist_stride : nullptr;
     const int k = a.top_k ? a.top_k[c] : 0;
     const T *logits = static_cast<const T *>(a.logits) + c * a.row_stride;
     const int start = row.first + warp * N * 32 + lane;
@@ -617,7 +638,14 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         at = __reduce_min_sync(~0u, s.at[lane]);
         const ulonglong2 all = row.tell(at, 0);  // (by all lanes: a barrier of the cluster)
         at = __reduce_min_sync(~0u, lane < row.blocks ? (uint32_t)all.x : ~0u);
-        if (threadIdx.x == 0 && row.rank == 0) {
+        if constexpr (kDist) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int i = start + j * 32;
+                if (i < a.V) dist[i] = top > kNone && i == (int)at ? 1.0f : 0.0f;
+            }
+        }
+        if (threadIdx.x == 0 && row.rank == 0 && (!kDist || a.ids)) {
             a.ids[c] = top <= kNone ? -1 : (int)at;
             if (a.probs) a.probs[c] = top <= kNone ? 0.0f : 1.0f;
         }
@@ -716,11 +744,18 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
             row.listed += __popc(who);
         }
         __syncwarp();
+        if constexpr (kDist) {  // (the barriers in collect() are between these zeros and what is written over them)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (start + j * 32 < a.V) dist[start + j * 32] = 0.0f;
+        }
         const int n = row.collect();
         if (n <= kSettle) {
             if (row.rank == 0)
                 row.settle(n, by_k ? k : a.V, mass, [&](uint64_t m) { return !by_p ? ~0ull : weighed ? want : goal(m); }, floor_w, u,
-                           a.ids + c, a.probs ? a.probs + c : nullptr);
+                           !kDist || a.ids ? a.ids + c : nullptr, a.probs ? a.probs + c : nullptr, [&](int at, uint64_t w, uint64_t sum) {
+                               if constexpr (kDist) dist[at] = part_of(w, inverse(sum));
+                           });
             return;
         }
     }
@@ -768,21 +803,33 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
                                [&](uint64_t) { return ties; }, &total, &value);
         last = (int)__reduce_max_sync(~0u, (uint32_t)row.tell((uint64_t)(i + 1), 0).x) - 1;
     }
-    const int i = row.walk([&](float x, float y) { return weigh(x, y, sc, s.table); }, [&](int at, float l, uint64_t v) {
-        return (l > tau || (l == tau && at <= last)) && v >= floor_w;
-    }, [&](uint64_t sum) { return taken(sum, u); }, &total, &value);
-    if (i >= 0 && threadIdx.x == 0) {
+    auto stays = [&](int at, float l, uint64_t v) { return (l > tau || (l == tau && at <= last)) && v >= floor_w; };
+    const int i = row.walk([&](float x, float y) { return weigh(x, y, sc, s.table); }, stays,
+                           [&](uint64_t sum) { return taken(sum, u); }, &total, &value);
+    if constexpr (kDist) {
+        const Inverse inv = inverse(total);
+        for (int i0 = 0; i0 < row.listed; i0 += 64) {
+            const int i1 = i0 + lane, i2 = i1 + 32;
+            const float la = row.list[i1], lb = row.list[i2];
+            const Two v = weigh(la, lb, sc, s.table);
+            const int base = row.first + warp * N * 32;
+            const int at1 = base + (row.whole ? i1 : (int)row.place[i1]), at2 = base + (row.whole ? i2 : (int)row.place[i2]);
+            if (row.whole ? at1 < a.V : i1 < row.listed && stays(at1, la, v.a)) dist[at1] = part_of(v.a, inv);
+            if (row.whole ? at2 < a.V : i2 < row.listed && stays(at2, lb, v.b)) dist[at2] = part_of(v.b, inv);
+        }
+    }
+    if (i >= 0 && threadIdx.x == 0 && (!kDist || a.ids)) {
         a.ids[c] = i;
         if (a.probs) a.probs[c] = (float)((double)value / (double)total);
     }
 }
 
-template <typename T, int N>
+template <typename T, int N, bool kDist>
 cudaError_t launch_part(const Sample &a, int blocks, cudaStream_t s) {
     constexpr int kSmem = sizeof(Shared) + N * kSampleThreads * (sizeof(float) + sizeof(uint16_t));
-    cudaError_t e = cudaFuncSetAttribute(k_sample<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k_sample<T, N, kDist>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess && blocks > 8)
-        e = cudaFuncSetAttribute(k_sample<T, N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(k_sample<T, N, kDist>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.n);
@@ -797,10 +844,10 @@ cudaError_t launch_part(const Sample &a, int blocks, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sample<T, N>, a);
+    return cudaLaunchKernelEx(&cfg, k_sample<T, N, kDist>, a);
 }
 
-template <typename T>
+template <typename T, bool kDist>
 cudaError_t launch(const Sample &a, cudaStream_t s) {
     // Few rows: many blocks each, for the shortest call.  Many: few blocks each, as those of a row wait for one another
     // (256 rows of 129,280 logits of all kinds: eight blocks a row 215 us, four 149, before few
@@ -811,16 +858,16 @@ cudaError_t launch(const Sample &a, cudaStream_t s) {
         if (n < least || blocks == kMaxBlocks) n *= 2;
         else blocks *= 2;
     }
-    return n == 8 ? launch_part<T, 8>(a, blocks, s) : n == 16 ? launch_part<T, 16>(a, blocks, s) : launch_part<T, 32>(a, blocks, s);
+    return n == 8 ? launch_part<T, 8, kDist>(a, blocks, s) : n == 16 ? launch_part<T, 16, kDist>(a, blocks, s) : launch_part<T, 32, kDist>(a, blocks, s);
 }
 static_assert(CBQ_SAMPLE_MAX_V <= kMaxBlocks * 32 * kSampleThreads, "the longest row fits a cluster");
 
 }  // namespace
 
 cudaError_t launch_sample(const Sample &a, cudaStream_t s) {
-    if (a.dtype == CBQ_F32) return launch<float>(a, s);
-    if (a.dtype == CBQ_BF16) return launch<__nv_bfloat16>(a, s);
-    return launch<__half>(a, s);
+    if (a.dtype == CBQ_F32) return a.dist ? launch<float, true>(a, s) : launch<float, false>(a, s);
+    if (a.dtype == CBQ_BF16) return a.dist ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s);
+    return a.dist ? launch<__half, true>(a, s) : launch<__half, false>(a, s);
 }
 
 }  // namespace cbq

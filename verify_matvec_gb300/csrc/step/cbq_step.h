@@ -1,6 +1,7 @@
 // cbq_step.h -- the launchers of the operators between the quantized products
-// (positions, attention over the paged cache, sampling), shared by the C-ABI
-// layer and their translation units.  Not part of the public ABI.
+// (positions, attention over the paged cache, sampling) and behind the logits
+// (distributions, verification, the cache's upkeep), shared by the C-ABI layer
+// and their translation units.  Not part of the public ABI.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -67,7 +68,55 @@ struct Sample {
     const float *top_p, *min_p, *u;
     int32_t *ids;
     float *probs;
+    float *dist;  // cbq_probs: the whole distribution (u and ids may be null then)
+    int64_t dist_stride;
 };
 cudaError_t launch_sample(const Sample &a, cudaStream_t s);
+
+// One call of the verification (the arguments of cbq_verify).
+struct Verify {
+    const float *probs;
+    int64_t probs_stride;
+    const float *draft;
+    int64_t draft_stride;
+    int V;
+    const int32_t *tokens, *parent;
+    int64_t total_tok;
+    const int32_t *start;
+    int n_seq, max_tok;
+    const float *u, *u_next;
+    int32_t *path, *count, *next;
+    unsigned *err;
+};
+cudaError_t launch_verify(const Verify &a, cudaStream_t s);
+
+// One call of the accepted drafts' move (the arguments of cbq_kv_commit).
+struct KvCommit {
+    cbq_kv_cache c;
+    int layers;
+    int64_t layer_stride;
+    const int32_t *table;
+    int table_width, n_seq;
+    const int32_t *ctx, *path;
+    int max_tok;
+    const int32_t *count;
+    int32_t *ctx_out;
+    unsigned *err;
+};
+cudaError_t launch_kv_commit(const KvCommit &a, cudaStream_t s);
+
+// One call of the 8-bit pages' making (the arguments of cbq_kv_quantize).
+struct KvQuantize {
+    cbq_kv_cache from;
+    int64_t from_layer;
+    const int32_t *src;
+    cbq_kv_cache8 to;
+    int64_t to_layer, scale_layer;
+    const int32_t *dst;
+    int layers;
+    int64_t n;
+    unsigned *err;
+};
+cudaError_t launch_kv_quantize(const KvQuantize &a, cudaStream_t s);
 
 }  // namespace cbq
