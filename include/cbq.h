@@ -672,6 +672,41 @@ int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const i
                     const cbq_kv_cache8 *to, int64_t to_layer_stride, int64_t scale_layer_stride,
                     const int32_t *dst_dev, int layers, int64_t n, unsigned int *err_dev, void *stream);
 
+/* cbq_tree_attention over a context whose first old_dev[s] places are in the
+ * 8-bit cache: place p < old_dev[s] of sequence s is token p % old->page_size
+ * of its page table8_dev[s*table8_width + p / old->page_size], and every other
+ * place p, the drafts' among them, token p % page_size of page
+ * table_dev[s*table_width + p / page_size] of the 16-bit cache as ever (what
+ * the table says of old places is not read).  Formulas, masks, drafts, NaN and
+ * rows that see nothing are cbq_tree_attention's, with k and v what the 8-bit
+ * numbers and their scales stand for.  max_old bounds old_dev[s] and max_new
+ * the places behind, ctx_dev[s] + n_s - old_dev[s]: they size the launch.  A
+ * sequence beyond them, beyond its tables, or with old_dev[s] outside
+ * 0..ctx_dev[s], is cut to them (first the old places, then the ones behind)
+ * and sets CBQ_DEVERR_BAD_LENGTH; page ids as in cbq_tree_attention.
+ * Scores, maxima and sums are fp32.  Old places' products take their numbers
+ * unrounded as fp16, the query as fp16 numbers of its row's own power of two
+ * (what is below 2^-30 of the row's largest loses bits), and the weights times
+ * the values' scales rounded to fp16 relative to the row's largest: those
+ * below 2^-24 of it lose bits.  Scales may be any positive numbers from 2^-80 to
+ * 2^112 (of values above 2^120, which take larger ones, small weights are lost).
+ * old->kv_heads and head_dim are the cache's.  max_old = 0 with old_dev all
+ * zero is cbq_tree_attention.  Speed: heads of 64, 128 and 256 with k, v, out
+ * and all rows of both caches on 16 bytes take the tensor cores; every other
+ * layout a warp a row, one key after another.  ws_dev, out_dtype, lse_dev,
+ * err_dev and the other arguments as cbq_tree_attention.
+ * Errors: those of cbq_tree_attention, and EINVAL (a bad 8-bit cache; max_old
+ * outside 0..CBQ_TREE_MAX_LEN; max_new outside 1..CBQ_TREE_MAX_LEN; their sum
+ * above that; table8_width < 1). */
+int cbq_tree_attention8_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new,
+                                  int q_heads, int kv_heads, int head_dim, int64_t *bytes);
+int cbq_tree_attention8(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
+                        const cbq_kv_cache8 *old, const int32_t *table8_dev, int table8_width, const int32_t *old_dev,
+                        const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
+                        const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,
+                        int64_t max_old, int64_t max_new, float scale, void *out_dev, int out_dtype, float *lse_dev,
+                        void *ws_dev, int64_t ws_bytes, unsigned int *err_dev, void *stream);
+
 /* ---- checking entry points (used by the parity tests) ---------------- */
 
 /* Per-block int32 dots s_dev[c][r][b] (n x M x K/32) of W with plain int8

@@ -155,3 +155,26 @@ def quantize(x, block):
             e[i] = k
     scale = 2.0 ** e
     return e4m3(y / scale[:, :, None, :, None]).reshape(x.shape), scale
+
+
+def attention(q, seqs, scale):
+    """q (rows, heads, dim); seqs: (first row, keys (len, kv, dim), values, seen
+    (rows of the sequence, len)).  out, lse, sum w|v|, and the largest sum |q k|
+    |scale| of a seen key."""
+    q = np.asarray(q, dtype=np.float64)
+    out, lse = np.zeros(q.shape), np.full(q.shape[:2], -np.inf)
+    absv, big = np.zeros(q.shape), np.zeros(q.shape[:2])
+    for row0, k, v, seen in seqs:
+        group = q.shape[1] // k.shape[1]
+        for i in range(seen.shape[0]):
+            if not seen[i].any():
+                continue
+            for h in range(q.shape[1]):
+                kk, vv, row = k[seen[i], h // group], v[seen[i], h // group], q[row0 + i, h]
+                x = kk @ row * scale
+                w = np.exp(x - x.max())
+                z = w.sum()
+                out[row0 + i, h], absv[row0 + i, h] = w / z @ vv, w / z @ np.abs(vv)
+                lse[row0 + i, h] = x.max() + np.log(z)
+                big[row0 + i, h] = (np.abs(kk) @ np.abs(row)).max() * abs(scale)
+    return out, lse, absv, big

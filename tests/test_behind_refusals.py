@@ -95,3 +95,28 @@ def test_the_references_rounding():
     mid = (all_of[1:] + all_of[:-1]) / 2
     even = np.where(np.arange(126) % 2 == 0, all_of[:-1], all_of[1:])
     assert np.array_equal(behind_ref.e4m3(mid), even) and np.array_equal(behind_ref.e4m3(-mid), -even)
+
+
+def test_tree_attention8_refusals(lib):
+    good = dict(q=A, qt=32, qh=8, heads=4, total=3, c8=cache8(), t8=A, w8=1, old=A, cache=_cache(), table=A, width=2,
+                n_seq=1, ctx=A, start=A, mask=A, max_tok=3, max_old=4, max_new=8, scale=1.0, out=P(0x20000),
+                out_dtype=1, lse=None, ws=A, ws_bytes=1 << 40, err=None, stream=None)
+    limits = [dict(heads=0), dict(heads=3), dict(heads=1026), dict(total=0), dict(total=(1 << 24) + 1), dict(n_seq=0),
+              dict(n_seq=65536), dict(max_tok=0), dict(max_tok=65), dict(max_old=-1), dict(max_old=(1 << 30) + 1),
+              dict(max_old=1 << 30), dict(max_new=0), dict(max_new=(1 << 30) + 1), dict(max_new=(1 << 30) - 3)]
+    _refused(lib.cbq_tree_attention8, good, limits + [
+        dict(q=None), dict(t8=None), dict(old=None), dict(table=None), dict(ctx=None), dict(start=None),
+        dict(mask=None), dict(out=None), dict(ws=None), dict(c8=None), dict(cache=None), dict(qt=-1), dict(qh=-1),
+        dict(w8=0), dict(width=0), dict(scale=float("inf")), dict(out_dtype=2), dict(out_dtype=9), dict(ws=P(0x10008)),
+        dict(ws_bytes=0), dict(mask=P(0x10004)), dict(q=P(0x10001)), dict(lse=P(0x10002)), dict(err=P(0x10002)),
+        dict(t8=P(0x10002)), dict(old=P(0x10002)), dict(c8=cache8(kv_heads=1)), dict(c8=cache8(head_dim=4))] + [
+        dict(cache=_cache(**c)) for c in BAD_CACHES] + [dict(c8=cache8(**c)) for c in BAD_CACHES8])
+    b = ctypes.c_int64()
+    good = dict(n_seq=1, total=3, max_tok=3, max_old=4, max_new=8, heads=4, kv=2, dim=8, bytes=ctypes.byref(b))
+    assert lib.cbq_tree_attention8_workspace(*good.values()) == cbq.CBQ_OK and b.value >= 16
+    _refused(lib.cbq_tree_attention8_workspace, good, limits + [dict(kv=0), dict(kv=257), dict(dim=0), dict(dim=257),
+                                                                dict(bytes=None)])
+    for old, new in ((1 << 29, 1 << 29), (0, 1 << 30), ((1 << 30) - 1, 1)):  # the ends: a plan is found at once
+        for n_seq, heads in ((1, 2), (65535, 1024)):
+            got = lib.cbq_tree_attention8_workspace(n_seq, 64, 64, old, new, heads, 2, 128, ctypes.byref(b))
+            assert got == cbq.CBQ_OK and b.value >= 16

@@ -110,6 +110,9 @@ _SIGS = {
     "cbq_verify": ([_P, _I64, _P, _I64, _I, _P, _P, _I64, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
     "cbq_kv_commit": ([_KV, _I, _I64, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P], _I),
     "cbq_kv_quantize": ([_KV, _I64, _P, _KV8, _I64, _I64, _P, _I, _I64, _P, _P], _I),
+    "cbq_tree_attention8_workspace": ([_I, _I64, _I, _I64, _I64, _I, _I, _I, ctypes.POINTER(_I64)], _I),
+    "cbq_tree_attention8": ([_P, _I64, _I64, _I, _I64, _KV8, _P, _I, _P, _KV, _P, _I, _I, _P, _P, _P, _I, _I64, _I64, _F, _P,
+                             _I, _P, _P, _I64, _P, _P], _I),
     "cbq_moe_debug_intermediate": ([_P, _I, _P, _P, _P, _P], _I),
 }
 
@@ -939,3 +942,59 @@ def cbq_kv_quantize(kc, vc, src, k8, v8, ks, vs, dst, err=None, stream=None):
     _check(load().cbq_kv_quantize(c, stride, _vec(src, i32, n, "src"), c8, stride8, scale_stride,
                                   _vec(dst, i32, n, "dst"), layers, n, _opt_vec(err, i32, 1, "err"),
                                   _raw_stream(stream, kc)), "cbq_kv_quantize")
+
+
+@functools.lru_cache(1024)
+def cbq_tree_attention8_workspace(n_seq: int, total_tok: int, max_tok: int, max_old: int, max_new: int, q_heads: int,
+                                  kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of cbq_tree_attention8 for these limits."""
+    b = ctypes.c_int64()
+    _check(load().cbq_tree_attention8_workspace(n_seq, total_tok, max_tok, max_old, max_new, q_heads, kv_heads, head_dim,
+                                                ctypes.byref(b)), "cbq_tree_attention8_workspace")
+    return b.value
+
+
+def cbq_tree_attention8(q, k8, v8, ks, vs, table8, old, kc, vc, table, ctx, start, mask, max_tok: int, max_old: int,
+                        max_new: int, scale: float | None = None, out=None, with_lse: bool = False, workspace=None,
+                        err=None, stream=None):
+    """cbq_tree_attention over contexts whose first old (sequences) int32 places
+    are in the 8-bit cache k8, v8, ks, vs (as cbq_kv_quantize writes it), by
+    table8 (sequences, width) int32 page ids; the places behind them and the
+    drafts are in kc, vc by table, in which a place has the number that it would
+    have had.  max_old bounds old, max_new the places behind (ctx + drafts -
+    old).  workspace: a uint8 tensor of cbq_tree_attention8_workspace bytes."""
+    torch = _torch()
+    shape, dev, i32 = q.shape, q.device, torch.int32
+    n, heads, dim = shape
+    c = _cache(kc, vc)
+    c8, layers, _, _ = _cache8(k8, v8, ks, vs)
+    if layers != 1 or k8.dim() != 4:
+        raise ValueError("k8 and v8 must be (pages, page_size, kv_heads, dim)")
+    if q.dtype != kc.dtype or dim != c.head_dim:
+        raise ValueError("q must have the cache's dtype and dim")
+    n_seq, width = table.shape
+    if table8.dim() != 2 or table8.shape[0] != n_seq:
+        raise ValueError("table8 must be (sequences, width)")
+    if out is None:
+        out = _new(shape, q.dtype, dev, stream)
+        op, od = out.data_ptr(), c.dtype
+    else:
+        if out.shape != shape:
+            raise ValueError("out must have the shape of q")
+        op, od = _vec(out, out.dtype, n * heads * dim, "out"), _dtype(out, "out")
+    lse = _new((n, heads), torch.float32, dev, stream) if with_lse else None
+    if workspace is None:
+        room = cbq_tree_attention8_workspace(n_seq, n, max_tok, max_old, max_new, heads, c.kv_heads, dim)
+        workspace = _least_workspace(dev) if room <= 16 else _new((room,), torch.uint8, dev, stream, returned=False)
+        wp = workspace.data_ptr()
+    else:
+        wp, room = _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel()
+    qp, qt, qh = _heads(q, "q")
+    _check(load().cbq_tree_attention8(qp, qt, qh, heads, n, c8, _vec(table8, i32, -1, "table8"), table8.shape[1],
+                                      _vec(old, i32, n_seq, "old"), c, _vec(table, i32, -1, "table"), width, n_seq,
+                                      _vec(ctx, i32, n_seq, "ctx"), _vec(start, i32, n_seq + 1, "start"),
+                                      _vec(mask, torch.int64, n, "mask"), max_tok, max_old, max_new,
+                                      dim ** -0.5 if scale is None else scale, op, od,
+                                      None if lse is None else lse.data_ptr(), wp, room, _opt_vec(err, i32, 1, "err"),
+                                      _raw_stream(stream, q)), "cbq_tree_attention8")
+    return (out, lse) if with_lse else out

@@ -994,4 +994,68 @@ int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const i
     return CBQ_OK;
 }
 
+namespace {
+
+bool good_old_limits(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new, int q_heads, int kv_heads,
+                     int head_dim) {
+    return max_old >= 0 && max_old <= CBQ_TREE_MAX_LEN && max_new >= 1 && max_new <= CBQ_TREE_MAX_LEN &&
+           good_tree_limits(n_seq, total_tok, max_tok, max_old + max_new, q_heads, kv_heads, head_dim);
+}
+
+}  // namespace
+
+int cbq_tree_attention8_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new, int q_heads,
+                                  int kv_heads, int head_dim, int64_t *bytes) {
+    if (!bytes || !good_old_limits(n_seq, total_tok, max_tok, max_old, max_new, q_heads, kv_heads, head_dim)) return CBQ_EINVAL;
+    *bytes = (int64_t)cbq::tree_attention8_workspace(n_seq, total_tok, max_tok, max_old, max_new, q_heads, kv_heads, head_dim);
+    return CBQ_OK;
+}
+
+int cbq_tree_attention8(const void *q_dev, int64_t q_tok_stride, int64_t q_head_stride, int q_heads, int64_t total_tok,
+                        const cbq_kv_cache8 *old, const int32_t *table8_dev, int table8_width, const int32_t *old_dev,
+                        const cbq_kv_cache *cache, const int32_t *table_dev, int table_width, int n_seq,
+                        const int32_t *ctx_dev, const int32_t *start_dev, const int64_t *mask_dev, int max_tok,
+                        int64_t max_old, int64_t max_new, float scale, void *out_dev, int out_dtype, float *lse_dev,
+                        void *ws_dev, int64_t ws_bytes, unsigned int *err_dev, void *stream) {
+    if (!good_cache(cache) || !good_cache8(old) || old->kv_heads != cache->kv_heads || old->head_dim != cache->head_dim ||
+        !good_old_limits(n_seq, total_tok, max_tok, max_old, max_new, q_heads, cache->kv_heads, cache->head_dim))
+        return CBQ_EINVAL;
+    const size_t need = cbq::tree_attention8_workspace(n_seq, total_tok, max_tok, max_old, max_new, q_heads, cache->kv_heads,
+                                                       cache->head_dim);
+    if (!q_dev || !table8_dev || !old_dev || !table_dev || !ctx_dev || !start_dev || !mask_dev || !out_dev || !ws_dev ||
+        q_tok_stride < 0 || q_head_stride < 0 || table8_width < 1 || table_width < 1 || !std::isfinite(scale) ||
+        (out_dtype != cache->dtype && out_dtype != CBQ_F32) || !aligned16(ws_dev) || ws_bytes < (int64_t)need ||
+        !aligned_to(q_dev, 2) || !aligned_to(out_dev, dtype_bytes(out_dtype)) || !aligned_to(table8_dev, 4) ||
+        !aligned_to(old_dev, 4) || !aligned_to(table_dev, 4) || !aligned_to(ctx_dev, 4) || !aligned_to(start_dev, 4) ||
+        !aligned_to(mask_dev, 8) || !aligned_to(lse_dev, 4) || !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    int dev = 0;
+    const int rc = check_device(&dev);
+    if (rc != CBQ_OK) return rc;
+    cbq::TreeAttention a = {};
+    a.q = q_dev;
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.q_heads = q_heads;
+    a.total_tok = total_tok;
+    a.c = *cache;
+    a.table = table_dev;
+    a.table_width = table_width;
+    a.n_seq = n_seq;
+    a.ctx = ctx_dev;
+    a.start = start_dev;
+    a.mask = mask_dev;
+    a.max_tok = max_tok;
+    a.max_len = max_old + max_new;
+    a.scale = scale;
+    a.out = out_dev;
+    a.out_f32 = out_dtype == CBQ_F32;
+    a.lse = lse_dev;
+    a.ws = ws_dev;
+    a.err = err_dev;
+    const cbq::OldPlaces b = {*old, table8_dev, table8_width, old_dev, max_old, max_new, 0, 0};
+    CBQ_CUDA(cbq::launch_tree_attention8(a, b, as_stream(stream)));
+    return CBQ_OK;
+}
+
 }  // extern "C"

@@ -26,16 +26,27 @@ namespace cbq {
 
 namespace {
 
+// An e4m3 number (all of them are fp16 numbers too).
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint16_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+    return r;
+}
+__device__ __forceinline__ float e4m3_f32(uint8_t b) {
+    const uint32_t two = e4m3_f16x2(b);
+    return __low2float(*reinterpret_cast<const __half2 *>(&two));
+}
+
 // Any head size and any strides: one warp per (token, head), the lanes hold
 // the head's values, a key at a time.  Bound by that chain: each key's look-up,
 // row of k, five shuffles and row of v follow one another, some 0.9 us (5 drafts
 // over 8,191 keys 7.0 ms with heads of 96, 8.2 with 192).  grid (q_heads, max_tok, n_seq).
-template <typename T>
-__global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
+template <typename T, typename Old>
+__global__ void __launch_bounds__(32) k_tree_general(TreeAttention a, Old b) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x, h = blockIdx.x, i = blockIdx.y, s = blockIdx.z, D = a.c.head_dim;
-    const Seq sq = sequence(a, s, lane == 0 && h == 0 && i == 0);
+    const Seq sq = sequence(a, b, s, lane == 0 && h == 0 && i == 0);
     if (i >= sq.n) return;
     const int64_t row = sq.row0 + i;
     const uint64_t mask = seen_drafts(a, sq, row);
@@ -48,19 +59,12 @@ __global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
         qv[j] = j * 32 + lane < D ? to_f32(q[j * 32 + lane]) : 0.0f;
     }
     float top = -INFINITY, sum = 0.0f;
-    for (int p = 0; p < sq.len; ++p) {
-        if (p >= sq.ctx && !(mask >> (p - sq.ctx) & 1)) continue;
-        const int64_t page = a.table[s * (int64_t)a.table_width + p / a.c.page_size];
-        if (page < 0 || page >= a.c.n_pages) {
-            if (a.err && lane == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-            continue;
-        }
-        const int64_t at = page * a.c.page_stride + p % a.c.page_size * a.c.tok_stride + g * a.c.head_stride;
-        const T *k = static_cast<const T *>(a.c.k) + at, *v = static_cast<const T *>(a.c.v) + at;
+    // one more key, of the head's values k and v as this lane reads them
+    auto see = [&](auto k, auto v) {
         float x = 0.0f;
 #pragma unroll
         for (int j = 0; j < kMaxDim / 32; ++j)
-            if (j * 32 + lane < D) x += qv[j] * to_f32(k[j * 32 + lane]);
+            if (j * 32 + lane < D) x += qv[j] * k(j * 32 + lane);
 #pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
         x *= a.scale;
@@ -70,8 +74,33 @@ __global__ void __launch_bounds__(32) k_tree_general(TreeAttention a) {
         sum = sum * keep + w;
 #pragma unroll
         for (int j = 0; j < kMaxDim / 32; ++j)
-            if (j * 32 + lane < D) acc[j] = acc[j] * keep + w * to_f32(v[j * 32 + lane]);
+            if (j * 32 + lane < D) acc[j] = acc[j] * keep + w * v(j * 32 + lane);
         top = now;
+    };
+    auto known = [&](int64_t page, int64_t pages) {
+        const bool good = page >= 0 && page < pages;
+        if (!good && a.err && lane == 0) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+        return good;
+    };
+    if constexpr (std::is_same_v<Old, OldPlaces>) {
+        for (int p = 0; p < sq.old; ++p) {
+            const int64_t page = b.table[s * (int64_t)b.table_width + p / b.c.page_size];
+            if (!known(page, b.c.n_pages)) continue;
+            const int t = p % b.c.page_size;
+            const int64_t at = page * b.c.page_stride + t * b.c.tok_stride + g * b.c.head_stride;
+            const int64_t of = page * b.c.scale_page_stride + t / b.c.block * b.c.scale_block_stride + g * b.c.scale_head_stride;
+            const uint8_t *k = static_cast<const uint8_t *>(b.c.k) + at, *v = static_cast<const uint8_t *>(b.c.v) + at;
+            const float ks = b.c.k_scale[of], vs = b.c.v_scale[of];
+            see([&](int d) { return ks * e4m3_f32(k[d]); }, [&](int d) { return vs * e4m3_f32(v[d]); });
+        }
+    }
+    for (int p = sq.from; p < sq.len; ++p) {
+        if (p >= sq.ctx && !(mask >> (p - sq.ctx) & 1)) continue;
+        const int64_t page = a.table[s * (int64_t)a.table_width + p / a.c.page_size];
+        if (!known(page, a.c.n_pages)) continue;
+        const int64_t at = page * a.c.page_stride + p % a.c.page_size * a.c.tok_stride + g * a.c.head_stride;
+        const T *k = static_cast<const T *>(a.c.k) + at, *v = static_cast<const T *>(a.c.v) + at;
+        see([&](int d) { return to_f32(k[d]); }, [&](int d) { return to_f32(v[d]); });
     }
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
     const int64_t o = (row * a.q_heads + h) * D;
@@ -151,7 +180,218 @@ struct Shape {
     static constexpr int kResult = kParts * kRows * D * 4;
     static_assert(kResult <= kRing && kRows * kPitch <= 2 * kTileBytes, "what lies in the ring fits it");
     static_assert(kKeys % 16 == 0, "16 keys a product");
+    // old places: half the bytes, so twice the tiles of 64 keys in the same ring (and 64 keys of the largest head too)
+    static constexpr int kTile8 = 64, kKeys8 = kTile8 / kParts, kCopied8 = kTile8 / 4, kTileBytes8 = kTile8 * D;
+    static constexpr int kStages8 = kRing / (2 * kTileBytes8) < 6 ? kRing / (2 * kTileBytes8) : 6;
 };
+
+// The old places' share of a block's shared memory: their scales, and which of a tile there are.
+template <typename S>
+struct OldShared {
+    float ks[S::kStages8][S::kTile8], vs[S::kStages8][S::kTile8];
+    uint32_t valid[S::kStages8][4];
+};
+
+__device__ __forceinline__ int chunk_of(const OldPlaces &b) { return b.chunk8; }
+__device__ __forceinline__ int chunk_of(NoOldPlaces) { return 1; }
+
+// The old places [begin, end) of a chunk, whose keys and values are e4m3 numbers
+// and scales, into the running o, m and l of this lane's rows.
+//   x = (scale log2(e) 2^k) ks (q 2^-k).k,   w = 2^(x - m),   l += w,
+//   o += (w vs) v,                           m = max (x + log2 vs):
+// the numbers of k and v go into the products as they are, as fp16, which holds
+// every e4m3 number; a row of q does too, scaled to a largest magnitude of 2^14
+// to 2^15 by its own power of two 2^k; the scale of a key comes to its score and
+// that of a value to its weight.  The maximum is of what the weights are with
+// their scales, so they stay within fp16 (and as in the kernel below, 2^10 above
+// the running maximum's); l may be larger than that by a block's scale, and
+// fp32 has the room: 2^-80 <= vs.
+// Fragments: the order of the summed axis is free as long as both sides have it,
+// so a lane takes 16 bytes side by side of a key's row for four products, and
+// the same 16 values of q; and the values come through a transposing load of
+// 16-bit pairs, whose even and odd bytes make the fragments of the even and of
+// the odd columns.
+template <typename T, int D, int WR>
+__device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlaces &b, const Seq &sq, OldShared<Shape<D, WR>> &sh,
+                                           uint8_t *smem, int begin, int end, int r0, int rows, int kvh, float (&o)[D / 8][4],
+                                           float (&m)[2], float (&l)[2]) {
+    using S = Shape<D, WR>;
+    constexpr int kPieces = D / 16;  // 16-byte pieces of a row
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR, ra = wr * 16 + lane / 4, t4 = lane % 4;
+    const int group = a.q_heads / a.c.kv_heads, s = blockIdx.z;
+    const int tiles = (end - begin + S::kTile8 - 1) / S::kTile8;
+    const int32_t *table = b.table + (int64_t)s * b.table_width;
+    const int64_t head = kvh * b.c.head_stride;
+    const uint32_t size = b.c.page_size;
+    auto page_of = [&](int t) {
+        const int p = begin + t * S::kTile8 + warp * S::kCopied8 + lane;
+        return lane < S::kCopied8 && p < end ? table[(uint32_t)p / size] : -1;
+    };
+    // Pieces of a row are permuted by the row: keys so that two rows of four pieces meet no bank conflict, values so that
+    // eight rows of one piece meet none.
+    auto place_k = [](int r, int d) { return r * D + (D > 64 ? d ^ (r & 1) * 4 : d) * 16; };
+    auto place_v = [](int r, int d) { return r * D + (D > 64 ? d ^ (r & 7) : d ^ (r >> 1 & 3)) * 16; };
+    auto fetch = [&](int t, int page) {
+        const int slot = t % S::kStages8;
+        const uint32_t p = begin + t * S::kTile8 + warp * S::kCopied8 + lane;
+        const bool in = lane < S::kCopied8 && p < (uint32_t)end, good = in && page >= 0 && page < b.c.n_pages;
+        if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+        const uint32_t within = p % size;
+        const int64_t at = good ? page * b.c.page_stride + (int64_t)within * b.c.tok_stride + head : -1;
+        const uint32_t bits = __ballot_sync(~0u, good);
+        if (lane == 0) sh.valid[slot][warp] = bits;
+        if (lane < S::kCopied8) {
+            const int64_t of = good ? page * b.c.scale_page_stride + (int64_t)(within / (uint32_t)b.c.block) * b.c.scale_block_stride +
+                                          kvh * b.c.scale_head_stride : 0;
+            copy4(smem_addr(&sh.ks[slot][warp * S::kCopied8 + lane]), b.c.k_scale + of, good);
+            copy4(smem_addr(&sh.vs[slot][warp * S::kCopied8 + lane]), b.c.v_scale + of, good);
+        }
+        const uint32_t ks = smem_addr(smem) + slot * 2 * S::kTileBytes8;
+#pragma unroll
+        for (int i = 0; i < S::kCopied8 * kPieces / 32; ++i) {
+            const int x = i * 32 + lane, r = x / kPieces, d = x % kPieces, row = warp * S::kCopied8 + r;
+            const int64_t from = __shfl_sync(~0u, at, r), off = from < 0 ? 0 : from + d * 16;
+            copy16(ks + place_k(row, d), static_cast<const uint8_t *>(b.c.k) + off, from >= 0);
+            copy16(ks + S::kTileBytes8 + place_v(row, d), static_cast<const uint8_t *>(b.c.v) + off, from >= 0);
+        }
+    };
+    static_assert(S::kCopied8 * kPieces % 32 == 0, "whole warps of copies");
+    int page = page_of(0);
+#pragma unroll
+    for (int t = 0; t < S::kStages8 - 1; ++t) {
+        const int now = page;
+        page = t + 1 < tiles ? page_of(t + 1) : -1;
+        if (t < tiles) fetch(t, now);
+        copy_commit();
+    }
+    // q of the two rows: 16 values side by side of each 64, as fp16
+    constexpr int kSets = D / 64;
+    uint32_t qf[kSets][4][4];  // [64 values][4 of them][fragment register]
+    float of_row[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = ra + half * 8;
+        float v[kSets][16];
+        float most = 0.0f;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
+        const T *from = static_cast<const T *>(a.q) + (sq.row0 + (r0 + (r < rows ? r : 0)) / group) * a.q_tok +
+                        (kvh * group + (r0 + (r < rows ? r : 0)) % group) * a.q_head + t4 * 16;
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+            __align__(16) T y[16];
+            if (whole) {
+                *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(from + g * 64);
+                *reinterpret_cast<uint4 *>(y + 8) = *reinterpret_cast<const uint4 *>(from + g * 64 + 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = from[g * 64 + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                v[g][e] = r < rows ? to_f32(y[e]) : 0.0f;
+                most = fmaxf(most, fabsf(v[g][e]));
+            }
+        }
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        const int k = most > 0.0f && most < INFINITY ? max((int)(__float_as_uint(most) >> 23) - 127 - 14, -100) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - k) << 23);
+        of_row[half] = a.scale * kLog2e * __uint_as_float((uint32_t)(127 + k) << 23);
+#pragma unroll
+        for (int g = 0; g < kSets; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qf[g][i][half] = pack2<__half>(v[g][i * 4] * down, v[g][i * 4 + 1] * down);
+                qf[g][i][half + 2] = pack2<__half>(v[g][i * 4 + 2] * down, v[g][i * 4 + 3] * down);
+            }
+    }
+    constexpr float kLower = 10.0f;
+    for (int t = 0; t < tiles; ++t) {
+        copy_wait<S::kStages8 - 2>();
+        __syncthreads();
+        if (t + S::kStages8 - 1 < tiles) {
+            fetch(t + S::kStages8 - 1, page);
+            if (t + S::kStages8 < tiles) page = page_of(t + S::kStages8);
+        }
+        copy_commit();
+        const int slot = t % S::kStages8;
+        const uint8_t *kt = smem + slot * 2 * S::kTileBytes8;
+        const uint32_t vt = smem_addr(kt) + S::kTileBytes8;
+
+        float x[S::kKeys8 / 8][4] = {};
+#pragma unroll
+        for (int j = 0; j < S::kKeys8 / 8; ++j) {
+            const int r = wk * S::kKeys8 + j * 8 + lane / 4;
+#pragma unroll
+            for (int g = 0; g < kSets; ++g) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(kt + place_k(r, g * 4 + t4));
+                mma<__half>(x[j], qf[g][0], e4m3_f16x2((uint16_t)w.x), e4m3_f16x2((uint16_t)(w.x >> 16)));
+                mma<__half>(x[j], qf[g][1], e4m3_f16x2((uint16_t)w.y), e4m3_f16x2((uint16_t)(w.y >> 16)));
+                mma<__half>(x[j], qf[g][2], e4m3_f16x2((uint16_t)w.z), e4m3_f16x2((uint16_t)(w.z >> 16)));
+                mma<__half>(x[j], qf[g][3], e4m3_f16x2((uint16_t)w.w), e4m3_f16x2((uint16_t)(w.w >> 16)));
+            }
+        }
+        uint64_t there = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) there |= (uint64_t)sh.valid[slot][w] << (w * S::kCopied8);
+        float2 vs[S::kKeys8 / 8];
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < S::kKeys8 / 8; ++j) {
+            const int key = wk * S::kKeys8 + j * 8 + t4 * 2;
+            const float2 ks = *reinterpret_cast<const float2 *>(&sh.ks[slot][key]);
+            vs[j] = *reinterpret_cast<const float2 *>(&sh.vs[slot][key]);
+            const float lv[2] = {fminf(fmaxf(log2_of(vs[j].x), -80.0f), 120.0f), fminf(fmaxf(log2_of(vs[j].y), -80.0f), 120.0f)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[j][e] *= of_row[e / 2] * (e % 2 ? ks.y : ks.x);
+                if (!(there >> (key + e % 2) & 1)) x[j][e] = -INFINITY;
+                top[e / 2] = fmaxf(top[e / 2], x[j][e] + lv[e % 2]);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 1));
+            top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2));
+            const float now = fmaxf(m[half], top[half] - kLower), shift = now == -INFINITY ? 0.0f : now;
+            const float keep = pow2(m[half] - shift);
+            m[half] = now;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S::kKeys8 / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w = pow2(x[j][half * 2 + e] - shift);
+                    sum += w;
+                    x[j][half * 2 + e] = w * (e ? vs[j].y : vs[j].x);
+                }
+            l[half] = l[half] * keep + sum;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                o[d][half * 2] *= keep;
+                o[d][half * 2 + 1] *= keep;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < S::kKeys8 / 16; ++j) {
+            const uint32_t p[4] = {pack2<__half>(x[2 * j][0], x[2 * j][1]), pack2<__half>(x[2 * j][2], x[2 * j][3]),
+                                   pack2<__half>(x[2 * j + 1][0], x[2 * j + 1][1]), pack2<__half>(x[2 * j + 1][2], x[2 * j + 1][3])};
+            const int r = wk * S::kKeys8 + j * 16 + lane % 16;
+#pragma unroll
+            for (int d = 0; d < kPieces; d += 2) {
+                uint32_t y[4];
+                ldsm4t(y, vt + place_v(r, d + lane / 16));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t y0 = __byte_perm(y[2 * h], 0, 0x3120), y1 = __byte_perm(y[2 * h + 1], 0, 0x3120);
+                    mma<__half>(o[2 * (d + h)], p, e4m3_f16x2((uint16_t)y0), e4m3_f16x2((uint16_t)y1));
+                    mma<__half>(o[2 * (d + h) + 1], p, e4m3_f16x2((uint16_t)(y0 >> 16)), e4m3_f16x2((uint16_t)(y1 >> 16)));
+                }
+            }
+        }
+    }
+    copy_wait<0>();
+}
 
 // Chunk c of one (sequence, kv head, row tile): see the top of the file.
 // Scores and sums are fp32; the weights 2^(x-m) are rounded to the cache's 16
@@ -165,25 +405,46 @@ struct Shape {
 // NaN and infinities first (they would make 0 * v NaN): such a value row is
 // zeroed and added by hand to the rows that see it.  A NaN that a row does see
 // makes its sum NaN, and so its results.
-template <typename T, int D, int WR>
+//
+// Old: OldPlaces where the first places of a sequence are in 8 bits.  The
+// blocks of its first n8 chunks are theirs then (old_places() above), the others
+// take the rest as ever, and the parts are joined as if all were of a kind.
+template <typename T, int D, int WR, typename Old>
 __global__ void __launch_bounds__(128, blocks_an_sm(D))
-    k_tree_attention(TreeAttention a, int chunk, int row_tiles, bool cluster, float *part_o, float2 *part_ml) {
+    k_tree_attention(TreeAttention a, Old b, int chunk, int row_tiles, bool cluster, float *part_o, float2 *part_ml) {
     using S = Shape<D, WR>;
+    constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t valid[S::kStages][4];
     __shared__ uint64_t drafts[S::kRows];
     __shared__ float2 ml[S::kParts][S::kRows], joined[S::kRows];
     pdl_wait();
     pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;
-    const Seq sq = sequence(a, s, tid == 0 && blockIdx.x == 0 && c == 0);
+    const Seq sq = sequence(a, b, s, tid == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, S::kRows);
-    const int begin = c * chunk, end = min(sq.len, begin + chunk);
+    int n8 = 0, parts8 = 0;  // blocks of old places that the grid has, and that this sequence needs
+    bool is8 = false;
+    if constexpr (kOld) {
+        n8 = b.n8;
+        parts8 = (sq.old + b.chunk8 - 1) / b.chunk8;
+        is8 = c < n8;
+    }
+    const int parts = parts8 + (sq.len - sq.from + chunk - 1) / chunk;
+    const int begin = is8 ? c * chunk_of(b) : sq.from + (c - n8) * chunk;
+    const int end = is8 ? min(sq.old, begin + chunk_of(b)) : min(sq.len, begin + chunk);
     // a row that has no keys at all is written by its first block
-    if (rows <= 0 || (begin >= end && c > 0)) return;
-    const bool alone = sq.len <= chunk;  // the only chunk of this sequence
+    if (rows <= 0 || (begin >= end && !(c == n8 && parts == 0))) return;
+    const bool alone = parts <= 1;  // the only chunk of this sequence
+    float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    const int wr = warp % WR, wk = warp / WR, ra = wr * 16 + lane / 4;  // this lane's rows are ra and ra + 8
+    if constexpr (kOld) {
+        __shared__ OldShared<S> old;
+        if (is8) old_places<T, D, WR>(a, b, sq, old, smem, begin, end, r0, rows, kvh, o, m, l);
+    }
+    if (!is8) {
 
     // copies: each warp brings kCopied rows of a tile; lane l < kCopied keeps the place of row l
     const int tiles = (end - begin + S::kTile - 1) / S::kTile;
@@ -261,8 +522,6 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     }
 
     constexpr float kLower = std::is_same_v<T, __half> ? 10.0f : 0.0f;
-    float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    const int ra = wr * 16 + lane / 4;  // this lane's rows are ra and ra + 8
     for (int t = 0; t < tiles; ++t) {
         copy_wait<S::kStages - 2>();
         __syncthreads();
@@ -417,6 +676,7 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
         }
     }
     copy_wait<0>();
+    }
 
     // join the warps that shared out the keys, then one division
 #pragma unroll
@@ -435,10 +695,17 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
 #pragma unroll
         for (int w = 0; w < S::kParts; ++w) top = fmaxf(top, ml[w][r].x);
         const float f = top == -INFINITY ? 1.0f : pow2(m[half] - top);
+        float *to = res + (wk * S::kRows + r) * D;
+        if (kOld && is8) {  // (two fragments have the even and the odd ones of 16 values)
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<float2 *>(res + (wk * S::kRows + r) * D + d * 8 + lane % 4 * 2) =
-                make_float2(o[d][half * 2] * f, o[d][half * 2 + 1] * f);
+            for (int d = 0; d < D / 16; ++d)
+                *reinterpret_cast<float4 *>(to + d * 16 + lane % 4 * 4) =
+                    make_float4(o[2 * d][half * 2] * f, o[2 * d + 1][half * 2] * f, o[2 * d][half * 2 + 1] * f, o[2 * d + 1][half * 2 + 1] * f);
+        } else {
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+                *reinterpret_cast<float2 *>(to + d * 8 + lane % 4 * 2) = make_float2(o[d][half * 2] * f, o[d][half * 2 + 1] * f);
+        }
     }
     __syncthreads();
     auto row_of = [&](int r) { return (sq.row0 + (r0 + r) / group) * a.q_heads + kvh * group + (r0 + r) % group; };
@@ -478,22 +745,23 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     }
     if (alone || !cluster) return;
     // the blocks of the sequence's chunks share out its values: each takes its part from all of them
-    const int chunks = (sq.len + chunk - 1) / chunk;
+    const int mine = is8 ? c : parts8 + c - n8;
+    auto rank_of = [&](int o) { return o < parts8 ? o : n8 + o - parts8; };
     cluster_sync();
-    for (int i = c * 128 + tid; i < rows * (D / 4); i += chunks * 128) {
+    for (int i = mine * 128 + tid; i < rows * (D / 4); i += parts * 128) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float2 m_of[kMaxCluster];
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int o = 0; o < kMaxCluster; ++o) {
-            m_of[o] = o < chunks ? peer_load2(peer(&joined[r], o)) : make_float2(-INFINITY, 0.0f);
+            m_of[o] = o < parts ? peer_load2(peer(&joined[r], rank_of(o))) : make_float2(-INFINITY, 0.0f);
             top = fmaxf(top, m_of[o].x);
         }
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int o = 0; o < kMaxCluster; ++o) {
-            if (o >= chunks) continue;
-            const float4 y = peer_load4(peer(res + r * D + d, o));
+            if (o >= parts) continue;
+            const float4 y = peer_load4(peer(res + r * D + d, rank_of(o)));
             const float f = top == -INFINITY ? 0.0f : pow2(m_of[o].x - top);
             sum += m_of[o].y * f;
             v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
@@ -511,8 +779,8 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
 // still runs (8,191 keys of one sequence 17.0 us before that, 14.6 with it).  The
 // wide kernel cuts the committed keys alone (and takes the drafts with the last
 // chunk).  grid (ceil(q_heads * W / 8), max_tok, n_seq).
-template <typename T, int D, int W>
-__global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
+template <typename T, int D, int W, typename Old>
+__global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, Old b, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
     constexpr int kEach = D / 32;  // values of a lane, side by side
     struct alignas(kEach * 4 < 16 ? kEach * 4 : 16) Values {
         float v[kEach];
@@ -522,9 +790,14 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, b
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, w = warp % W, h = blockIdx.x * (8 / W) + warp / W, i = blockIdx.y;
     // (the parts' kernel lets this one start when what the two are given is there: only the parts have to be waited for)
-    const Seq sq = sequence(a, blockIdx.z, false);
+    const Seq sq = sequence(a, b, blockIdx.z, false);
     pdl_wait();
-    const int chunks = ((wide ? sq.ctx : sq.len) + chunk - 1) / chunk;
+    int parts8 = 0, skip = 0;  // of old places, and the grid's blocks of those that this sequence did without
+    if constexpr (std::is_same_v<Old, OldPlaces>) {
+        parts8 = (sq.old + b.chunk8 - 1) / b.chunk8;
+        skip = b.n8 - parts8;
+    }
+    const int chunks = parts8 + ((wide ? sq.ctx : sq.len) - sq.from + chunk - 1) / chunk;
     if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;  // (all warps of a row alike)
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
     Values v = {};
@@ -534,12 +807,12 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, int chunk, b
         Values y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = c0 + j * W;
+            const int c = c0 + j * W, at = c < parts8 ? c : c + skip;
             p[j] = make_float2(-INFINITY, 0.0f);
             y[j] = {};
             if (c >= chunks) continue;
-            p[j] = part_ml[c * step + row];
-            y[j] = reinterpret_cast<const Values *>(part_o + (c * step + row) * D)[lane];
+            p[j] = part_ml[at * step + row];
+            y[j] = reinterpret_cast<const Values *>(part_o + (at * step + row) * D)[lane];
         }
         float now = top;
 #pragma unroll
@@ -659,43 +932,95 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
     return p;
 }
 
+// The same where max_old places are in 8 bits and max_new behind them: a block of old places takes 12 ns a key.
+Plan plan_old(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_heads, int kv_heads, int head_dim, int *n8, int *chunk8) {
+    Plan p = {};
+    const int rows = max_tok * (q_heads / kv_heads);
+    p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    const int block_rows = 16 * p.wr;
+    p.row_tiles = (rows + block_rows - 1) / block_rows;
+    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles, slots = kSms * blocks_an_sm(head_dim);
+    const double rest = 1.6 + 0.17 * std::min(rows, block_rows);
+    auto cuts = [](int64_t keys, int64_t chunk) { return (keys + chunk - 1) / chunk; };
+    double least = 0.0;
+    for (int64_t w = 0; w <= 4; ++w) {
+        // the shortest chunk, in recent keys (each worth two old ones), with which the blocks are no more than w waves
+        const int64_t cut = std::max<int64_t>(w * slots / blocks, 1 + (max_old > 0));
+        int64_t chunk = std::max<int64_t>(64, (cuts(max_old, 2) + max_new) / cut / 64 * 64);
+        while (cuts(max_old, 2 * chunk) + cuts(max_new, chunk) > std::min<int64_t>(cut, 65535)) chunk += std::max<int64_t>(64, chunk / 1024 * 64);
+        const int64_t m8 = cuts(max_old, 2 * chunk), m = m8 + cuts(max_new, chunk);
+        const bool cluster = m > 1 && m <= kMaxCluster && blocks * m <= slots;
+        const double each = (double)chunk * 0.024 + rest;
+        double t = (double)cuts(blocks * m, slots) * each;
+        if (n_seq > 1) t += 0.5 * (double)cuts(blocks * m / 2, slots) * each;
+        t += m == 1 ? 0.0 : cluster ? 1.5 : 2.5;
+        if (w == 0 || t < least) least = t, p.chunk = (int)chunk, p.n_chunks = (int)m, p.cluster = cluster, *n8 = (int)m8, *chunk8 = (int)std::min<int64_t>(2 * chunk, CBQ_TREE_MAX_LEN);
+    }
+    return p;
+}
+
+// What the parts of the rows take, for the second kernel to join.
+size_t parts_room(const Plan &p, int64_t total_tok, int q_heads, int head_dim) {
+    if (p.n_chunks == 1 || p.cluster) return 16;
+    const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
+    return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
+}
+
 bool tiled_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
-template <typename T, int D, int WR>
-cudaError_t launch_tiled(const TreeAttention &a, const Plan &p, cudaStream_t s) {
+template <typename T, int D, int WR, typename Old>
+cudaError_t launch_tiled(const TreeAttention &a, const Old &b, const Plan &p, cudaStream_t s) {
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
     float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
     const cudaError_t e = p.wide ? launch_tree_wide(a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
-                                 : launch_clusters(k_tree_attention<T, D, WR>,
+                                 : launch_clusters(k_tree_attention<T, D, WR, Old>,
                                                    dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
-                                                   p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, p.chunk, p.row_tiles,
+                                                   p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, b, p.chunk, p.row_tiles,
                                                    p.cluster, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1 || p.cluster) return e;
     // (before its loads went together: a warp for each of 1,024 rows of 19 chunks 21.3 us a call, eight warps 20.4; of
     // 2,048 rows 28.0 and 30.2; a ragged batch of 5,000 rows of up to 12 chunks 62 and 65)
     const unsigned heads = (unsigned)a.q_heads, toks = (unsigned)a.max_tok, seqs = (unsigned)a.n_seq;
-    return p.n_chunks > 8 && rows < 2048 ? launch_dependent(k_tree_join<T, D, 8>, dim3(heads, toks, seqs), 256, 0, s, a, p.chunk, p.wide, part_o, part_ml)
-                          : launch_dependent(k_tree_join<T, D, 1>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, p.chunk, p.wide,
-                                             part_o, part_ml);
+    return p.n_chunks > 8 && rows < 2048 ? launch_dependent(k_tree_join<T, D, 8, Old>, dim3(heads, toks, seqs), 256, 0, s, a, b, p.chunk, p.wide, part_o, part_ml)
+                          : launch_dependent(k_tree_join<T, D, 1, Old>, dim3((heads + 7) / 8, toks, seqs), 256, 0, s, a, b, p.chunk,
+                                             p.wide, part_o, part_ml);
 }
 
-template <typename T, int D>
-cudaError_t launch_dim(const TreeAttention &a, const Plan &p, cudaStream_t s) {
-    return p.wr == 1 ? launch_tiled<T, D, 1>(a, p, s) : p.wr == 2 ? launch_tiled<T, D, 2>(a, p, s) : launch_tiled<T, D, 4>(a, p, s);
+template <typename T, int D, typename Old>
+cudaError_t launch_dim(const TreeAttention &a, const Old &b, const Plan &p, cudaStream_t s) {
+    return p.wr == 1 ? launch_tiled<T, D, 1>(a, b, p, s) : p.wr == 2 ? launch_tiled<T, D, 2>(a, b, p, s) : launch_tiled<T, D, 4>(a, b, p, s);
+}
+
+template <typename T, typename Old>
+cudaError_t launch_planned(const TreeAttention &a, const Old &b, const Plan &p, cudaStream_t s) {
+    if (a.c.head_dim == 64) return launch_dim<T, 64>(a, b, p, s);
+    if (a.c.head_dim == 128) return launch_dim<T, 128>(a, b, p, s);
+    return launch_dim<T, 256>(a, b, p, s);
+}
+
+template <typename T, typename Old>
+cudaError_t launch_general(const TreeAttention &a, const Old &b, cudaStream_t s) {
+    return launch_dependent(k_tree_general<T, Old>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, a, b);
+}
+
+// 16-byte copies want every row of k and v on a 16-byte boundary, 16-byte stores every row of out.
+bool whole_rows(const TreeAttention &a) {
+    const uintptr_t ends = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | reinterpret_cast<uintptr_t>(a.out);
+    return tiled_dim(a.c.head_dim) && ends % 16 == 0 && (a.c.page_stride | a.c.tok_stride | a.c.head_stride) % 8 == 0;
 }
 
 template <typename T>
 cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
-    // 16-byte copies want every row of k and v on a 16-byte boundary, 16-byte stores every row of out
-    const uintptr_t ends = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | reinterpret_cast<uintptr_t>(a.out);
-    if (tiled_dim(a.c.head_dim) && ends % 16 == 0 && (a.c.page_stride | a.c.tok_stride | a.c.head_stride) % 8 == 0) {
-        const Plan p = plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads, a.c.head_dim);
-        if (a.c.head_dim == 64) return launch_dim<T, 64>(a, p, s);
-        if (a.c.head_dim == 128) return launch_dim<T, 128>(a, p, s);
-        return launch_dim<T, 256>(a, p, s);
-    }
-    return launch_dependent(k_tree_general<T>, dim3((unsigned)a.q_heads, (unsigned)a.max_tok, (unsigned)a.n_seq), 32, 0, s, a);
+    if (!whole_rows(a)) return launch_general<T>(a, NoOldPlaces{}, s);
+    return launch_planned<T>(a, NoOldPlaces{}, plan(a.n_seq, a.max_tok, a.max_len, a.q_heads, a.c.kv_heads, a.c.head_dim), s);
+}
+
+template <typename T>
+cudaError_t launch_type(const TreeAttention &a, OldPlaces b, cudaStream_t s) {
+    const uintptr_t ends = reinterpret_cast<uintptr_t>(b.c.k) | reinterpret_cast<uintptr_t>(b.c.v);
+    if (!whole_rows(a) || ends % 16 != 0 || (b.c.page_stride | b.c.tok_stride | b.c.head_stride) % 16 != 0) return launch_general<T>(a, b, s);
+    return launch_planned<T>(a, b, plan_old(a.n_seq, a.max_tok, b.max_old, b.max_new, a.q_heads, a.c.kv_heads, a.c.head_dim, &b.n8, &b.chunk8), s);
 }
 
 }  // namespace
@@ -703,14 +1028,22 @@ cudaError_t launch_type(const TreeAttention &a, cudaStream_t s) {
 size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
                                 int head_dim) {
     if (!tiled_dim(head_dim)) return 16;
-    const Plan p = plan(n_seq, max_tok, max_len, q_heads, kv_heads, head_dim);
-    if (p.n_chunks == 1 || p.cluster) return 16;
-    const size_t rows = (size_t)total_tok * q_heads * p.n_chunks;
-    return (rows * sizeof(float2) + 15) / 16 * 16 + rows * head_dim * sizeof(float);
+    return parts_room(plan(n_seq, max_tok, max_len, q_heads, kv_heads, head_dim), total_tok, q_heads, head_dim);
+}
+
+size_t tree_attention8_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new, int q_heads,
+                                 int kv_heads, int head_dim) {
+    if (!tiled_dim(head_dim)) return 16;
+    int n8, chunk8;
+    return parts_room(plan_old(n_seq, max_tok, max_old, max_new, q_heads, kv_heads, head_dim, &n8, &chunk8), total_tok, q_heads, head_dim);
 }
 
 cudaError_t launch_tree_attention(const TreeAttention &a, cudaStream_t s) {
     return a.c.dtype == CBQ_BF16 ? launch_type<__nv_bfloat16>(a, s) : launch_type<__half>(a, s);
+}
+
+cudaError_t launch_tree_attention8(const TreeAttention &a, const OldPlaces &b, cudaStream_t s) {
+    return a.c.dtype == CBQ_BF16 ? launch_type<__nv_bfloat16>(a, b, s) : launch_type<__half>(a, b, s);
 }
 
 }  // namespace cbq

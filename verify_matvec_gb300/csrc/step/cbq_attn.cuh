@@ -16,9 +16,13 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // What a block needs to know of a sequence, with everything out of range cut.
 struct Seq {
-    int64_t row0;  // its first row of q
+    int64_t row0;   // its first row of q
     int n, ctx, len;
+    int from, old;  // places in 8 bits: [0, old); in 16: [from, len)
 };
+
+// In place of OldPlaces where there are none.
+struct NoOldPlaces {};
 
 __device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool report) {
     const int64_t room = (int64_t)a.table_width * a.c.page_size;
@@ -34,7 +38,29 @@ __device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool repo
     if (ctx < 0) ctx = 0;
     cut |= ctx + n > most;
     if (cut && report && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_LENGTH);
-    return Seq{b0, (int)n, (int)(ctx < most ? ctx : most), (int)(ctx + n < most ? ctx + n : most)};
+    return Seq{b0, (int)n, (int)(ctx < most ? ctx : most), (int)(ctx + n < most ? ctx + n : most), 0, 0};
+}
+__device__ __forceinline__ Seq sequence(const TreeAttention &a, NoOldPlaces, int s, bool report) { return sequence(a, s, report); }
+
+// The same where the first places are in 8 bits: the places that are cut off
+// those are seen nowhere, the recent ones begin behind them all the same.
+__device__ __forceinline__ Seq sequence(const TreeAttention &a, const OldPlaces &b, int s, bool report) {
+    const int64_t room = (int64_t)a.table_width * a.c.page_size, room8 = (int64_t)b.table_width * b.c.page_size;
+    const int64_t b0 = __ldcg(a.start + s), b1 = __ldcg(a.start + s + 1);
+    int64_t n = b1 - b0, ctx = __ldcg(a.ctx + s), from = __ldcg(b.old + s);
+    bool cut = n > a.max_tok || ctx < 0 || from < 0 || from > ctx || from > CBQ_TREE_MAX_LEN;
+    if (b0 < 0 || b1 > a.total_tok || n < 0) {
+        n = 0;
+        cut = true;
+    }
+    n = min(n, (int64_t)a.max_tok);
+    ctx = max(ctx, (int64_t)0);
+    from = min(max(min(from, ctx), (int64_t)0), (int64_t)CBQ_TREE_MAX_LEN);
+    const int64_t old = min(from, min(b.max_old, room8));
+    const int64_t most = max(min(min(from + b.max_new, room), (int64_t)INT32_MAX - 65536), from);
+    cut |= old < from || ctx + n > most;
+    if (cut && report && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_LENGTH);
+    return Seq{b0, (int)n, (int)min(ctx, most), (int)min(ctx + n, most), (int)from, (int)old};
 }
 
 // Bits of the drafts that row's token sees, none beyond the sequence's own.
@@ -56,6 +82,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float pow2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float log2_of(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 

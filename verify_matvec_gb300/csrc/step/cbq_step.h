@@ -54,9 +54,23 @@ struct TreeAttention {
     unsigned *err;
     int stall;  // give-up test mode: the many-row kernel's first block copies nothing
 };
+// The older places of its sequences, in 8 bits (the further arguments of
+// cbq_tree_attention8; max_len is not used then), and how they are cut: blocks
+// [0, n8) of a sequence take chunk8 old places each, the ones behind the rest.
+struct OldPlaces {
+    cbq_kv_cache8 c;
+    const int32_t *table;
+    int table_width;
+    const int32_t *old;
+    int64_t max_old, max_new;
+    int n8, chunk8;
+};
 size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_len, int q_heads, int kv_heads,
                                 int head_dim);
 cudaError_t launch_tree_attention(const TreeAttention &a, cudaStream_t s);
+size_t tree_attention8_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new, int q_heads,
+                                 int kv_heads, int head_dim);
+cudaError_t launch_tree_attention8(const TreeAttention &a, const OldPlaces &b, cudaStream_t s);
 
 // One call of the sampler (the arguments of cbq_sample).
 struct Sample {
