@@ -750,8 +750,8 @@ int cbq_moe_debug_stall(cbq_moe *L, int mode);
  * Errors: EINVAL (null handle, mode outside 0..1). */
 int cbq_debug_mmq_stall(cbq_weights *W, int mode);
 
-/* Give-up test mode of the calling thread's cbq_tree_attention calls (0 turns
- * it off): with mode 1 the first block of the many-row kernel copies no tile,
+/* Give-up test mode of the calling thread's cbq_tree_attention and
+ * cbq_tree_attention8 calls (0 turns it off): with mode 1 the first block of the many-row kernel copies no tile,
  * so its roles' bounded waits give up after 1 s (CBQ_DEVERR_PIPE_TIMEOUT in
  * *err_dev), and it frees its tensor memory and ends.  Such a call returns
  * after about a second, sets only that bit, leaves that block's rows (of the

@@ -1053,6 +1053,7 @@ int cbq_tree_attention8(const void *q_dev, int64_t q_tok_stride, int64_t q_head_
     a.lse = lse_dev;
     a.ws = ws_dev;
     a.err = err_dev;
+    a.stall = t_tree_stall;
     const cbq::OldPlaces b = {*old, table8_dev, table8_width, old_dev, max_old, max_new, 0, 0};
     CBQ_CUDA(cbq::launch_tree_attention8(a, b, as_stream(stream)));
     return CBQ_OK;

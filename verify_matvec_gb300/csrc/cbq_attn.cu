@@ -26,17 +26,6 @@ namespace cbq {
 
 namespace {
 
-// An e4m3 number (all of them are fp16 numbers too).
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint16_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-    return r;
-}
-__device__ __forceinline__ float e4m3_f32(uint8_t b) {
-    const uint32_t two = e4m3_f16x2(b);
-    return __low2float(*reinterpret_cast<const __half2 *>(&two));
-}
-
 // Any head size and any strides: one warp per (token, head), the lanes hold
 // the head's values, a key at a time.  Bound by that chain: each key's look-up,
 // row of k, five shuffles and row of v follow one another, some 0.9 us (5 drafts
@@ -192,9 +181,6 @@ struct OldShared {
     uint32_t valid[S::kStages8][4];
 };
 
-__device__ __forceinline__ int chunk_of(const OldPlaces &b) { return b.chunk8; }
-__device__ __forceinline__ int chunk_of(NoOldPlaces) { return 1; }
-
 // The old places [begin, end) of a chunk, whose keys and values are e4m3 numbers
 // and scales, into the running o, m and l of this lane's rows.
 //   x = (scale log2(e) 2^k) ks (q 2^-k).k,   w = 2^(x - m),   l += w,
@@ -294,9 +280,9 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
         }
         most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
         most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-        const int k = most > 0.0f && most < INFINITY ? max((int)(__float_as_uint(most) >> 23) - 127 - 14, -100) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-        of_row[half] = a.scale * kLog2e * __uint_as_float((uint32_t)(127 + k) << 23);
+        const int k = row_exponent(most);
+        const float down = two_to(-k);
+        of_row[half] = a.scale * kLog2e * two_to(k);
 #pragma unroll
         for (int g = 0; g < kSets; ++g)
 #pragma unroll
@@ -341,7 +327,7 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
             const int key = wk * S::kKeys8 + j * 8 + t4 * 2;
             const float2 ks = *reinterpret_cast<const float2 *>(&sh.ks[slot][key]);
             vs[j] = *reinterpret_cast<const float2 *>(&sh.vs[slot][key]);
-            const float lv[2] = {fminf(fmaxf(log2_of(vs[j].x), -80.0f), 120.0f), fminf(fmaxf(log2_of(vs[j].y), -80.0f), 120.0f)};
+            const float lv[2] = {scale_log2(vs[j].x), scale_log2(vs[j].y)};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 x[j][e] *= of_row[e / 2] * (e % 2 ? ks.y : ks.x);
@@ -425,13 +411,9 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     const int group = a.q_heads / a.c.kv_heads;
     const Seq sq = sequence(a, b, s, tid == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, S::kRows);
-    int n8 = 0, parts8 = 0;  // blocks of old places that the grid has, and that this sequence needs
-    bool is8 = false;
-    if constexpr (kOld) {
-        n8 = b.n8;
-        parts8 = (sq.old + b.chunk8 - 1) / b.chunk8;
-        is8 = c < n8;
-    }
+    // blocks of old places that the grid has, and that this sequence needs
+    const int n8 = old_blocks(b), parts8 = (sq.old + chunk_of(b) - 1) / chunk_of(b);
+    const bool is8 = kOld && c < n8;
     const int parts = parts8 + (sq.len - sq.from + chunk - 1) / chunk;
     const int begin = is8 ? c * chunk_of(b) : sq.from + (c - n8) * chunk;
     const int end = is8 ? min(sq.old, begin + chunk_of(b)) : min(sq.len, begin + chunk);
@@ -792,12 +774,10 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, Old b, int c
     // (the parts' kernel lets this one start when what the two are given is there: only the parts have to be waited for)
     const Seq sq = sequence(a, b, blockIdx.z, false);
     pdl_wait();
-    int parts8 = 0, skip = 0;  // of old places, and the grid's blocks of those that this sequence did without
-    if constexpr (std::is_same_v<Old, OldPlaces>) {
-        parts8 = (sq.old + b.chunk8 - 1) / b.chunk8;
-        skip = b.n8 - parts8;
-    }
-    const int chunks = parts8 + ((wide ? sq.ctx : sq.len) - sq.from + chunk - 1) / chunk;
+    // parts of old places, and the grid's blocks of those that this sequence did without
+    const int parts8 = (sq.old + chunk_of(b) - 1) / chunk_of(b), skip = old_blocks(b) - parts8;
+    const int recent = ((wide ? sq.ctx : sq.len) - sq.from + chunk - 1) / chunk;
+    const int chunks = parts8 + (wide ? max(recent, 1) : recent);
     if (i >= sq.n || h >= a.q_heads || chunks <= 1) return;  // (all warps of a row alike)
     const int64_t row = (sq.row0 + i) * a.q_heads + h, step = a.total_tok * a.q_heads;
     Values v = {};
@@ -936,10 +916,27 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
 Plan plan_old(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_heads, int kv_heads, int head_dim, int *n8, int *chunk8) {
     Plan p = {};
     const int rows = max_tok * (q_heads / kv_heads);
+    p.wide = wide_rows(n_seq, rows, max_old + max_new, kv_heads, head_dim);
     p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    const int block_rows = 16 * p.wr;
+    const int block_rows = p.wide ? kWideRows : 16 * p.wr;
     p.row_tiles = (rows + block_rows - 1) / block_rows;
-    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles, slots = kSms * blocks_an_sm(head_dim);
+    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
+    if (p.wide) {  // the costs of plan(), the same for a key of either kind
+        const double part_us = (double)n_seq * kv_heads * rows * head_dim * 8.0 / 5e6;
+        const int64_t most = n_seq > 1 ? std::max(2048, 32 * rows) : CBQ_TREE_MAX_LEN;  // (keys of a block, where lengths may differ)
+        double least = 0.0;
+        int64_t last = 0;
+        for (int64_t cut = 1; cut <= 64; ++cut) {
+            const int64_t chunk = std::min((max_old + max_new + cut - 1) / cut, most) / 64 * 64 + 64;
+            const int64_t m8 = (max_old + chunk - 1) / chunk, m = m8 + (max_new + chunk - 1) / chunk;
+            if (chunk == last || m > 65535) continue;
+            last = chunk;
+            const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)chunk * 0.01 + 6.0) + (m > 1 ? 3.0 + part_us * m : 0.0);
+            if (p.chunk == 0 || t < least) least = t, p.chunk = *chunk8 = (int)chunk, p.n_chunks = (int)m, *n8 = (int)m8;
+        }
+        return p;
+    }
+    const int64_t slots = kSms * blocks_an_sm(head_dim);
     const double rest = 1.6 + 0.17 * std::min(rows, block_rows);
     auto cuts = [](int64_t keys, int64_t chunk) { return (keys + chunk - 1) / chunk; };
     double least = 0.0;
@@ -973,7 +970,7 @@ cudaError_t launch_tiled(const TreeAttention &a, const Old &b, const Plan &p, cu
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
     float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
-    const cudaError_t e = p.wide ? launch_tree_wide(a, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
+    const cudaError_t e = p.wide ? launch_tree_wide(a, b, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
                                  : launch_clusters(k_tree_attention<T, D, WR, Old>,
                                                    dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
                                                    p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, b, p.chunk, p.row_tiles,

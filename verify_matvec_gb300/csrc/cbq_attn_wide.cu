@@ -43,6 +43,7 @@ namespace {
 constexpr int kGroup = 128;                   // rows of a group
 constexpr int kTile = 64;                     // keys of a tile
 constexpr int kStages = 5;
+constexpr int kOldStages = 3, kRaw = 4;       // old places: of their tiles as fp16, and as they are in memory (two a copying warp)
 constexpr int kCopyWarp = 8, kScoreWarp = 10, kSumWarp = 11, kWideThreads = 12 * 32;  // (more warps would leave 128 registers a thread)
 constexpr int kTmemCols = 512;
 
@@ -65,8 +66,22 @@ struct WideShared {
     uint32_t odd[2];                          // drafts whose values are not all finite
     uint32_t tmem_slot;
     int abort;
-    float2 ml[kGroup];
+    union {
+        float2 ml[kGroup];
+        float of_row[2 * kGroup];  // old places: each row's factor on its scores, read before ml is written
+    };
 };
+
+// Of a block of old places: the scales of a tile's keys and values, and, where
+// those are all equal, of the keys, log2 of the values', one over that, and 1.
+struct OldShared {
+    struct alignas(16) Tile {
+        float ks[kTile], vs[kTile];
+        float4 one;
+    } tile[kOldStages];
+};
+static_assert(sizeof(WideShared) + sizeof(OldShared) <= 3072, "beside the tiles no more is left");
+struct NoOldShared {};
 
 // Descriptor of a tile in shared memory with 128-byte rows, swizzled: eight
 // rows are 1024 bytes; `lead` bytes to the next 64 columns where rows are the
@@ -136,15 +151,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// log2 of a scale within a tenth, for a maximum: its bits are that, but for the
+// curve between two powers of two.
+__device__ __forceinline__ float near_log2(float v) {
+    const float bits = __uint_as_float(__float_as_uint(v) >> 8 & 0x7FFFFFu | 0x4B000000u);  // 2^23 + the exponent and 15 bits behind it
+    return fminf(fmaxf(__fmaf_rn(bits, 0x1p-15f, -256.0f - 127.0f), -80.0f), 120.0f);
+}
 // The eight warps of the two groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A place in the ring and how often it has come round (parities by its low bit).
 struct Place {
-    int slot = 0, round = 0;
+    int slot = 0, round = 0, stages = kStages;
     __device__ __forceinline__ void step(int by) {
         slot += by;
-        if (slot >= kStages) slot -= kStages, ++round;
+        if (slot >= stages) slot -= stages, ++round;
     }
 };
 
@@ -169,23 +190,159 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
     return __all_sync(~0u, wait_for(s, bar, parity, err));
 }
 
-template <typename T, int D>
+// The copying warps of a block of old places: tiles of 64 keys come in as they
+// are, two ahead a warp, and go into the ring as fp16.  A tile costs a warp some
+// 600 instructions, of which the two have 2,000 clocks each.  A lane takes 16
+// numbers a load, lanes so over rows and pieces that neither the loads (odd
+// rows' halves change places in the raw tile) nor the stores meet a conflict.
+// Tiles whose scales are all equal say so: most are, as scales are powers of two.
+template <int D>
+__device__ __forceinline__ void copy_old(const TreeAttention &a, const OldPlaces &b, WideShared &sh, OldShared &old, uint8_t *ring, int begin,
+                                         int end, int tiles, int kvh, int s, int cw, int lane) {
+    constexpr int kTileBytes = kTile * D * 2, kHalf = kTile * 128, kRawBytes = kTile * D, kPieces = D / 16;
+    uint8_t *raw = ring + kOldStages * 2 * kTileBytes + cw * (kRaw / 2) * 2 * kRawBytes;
+    const int32_t *table = b.table + (int64_t)s * b.table_width;
+    const int64_t head = kvh * b.c.head_stride, scale_head = kvh * b.c.scale_head_stride;
+    const uint32_t size = b.c.page_size, pages_on = 2 * kTile / size, tokens_on = 2 * kTile % size;
+    uint32_t entry[2], token[2];
+    int p = begin + cw * kTile + lane;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) entry[e] = (uint32_t)(p + 32 * e) / size, token[e] = (uint32_t)(p + 32 * e) % size;
+    struct Look {
+        int page[2], within[2];  // (as for the 16-bit tiles below)
+    };
+    auto look = [&]() {
+        Look l;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool key = p + 32 * e < end;
+            l.page[e] = key ? table[entry[e]] : -1;
+            l.within[e] = key ? (int)token[e] : -1;
+            entry[e] += pages_on;
+            token[e] += tokens_on;
+            if (token[e] >= size) token[e] -= size, ++entry[e];
+        }
+        p += 2 * kTile;
+        return l;
+    };
+    struct Flight {
+        uint32_t bits[2];
+        float ks[2], vs[2];
+    };
+    auto swap = [](int key) { return D > 64 ? (key & 1) * 4 : 0; };
+    auto issue = [&](const Look &now, Flight &f, uint8_t *to) {
+        int64_t at[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool good = now.within[e] >= 0 && now.page[e] >= 0 && now.page[e] < b.c.n_pages;
+            if (now.within[e] >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+            at[e] = good ? now.page[e] * b.c.page_stride + now.within[e] * b.c.tok_stride + head : 0;
+            f.bits[e] = __ballot_sync(~0u, good);
+            f.ks[e] = f.vs[e] = 0.0f;
+            if (good) {
+                const int64_t of = now.page[e] * b.c.scale_page_stride + (uint32_t)now.within[e] / (uint32_t)b.c.block * b.c.scale_block_stride + scale_head;
+                f.ks[e] = b.c.k_scale[of];
+                f.vs[e] = b.c.v_scale[of];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kTile * kPieces / 32; ++h) {
+            const int key = (h * 32 + lane) / kPieces, d = lane % kPieces;
+            const int64_t off = __shfl_sync(~0u, at[h * 32 / kPieces / 32], key % 32) + d * 16;
+            const bool good = f.bits[h * 32 / kPieces / 32] >> key % 32 & 1;
+            const uint32_t dst = smem_addr(to) + key * D + (d ^ swap(key)) * 16;
+            copy16(dst, static_cast<const char *>(b.c.k) + off, good);
+            copy16(dst + kRawBytes, static_cast<const char *>(b.c.v) + off, good);
+        }
+    };
+    Flight flight[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (cw + 2 * j < tiles) issue(look(), flight[j], raw + j * 2 * kRawBytes);
+        copy_commit();
+    }
+    Look next = look();
+    Place put;
+    put.stages = kOldStages;
+    if (cw) put.step(1);
+    // (in the give-up test mode no tile of the first block ever lands, as in the kernel)
+    bool ok = !(a.stall && (blockIdx.x | blockIdx.y | blockIdx.z) == 0);
+    for (int t0 = cw; t0 < tiles && ok; t0 += 4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = t0 + 2 * j;
+            if (t >= tiles) break;
+            copy_wait<1>();
+            __syncwarp();
+            if (t >= kOldStages) ok = warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err);
+            if (!ok) break;
+            const uint8_t *from = raw + j * 2 * kRawBytes;
+            uint8_t *to = ring + put.slot * 2 * kTileBytes;
+#pragma unroll
+            for (int i = 0; i < 2 * (D / 64) * 8; ++i) {  // keys, then values; halves of 64 columns; eight rows
+                const int of_v = i / (D / 64 * 8), half = i / 8 % (D / 64), r = i % 8 * 8 + lane / 4, d = half * 4 + lane % 4;
+                const uint4 w = *reinterpret_cast<const uint4 *>(from + of_v * kRawBytes + r * D + (d ^ swap(r)) * 16);
+                uint8_t *row = to + of_v * kTileBytes + half * kHalf + r * 128;
+                auto wide = [](uint32_t x, uint32_t y) {
+                    return make_uint4(e4m3_f16x2((uint16_t)x), e4m3_f16x2((uint16_t)(x >> 16)), e4m3_f16x2((uint16_t)y), e4m3_f16x2((uint16_t)(y >> 16)));
+                };
+                *reinterpret_cast<uint4 *>(row + ((lane % 4 * 2 ^ r) & 7) * 16) = wide(w.x, w.y);
+                *reinterpret_cast<uint4 *>(row + ((lane % 4 * 2 + 1 ^ r) & 7) * 16) = wide(w.z, w.w);
+            }
+            const Flight f = flight[j];
+            OldShared::Tile &tile = old.tile[put.slot];
+            // (that of the first key there is, for all that are not there)
+            const int lead = f.bits[0] ? __ffs(f.bits[0]) - 1 : f.bits[1] ? __ffs(f.bits[1]) - 1 : 0;
+            const float k0 = __shfl_sync(~0u, f.bits[0] ? f.ks[0] : f.ks[1], lead), v0 = __shfl_sync(~0u, f.bits[0] ? f.vs[0] : f.vs[1], lead);
+            bool same = k0 > 0.0f && v0 >= 0x1p-80f && v0 <= 0x1p112f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                tile.ks[e * 32 + lane] = f.ks[e];
+                tile.vs[e * 32 + lane] = f.vs[e];
+                same = same && (!(f.bits[e] >> lane & 1) || (f.ks[e] == k0 && f.vs[e] == v0));
+            }
+            same = __all_sync(~0u, same);
+            if (lane == 0) {
+                tile.one = make_float4(k0, log2_of(v0), 1.0f / v0, same ? 1.0f : 0.0f);
+                sh.valid[put.slot][0] = f.bits[0];
+                sh.valid[put.slot][1] = f.bits[1];
+            }
+            __syncwarp();  // (and the raw tile has been read)
+            // (the writes are handed to the tensor cores by the fence of the warp that issues the products)
+            mbar_arrive(smem_addr(&sh.full[put.slot]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.full[put.slot]));
+            if (t + 4 < tiles) {
+                issue(next, flight[j], raw + j * 2 * kRawBytes);
+                next = look();
+            }
+            copy_commit();
+            put.step(2);
+        }
+    }
+    copy_wait<0>();
+}
+
+template <typename T, int D, typename Old>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    k_tree_wide(const __grid_constant__ TreeAttention a, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
+    k_tree_wide(const __grid_constant__ TreeAttention a, const __grid_constant__ Old b, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
+    constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
     constexpr uint32_t kQHalf = kGroup * 128, kHalf = kTile * 128;  // bytes of 64 columns
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WideShared sh;
+    __shared__ std::conditional_t<kOld, OldShared, NoOldShared> old;
     pdl_wait();
     pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kWideRows, c = blockIdx.y, s = blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;
-    const Seq sq = sequence(a, s, threadIdx.x == 0 && blockIdx.x == 0 && c == 0);
+    const Seq sq = sequence(a, b, s, threadIdx.x == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, kWideRows);
-    const int begin = c * chunk, end = min(sq.ctx, begin + chunk);
-    if (rows <= 0 || (begin >= end && c > 0)) return;
-    const bool last = end == sq.ctx, alone = last && c == 0;  // with the drafts; the only chunk
+    const int n8 = old_blocks(b);
+    const bool is8 = kOld && c < n8;
+    const int begin = is8 ? c * chunk_of(b) : sq.from + (c - n8) * chunk, end = is8 ? min(sq.old, begin + chunk_of(b)) : min(sq.ctx, begin + chunk);
+    if (rows <= 0 || (begin >= end && c != n8)) return;
+    const bool last = !is8 && end == sq.ctx, alone = last && c == n8 && sq.old == 0;  // with the drafts; the only chunk
     const bool split = rows <= kGroup;  // the groups share out the key tiles
     const int old_tiles = (end - begin + kTile - 1) / kTile, tiles = old_tiles + (last ? 1 : 0);
     const int items = split ? tiles : 2 * tiles;
@@ -243,6 +400,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 v[x] = *reinterpret_cast<const uint4 *>(y);
             }
         }
+        if constexpr (kOld) {
+            if (is8) {  // as fp16, each row by its own power of two
+#pragma unroll
+                for (int x = 0; x < kAtOnce; ++x) {
+                    const int i = me + x * kOthers, r = i / (D / 8);
+                    const uint32_t two[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                    float y[8], most = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint16_t h = (uint16_t)(two[e / 2] >> e % 2 * 16);
+                        y[e] = to_f32(*reinterpret_cast<const T *>(&h));
+                        most = fmaxf(most, fabsf(y[e]));
+                    }
+#pragma unroll
+                    for (int o = D / 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));  // (a row's pieces are neighbours)
+                    const int k = row_exponent(most);
+                    const float down = two_to(-k);
+                    v[x] = make_uint4(pack2<__half>(y[0] * down, y[1] * down), pack2<__half>(y[2] * down, y[3] * down),
+                                      pack2<__half>(y[4] * down, y[5] * down), pack2<__half>(y[6] * down, y[7] * down));
+                    if (i < pieces && i % (D / 8) == 0) sh.of_row[r] = fmaxf(fabsf(a.scale) * kLog2e * two_to(k), 1e-45f);
+                }
+            }
+        }
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
             const int i = me + x * kOthers, r = i / (D / 8), d = i % (D / 8);
@@ -254,7 +434,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         asm volatile("bar.sync 2, %0;" ::"n"(kOthers) : "memory");
     }
 
-    if (copies) {
+    bool copied = false;
+    if constexpr (kOld) {
+        if (copies && is8) {
+            copy_old<D>(a, b, sh, old, smem + 2 * kQBytes, begin, end, tiles, kvh, s, warp - kCopyWarp, lane);
+            copied = true;
+        }
+    }
+    const int stages = is8 ? kOldStages : kStages;
+    if (copied) {
+    } else if (copies) {
         // copies: the two warps take tiles in turn (what a tile costs a warp is mostly waits and look-ups); lane l keeps
         // the places of keys l and l + 32
         const int cw = warp - kCopyWarp;
@@ -377,6 +566,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // item i: group i % 2, tile i (keys shared out) or i / 2
         bool ok = true;
         Place at;
+        at.stages = stages;
+        const uint32_t score_desc = is8 ? wide_idesc<__half, kTile, false>() : wide_idesc<T, kTile, false>();
+        const uint32_t sum_desc = is8 ? wide_idesc<__half, D, true>() : wide_idesc<T, D, true>();
         if (warp == kScoreWarp) {
             for (int i = 0; i < items; ++i) {
                 const int g = i & 1, n = i >> 1, b = n & 1;
@@ -395,7 +587,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
                     mma_ss(s_at, tile_desc(q + j / 4 * kQHalf + j % 4 * 32, 16), tile_desc(k_at + j / 4 * kHalf + j % 4 * 32, 16),
-                           wide_idesc<T, kTile, false>(), j > 0);
+                           score_desc, j > 0);
                 commit(sh.scored[g][b]);
                 if (split || g == 1) at.step(1);
             }
@@ -408,8 +600,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint32_t v_at = ring + (at.slot * 2 + 1) * kTileBytes, p_at = tmem + Cols<D>::s(g, n & 1);
 #pragma unroll
                 for (int j = 0; j < kTile / 16; ++j)
-                    mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2048, kHalf), wide_idesc<T, D, true>(),
-                           n > 0 || j > 0);
+                    mma_ts(tmem + Cols<D>::o(g), p_at + j * 8, tile_desc(v_at + j * 2048, kHalf), sum_desc, n > 0 || j > 0);
                 commit(sh.summed[g][n & 1]);
                 if (split || g == 1) {
                     commit(sh.empty[at.slot]);
@@ -428,7 +619,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // weights: thread = row of its group
         const int g = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-        constexpr float kLower = std::is_same_v<T, __half> ? 10.0f : 0.0f, kGrow = std::is_same_v<T, __half> ? 5.0f : 8.0f;
+        const bool half = std::is_same_v<T, __half> || is8;  // what the weights are for the product with v
+        const float kLower = half ? 10.0f : 0.0f, kGrow = half ? 5.0f : 8.0f;
         float m = -INFINITY, l = 0.0f;  // weights are 2^(x - m): m is the maximum less kLower, or up to kGrow below that
         const int row_in = (split ? 0 : g * kGroup) + r;
         const bool live = row_in < rows;
@@ -437,6 +629,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         bool ok = true;
         int n = 0;  // items of this group so far
         Place at;
+        at.stages = stages;
+        float of_row = sc;
+        if constexpr (kOld)
+            if (is8) of_row = sh.of_row[live ? row_in : 0];
         if (split && g) at.step(1);
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
@@ -451,6 +647,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if ((split ? i : i >> 1) >= old_tiles) there[0] &= (uint32_t)sees, there[1] &= (uint32_t)(sees >> 32);
             tm_wait_ld();
             if (!ok) break;
+            // old places: the scores' factors; where the scales are all equal, the row's takes theirs with it
+            bool each = false;
+            float lv = 0.0f, per_v = 1.0f, sc = of_row;
+            if constexpr (kOld) {
+                if (is8) {
+                    const float4 one = old.tile[slot].one;
+                    each = one.w == 0.0f;
+                    if (!each) {
+                        sc = fmaxf(of_row * one.x, 1e-45f), lv = one.y, per_v = one.z;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4) {
+                            const float4 ks = *reinterpret_cast<const float4 *>(&old.tile[slot].ks[j]);
+                            x[j >> 5][j & 31] = __float_as_uint(__uint_as_float(x[j >> 5][j & 31]) * ks.x);
+                            x[j >> 5][(j & 31) + 1] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 1]) * ks.y);
+                            x[j >> 5][(j & 31) + 2] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 2]) * ks.z);
+                            x[j >> 5][(j & 31) + 3] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 3]) * ks.w);
+                        }
+                    }
+                }
+            }
             if ((there[0] & there[1]) != ~0u) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -462,7 +679,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
             for (int j = 0; j < 64; j += 2)
                 top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1]));
-            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc - kLower;
+            float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc + (lv - kLower);
+            if constexpr (kOld) {
+                if (each) {  // (each key's score with its value's scale)
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&old.tile[slot].vs[j]);
+                        const float4 l = make_float4(near_log2(v.x), near_log2(v.y), near_log2(v.z), near_log2(v.w));
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1])),
+                                                    make_float2(sc, sc), make_float2(l.x, l.y));
+                        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][(j & 31) + 2]), __uint_as_float(x[j >> 5][(j & 31) + 3])),
+                                                    make_float2(sc, sc), make_float2(l.z, l.w));
+                        most = max3(max3(most, y.x, y.y), z.x, z.y);
+                    }
+                    now = most - kLower;
+                }
+            }
             const bool grown = now > m + kGrow || (m == -INFINITY && now > -INFINITY);
             const float keep = grown ? pow2(m - now) : 1.0f;
             if (grown) m = now, l *= keep;
@@ -481,18 +714,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     tm_st(lanes + Cols<D>::o(g) + d, o);
                 }
             }
-            const float less = m == -INFINITY ? 0.0f : -m;
+            const float less = m == -INFINITY ? 0.0f : lv - m;
             const float2 sc2 = make_float2(sc, sc), less2 = make_float2(less, less);
             float2 sum[2] = {};
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), sc2, less2);
-                const float2 w = make_float2(pow2(y.x), pow2(y.y));
+                float2 w = make_float2(pow2(y.x), pow2(y.y));
                 sum[j & 1] = __fadd2_rn(sum[j & 1], w);
-                p[j] = pack2<T>(w.x, w.y);
+                if constexpr (kOld)
+                    if (each) w = __fmul2_rn(w, *reinterpret_cast<const float2 *>(&old.tile[slot].vs[2 * j]));
+                p[j] = kOld && is8 ? pack2<__half>(w.x, w.y) : pack2<T>(w.x, w.y);
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * per_v;
             tm_st(s_at, p);
             tm_wait_st();
             fence_before();
@@ -639,22 +874,33 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
 }
 
-template <typename T, int D>
-cudaError_t launch_wide(const TreeAttention &a, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
+template <typename T, int D, typename Old>
+cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
     constexpr size_t kSmem = 2 * kGroup * D * 2 + kStages * 2 * kTile * D * 2;
     static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
-    return launch_dependent(k_tree_wide<T, D>, dim3((unsigned)(a.c.kv_heads * row_tiles), (unsigned)n_chunks, (unsigned)a.n_seq),
-                            kWideThreads, kSmem, s, a, chunk, row_tiles, part_o, part_ml);
+    static_assert(kOldStages * 2 + kRaw <= kStages * 2, "and so do the old places' tiles, of 16 bits and of 8");
+    return launch_dependent(k_tree_wide<T, D, Old>, dim3((unsigned)(a.c.kv_heads * row_tiles), (unsigned)n_chunks, (unsigned)a.n_seq),
+                            kWideThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
+}
+
+template <typename Old>
+cudaError_t launch_any(const TreeAttention &a, const Old &b, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
+    if (a.c.dtype == CBQ_BF16)
+        return a.c.head_dim == 64 ? launch_wide<__nv_bfloat16, 64>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
+                                  : launch_wide<__nv_bfloat16, 128>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+    return a.c.head_dim == 64 ? launch_wide<__half, 64>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
+                              : launch_wide<__half, 128>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_wide(const TreeAttention &a, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
-    if (a.c.dtype == CBQ_BF16)
-        return a.c.head_dim == 64 ? launch_wide<__nv_bfloat16, 64>(a, chunk, n_chunks, row_tiles, part_o, part_ml, s)
-                                  : launch_wide<__nv_bfloat16, 128>(a, chunk, n_chunks, row_tiles, part_o, part_ml, s);
-    return a.c.head_dim == 64 ? launch_wide<__half, 64>(a, chunk, n_chunks, row_tiles, part_o, part_ml, s)
-                              : launch_wide<__half, 128>(a, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+cudaError_t launch_tree_wide(const TreeAttention &a, NoOldPlaces b, int chunk, int n_chunks, int row_tiles, float *part_o,
+                             float2 *part_ml, cudaStream_t s) {
+    return launch_any(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+}
+cudaError_t launch_tree_wide(const TreeAttention &a, const OldPlaces &b, int chunk, int n_chunks, int row_tiles, float *part_o,
+                             float2 *part_ml, cudaStream_t s) {
+    return launch_any(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
 }
 
 }  // namespace cbq

@@ -23,6 +23,10 @@ struct Seq {
 
 // In place of OldPlaces where there are none.
 struct NoOldPlaces {};
+__device__ __forceinline__ int chunk_of(const OldPlaces &b) { return b.chunk8; }
+__device__ __forceinline__ int chunk_of(NoOldPlaces) { return 1; }
+__device__ __forceinline__ int old_blocks(const OldPlaces &b) { return b.n8; }
+__device__ __forceinline__ int old_blocks(NoOldPlaces) { return 0; }
 
 __device__ __forceinline__ Seq sequence(const TreeAttention &a, int s, bool report) {
     const int64_t room = (int64_t)a.table_width * a.c.page_size;
@@ -91,11 +95,33 @@ __device__ __forceinline__ float log2_of(float x) {
     return r;
 }
 
+// Two e4m3 numbers as fp16, which holds all of them.
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint16_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+    return r;
+}
+__device__ __forceinline__ float e4m3_f32(uint8_t b) {
+    const uint32_t two = e4m3_f16x2(b);
+    return __low2float(*reinterpret_cast<const __half2 *>(&two));
+}
+
+// The power of two 2^k by which a row of q is held smaller as fp16: its largest
+// magnitude comes to 2^14 .. 2^15.
+__device__ __forceinline__ int row_exponent(float most) {
+    return most > 0.0f && most < INFINITY ? max((int)(__float_as_uint(most) >> 23) - 127 - 14, -100) : 0;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// A scale's logarithm as the running maxima count it.
+__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(log2_of(v), -80.0f), 120.0f); }
+
 // The wide kernel (cbq_attn_wide.cu; head sizes 64 and 128): 256 rows of a kv
 // head a block, the committed keys from c * chunk on in block c, and the drafts
-// in the sequence's last.
+// in the sequence's last; with old places, those in the first b.n8 blocks.
 constexpr int kWideRows = 256;
-cudaError_t launch_tree_wide(const TreeAttention &a, int chunk, int n_chunks, int row_tiles, float *part_o,
+cudaError_t launch_tree_wide(const TreeAttention &a, NoOldPlaces b, int chunk, int n_chunks, int row_tiles, float *part_o,
+                             float2 *part_ml, cudaStream_t s);
+cudaError_t launch_tree_wide(const TreeAttention &a, const OldPlaces &b, int chunk, int n_chunks, int row_tiles, float *part_o,
                              float2 *part_ml, cudaStream_t s);
 
 }  // namespace cbq
