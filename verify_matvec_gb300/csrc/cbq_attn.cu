@@ -169,9 +169,10 @@ struct Shape {
     static constexpr int kResult = kParts * kRows * D * 4;
     static_assert(kResult <= kRing && kRows * kPitch <= 2 * kTileBytes, "what lies in the ring fits it");
     static_assert(kKeys % 16 == 0, "16 keys a product");
-    // old places: half the bytes, so twice the tiles of 64 keys in the same ring (and 64 keys of the largest head too)
-    static constexpr int kTile8 = 64, kKeys8 = kTile8 / kParts, kCopied8 = kTile8 / 4, kTileBytes8 = kTile8 * D;
-    static constexpr int kStages8 = kRing / (2 * kTileBytes8) < 6 ? kRing / (2 * kTileBytes8) : 6;
+    // old places: half the bytes, so twice the keys in the same ring
+    static constexpr int kTile8 = 2 * kTile, kKeys8 = kTile8 / kParts, kCopied8 = kTile8 / 4, kTileBytes8 = kTile8 * D;
+    static constexpr int kStages8 = kRing / (2 * kTileBytes8);
+    static_assert(kStages8 >= 3, "which is without the rows' padding");
 };
 
 // The old places' share of a block's shared memory: their scales, and which of a tile there are.
@@ -208,26 +209,34 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
     const int tiles = (end - begin + S::kTile8 - 1) / S::kTile8;
     const int32_t *table = b.table + (int64_t)s * b.table_width;
     const int64_t head = kvh * b.c.head_stride;
-    const uint32_t size = b.c.page_size;
-    auto page_of = [&](int t) {
-        const int p = begin + t * S::kTile8 + warp * S::kCopied8 + lane;
-        return lane < S::kCopied8 && p < end ? table[(uint32_t)p / size] : -1;
+    // keys are looked up in order: the next tile's key is some pages and tokens on (no divisions)
+    const uint32_t size = b.c.page_size, pages_on = S::kTile8 / size, tokens_on = S::kTile8 % size;
+    int p = begin + warp * S::kCopied8 + lane;  // this lane's row of the tile that is looked up next
+    uint32_t entry = (uint32_t)p / size, token = (uint32_t)p % size;
+    struct Look {
+        int page, within;  // the id of the key's page, and the token within (-1 where there is no such key)
+    };
+    auto look = [&] {
+        const bool key = lane < S::kCopied8 && p < end;
+        const Look l = {key ? table[entry] : -1, key ? (int)token : -1};
+        p += S::kTile8;
+        entry += pages_on;
+        token += tokens_on;
+        if (token >= size) token -= size, ++entry;
+        return l;
     };
     // Pieces of a row are permuted by the row: keys so that two rows of four pieces meet no bank conflict, values so that
     // eight rows of one piece meet none.
     auto place_k = [](int r, int d) { return r * D + (D > 64 ? d ^ (r & 1) * 4 : d) * 16; };
     auto place_v = [](int r, int d) { return r * D + (D > 64 ? d ^ (r & 7) : d ^ (r >> 1 & 3)) * 16; };
-    auto fetch = [&](int t, int page) {
-        const int slot = t % S::kStages8;
-        const uint32_t p = begin + t * S::kTile8 + warp * S::kCopied8 + lane;
-        const bool in = lane < S::kCopied8 && p < (uint32_t)end, good = in && page >= 0 && page < b.c.n_pages;
+    auto fetch = [&](int slot, const Look &now) {
+        const bool in = now.within >= 0, good = in && now.page >= 0 && now.page < b.c.n_pages;
         if (in && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-        const uint32_t within = p % size;
-        const int64_t at = good ? page * b.c.page_stride + (int64_t)within * b.c.tok_stride + head : -1;
+        const int64_t at = good ? now.page * b.c.page_stride + now.within * b.c.tok_stride + head : -1;
         const uint32_t bits = __ballot_sync(~0u, good);
         if (lane == 0) sh.valid[slot][warp] = bits;
         if (lane < S::kCopied8) {
-            const int64_t of = good ? page * b.c.scale_page_stride + (int64_t)(within / (uint32_t)b.c.block) * b.c.scale_block_stride +
+            const int64_t of = good ? now.page * b.c.scale_page_stride + (uint32_t)now.within / (uint32_t)b.c.block * b.c.scale_block_stride +
                                           kvh * b.c.scale_head_stride : 0;
             copy4(smem_addr(&sh.ks[slot][warp * S::kCopied8 + lane]), b.c.k_scale + of, good);
             copy4(smem_addr(&sh.vs[slot][warp * S::kCopied8 + lane]), b.c.v_scale + of, good);
@@ -242,11 +251,11 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
         }
     };
     static_assert(S::kCopied8 * kPieces % 32 == 0, "whole warps of copies");
-    int page = page_of(0);
+    Look next = look();
 #pragma unroll
     for (int t = 0; t < S::kStages8 - 1; ++t) {
-        const int now = page;
-        page = t + 1 < tiles ? page_of(t + 1) : -1;
+        const Look now = next;
+        next = look();
         if (t < tiles) fetch(t, now);
         copy_commit();
     }
@@ -295,12 +304,12 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
     for (int t = 0; t < tiles; ++t) {
         copy_wait<S::kStages8 - 2>();
         __syncthreads();
+        const int slot = t % S::kStages8;
         if (t + S::kStages8 - 1 < tiles) {
-            fetch(t + S::kStages8 - 1, page);
-            if (t + S::kStages8 < tiles) page = page_of(t + S::kStages8);
+            fetch(slot ? slot - 1 : S::kStages8 - 1, next);
+            next = look();
         }
         copy_commit();
-        const int slot = t % S::kStages8;
         const uint8_t *kt = smem + slot * 2 * S::kTileBytes8;
         const uint32_t vt = smem_addr(kt) + S::kTileBytes8;
 
@@ -317,9 +326,11 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
                 mma<__half>(x[j], qf[g][3], e4m3_f16x2((uint16_t)w.w), e4m3_f16x2((uint16_t)(w.w >> 16)));
             }
         }
-        uint64_t there = 0;
+        // of this warp's keys, those that there are
+        constexpr uint32_t kAll = S::kCopied8 == 32 ? ~0u : (1u << S::kCopied8) - 1;
+        uint32_t there = kAll;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) there |= (uint64_t)sh.valid[slot][w] << (w * S::kCopied8);
+        for (int w = 0; w < S::kKeys8 / S::kCopied8; ++w) there &= sh.valid[slot][wk * (S::kKeys8 / S::kCopied8) + w];
         float2 vs[S::kKeys8 / 8];
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -331,7 +342,7 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 x[j][e] *= of_row[e / 2] * (e % 2 ? ks.y : ks.x);
-                if (!(there >> (key + e % 2) & 1)) x[j][e] = -INFINITY;
+                if (there != kAll && !(sh.valid[slot][key / S::kCopied8] >> ((key + e % 2) % S::kCopied8) & 1)) x[j][e] = -INFINITY;
                 top[e / 2] = fmaxf(top[e / 2], x[j][e] + lv[e % 2]);
             }
         }
@@ -912,7 +923,10 @@ Plan plan(int n_seq, int max_tok, int64_t max_len, int q_heads, int kv_heads, in
     return p;
 }
 
-// The same where max_old places are in 8 bits and max_new behind them: a block of old places takes 12 ns a key.
+// The same where max_old places are in 8 bits and max_new behind them.  Blocks
+// of either kind run beside one another: the recent places' fill what the old
+// places' waves leave free.  A block of old places takes 12 ns a key (the wide
+// kernel 10 as ever), and chunks of recent places are no longer to a block.
 Plan plan_old(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_heads, int kv_heads, int head_dim, int *n8, int *chunk8) {
     Plan p = {};
     const int rows = max_tok * (q_heads / kv_heads);
@@ -920,38 +934,41 @@ Plan plan_old(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_he
     p.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     const int block_rows = p.wide ? kWideRows : 16 * p.wr;
     p.row_tiles = (rows + block_rows - 1) / block_rows;
-    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles;
-    if (p.wide) {  // the costs of plan(), the same for a key of either kind
-        const double part_us = (double)n_seq * kv_heads * rows * head_dim * 8.0 / 5e6;
-        const int64_t most = n_seq > 1 ? std::max(2048, 32 * rows) : CBQ_TREE_MAX_LEN;  // (keys of a block, where lengths may differ)
-        double least = 0.0;
-        int64_t last = 0;
-        for (int64_t cut = 1; cut <= 64; ++cut) {
-            const int64_t chunk = std::min((max_old + max_new + cut - 1) / cut, most) / 64 * 64 + 64;
-            const int64_t m8 = (max_old + chunk - 1) / chunk, m = m8 + (max_new + chunk - 1) / chunk;
-            if (chunk == last || m > 65535) continue;
-            last = chunk;
-            const double t = (double)((blocks * m + kSms - 1) / kSms) * ((double)chunk * 0.01 + 6.0) + (m > 1 ? 3.0 + part_us * m : 0.0);
-            if (p.chunk == 0 || t < least) least = t, p.chunk = *chunk8 = (int)chunk, p.n_chunks = (int)m, *n8 = (int)m8;
-        }
-        return p;
-    }
-    const int64_t slots = kSms * blocks_an_sm(head_dim);
-    const double rest = 1.6 + 0.17 * std::min(rows, block_rows);
+    const int64_t blocks = (int64_t)n_seq * kv_heads * p.row_tiles, slots = p.wide ? kSms : kSms * blocks_an_sm(head_dim);
+    const double old_us = p.wide ? 0.010 : 0.012, new_us = p.wide ? 0.010 : 0.024, rest = p.wide ? 6.0 : 1.6 + 0.17 * std::min(rows, block_rows);
+    const double part_us = p.wide ? (double)n_seq * kv_heads * rows * head_dim * 8.0 / 5e6 : 0.0;
     auto cuts = [](int64_t keys, int64_t chunk) { return (keys + chunk - 1) / chunk; };
+    auto up64 = [](int64_t keys) { return (keys + 63) / 64 * 64; };
+    // several sequences may differ in length: no block takes much longer than others
+    const int64_t most = n_seq > 1 && p.wide ? std::max(2048, 32 * rows) : CBQ_TREE_MAX_LEN;
     double least = 0.0;
-    for (int64_t w = 0; w <= 4; ++w) {
-        // the shortest chunk, in recent keys (each worth two old ones), with which the blocks are no more than w waves
-        const int64_t cut = std::max<int64_t>(w * slots / blocks, 1 + (max_old > 0));
-        int64_t chunk = std::max<int64_t>(64, (cuts(max_old, 2) + max_new) / cut / 64 * 64);
-        while (cuts(max_old, 2 * chunk) + cuts(max_new, chunk) > std::min<int64_t>(cut, 65535)) chunk += std::max<int64_t>(64, chunk / 1024 * 64);
-        const int64_t m8 = cuts(max_old, 2 * chunk), m = m8 + cuts(max_new, chunk);
-        const bool cluster = m > 1 && m <= kMaxCluster && blocks * m <= slots;
-        const double each = (double)chunk * 0.024 + rest;
-        double t = (double)cuts(blocks * m, slots) * each;
-        if (n_seq > 1) t += 0.5 * (double)cuts(blocks * m / 2, slots) * each;
-        t += m == 1 ? 0.0 : cluster ? 1.5 : 2.5;
-        if (w == 0 || t < least) least = t, p.chunk = (int)chunk, p.n_chunks = (int)m, p.cluster = cluster, *n8 = (int)m8, *chunk8 = (int)std::min<int64_t>(2 * chunk, CBQ_TREE_MAX_LEN);
+    int64_t last = -1;
+    auto look = [&](int64_t m) {  // old places in m chunks
+        const int64_t c8 = max_old == 0 ? 64 : std::max<int64_t>(up64(std::min(cuts(max_old, std::max<int64_t>(m, 1)), most)), up64(cuts(max_old, 16384)));
+        const int64_t m8 = cuts(max_old, c8);
+        if (m8 == last) return;
+        last = m8;
+        int64_t c16 = max_old == 0 ? up64(cuts(max_new, std::max<int64_t>(m, 1))) : up64((int64_t)(c8 * old_us / new_us));
+        c16 = std::max(std::min(c16, up64(max_new)), up64(cuts(max_new, 16384)));
+        const int64_t m16 = cuts(max_new, c16), n = m8 + m16;
+        const bool cluster = !p.wide && n > 1 && n <= kMaxCluster && blocks * n <= slots;
+        const double t8 = c8 * old_us + rest, t16 = c16 * new_us + rest;
+        auto span = [&](int64_t b8, int64_t b16) {
+            const int64_t waves = cuts(b8, slots);
+            const double idle = (double)(waves * slots - b8) * t8, work = (double)b16 * t16;
+            return std::max(waves * t8 + std::max(work - idle, 0.0) / (double)slots, b8 ? t8 : cuts(b16, slots) * t16);
+        };
+        double t = span(blocks * m8, blocks * m16);
+        if (n_seq > 1) t += 0.5 * span((blocks * m8 + 1) / 2, (blocks * m16 + 1) / 2);
+        t += n == 1 ? 0.0 : cluster ? 1.5 : p.wide ? 3.0 + part_us * n : 2.5;
+        if (p.chunk && t >= least) return;
+        least = t, p.chunk = (int)c16, p.n_chunks = (int)n, p.cluster = cluster;
+        *n8 = (int)m8, *chunk8 = (int)std::min<int64_t>(c8, CBQ_TREE_MAX_LEN);
+    };
+    for (int64_t m = 1; m < kMaxCluster; ++m) look(m);
+    for (int64_t w = 1; w <= 4; ++w) {
+        look((w * slots - blocks) / blocks);
+        look(w * slots / blocks);
     }
     return p;
 }

@@ -43,8 +43,18 @@ namespace {
 constexpr int kGroup = 128;                   // rows of a group
 constexpr int kTile = 64;                     // keys of a tile
 constexpr int kStages = 5;
-constexpr int kOldStages = 3, kRaw = 4;       // old places: of their tiles as fp16, and as they are in memory (two a copying warp)
-constexpr int kCopyWarp = 8, kScoreWarp = 10, kSumWarp = 11, kWideThreads = 12 * 32;  // (more warps would leave 128 registers a thread)
+constexpr int kOldStages = 3, kRaw = 4;       // old places: of their tiles as fp16, and as they are in memory
+constexpr int kCopyWarp = 8;                  // behind the weights' warps
+// The other roles.  With old places four more warps turn their tiles into fp16,
+// and the registers that a block of 16 warps is launched with (128 a thread) are
+// shared out: 168 to the weights' warps, 88 to the others (256 * 168 + 256 * 88 =
+// 512 * 128).
+template <bool kOld>
+struct Roles {
+    static constexpr int kScoreWarp = kOld ? 12 : 10, kSumWarp = kScoreWarp + 1, kCopy = kOld ? 14 : kCopyWarp;  // (two copy)
+    static constexpr int kThreads = kOld ? 512 : 384;             // (without: more warps would leave 128 registers a thread)
+    static constexpr int kOthers = (kCopyWarp + 2) * 32;          // threads of the weights' and the products' warps
+};
 constexpr int kTmemCols = 512;
 
 // Columns of tensor memory: a group's scores, two items' (the weights of an
@@ -62,6 +72,7 @@ struct WideShared {
     // warp of a group may be at the next item while another is still at this one.
     uint64_t scored[2][2], weighed[2][2], summed[2][2];
     uint64_t done[2];
+    uint64_t raw_full[kRaw], raw_empty[kRaw]; // old places: a tile has come in as it is; it has been read
     uint32_t valid[kStages][2];               // keys of a tile that exist
     uint32_t odd[2];                          // drafts whose values are not all finite
     uint32_t tmem_slot;
@@ -72,12 +83,12 @@ struct WideShared {
     };
 };
 
-// Of a block of old places: the scales of a tile's keys and values, and, where
-// those are all equal, of the keys, log2 of the values', one over that, and 1.
+// Of a tile of old places: the scales of its keys and values, if a copying warp
+// says that some of its keys' are not the chunk's.
 struct OldShared {
     struct alignas(16) Tile {
         float ks[kTile], vs[kTile];
-        float4 one;
+        uint8_t odd[4];
     } tile[kOldStages];
 };
 static_assert(sizeof(WideShared) + sizeof(OldShared) <= 3072, "beside the tiles no more is left");
@@ -157,6 +168,22 @@ __device__ __forceinline__ float near_log2(float v) {
     const float bits = __uint_as_float(__float_as_uint(v) >> 8 & 0x7FFFFFu | 0x4B000000u);  // 2^23 + the exponent and 15 bits behind it
     return fminf(fmaxf(__fmaf_rn(bits, 0x1p-15f, -256.0f - 127.0f), -80.0f), 120.0f);
 }
+// The weights 2^(x sc + less) of 64 scores, as numbers of P for the product with
+// v (kEach: each by its scale first), and their sum.
+template <typename P, bool kEach>
+__device__ __forceinline__ float weigh(const uint32_t (&x)[2][32], float sc, float less, const float *vs, uint32_t (&p)[32]) {
+    const float2 sc2 = make_float2(sc, sc), less2 = make_float2(less, less);
+    float2 sum[2] = {};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), sc2, less2);
+        float2 w = make_float2(pow2(y.x), pow2(y.y));
+        sum[j & 1] = __fadd2_rn(sum[j & 1], w);
+        if constexpr (kEach) w = __fmul2_rn(w, *reinterpret_cast<const float2 *>(vs + 2 * j));
+        p[j] = pack2<P>(w.x, w.y);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
 // The eight warps of the two groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -190,142 +217,229 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
     return __all_sync(~0u, wait_for(s, bar, parity, err));
 }
 
-// The copying warps of a block of old places: tiles of 64 keys come in as they
-// are, two ahead a warp, and go into the ring as fp16.  A tile costs a warp some
-// 600 instructions, of which the two have 2,000 clocks each.  A lane takes 16
-// numbers a load, lanes so over rows and pieces that neither the loads (odd
-// rows' halves change places in the raw tile) nor the stores meet a conflict.
-// Tiles whose scales are all equal say so: most are, as scales are powers of two.
-template <int D>
-__device__ __forceinline__ void copy_old(const TreeAttention &a, const OldPlaces &b, WideShared &sh, OldShared &old, uint8_t *ring, int begin,
-                                         int end, int tiles, int kvh, int s, int cw, int lane) {
-    constexpr int kTileBytes = kTile * D * 2, kHalf = kTile * 128, kRawBytes = kTile * D, kPieces = D / 16;
-    uint8_t *raw = ring + kOldStages * 2 * kTileBytes + cw * (kRaw / 2) * 2 * kRawBytes;
-    const int32_t *table = b.table + (int64_t)s * b.table_width;
-    const int64_t head = kvh * b.c.head_stride, scale_head = kvh * b.c.scale_head_stride;
-    const uint32_t size = b.c.page_size, pages_on = 2 * kTile / size, tokens_on = 2 * kTile % size;
-    uint32_t entry[2], token[2];
-    int p = begin + cw * kTile + lane;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) entry[e] = (uint32_t)(p + 32 * e) / size, token[e] = (uint32_t)(p + 32 * e) % size;
-    struct Look {
-        int page[2], within[2];  // (as for the 16-bit tiles below)
-    };
-    auto look = [&]() {
-        Look l;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const bool key = p + 32 * e < end;
-            l.page[e] = key ? table[entry[e]] : -1;
-            l.within[e] = key ? (int)token[e] : -1;
-            entry[e] += pages_on;
-            token[e] += tokens_on;
-            if (token[e] >= size) token[e] -= size, ++entry[e];
-        }
-        p += 2 * kTile;
-        return l;
-    };
-    struct Flight {
-        uint32_t bits[2];
-        float ks[2], vs[2];
-    };
-    auto swap = [](int key) { return D > 64 ? (key & 1) * 4 : 0; };
-    auto issue = [&](const Look &now, Flight &f, uint8_t *to) {
-        int64_t at[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const bool good = now.within[e] >= 0 && now.page[e] >= 0 && now.page[e] < b.c.n_pages;
-            if (now.within[e] >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
-            at[e] = good ? now.page[e] * b.c.page_stride + now.within[e] * b.c.tok_stride + head : 0;
-            f.bits[e] = __ballot_sync(~0u, good);
-            f.ks[e] = f.vs[e] = 0.0f;
-            if (good) {
-                const int64_t of = now.page[e] * b.c.scale_page_stride + (uint32_t)now.within[e] / (uint32_t)b.c.block * b.c.scale_block_stride + scale_head;
-                f.ks[e] = b.c.k_scale[of];
-                f.vs[e] = b.c.v_scale[of];
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < kTile * kPieces / 32; ++h) {
-            const int key = (h * 32 + lane) / kPieces, d = lane % kPieces;
-            const int64_t off = __shfl_sync(~0u, at[h * 32 / kPieces / 32], key % 32) + d * 16;
-            const bool good = f.bits[h * 32 / kPieces / 32] >> key % 32 & 1;
-            const uint32_t dst = smem_addr(to) + key * D + (d ^ swap(key)) * 16;
-            copy16(dst, static_cast<const char *>(b.c.k) + off, good);
-            copy16(dst + kRawBytes, static_cast<const char *>(b.c.v) + off, good);
-        }
-    };
-    Flight flight[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (cw + 2 * j < tiles) issue(look(), flight[j], raw + j * 2 * kRawBytes);
-        copy_commit();
+// A chunk's scales: those of its first key stand for all, as long as what a
+// key's are more or less can go into its numbers: powers of two from 2^-15 (an
+// e4m3 number has its last bit at 2^-9 or above, an fp16 number at 2^-24) to 2^7
+// (448 * 2^7 < 65504).  A key that this does not hold for keeps its own, and the
+// weights' warps look at every key of its tile, which costs them as much again
+// as the weights themselves.
+struct ChunkScales {
+    float k, v;
+};
+__device__ __forceinline__ ChunkScales chunk_scales(const OldPlaces &b, int s, int kvh, int begin) {
+    const int64_t page = b.table[(int64_t)s * b.table_width + begin / b.c.page_size];
+    ChunkScales r = {1.0f, 1.0f};
+    if (page >= 0 && page < b.c.n_pages) {
+        const int64_t of = page * b.c.scale_page_stride + begin % b.c.page_size / b.c.block * b.c.scale_block_stride + kvh * b.c.scale_head_stride;
+        const float k = b.c.k_scale[of], v = b.c.v_scale[of];
+        if (k >= 0x1p-80f && k <= 0x1p112f && v >= 0x1p-80f && v <= 0x1p112f) r = {k, v};
     }
-    Look next = look();
-    Place put;
-    put.stages = kOldStages;
-    if (cw) put.step(1);
-    // (in the give-up test mode no tile of the first block ever lands, as in the kernel)
-    bool ok = !(a.stall && (blockIdx.x | blockIdx.y | blockIdx.z) == 0);
-    for (int t0 = cw; t0 < tiles && ok; t0 += 4) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = t0 + 2 * j;
-            if (t >= tiles) break;
-            copy_wait<1>();
-            __syncwarp();
-            if (t >= kOldStages) ok = warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err);
-            if (!ok) break;
-            const uint8_t *from = raw + j * 2 * kRawBytes;
-            uint8_t *to = ring + put.slot * 2 * kTileBytes;
-#pragma unroll
-            for (int i = 0; i < 2 * (D / 64) * 8; ++i) {  // keys, then values; halves of 64 columns; eight rows
-                const int of_v = i / (D / 64 * 8), half = i / 8 % (D / 64), r = i % 8 * 8 + lane / 4, d = half * 4 + lane % 4;
-                const uint4 w = *reinterpret_cast<const uint4 *>(from + of_v * kRawBytes + r * D + (d ^ swap(r)) * 16);
-                uint8_t *row = to + of_v * kTileBytes + half * kHalf + r * 128;
-                auto wide = [](uint32_t x, uint32_t y) {
-                    return make_uint4(e4m3_f16x2((uint16_t)x), e4m3_f16x2((uint16_t)(x >> 16)), e4m3_f16x2((uint16_t)y), e4m3_f16x2((uint16_t)(y >> 16)));
-                };
-                *reinterpret_cast<uint4 *>(row + ((lane % 4 * 2 ^ r) & 7) * 16) = wide(w.x, w.y);
-                *reinterpret_cast<uint4 *>(row + ((lane % 4 * 2 + 1 ^ r) & 7) * 16) = wide(w.z, w.w);
-            }
-            const Flight f = flight[j];
-            OldShared::Tile &tile = old.tile[put.slot];
-            // (that of the first key there is, for all that are not there)
-            const int lead = f.bits[0] ? __ffs(f.bits[0]) - 1 : f.bits[1] ? __ffs(f.bits[1]) - 1 : 0;
-            const float k0 = __shfl_sync(~0u, f.bits[0] ? f.ks[0] : f.ks[1], lead), v0 = __shfl_sync(~0u, f.bits[0] ? f.vs[0] : f.vs[1], lead);
-            bool same = k0 > 0.0f && v0 >= 0x1p-80f && v0 <= 0x1p112f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                tile.ks[e * 32 + lane] = f.ks[e];
-                tile.vs[e * 32 + lane] = f.vs[e];
-                same = same && (!(f.bits[e] >> lane & 1) || (f.ks[e] == k0 && f.vs[e] == v0));
-            }
-            same = __all_sync(~0u, same);
-            if (lane == 0) {
-                tile.one = make_float4(k0, log2_of(v0), 1.0f / v0, same ? 1.0f : 0.0f);
-                sh.valid[put.slot][0] = f.bits[0];
-                sh.valid[put.slot][1] = f.bits[1];
-            }
-            __syncwarp();  // (and the raw tile has been read)
-            // (the writes are handed to the tensor cores by the fence of the warp that issues the products)
-            mbar_arrive(smem_addr(&sh.full[put.slot]));
-            if (lane == 0) mbar_arrive(smem_addr(&sh.full[put.slot]));
-            if (t + 4 < tiles) {
-                issue(next, flight[j], raw + j * 2 * kRawBytes);
-                next = look();
-            }
-            copy_commit();
-            put.step(2);
-        }
-    }
-    copy_wait<0>();
+    return r;
 }
 
+// A block of old places, copying and widening: the two copying warps bring its
+// tiles in as they are, in turn and up to four ahead; each of four more takes 16
+// keys of every tile into the ring as fp16, 16 numbers a load, of rows and halves
+// so that neither the loads nor the stores meet a conflict.  The copies are 32 a
+// tile, of four keys' lines each, and take the SM some 40 clocks apiece, whoever
+// issues them (and bulk copies of a row each 64): 1,300 clocks a tile, beside
+// which the other 1,000 go on.  (Four warps that did both, and so all did the
+// same at a time, took 2,500 a tile.)
+// kWhole: pages and blocks are multiples of 16 tokens, so the 16 keys have one
+// page and one pair of scales.
+template <int D, bool kWhole>
+struct OldTiles {
+    static constexpr int kTileBytes = kTile * D * 2, kHalf = kTile * 128, kRawBytes = kTile * D, kPieces = D / 16, kRows = 16;
+    const TreeAttention &a;
+    const OldPlaces &b;
+    WideShared &sh;
+    OldShared &old;
+    uint8_t *ring;
+    int lane, w;  // which of the warps of its role
+    int begin, end, tiles, kvh, s;
+
+    __device__ __forceinline__ uint8_t *raw(int slot) const { return ring + kOldStages * 2 * kTileBytes + slot * 2 * kRawBytes; }
+
+    // Keys are looked up in order: the next tile's key is some pages and tokens on (no divisions).
+    struct Keys {
+        uint32_t entry, token;
+        int p;
+    };
+    struct Look {
+        int page, within;  // the id of a key's page, and the token within (-1 where there is no such key)
+        int left;          // keys from this one on
+    };
+    __device__ __forceinline__ Keys keys_from(int p) const { return Keys{(uint32_t)p / (uint32_t)b.c.page_size, (uint32_t)p % (uint32_t)b.c.page_size, p}; }
+    __device__ __forceinline__ Look look(Keys &k, uint32_t pages_on, uint32_t tokens_on, int on, bool any) const {
+        const bool key = any && k.p < end;
+        const Look l = {key ? b.table[(int64_t)s * b.table_width + k.entry] : -1, key ? (int)k.token : -1, end - k.p};
+        k.entry += pages_on;
+        k.token += tokens_on;
+        if (k.token >= (uint32_t)b.c.page_size) k.token -= b.c.page_size, ++k.entry;
+        k.p += on;
+        return l;
+    }
+    __device__ __forceinline__ bool is_there(const Look &l) const { return l.within >= 0 && l.page >= 0 && l.page < b.c.n_pages; }
+
+    __device__ __forceinline__ void copy() const {
+        const uint32_t size = b.c.page_size, pages_on = 2 * kTile / size, tokens_on = 2 * kTile % size;
+        const int64_t head = kvh * b.c.head_stride;
+        Keys keys[2] = {keys_from(begin + w * kTile + lane), keys_from(begin + w * kTile + lane + 32)};  // this lane's
+        Look next[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) next[e] = look(keys[e], pages_on, tokens_on, 2 * kTile, true);
+        constexpr int kKeys = 32 / kPieces;  // lane l copies piece l % kPieces of keys l / kPieces, and so many on
+        const uint32_t dst0 = smem_addr(raw(0)) + lane * 16;
+        const char *from = static_cast<const char *>(b.c.k) + lane % kPieces * 16;
+        const int64_t to_v = static_cast<const char *>(b.c.v) - static_cast<const char *>(b.c.k);
+        // (in the give-up test mode no tile of the first block ever lands, and every role's wait for it runs out)
+        bool ok = !(a.stall && (blockIdx.x | blockIdx.y | blockIdx.z) == 0);
+        for (int t = w; t < tiles && ok; t += 2) {
+            int64_t at[2];
+            uint32_t bits[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const Look now = next[e];
+                next[e] = look(keys[e], pages_on, tokens_on, 2 * kTile, true);
+                const bool good = is_there(now);
+                if (now.within >= 0 && !good && a.err) atomicOr(a.err, CBQ_DEVERR_BAD_SLOT);
+                at[e] = good ? now.page * b.c.page_stride + now.within * b.c.tok_stride + head : 0;
+                bits[e] = __ballot_sync(~0u, good);
+            }
+            const int slot = t % kRaw;
+            if (t >= kRaw) ok = warp_wait(sh, sh.raw_empty[slot], (t / kRaw - 1) & 1, a.err);
+            if (!ok) break;
+            const uint32_t dst = dst0 + slot * 2 * kRawBytes;
+#pragma unroll
+            for (int h0 = 0; h0 < kTile / kKeys; h0 += 8) {
+                const char *src[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) src[i] = from + __shfl_sync(~0u, at[(h0 + i) * kKeys / 32], (h0 + i) * kKeys % 32 + lane / kPieces);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int h = h0 + i;
+                    const bool there = bits[h * kKeys / 32] >> (h * kKeys % 32 + lane / kPieces) & 1;
+                    copy16(dst + h * kKeys * D, src[i], there);
+                    copy16(dst + h * kKeys * D + kRawBytes, src[i] + to_v, there);
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.raw_full[slot])) : "memory");
+        }
+        copy_commit();
+        copy_wait<0>();
+    }
+
+    // This warp's rows of a tile as it is to those of a tile as fp16; kCareful: rows that are not there become zeros, the
+    // others are multiplied by what their scales are of the chunk's (two fp16 numbers of the same; of row l in lane l).
+    template <bool kCareful>
+    __device__ __forceinline__ void turn(const uint8_t *from, uint8_t *to, uint32_t bits, const uint32_t (&part)[2]) const {
+        constexpr int kSets = 2 * (D / 64);  // keys and values; the halves of their columns
+        const int r0 = w * kRows + lane / 4, odd = lane / 4 & 1;
+        uint4 x[kSets][2];
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)  // (odd rows the other half first)
+                x[k][i] = *reinterpret_cast<const uint4 *>(from + k / (D / 64) * kRawBytes + (r0 + i * 8) * D + (D > 64 ? (k % 2 ^ odd) * 64 : 0) + lane % 4 * 16);
+        const int p0 = (lane % 4 * 2 ^ lane / 4) * 16;  // (rows eight apart have their pieces in the same order)
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+            const int of_v = k / (D / 64), half = D > 64 ? k % 2 ^ odd : 0;
+            uint8_t *out = to + of_v * kTileBytes + half * kHalf + r0 * 128;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t y[8];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t two = c == 0 ? x[k][i].x : c == 1 ? x[k][i].y : c == 2 ? x[k][i].z : x[k][i].w;
+                    if (kCareful && !(bits >> (i * 8 + lane / 4) & 1)) two = 0;
+                    y[2 * c] = e4m3_f16x2((uint16_t)two);
+                    y[2 * c + 1] = e4m3_f16x2((uint16_t)(two >> 16));
+                }
+                if constexpr (kCareful) {
+                    const uint32_t f = kWhole ? part[of_v] : __shfl_sync(~0u, part[of_v], i * 8 + lane / 4);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[c]), *reinterpret_cast<const __half2 *>(&f));
+                        y[c] = *reinterpret_cast<const uint32_t *>(&z);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(out + i * 1024 + p0) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(out + i * 1024 + (p0 ^ 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void widen(ChunkScales of_chunk) const {
+        const uint32_t size = b.c.page_size, pages_on = kTile / size, tokens_on = kTile % size;
+        const int64_t scale_head = kvh * b.c.scale_head_stride;
+        const float per_k = 1.0f / of_chunk.k, per_v = 1.0f / of_chunk.v;
+        const bool chunk_power = ((__float_as_uint(of_chunk.k) | __float_as_uint(of_chunk.v)) & 0x7FFFFFu) == 0;
+        Keys keys = keys_from(begin + w * kRows + (kWhole ? 0 : lane));  // the warp's first, or this lane's (of 16)
+        auto look_on = [&] { return look(keys, pages_on, tokens_on, kTile, kWhole || lane < kRows); };
+        struct Ahead {
+            uint32_t bits;
+            float ks, vs;
+        };
+        auto ask = [&](const Look &now) {
+            const bool good = is_there(now);
+            Ahead f = {kWhole ? (good ? 0xFFFFu >> max(kRows - now.left, 0) : 0) : __ballot_sync(~0u, good), of_chunk.k, of_chunk.v};
+            if (good) {
+                const int64_t of = now.page * b.c.scale_page_stride + (uint32_t)now.within / (uint32_t)b.c.block * b.c.scale_block_stride + scale_head;
+                f.ks = b.c.k_scale[of];
+                f.vs = b.c.v_scale[of];
+            }
+            return f;
+        };
+        Ahead next = ask(look_on());
+        Look after = look_on();
+        Place put;
+        put.stages = kOldStages;
+        for (int t = 0; t < tiles; ++t, put.step(1)) {
+            const Ahead f = next;
+            next = ask(after);
+            after = look_on();
+            const int slot = t % kRaw;
+            if (!warp_wait(sh, sh.raw_full[slot], t / kRaw & 1, a.err)) break;
+            if (t >= kOldStages && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
+            const float pk = f.ks * per_k, pv = f.vs * per_v;
+            const bool one = pk == 1.0f && pv == 1.0f;
+            const bool fits = chunk_power && pk >= 0x1p-15f && pk <= 0x1p7f && pv >= 0x1p-15f && pv <= 0x1p7f &&
+                              ((__float_as_uint(f.ks) | __float_as_uint(f.vs)) & 0x7FFFFFu) == 0;
+            const bool even = __all_sync(~0u, one), folds = __all_sync(~0u, one || fits);
+            uint8_t *to = ring + put.slot * 2 * kTileBytes;
+            uint32_t part[2] = {0x3C003C00u, 0x3C003C00u};  // ones
+            OldShared::Tile &tile = old.tile[put.slot];
+            if (even && f.bits == 0xFFFFu) {
+                turn<false>(raw(slot), to, f.bits, part);
+            } else {
+                if (folds) part[0] = pack2<__half>(pk, pk), part[1] = pack2<__half>(pv, pv);
+                turn<true>(raw(slot), to, f.bits, part);
+            }
+            if (lane < kRows) {
+                tile.ks[w * kRows + lane] = folds ? of_chunk.k : f.ks;
+                tile.vs[w * kRows + lane] = folds ? of_chunk.v : f.vs;
+            }
+            if (lane == 0) {
+                tile.odd[w] = !folds;
+                reinterpret_cast<uint16_t *>(sh.valid[put.slot])[w] = (uint16_t)f.bits;
+            }
+            // One word for the warp (arrivals of 32 lanes at one place follow one another).  The writes are handed to the
+            // tensor cores by the fence of the warp that issues the products.
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&sh.full[put.slot]));
+                mbar_arrive(smem_addr(&sh.raw_empty[slot]));
+            }
+        }
+    }
+};
+
 template <typename T, int D, typename Old>
-__global__ void __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThreads, 1)
     k_tree_wide(const __grid_constant__ TreeAttention a, const __grid_constant__ Old b, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
     constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
+    constexpr int kScoreWarp = Roles<kOld>::kScoreWarp, kSumWarp = Roles<kOld>::kSumWarp, kCopy = Roles<kOld>::kCopy, kOthers = Roles<kOld>::kOthers;
     constexpr uint32_t kQHalf = kGroup * 128, kHalf = kTile * 128;  // bytes of 64 columns
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -352,7 +466,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), 32 + 1);  // the copying warp's copies, and its word on valid[]
+            mbar_init(smem_addr(&sh.full[i]), is8 ? 4 : 32 + 1);  // the widening warps; the copying warp's copies, and its word on valid[]
             mbar_init(smem_addr(&sh.empty[i]), 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -361,6 +475,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 mbar_init(smem_addr(&sh.weighed[g][b]), 4);
                 mbar_init(smem_addr(&sh.summed[g][b]), 1);
             }
+        }
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(smem_addr(&sh.raw_full[i]), 32);
+            mbar_init(smem_addr(&sh.raw_empty[i]), 4);
         }
         mbar_init(smem_addr(&sh.done[0]), 1);
         mbar_init(smem_addr(&sh.done[1]), 1);
@@ -376,14 +494,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t q_at = smem_addr(smem), ring = q_at + 2 * kQBytes;
     const int32_t *table = a.table + (int64_t)s * a.table_width;
 
-    const bool copies = warp >= kCopyWarp && warp < kScoreWarp;
-    if (!copies) {
+    const bool multiplies = warp == kScoreWarp || warp == kSumWarp, copies = warp >= kCopy && warp < kCopy + 2;
+    ChunkScales of_chunk = {1.0f, 1.0f};
+    if constexpr (kOld) {
+        if (is8) of_chunk = chunk_scales(b, s, kvh, begin);
+    }
+    if (warp < kCopyWarp || multiplies) {
         // q of the rows, the sign of the scale with it; absent rows are zero
         const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
         // (all loads under way at once: a second round would wait behind the copies of five tiles, some 3 us)
-        constexpr int kOthers = kWideThreads - 64, kAtOnce = (2 * kGroup * (D / 8) + kOthers - 1) / kOthers;
-        const int me = warp < kCopyWarp ? tid : tid - 64, pieces = (split ? 1 : 2) * kGroup * (D / 8);
+        constexpr int kAtOnce = (2 * kGroup * (D / 8) + kOthers - 1) / kOthers;
+        const int me = warp < kCopyWarp ? tid : tid - (kScoreWarp - kCopyWarp) * 32, pieces = (split ? 1 : 2) * kGroup * (D / 8);
         uint4 v[kAtOnce];
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
@@ -434,19 +556,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         asm volatile("bar.sync 2, %0;" ::"n"(kOthers) : "memory");
     }
 
-    bool copied = false;
-    if constexpr (kOld) {
-        if (copies && is8) {
-            copy_old<D>(a, b, sh, old, smem + 2 * kQBytes, begin, end, tiles, kvh, s, warp - kCopyWarp, lane);
-            copied = true;
-        }
-    }
     const int stages = is8 ? kOldStages : kStages;
-    if (copied) {
+    if (warp >= kCopyWarp) {
+    if constexpr (kOld) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (is8 && !multiplies) {
+        if constexpr (kOld) {
+            const int w = copies ? warp - kCopy : warp - kCopyWarp;
+            if (b.c.page_size % 16 == 0 && b.c.block % 16 == 0) {
+                const OldTiles<D, true> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
+                if (copies) tiles_of.copy();
+                else tiles_of.widen(of_chunk);
+            } else {
+                const OldTiles<D, false> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
+                if (copies) tiles_of.copy();
+                else tiles_of.widen(of_chunk);
+            }
+        }
     } else if (copies) {
         // copies: the two warps take tiles in turn (what a tile costs a warp is mostly waits and look-ups); lane l keeps
         // the places of keys l and l + 32
-        const int cw = warp - kCopyWarp;
+        const int cw = warp - kCopy;
         const int64_t head = kvh * a.c.head_stride;
         // Keys are looked up in order: the page of the next tile's key is some pages and tokens on (no divisions).
         const uint32_t size = a.c.page_size, pages_on = 2 * kTile / size, tokens_on = 2 * kTile % size;
@@ -562,7 +691,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         copy_commit();
         copy_wait<0>();
-    } else if (warp >= kScoreWarp) {
+    } else if (multiplies) {
         // item i: group i % 2, tile i (keys shared out) or i / 2
         bool ok = true;
         Place at;
@@ -615,7 +744,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         bool all = false;
         while (!(all = mbar_try_wait(smem_addr(&done), 0u)) && global_ns() - t0 < kWaitLimitNs) {}
         if (!all && a.err) atomicOr(a.err, kErrPipeTimeout);
+    }
     } else {
+        if constexpr (kOld) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // weights: thread = row of its group
         const int g = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
@@ -630,9 +761,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         int n = 0;  // items of this group so far
         Place at;
         at.stages = stages;
-        float of_row = sc;
-        if constexpr (kOld)
-            if (is8) of_row = sh.of_row[live ? row_in : 0];
+        float of_row = sc, one_sc = sc, one_lv = 0.0f, one_v = 1.0f;  // old places: the last three with the chunk's scales
+        if constexpr (kOld) {
+            if (is8) {
+                of_row = sh.of_row[live ? row_in : 0];
+                one_sc = fmaxf(of_row * of_chunk.k, 1e-45f), one_lv = log2_of(of_chunk.v), one_v = 1.0f / of_chunk.v;
+            }
+        }
         if (split && g) at.step(1);
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
@@ -647,24 +782,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if ((split ? i : i >> 1) >= old_tiles) there[0] &= (uint32_t)sees, there[1] &= (uint32_t)(sees >> 32);
             tm_wait_ld();
             if (!ok) break;
-            // old places: the scores' factors; where the scales are all equal, the row's takes theirs with it
-            bool each = false;
-            float lv = 0.0f, per_v = 1.0f, sc = of_row;
+            bool each = false;  // each key has scales of its own
+            float lv = one_lv, per_v = one_v, sc = one_sc;
             if constexpr (kOld) {
-                if (is8) {
-                    const float4 one = old.tile[slot].one;
-                    each = one.w == 0.0f;
-                    if (!each) {
-                        sc = fmaxf(of_row * one.x, 1e-45f), lv = one.y, per_v = one.z;
-                    } else {
+                if (is8 && *reinterpret_cast<const uint32_t *>(old.tile[slot].odd)) {
+                    each = true;
+                    lv = 0.0f, per_v = 1.0f, sc = of_row;
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4) {
-                            const float4 ks = *reinterpret_cast<const float4 *>(&old.tile[slot].ks[j]);
-                            x[j >> 5][j & 31] = __float_as_uint(__uint_as_float(x[j >> 5][j & 31]) * ks.x);
-                            x[j >> 5][(j & 31) + 1] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 1]) * ks.y);
-                            x[j >> 5][(j & 31) + 2] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 2]) * ks.z);
-                            x[j >> 5][(j & 31) + 3] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 3]) * ks.w);
-                        }
+                    for (int j = 0; j < 64; j += 4) {
+                        const float4 ks = *reinterpret_cast<const float4 *>(&old.tile[slot].ks[j]);
+                        x[j >> 5][j & 31] = __float_as_uint(__uint_as_float(x[j >> 5][j & 31]) * ks.x);
+                        x[j >> 5][(j & 31) + 1] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 1]) * ks.y);
+                        x[j >> 5][(j & 31) + 2] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 2]) * ks.z);
+                        x[j >> 5][(j & 31) + 3] = __float_as_uint(__uint_as_float(x[j >> 5][(j & 31) + 3]) * ks.w);
                     }
                 }
             }
@@ -715,19 +845,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
             }
             const float less = m == -INFINITY ? 0.0f : lv - m;
-            const float2 sc2 = make_float2(sc, sc), less2 = make_float2(less, less);
-            float2 sum[2] = {};
             uint32_t p[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), sc2, less2);
-                float2 w = make_float2(pow2(y.x), pow2(y.y));
-                sum[j & 1] = __fadd2_rn(sum[j & 1], w);
-                if constexpr (kOld)
-                    if (each) w = __fmul2_rn(w, *reinterpret_cast<const float2 *>(&old.tile[slot].vs[2 * j]));
-                p[j] = kOld && is8 ? pack2<__half>(w.x, w.y) : pack2<T>(w.x, w.y);
-            }
-            l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * per_v;
+            float sum;
+            if constexpr (!kOld) sum = weigh<T, false>(x, sc, less, nullptr, p);
+            else if (each) sum = weigh<__half, true>(x, sc, less, old.tile[slot].vs, p);
+            else if (is8) sum = weigh<__half, false>(x, sc, less, nullptr, p);
+            else sum = weigh<T, false>(x, sc, less, nullptr, p);
+            l += sum * per_v;
             tm_st(s_at, p);
             tm_wait_st();
             fence_before();
@@ -880,7 +1004,7 @@ cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_c
     static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
     static_assert(kOldStages * 2 + kRaw <= kStages * 2, "and so do the old places' tiles, of 16 bits and of 8");
     return launch_dependent(k_tree_wide<T, D, Old>, dim3((unsigned)(a.c.kv_heads * row_tiles), (unsigned)n_chunks, (unsigned)a.n_seq),
-                            kWideThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
+                            Roles<std::is_same_v<Old, OldPlaces>>::kThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
 }
 
 template <typename Old>
