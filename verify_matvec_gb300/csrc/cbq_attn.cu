@@ -200,12 +200,12 @@ struct OldShared {
 // the odd columns.
 template <typename T, int D, int WR>
 __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlaces &b, const Seq &sq, OldShared<Shape<D, WR>> &sh,
-                                           uint8_t *smem, int begin, int end, int r0, int rows, int kvh, float (&o)[D / 8][4],
+                                           uint8_t *smem, int begin, int end, int r0, int rows, int kvh, int s, float (&o)[D / 8][4],
                                            float (&m)[2], float (&l)[2]) {
     using S = Shape<D, WR>;
     constexpr int kPieces = D / 16;  // 16-byte pieces of a row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp % WR, wk = warp / WR, ra = wr * 16 + lane / 4, t4 = lane % 4;
-    const int group = a.q_heads / a.c.kv_heads, s = blockIdx.z;
+    const int group = a.q_heads / a.c.kv_heads;
     const int tiles = (end - begin + S::kTile8 - 1) / S::kTile8;
     const int32_t *table = b.table + (int64_t)s * b.table_width;
     const int64_t head = kvh * b.c.head_stride;
@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     pdl_wait();
     pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows, c = blockIdx.y, s = blockIdx.z;
+    const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * S::kRows;
+    const bool turned = kOld && !cluster;  // (the old places of all sequences first: their blocks take longer)
+    const int c = turned ? blockIdx.z : blockIdx.y, s = turned ? blockIdx.y : blockIdx.z;
     const int group = a.q_heads / a.c.kv_heads;
     const Seq sq = sequence(a, b, s, tid == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, S::kRows);
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
     const int wr = warp % WR, wk = warp / WR, ra = wr * 16 + lane / 4;  // this lane's rows are ra and ra + 8
     if constexpr (kOld) {
         __shared__ OldShared<S> old;
-        if (is8) old_places<T, D, WR>(a, b, sq, old, smem, begin, end, r0, rows, kvh, o, m, l);
+        if (is8) old_places<T, D, WR>(a, b, sq, old, smem, begin, end, r0, rows, kvh, s, o, m, l);
     }
     if (!is8) {
 
@@ -987,9 +989,11 @@ cudaError_t launch_tiled(const TreeAttention &a, const Old &b, const Plan &p, cu
     const size_t rows = (size_t)a.total_tok * a.q_heads;
     float2 *part_ml = static_cast<float2 *>(a.ws);
     float *part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + (rows * p.n_chunks * sizeof(float2) + 15) / 16 * 16);
+    const unsigned x = (unsigned)(a.c.kv_heads * p.row_tiles);
     const cudaError_t e = p.wide ? launch_tree_wide(a, b, p.chunk, p.n_chunks, p.row_tiles, part_o, part_ml, s)
                                  : launch_clusters(k_tree_attention<T, D, WR, Old>,
-                                                   dim3((unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)p.n_chunks, (unsigned)a.n_seq),
+                                                   std::is_same_v<Old, OldPlaces> && !p.cluster ? dim3(x, (unsigned)a.n_seq, (unsigned)p.n_chunks)
+                                                                                                : dim3(x, (unsigned)p.n_chunks, (unsigned)a.n_seq),
                                                    p.cluster ? p.n_chunks : 1, 128, Shape<D, WR>::kSmem, s, a, b, p.chunk, p.row_tiles,
                                                    p.cluster, part_o, part_ml);
     if (e != cudaSuccess || p.n_chunks == 1 || p.cluster) return e;

@@ -83,12 +83,12 @@ struct WideShared {
     };
 };
 
-// Of a tile of old places: the scales of its keys and values, if a copying warp
-// says that some of its keys' are not the chunk's.
+// Of a tile of old places: the scales of each 16 keys, where those are equal (of
+// the keys, log2 of the values', one over that, and 1), and of each key.
 struct OldShared {
     struct alignas(16) Tile {
+        float4 group[4];
         float ks[kTile], vs[kTile];
-        uint8_t odd[4];
     } tile[kOldStages];
 };
 static_assert(sizeof(WideShared) + sizeof(OldShared) <= 3072, "beside the tiles no more is left");
@@ -168,21 +168,16 @@ __device__ __forceinline__ float near_log2(float v) {
     const float bits = __uint_as_float(__float_as_uint(v) >> 8 & 0x7FFFFFu | 0x4B000000u);  // 2^23 + the exponent and 15 bits behind it
     return fminf(fmaxf(__fmaf_rn(bits, 0x1p-15f, -256.0f - 127.0f), -80.0f), 120.0f);
 }
-// The weights 2^(x sc + less) of 64 scores, as numbers of P for the product with
-// v (kEach: each by its scale first), and their sum.
-template <typename P, bool kEach>
-__device__ __forceinline__ float weigh(const uint32_t (&x)[2][32], float sc, float less, const float *vs, uint32_t (&p)[32]) {
-    const float2 sc2 = make_float2(sc, sc), less2 = make_float2(less, less);
-    float2 sum[2] = {};
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), sc2, less2);
-        float2 w = make_float2(pow2(y.x), pow2(y.y));
-        sum[j & 1] = __fadd2_rn(sum[j & 1], w);
-        if constexpr (kEach) w = __fmul2_rn(w, *reinterpret_cast<const float2 *>(vs + 2 * j));
-        p[j] = pack2<P>(w.x, w.y);
-    }
-    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+// The weights 2^(x sc + less) of scores 2 j and 2 j + 1, added to sum, and (with
+// vs: each by its scale) as numbers of P for the product with v.
+template <typename P>
+__device__ __forceinline__ void weigh(const uint32_t (&x)[2][32], int j, float sc, float less, float2 &sum, uint32_t (&p)[32], const float2 *vs = nullptr) {
+    const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 4][2 * j & 31]), __uint_as_float(x[j >> 4][(2 * j + 1) & 31])), make_float2(sc, sc),
+                                make_float2(less, less));
+    float2 w = make_float2(pow2(y.x), pow2(y.y));
+    sum = __fadd2_rn(sum, w);
+    if (vs) w = __fmul2_rn(w, vs[j]);
+    p[j] = pack2<P>(w.x, w.y);
 }
 // The eight warps of the two groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -217,26 +212,6 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
     return __all_sync(~0u, wait_for(s, bar, parity, err));
 }
 
-// A chunk's scales: those of its first key stand for all, as long as what a
-// key's are more or less can go into its numbers: powers of two from 2^-15 (an
-// e4m3 number has its last bit at 2^-9 or above, an fp16 number at 2^-24) to 2^7
-// (448 * 2^7 < 65504).  A key that this does not hold for keeps its own, and the
-// weights' warps look at every key of its tile, which costs them as much again
-// as the weights themselves.
-struct ChunkScales {
-    float k, v;
-};
-__device__ __forceinline__ ChunkScales chunk_scales(const OldPlaces &b, int s, int kvh, int begin) {
-    const int64_t page = b.table[(int64_t)s * b.table_width + begin / b.c.page_size];
-    ChunkScales r = {1.0f, 1.0f};
-    if (page >= 0 && page < b.c.n_pages) {
-        const int64_t of = page * b.c.scale_page_stride + begin % b.c.page_size / b.c.block * b.c.scale_block_stride + kvh * b.c.scale_head_stride;
-        const float k = b.c.k_scale[of], v = b.c.v_scale[of];
-        if (k >= 0x1p-80f && k <= 0x1p112f && v >= 0x1p-80f && v <= 0x1p112f) r = {k, v};
-    }
-    return r;
-}
-
 // A block of old places, copying and widening: the two copying warps bring its
 // tiles in as they are, in turn and up to four ahead; each of four more takes 16
 // keys of every tile into the ring as fp16, 16 numbers a load, of rows and halves
@@ -246,7 +221,10 @@ __device__ __forceinline__ ChunkScales chunk_scales(const OldPlaces &b, int s, i
 // which the other 1,000 go on.  (Four warps that did both, and so all did the
 // same at a time, took 2,500 a tile.)
 // kWhole: pages and blocks are multiples of 16 tokens, so the 16 keys have one
-// page and one pair of scales.
+// page and one pair of scales.  Scales go to the weights' warps, for each 16
+// keys: there they cost next to nothing, while a scale a key costs as much again
+// as the weights themselves.  (Multiplied into the fp16 numbers here they made
+// 343 us of 8 trees of 64 drafts 458.)
 template <int D, bool kWhole>
 struct OldTiles {
     static constexpr int kTileBytes = kTile * D * 2, kHalf = kTile * 128, kRawBytes = kTile * D, kPieces = D / 16, kRows = 16;
@@ -329,10 +307,9 @@ struct OldTiles {
         copy_wait<0>();
     }
 
-    // This warp's rows of a tile as it is to those of a tile as fp16; kCareful: rows that are not there become zeros, the
-    // others are multiplied by what their scales are of the chunk's (two fp16 numbers of the same; of row l in lane l).
-    template <bool kCareful>
-    __device__ __forceinline__ void turn(const uint8_t *from, uint8_t *to, uint32_t bits, const uint32_t (&part)[2]) const {
+    // This warp's rows of a tile as it is to those of a tile as fp16; kSome: those that are not there become zeros.
+    template <bool kSome>
+    __device__ __forceinline__ void turn(const uint8_t *from, uint8_t *to, uint32_t bits) const {
         constexpr int kSets = 2 * (D / 64);  // keys and values; the halves of their columns
         const int r0 = w * kRows + lane / 4, odd = lane / 4 & 1;
         uint4 x[kSets][2];
@@ -344,25 +321,16 @@ struct OldTiles {
         const int p0 = (lane % 4 * 2 ^ lane / 4) * 16;  // (rows eight apart have their pieces in the same order)
 #pragma unroll
         for (int k = 0; k < kSets; ++k) {
-            const int of_v = k / (D / 64), half = D > 64 ? k % 2 ^ odd : 0;
-            uint8_t *out = to + of_v * kTileBytes + half * kHalf + r0 * 128;
+            uint8_t *out = to + k / (D / 64) * kTileBytes + (D > 64 ? (k % 2 ^ odd) * kHalf : 0) + r0 * 128;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t y[8];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t two = c == 0 ? x[k][i].x : c == 1 ? x[k][i].y : c == 2 ? x[k][i].z : x[k][i].w;
-                    if (kCareful && !(bits >> (i * 8 + lane / 4) & 1)) two = 0;
+                    if (kSome && !(bits >> (i * 8 + lane / 4) & 1)) two = 0;
                     y[2 * c] = e4m3_f16x2((uint16_t)two);
                     y[2 * c + 1] = e4m3_f16x2((uint16_t)(two >> 16));
-                }
-                if constexpr (kCareful) {
-                    const uint32_t f = kWhole ? part[of_v] : __shfl_sync(~0u, part[of_v], i * 8 + lane / 4);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[c]), *reinterpret_cast<const __half2 *>(&f));
-                        y[c] = *reinterpret_cast<const uint32_t *>(&z);
-                    }
                 }
                 *reinterpret_cast<uint4 *>(out + i * 1024 + p0) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4 *>(out + i * 1024 + (p0 ^ 16)) = make_uint4(y[4], y[5], y[6], y[7]);
@@ -370,58 +338,75 @@ struct OldTiles {
         }
     }
 
-    __device__ __forceinline__ void widen(ChunkScales of_chunk) const {
+    // What a widening warp needs to know of its rows of a tile: which there are, and the scales (of row l in lane l, or of all).
+    struct Rows {
+        uint32_t bits;
+        float ks, vs;
+    };
+    __device__ __forceinline__ Rows ask(const Look &now) const {
+        const bool good = is_there(now);
+        Rows f = {kWhole ? (good ? 0xFFFFu >> max(kRows - now.left, 0) : 0) : __ballot_sync(~0u, good), 1.0f, 1.0f};
+        if (good) {
+            const int64_t of = now.page * b.c.scale_page_stride + (uint32_t)now.within / (uint32_t)b.c.block * b.c.scale_block_stride + kvh * b.c.scale_head_stride;
+            f.ks = b.c.k_scale[of];
+            f.vs = b.c.v_scale[of];
+        }
+        return f;
+    }
+
+    __device__ __forceinline__ void widen() const {
         const uint32_t size = b.c.page_size, pages_on = kTile / size, tokens_on = kTile % size;
-        const int64_t scale_head = kvh * b.c.scale_head_stride;
-        const float per_k = 1.0f / of_chunk.k, per_v = 1.0f / of_chunk.v;
-        const bool chunk_power = ((__float_as_uint(of_chunk.k) | __float_as_uint(of_chunk.v)) & 0x7FFFFFu) == 0;
-        Keys keys = keys_from(begin + w * kRows + (kWhole ? 0 : lane));  // the warp's first, or this lane's (of 16)
-        auto look_on = [&] { return look(keys, pages_on, tokens_on, kTile, kWhole || lane < kRows); };
-        struct Ahead {
-            uint32_t bits;
-            float ks, vs;
+        // kWhole: lane l asks for tile l of 32, once in as many tiles (asking for each took 500 clocks of a tile's 2,000);
+        // page ids are loaded half of them ahead, scales a quarter.
+        Rows many = {}, more = {};
+        Look later = {};
+        auto look_at = [&](int t) {
+            Keys k = keys_from(begin + (t + lane) * kTile + w * kRows);
+            return look(k, 0, 0, 0, t + lane < tiles);
         };
-        auto ask = [&](const Look &now) {
-            const bool good = is_there(now);
-            Ahead f = {kWhole ? (good ? 0xFFFFu >> max(kRows - now.left, 0) : 0) : __ballot_sync(~0u, good), of_chunk.k, of_chunk.v};
-            if (good) {
-                const int64_t of = now.page * b.c.scale_page_stride + (uint32_t)now.within / (uint32_t)b.c.block * b.c.scale_block_stride + scale_head;
-                f.ks = b.c.k_scale[of];
-                f.vs = b.c.v_scale[of];
-            }
-            return f;
-        };
-        Ahead next = ask(look_on());
-        Look after = look_on();
+        // otherwise each lane looks its own key up, a tile ahead
+        Keys keys = keys_from(begin + w * kRows + lane);
+        auto look_on = [&] { return look(keys, pages_on, tokens_on, kTile, lane < kRows); };
+        Rows next = {};
+        Look after = {};
+        if constexpr (kWhole) {
+            more = ask(look_at(0));
+        } else {
+            next = ask(look_on());
+            after = look_on();
+        }
         Place put;
         put.stages = kOldStages;
         for (int t = 0; t < tiles; ++t, put.step(1)) {
-            const Ahead f = next;
-            next = ask(after);
-            after = look_on();
+            Rows f;
+            if constexpr (kWhole) {
+                if (t % 32 == 0) many = more;
+                if (t % 32 == 16) later = look_at(t + 16);
+                if (t % 32 == 24) more = ask(later);
+                f = {__shfl_sync(~0u, many.bits, t % 32), __shfl_sync(~0u, many.ks, t % 32), __shfl_sync(~0u, many.vs, t % 32)};
+            } else {
+                f = next;
+                next = ask(after);
+                after = look_on();
+            }
             const int slot = t % kRaw;
             if (!warp_wait(sh, sh.raw_full[slot], t / kRaw & 1, a.err)) break;
             if (t >= kOldStages && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
-            const float pk = f.ks * per_k, pv = f.vs * per_v;
-            const bool one = pk == 1.0f && pv == 1.0f;
-            const bool fits = chunk_power && pk >= 0x1p-15f && pk <= 0x1p7f && pv >= 0x1p-15f && pv <= 0x1p7f &&
-                              ((__float_as_uint(f.ks) | __float_as_uint(f.vs)) & 0x7FFFFFu) == 0;
-            const bool even = __all_sync(~0u, one), folds = __all_sync(~0u, one || fits);
             uint8_t *to = ring + put.slot * 2 * kTileBytes;
-            uint32_t part[2] = {0x3C003C00u, 0x3C003C00u};  // ones
+            if (f.bits == 0xFFFFu) turn<false>(raw(slot), to, f.bits);
+            else turn<true>(raw(slot), to, f.bits);
+            // one pair of scales for the 16 keys, if it is one (and no number that the weights' warps could not take so)
+            const int lead = f.bits ? __ffs(f.bits) - 1 : 0;
+            const float k0 = kWhole ? f.ks : __shfl_sync(~0u, f.ks, lead), v0 = kWhole ? f.vs : __shfl_sync(~0u, f.vs, lead);
+            bool one = k0 >= 0x1p-100f && v0 >= 0x1p-80f && v0 <= 0x1p112f;
+            if constexpr (!kWhole) one = __all_sync(~0u, one && (!(f.bits >> (lane & 15) & 1) || lane >= kRows || (f.ks == k0 && f.vs == v0)));
             OldShared::Tile &tile = old.tile[put.slot];
-            if (even && f.bits == 0xFFFFu) {
-                turn<false>(raw(slot), to, f.bits, part);
-            } else {
-                if (folds) part[0] = pack2<__half>(pk, pk), part[1] = pack2<__half>(pv, pv);
-                turn<true>(raw(slot), to, f.bits, part);
-            }
             if (lane < kRows) {
-                tile.ks[w * kRows + lane] = folds ? of_chunk.k : f.ks;
-                tile.vs[w * kRows + lane] = folds ? of_chunk.v : f.vs;
+                tile.ks[w * kRows + lane] = f.ks;
+                tile.vs[w * kRows + lane] = f.vs;
             }
             if (lane == 0) {
-                tile.odd[w] = !folds;
+                tile.group[w] = make_float4(k0, log2_of(v0), 1.0f / v0, one ? 1.0f : 0.0f);
                 reinterpret_cast<uint16_t *>(sh.valid[put.slot])[w] = (uint16_t)f.bits;
             }
             // One word for the warp (arrivals of 32 lanes at one place follow one another).  The writes are handed to the
@@ -448,7 +433,8 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
     pdl_wait();
     pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kWideRows, c = blockIdx.y, s = blockIdx.z;
+    const int kvh = blockIdx.x / row_tiles, r0 = blockIdx.x % row_tiles * kWideRows;
+    const int c = kOld ? blockIdx.z : blockIdx.y, s = kOld ? blockIdx.y : blockIdx.z;  // (old places first: their blocks take longer)
     const int group = a.q_heads / a.c.kv_heads;
     const Seq sq = sequence(a, b, s, threadIdx.x == 0 && blockIdx.x == 0 && c == 0);
     const int rows = min(sq.n * group - r0, kWideRows);
@@ -495,10 +481,6 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
     const int32_t *table = a.table + (int64_t)s * a.table_width;
 
     const bool multiplies = warp == kScoreWarp || warp == kSumWarp, copies = warp >= kCopy && warp < kCopy + 2;
-    ChunkScales of_chunk = {1.0f, 1.0f};
-    if constexpr (kOld) {
-        if (is8) of_chunk = chunk_scales(b, s, kvh, begin);
-    }
     if (warp < kCopyWarp || multiplies) {
         // q of the rows, the sign of the scale with it; absent rows are zero
         const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
@@ -565,11 +547,11 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             if (b.c.page_size % 16 == 0 && b.c.block % 16 == 0) {
                 const OldTiles<D, true> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
                 if (copies) tiles_of.copy();
-                else tiles_of.widen(of_chunk);
+                else tiles_of.widen();
             } else {
                 const OldTiles<D, false> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
                 if (copies) tiles_of.copy();
-                else tiles_of.widen(of_chunk);
+                else tiles_of.widen();
             }
         }
     } else if (copies) {
@@ -761,13 +743,9 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         int n = 0;  // items of this group so far
         Place at;
         at.stages = stages;
-        float of_row = sc, one_sc = sc, one_lv = 0.0f, one_v = 1.0f;  // old places: the last three with the chunk's scales
-        if constexpr (kOld) {
-            if (is8) {
-                of_row = sh.of_row[live ? row_in : 0];
-                one_sc = fmaxf(of_row * of_chunk.k, 1e-45f), one_lv = log2_of(of_chunk.v), one_v = 1.0f / of_chunk.v;
-            }
-        }
+        float of_row = sc;
+        if constexpr (kOld)
+            if (is8) of_row = sh.of_row[live ? row_in : 0];
         if (split && g) at.step(1);
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
@@ -782,12 +760,21 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             if ((split ? i : i >> 1) >= old_tiles) there[0] &= (uint32_t)sees, there[1] &= (uint32_t)(sees >> 32);
             tm_wait_ld();
             if (!ok) break;
+            // old places: the factors on the scores of each 16 keys, log2 of those on their weights, and one over those
             bool each = false;  // each key has scales of its own
-            float lv = one_lv, per_v = one_v, sc = one_sc;
+            float of_group[4] = {of_row, of_row, of_row, of_row}, lv[4] = {}, per_v[4] = {1.0f, 1.0f, 1.0f, 1.0f};
             if constexpr (kOld) {
-                if (is8 && *reinterpret_cast<const uint32_t *>(old.tile[slot].odd)) {
-                    each = true;
-                    lv = 0.0f, per_v = 1.0f, sc = of_row;
+                if (is8) {
+                    float all = 1.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 y = old.tile[slot].group[k];
+                        of_group[k] = fmaxf(of_row * y.x, 1e-45f), lv[k] = y.y, per_v[k] = y.z;
+                        all *= y.w;
+                    }
+                    each = all == 0.0f;
+                }
+                if (each) {
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
                         const float4 ks = *reinterpret_cast<const float4 *>(&old.tile[slot].ks[j]);
@@ -807,24 +794,30 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 64; j += 2)
-                top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1]));
-            float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc + (lv - kLower);
-            if constexpr (kOld) {
-                if (each) {  // (each key's score with its value's scale)
-                    float most = -INFINITY;
+            for (int i = 0; i < 32; ++i) {
+                const int k = i & 3, j = kOld ? k * 16 + i / 4 * 2 : i * 2;  // (with old places the tops of each 16)
+                top[k] = max3(top[k], __uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1]));
+            }
+            float now;
+            if constexpr (!kOld) {
+                now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc - kLower;
+            } else if (!each) {
+                now = fmaxf(fmaxf(top[0] * of_group[0] + lv[0], top[1] * of_group[1] + lv[1]), fmaxf(top[2] * of_group[2] + lv[2], top[3] * of_group[3] + lv[3])) - kLower;
+            } else {  // each key's score with its value's scale
+                float most = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&old.tile[slot].vs[j]);
-                        const float4 l = make_float4(near_log2(v.x), near_log2(v.y), near_log2(v.z), near_log2(v.w));
-                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1])),
-                                                    make_float2(sc, sc), make_float2(l.x, l.y));
-                        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][(j & 31) + 2]), __uint_as_float(x[j >> 5][(j & 31) + 3])),
-                                                    make_float2(sc, sc), make_float2(l.z, l.w));
-                        most = max3(max3(most, y.x, y.y), z.x, z.y);
-                    }
-                    now = most - kLower;
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&old.tile[slot].vs[j]);
+                    const float4 l = make_float4(near_log2(v.x), near_log2(v.y), near_log2(v.z), near_log2(v.w));
+                    const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1])),
+                                                make_float2(of_row, of_row), make_float2(l.x, l.y));
+                    const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[j >> 5][(j & 31) + 2]), __uint_as_float(x[j >> 5][(j & 31) + 3])),
+                                                make_float2(of_row, of_row), make_float2(l.z, l.w));
+                    most = max3(max3(most, y.x, y.y), z.x, z.y);
                 }
+                now = most - kLower;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) of_group[k] = of_row, lv[k] = 0.0f, per_v[k] = 1.0f;
             }
             const bool grown = now > m + kGrow || (m == -INFINITY && now > -INFINITY);
             const float keep = grown ? pow2(m - now) : 1.0f;
@@ -844,14 +837,32 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
                     tm_st(lanes + Cols<D>::o(g) + d, o);
                 }
             }
-            const float less = m == -INFINITY ? 0.0f : lv - m;
+            const float less = m == -INFINITY ? 0.0f : -m;
             uint32_t p[32];
-            float sum;
-            if constexpr (!kOld) sum = weigh<T, false>(x, sc, less, nullptr, p);
-            else if (each) sum = weigh<__half, true>(x, sc, less, old.tile[slot].vs, p);
-            else if (is8) sum = weigh<__half, false>(x, sc, less, nullptr, p);
-            else sum = weigh<T, false>(x, sc, less, nullptr, p);
-            l += sum * per_v;
+            if constexpr (!kOld) {
+                float2 sum[2] = {};
+#pragma unroll
+                for (int j = 0; j < 32; ++j) weigh<T>(x, j, sc, less, sum[j & 1], p);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) lv[k] += less;
+                float2 sum[4] = {};
+                auto all = [&](auto weigh_one) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int k = i & 3;
+                        weigh_one(k * 8 + i / 4, of_group[k], lv[k], sum[k]);
+                    }
+                };
+                if (each)
+                    all([&](int j, float f, float add, float2 &to) {
+                        weigh<__half>(x, j, f, add, to, p, reinterpret_cast<const float2 *>(old.tile[slot].vs));
+                    });
+                else if (is8) all([&](int j, float f, float add, float2 &to) { weigh<__half>(x, j, f, add, to, p); });
+                else all([&](int j, float f, float add, float2 &to) { weigh<T>(x, j, f, add, to, p); });
+                l += ((sum[0].x + sum[0].y) * per_v[0] + (sum[1].x + sum[1].y) * per_v[1]) + ((sum[2].x + sum[2].y) * per_v[2] + (sum[3].x + sum[3].y) * per_v[3]);
+            }
             tm_st(s_at, p);
             tm_wait_st();
             fence_before();
@@ -1003,8 +1014,10 @@ cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_c
     constexpr size_t kSmem = 2 * kGroup * D * 2 + kStages * 2 * kTile * D * 2;
     static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
     static_assert(kOldStages * 2 + kRaw <= kStages * 2, "and so do the old places' tiles, of 16 bits and of 8");
-    return launch_dependent(k_tree_wide<T, D, Old>, dim3((unsigned)(a.c.kv_heads * row_tiles), (unsigned)n_chunks, (unsigned)a.n_seq),
-                            Roles<std::is_same_v<Old, OldPlaces>>::kThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
+    constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
+    const unsigned x = (unsigned)(a.c.kv_heads * row_tiles);
+    return launch_dependent(k_tree_wide<T, D, Old>, kOld ? dim3(x, (unsigned)a.n_seq, (unsigned)n_chunks) : dim3(x, (unsigned)n_chunks, (unsigned)a.n_seq),
+                            Roles<kOld>::kThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
 }
 
 template <typename Old>
