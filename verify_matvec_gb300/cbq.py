@@ -875,11 +875,18 @@ def cbq_verify(probs, draft, tokens, parent, start, u, u_next, max_tok: int, pat
 def _layers(kc, vc):
     """(cbq_kv_cache, layers, layer stride) of two CUDA tensors (pages,
     page_size, kv_heads, dim), or (layers, pages, page_size, kv_heads, dim)."""
-    if kc.dim() != 5:
+    shape, st = kc.shape, kc.stride()
+    if len(shape) != 5:
         return _cache(kc, vc), 1, 0
-    if kc.shape != vc.shape or kc.stride() != vc.stride():
+    if not kc.is_cuda or not vc.is_cuda or kc.dtype != vc.dtype:
+        raise TypeError("kc and vc must be CUDA tensors of one dtype")
+    if shape != vc.shape or st != vc.stride():
         raise ValueError("kc and vc must be of one shape and strides")
-    return _cache(kc[0], vc[0]), kc.shape[0], kc.stride(0)
+    layers, pages, page, heads, dim = shape
+    if st[4] != 1 and dim != 1:
+        raise ValueError("the cache's last axis must be contiguous")
+    return (cbq_kv_cache(kc.data_ptr(), vc.data_ptr(), _dtype(kc, "kc"), heads, dim, page, pages, st[1], st[2], st[3]),
+            layers, st[0])
 
 
 def cbq_kv_commit(kc, vc, table, ctx, path, count, out=None, err=None, stream=None):

@@ -13,7 +13,7 @@ namespace {
 
 // ------------------------------------------------------- accepted drafts --
 
-constexpr int kCommitThreads = 128;
+constexpr int kCommitThreads = 256;
 constexpr int kAtOnce = 8;  // tokens whose loads are under way together
 
 // The tokens of a sequence that move, in ascending order, as offsets into the
@@ -22,9 +22,9 @@ constexpr int kAtOnce = 8;  // tokens whose loads are under way together
 // 16 bytes of all tokens in that order, eight loads ahead of their stores,
 // needs no other's word and no room in between.
 //
-// grid (2 * blocks of a token's row, layers, n_seq): keys, then values.
+// grid (blocks of a slice of the layers' rows, keys' and values'; slices; n_seq).
 template <typename V>
-__global__ void __launch_bounds__(kCommitThreads) k_commit(KvCommit a, int row_blocks) {
+__global__ void __launch_bounds__(kCommitThreads) k_commit(KvCommit a, int layers_a_slice) {
     __shared__ int64_t from[CBQ_TREE_MAX], to[CBQ_TREE_MAX];
     __shared__ int32_t path[CBQ_TREE_MAX];
     __shared__ unsigned bad[2], moves[2];
@@ -74,10 +74,11 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(KvCommit a, int row_b
     __syncthreads();
     const int n = __popc(moves[0]) + __popc(moves[1]);
     constexpr int kEach = sizeof(V) / 2;
-    const int x = (int)(blockIdx.x % row_blocks) * kCommitThreads + tid, per_head = a.c.head_dim / kEach;
-    if (x >= a.c.kv_heads * per_head) return;
-    uint16_t *base = static_cast<uint16_t *>((int)blockIdx.x < row_blocks ? a.c.k : a.c.v) + blockIdx.y * a.layer_stride +
-                     x / per_head * a.c.head_stride + x % per_head * kEach;
+    const uint32_t per_head = a.c.head_dim / kEach, row = a.c.kv_heads * per_head, x = blockIdx.x * kCommitThreads + tid;
+    const uint32_t of = x / row, at = x % row, layer = blockIdx.y * layers_a_slice + (of >> 1);
+    if (of >> 1 >= (uint32_t)layers_a_slice || layer >= (uint32_t)a.layers) return;
+    uint16_t *base = static_cast<uint16_t *>(of & 1 ? a.c.v : a.c.k) + layer * a.layer_stride + at / per_head * a.c.head_stride +
+                     at % per_head * kEach;
     for (int i0 = 0; i0 < n; i0 += kAtOnce) {
         V v[kAtOnce];
 #pragma unroll
@@ -91,8 +92,10 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(KvCommit a, int row_b
 
 template <typename V>
 cudaError_t launch_moves(const KvCommit &a, cudaStream_t s) {
-    const int row = a.c.kv_heads * (a.c.head_dim / (int)(sizeof(V) / 2)), row_blocks = (row + kCommitThreads - 1) / kCommitThreads;
-    return launch_dependent(k_commit<V>, dim3(2u * row_blocks, (unsigned)a.layers, (unsigned)a.n_seq), kCommitThreads, 0, s, a, row_blocks);
+    // (slices, so that a thread's number within its own has 32 bits: nearly always there is one)
+    const int row = a.c.kv_heads * (a.c.head_dim / (int)(sizeof(V) / 2)), slice = std::min(a.layers, (1 << 30) / (2 * row));
+    const int blocks = (2 * slice * row + kCommitThreads - 1) / kCommitThreads, slices = (a.layers + slice - 1) / slice;
+    return launch_dependent(k_commit<V>, dim3((unsigned)blocks, (unsigned)slices, (unsigned)a.n_seq), kCommitThreads, 0, s, a, slice);
 }
 
 // ---------------------------------------------------------- 8-bit pages --
@@ -100,28 +103,39 @@ cudaError_t launch_moves(const KvCommit &a, cudaStream_t s) {
 constexpr int kQuantThreads = 256, kQuantWarps = kQuantThreads / 32;
 constexpr int kHeld = 8;  // 16-byte pieces of a thread that stay in registers
 
-// Of two 16-bit floats, the larger magnitude of the finite ones, as bits.
-template <typename T>
-__device__ __forceinline__ uint32_t magnitude(uint32_t two, uint32_t most) {
-    constexpr uint32_t kInf = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
-    const uint32_t lo = two & 0x7FFFu, hi = two >> 16 & 0x7FFFu;
-    if (lo < kInf) most = max(most, lo);
-    if (hi < kInf) most = max(most, hi);
-    return most;
-}
 template <typename T>
 __device__ __forceinline__ float of_bits(uint32_t b) {
     const uint16_t h = (uint16_t)b;
     return to_f32(*reinterpret_cast<const T *>(&h));
 }
-// Two numbers as e4m3, the first in the low byte; what is not finite becomes NaN.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+template <typename T>
+constexpr uint32_t kInfinity = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+
+// The larger magnitudes, as bits, of two 16-bit floats each.
+__device__ __forceinline__ uint32_t larger(uint32_t most, uint32_t two) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(most), "r"(two & 0x7FFF7FFFu));
+    return r;
+}
+// The same with 0 for what is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t larger_finite(uint32_t most, uint32_t two) {
+    if ((two & 0x7FFFu) >= kInfinity<T>) two &= 0xFFFF0000u;
+    if ((two >> 16 & 0x7FFFu) >= kInfinity<T>) two &= 0xFFFFu;
+    return larger(most, two);
+}
+// Two numbers as e4m3, the first in the low byte.  kOdd: some may not be finite, and become NaN.
+template <typename T, bool kOdd>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two, float down) {
+    const float lo = of_bits<T>(two) * down, hi = of_bits<T>(two >> 16) * down;
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    uint32_t two = r;
-    if (fabsf(lo) == INFINITY) two = (two & 0xFF00u) | 0x7Fu;
-    if (fabsf(hi) == INFINITY) two = (two & 0xFFu) | 0x7F00u;
-    return two;
+    uint32_t y = r;
+    if constexpr (kOdd) {
+        if (fabsf(lo) == INFINITY) y = (y & 0xFF00u) | 0x7Fu;
+        if (fabsf(hi) == INFINITY) y = (y & 0xFFu) | 0x7F00u;
+    }
+    return y;
 }
 // The exponent of a block's scale from the largest magnitude m 2^k, 1 <= m < 2: 448 = 1.75 * 2^8.
 __device__ __forceinline__ int scale_exponent(float most) {
@@ -137,13 +151,13 @@ __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127)
 // Neighbouring units are neighbouring heads, whose rows lie side by side.
 // grid (units of a layer / units a block, layers, 2): keys, then values.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kQuantThreads) k_quantize(KvQuantize a, int warps, int64_t units) {
+__global__ void __launch_bounds__(kQuantThreads) k_quantize(KvQuantize a, int warps, uint32_t units) {
     __shared__ uint32_t of_warp[kQuantWarps];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.to.kv_heads, dim = a.to.head_dim, block = a.to.block;
-    const int per_page = a.to.page_size / block;
-    const int64_t u = (int64_t)blockIdx.x * (kQuantWarps / warps) + warp / warps, i = u / (heads * per_page);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = a.to.head_dim, block = a.to.block;
+    const uint32_t heads = a.to.kv_heads, per_page = a.to.page_size / block;
+    const uint32_t u = blockIdx.x * (kQuantWarps / warps) + warp / warps, i = u / (heads * per_page);
     const int h = (int)(u % heads), b = (int)(u / heads % per_page), me = warp % warps * 32 + lane, step = warps * 32;
     int64_t src = -1, dst = -1;
     if (u < units) {
@@ -158,43 +172,73 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize(KvQuantize a, int wa
                  (int64_t)b * block * a.from.tok_stride + h * a.from.head_stride;
     uint8_t *y = static_cast<uint8_t *>(blockIdx.z ? a.to.v : a.to.k) + blockIdx.y * a.to_layer + dst * a.to.page_stride +
                  (int64_t)b * block * a.to.tok_stride + h * a.to.head_stride;
+    // A thread's pieces: in token t the d-th of a row, then some rows and pieces on (no divisions).
     constexpr int kEach = kVec ? 8 : 1;
-    const int per_row = dim / kEach, pieces = on ? block * per_row : 0;
-    auto load = [&](int p) {
-        const T *at = x + (int64_t)(p / per_row) * a.from.tok_stride + p % per_row * kEach;
+    const int per_row = dim / kEach, pieces = on ? block * per_row : 0, rows_on = step / per_row, pieces_on = step % per_row;
+    struct Place {
+        int t, d;
+    };
+    const Place first = {me / per_row, me % per_row};
+    auto next = [&](Place &p) {
+        p.t += rows_on;
+        p.d += pieces_on;
+        if (p.d >= per_row) p.d -= per_row, ++p.t;
+    };
+    auto load = [&](const Place &p) {
+        const T *at = x + (int64_t)p.t * a.from.tok_stride + p.d * kEach;
         if constexpr (kVec) return *reinterpret_cast<const uint4 *>(at);
         else return make_uint4(*reinterpret_cast<const uint16_t *>(at), 0, 0, 0);
     };
     uint4 v[kHeld];
-    uint32_t most = 0;
-    auto look = [&](const uint4 &w) {
-        most = magnitude<T>(w.x, most);
-        if constexpr (kVec) most = magnitude<T>(w.y, most), most = magnitude<T>(w.z, most), most = magnitude<T>(w.w, most);
+    Place p = first;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j, next(p)) v[j] = me + j * step < pieces ? load(p) : make_uint4(0, 0, 0, 0);
+    // the largest magnitude of all, and only where that is not finite once more of the finite ones
+    auto largest = [&](auto of) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            most = of(most, v[j].x);
+            if constexpr (kVec) most = of(most, v[j].y), most = of(most, v[j].z), most = of(most, v[j].w);
+        }
+        Place q = p;
+        for (int k = me + kHeld * step; k < pieces; k += step, next(q)) {
+            const uint4 w = load(q);
+            most = of(most, w.x);
+            if constexpr (kVec) most = of(most, w.y), most = of(most, w.z), most = of(most, w.w);
+        }
+        most = __reduce_max_sync(~0u, max(most & 0xFFFFu, most >> 16));
+        if (warps > 1) {
+            __syncthreads();
+            if (lane == 0) of_warp[warp] = most;
+            __syncthreads();
+            for (int w = warp / warps * warps, j = 0; j < warps; ++j) most = max(most, of_warp[w + j]);
+        }
+        return most;
     };
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) v[j] = me + j * step < pieces ? load(me + j * step) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) look(v[j]);
-    for (int p = me + kHeld * step; p < pieces; p += step) look(load(p));
-    most = __reduce_max_sync(~0u, most);
-    if (warps > 1) {
-        if (lane == 0) of_warp[warp] = most;
-        __syncthreads();
-        for (int w = warp / warps * warps, j = 0; j < warps; ++j) most = max(most, of_warp[w + j]);
+    uint32_t most = largest([](uint32_t m, uint32_t two) { return larger(m, two); });
+    const bool odd = most >= kInfinity<T>;
+    if (warps > 1 ? __syncthreads_or(odd) : __any_sync(~0u, odd)) {
+        const uint32_t finite = largest([](uint32_t m, uint32_t two) { return larger_finite<T>(m, two); });
+        if (odd) most = finite;
     }
     if (!on) return;
     const int e = scale_exponent(of_bits<T>(most));
     const float down = two_to(-e);
-    auto store = [&](int p, const uint4 &w) {
-        uint8_t *at = y + (int64_t)(p / per_row) * a.to.tok_stride + p % per_row * kEach;
-        auto pair = [&](uint32_t two) { return e4m3_pair(of_bits<T>(two) * down, of_bits<T>(two >> 16) * down); };
-        if constexpr (kVec) *reinterpret_cast<uint2 *>(at) = make_uint2(pair(w.x) | pair(w.y) << 16, pair(w.z) | pair(w.w) << 16);
-        else *at = (uint8_t)pair(w.x);
-    };
+    auto store_all = [&](auto pair) {
+        auto store = [&](const Place &p, const uint4 &w) {
+            uint8_t *at = y + (int64_t)p.t * a.to.tok_stride + p.d * kEach;
+            if constexpr (kVec) *reinterpret_cast<uint2 *>(at) = make_uint2(pair(w.x) | pair(w.y) << 16, pair(w.z) | pair(w.w) << 16);
+            else *at = (uint8_t)pair(w.x);
+        };
+        Place p = first;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (me + j * step < pieces) store(me + j * step, v[j]);
-    for (int p = me + kHeld * step; p < pieces; p += step) store(p, load(p));
+        for (int j = 0; j < kHeld; ++j, next(p))
+            if (me + j * step < pieces) store(p, v[j]);
+        for (int k = me + kHeld * step; k < pieces; k += step, next(p)) store(p, load(p));
+    };
+    if (odd) store_all([&](uint32_t two) { return e4m3_pair<T, true>(two, down); });
+    else store_all([&](uint32_t two) { return e4m3_pair<T, false>(two, down); });
     if (me == 0)
         (blockIdx.z ? a.to.v_scale : a.to.k_scale)[blockIdx.y * a.scale_layer + dst * a.to.scale_page_stride +
                                                    b * a.to.scale_block_stride + h * a.to.scale_head_stride] = two_to(e);
@@ -206,7 +250,7 @@ cudaError_t launch_pages(const KvQuantize &a, cudaStream_t s) {
     int warps = 1;
     while (warps < kQuantWarps && pieces > (int64_t)warps * 32 * kHeld) warps *= 2;
     const int64_t each = kQuantWarps / warps, blocks = (units + each - 1) / each;
-    return launch_dependent(k_quantize<T, kVec>, dim3((unsigned)blocks, (unsigned)a.layers, 2), kQuantThreads, 0, s, a, warps, units);
+    return launch_dependent(k_quantize<T, kVec>, dim3((unsigned)blocks, (unsigned)a.layers, 2), kQuantThreads, 0, s, a, warps, (uint32_t)units);
 }
 
 template <typename T>

@@ -27,26 +27,31 @@ namespace cbq {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMost = 8;     // blocks of a cluster
+constexpr int kMost = 16;    // blocks of a cluster
 constexpr int kTile = 128;   // tokens that a warp takes at a time, four a lane side by side
 
-// A number as two: v = hi + lo, |lo| at most half a unit of hi's last place.
-struct Pair {
-    float hi, lo;
+// Numbers as two, two at a time: v = hi + lo, |lo| at most half a unit of hi's
+// last place.  A packed instruction does the arithmetic of both.
+struct Pairs {
+    float2 hi, lo;
 };
-__device__ __forceinline__ void add(Pair &s, float x, float low) {
-    const float t = s.hi + x, z = t - s.hi;
-    s.lo += ((s.hi - (t - z)) + (x - z)) + low;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 less(float2 a, float2 b) { return __ffma2_rn(b, both(-1.0f), a); }  // a - b
+__device__ __forceinline__ void add(Pairs &s, Pairs x) {
+    const float2 t = __fadd2_rn(s.hi, x.hi), z = less(t, s.hi);
+    s.lo = __fadd2_rn(s.lo, __fadd2_rn(__fadd2_rn(less(s.hi, less(t, z)), less(x.hi, z)), x.lo));
     s.hi = t;
 }
-__device__ __forceinline__ double value(Pair s) { return (double)s.hi + (double)s.lo; }
 
-// What is left of p at one token: max(p - c q, 0), c = ch + cl; NaN gives 0.
-__device__ __forceinline__ Pair left_of(float p, float q, float ch, float cl) {
-    const float h = ch * q, e = __fmaf_rn(ch, q, -h);  // h + e = ch q
-    const float t = p - h, z = t - p;
-    const float low = ((p - (t - z)) - (h + z)) - __fmaf_rn(cl, q, e);
-    return t > 0.0f || (t == 0.0f && low > 0.0f) ? Pair{t, low} : Pair{0.0f, 0.0f};
+// What is left of p at two tokens: max(p - c q, 0), c = ch + cl; NaN gives 0.
+template <bool kOne>  // c is 1
+__device__ __forceinline__ Pairs left_of(float2 p, float2 q, float ch, float cl) {
+    const float2 h = kOne ? q : __fmul2_rn(q, both(ch));
+    const float2 t = less(p, h), z = less(t, p);
+    float2 low = less(less(p, less(t, z)), __fadd2_rn(h, z));                                    // t + low = p - h
+    if (!kOne) low = __ffma2_rn(q, both(-cl), __fadd2_rn(low, __ffma2_rn(q, both(-ch), h)));     // h + the rest = ch q
+    auto kept = [](float t, float low) { return t > 0.0f ? low : t == 0.0f ? fmaxf(low, 0.0f) : 0.0f; };
+    return Pairs{make_float2(fmaxf(t.x, 0.0f), fmaxf(t.y, 0.0f)), make_float2(kept(t.x, low.x), kept(t.y, low.y))};
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -63,9 +68,10 @@ struct Shared {
     int gone[CBQ_TREE_MAX];          // chosen drafts: the tokens taken out at this node
     double warp[kWarps];             // sums of the warps' stretches
     double blocks[2][kMost];         // and of the blocks', of two passes in turn
+    double tiles[kWarps];            // of the owner's tiles
     double c, left, goal;
     float ch, cl;                    // c as two
-    int at, n_gone, next, count, owner;
+    int at, n_gone, next, count, owner, hit;
     bool draws, summed, some;        // the walk has ended; the sums at hand are those of this node and c; they are not zero
 };
 
@@ -124,69 +130,71 @@ struct Row {
         }
         return v;
     }
-    __device__ __forceinline__ void rest(const Shared &s, int t, int lane, float4 x, float4 y, Pair (&r)[4]) const {
+    __device__ __forceinline__ void rest(const Shared &s, int t, int lane, Pairs (&r)[2]) const {
+        const float4 x = load(p, t, lane);
+        const float2 a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
         if (kDrawn && q) {
-            r[0] = left_of(x.x, y.x, ch, cl), r[1] = left_of(x.y, y.y, ch, cl);
-            r[2] = left_of(x.z, y.z, ch, cl), r[3] = left_of(x.w, y.w, ch, cl);
+            const float4 y = load(q, t, lane);
+            const float2 c = make_float2(y.x, y.y), d = make_float2(y.z, y.w);
+            if (ch == 1.0f && cl == 0.0f) r[0] = left_of<true>(a, c, ch, cl), r[1] = left_of<true>(b, d, ch, cl);
+            else r[0] = left_of<false>(a, c, ch, cl), r[1] = left_of<false>(b, d, ch, cl);
         } else {
             // (NaN gives 0)
-            r[0] = {fmaxf(x.x, 0.0f), 0.0f}, r[1] = {fmaxf(x.y, 0.0f), 0.0f}, r[2] = {fmaxf(x.z, 0.0f), 0.0f}, r[3] = {fmaxf(x.w, 0.0f), 0.0f};
+            r[0] = {make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f)), make_float2(0.0f, 0.0f)};
+            r[1] = {make_float2(fmaxf(b.x, 0.0f), fmaxf(b.y, 0.0f)), make_float2(0.0f, 0.0f)};
             if (!kDrawn) {
                 for (int k = 0; k < s.n_gone; ++k) {
                     const int g = s.gone[k] - (t * kTile + lane * 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (g == e) r[e].hi = 0.0f;
+                    if (g == 0) r[0].hi.x = 0.0f;
+                    if (g == 1) r[0].hi.y = 0.0f;
+                    if (g == 2) r[1].hi.x = 0.0f;
+                    if (g == 3) r[1].hi.y = 0.0f;
                 }
             }
         }
     }
 };
 
-// The token of this warp's tiles at which the sum passes `goal`; the last with
-// any weight where rounding leaves the goal behind it.
-template <typename R>
-__device__ int draw(const Shared &s, const R &row, int t0, int t1, int lane, double goal) {
-    int last = -1;
-    double before = 0.0;
-    for (int t = t0; t < t1; ++t) {
-        Pair r[4];
-        row.rest(s, t, lane, row.load(row.p, t, lane), row.q ? row.load(row.q, t, lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f), r);
-        double upto[4];
-        double sum = 0.0;
-        int mine = -1;
+// The sum of a warp's numbers, by all its lanes.
+__device__ __forceinline__ double warp_sum(Pairs s) {
+    Pairs t = {make_float2(s.hi.x, 0.0f), make_float2(s.lo.x, 0.0f)};
+    add(t, Pairs{make_float2(s.hi.y, 0.0f), make_float2(s.lo.y, 0.0f)});
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            upto[e] = sum += value(r[e]);
-            if (r[e].hi > 0.0f || r[e].lo > 0.0f) mine = t * kTile + lane * 4 + e;
-        }
-        double scan = sum;
+    for (int o = 16; o; o >>= 1)
+        add(t, Pairs{make_float2(__shfl_xor_sync(~0u, t.hi.x, o), 0.0f), make_float2(__shfl_xor_sync(~0u, t.lo.x, o), 0.0f)});
+    return (double)t.hi.x + (double)t.lo.x;
+}
+
+// The token of a tile, by the warp that has it, at which the sum passes `goal`;
+// the last with any weight where rounding leaves the goal behind it (-1: none).
+__device__ __forceinline__ int pick(const Pairs (&r)[2], int t, int lane, double goal) {
+    const float hi[4] = {r[0].hi.x, r[0].hi.y, r[1].hi.x, r[1].hi.y}, lo[4] = {r[0].lo.x, r[0].lo.y, r[1].lo.x, r[1].lo.y};
+    double upto[4], sum = 0.0;
+    int mine = -1;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(~0u, scan, o);
-            if (lane >= o) scan += u;
-        }
-        const unsigned past = __ballot_sync(~0u, before + scan > goal);
-        if (past) {
-            const int lead = __ffs(past) - 1;
-            int token = -1;
-            const double base = before + (scan - sum);
-#pragma unroll
-            for (int e = 3; e >= 0; --e)
-                if (base + upto[e] > goal && (r[e].hi > 0.0f || r[e].lo > 0.0f)) token = t * kTile + lane * 4 + e;
-            if (token < 0) token = mine;  // (rounding: the lane's last)
-            token = __shfl_sync(~0u, token, lead);
-            if (token >= 0) return token;
-        }
-        last = max(last, (int)__reduce_max_sync(~0u, (unsigned)(mine + 1)) - 1);
-        before += __shfl_sync(~0u, scan, 31);
+    for (int e = 0; e < 4; ++e) {
+        upto[e] = sum += (double)hi[e] + (double)lo[e];
+        if (hi[e] > 0.0f || lo[e] > 0.0f) mine = t * kTile + lane * 4 + e;
     }
-    return last;
+    double scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(~0u, scan, o);
+        if (lane >= o) scan += u;
+    }
+    const int last = (int)__reduce_max_sync(~0u, (unsigned)(mine + 1)) - 1;
+    const unsigned past = __ballot_sync(~0u, scan > goal && mine >= 0);
+    if (!past) return last;
+    int token = mine;  // (rounding: the lane's last)
+#pragma unroll
+    for (int e = 3; e >= 0; --e)
+        if (scan - sum + upto[e] > goal && (hi[e] > 0.0f || lo[e] > 0.0f)) token = t * kTile + lane * 4 + e;
+    return __shfl_sync(~0u, token, __ffs(past) - 1);
 }
 
 // grid (1, blocks of the cluster, n_seq).
 template <bool kDrawn, bool kVec>
-__global__ void __launch_bounds__(kThreads) k_verify(Verify a) {
+__global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
     __shared__ Shared s;
     pdl_trigger();
     pdl_wait();
@@ -240,20 +248,16 @@ __global__ void __launch_bounds__(kThreads) k_verify(Verify a) {
         row.q = kDrawn && row.ch > 0.0f ? a.draft + r * a.draft_stride : nullptr;
         if (!s.summed) {
             turn ^= 1;  // (a buffer is written again two passes on: all have read it by then)
-            Pair sum = {0.0f, 0.0f};
+            Pairs sum = {};
 #pragma unroll 4
             for (int t = t0; t < t1; ++t) {
-                Pair v[4];
-                row.rest(s, t, lane, row.load(row.p, t, lane), row.q ? row.load(row.q, t, lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f), v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) add(sum, v[e].hi, v[e].lo);
+                Pairs r[2];
+                row.rest(s, t, lane, r);
+                add(sum, r[0]);
+                add(sum, r[1]);
             }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const float hi = __shfl_xor_sync(~0u, sum.hi, o), lo = __shfl_xor_sync(~0u, sum.lo, o);
-                add(sum, hi, lo);
-            }
-            if (lane == 0) s.warp[warp] = value(sum);
+            const double of_warp = warp_sum(sum);
+            if (lane == 0) s.warp[warp] = of_warp;
             __syncthreads();
             if (warp == 0) {
                 double v = lane < kWarps ? s.warp[lane] : 0.0;
@@ -309,17 +313,60 @@ __global__ void __launch_bounds__(kThreads) k_verify(Verify a) {
         s.goal = goal - before;
     }
     __syncthreads();
-    if (warp != s.owner) return;
-    const int token = draw(s, row, t0, t1, lane, s.goal);
-    if (lane == 0) a.next[seq] = token;
+    if (s.owner < 0) return;
+    // the block shares out the tiles of the warp whose stretch it is
+    const int o0 = min((rank * kWarps + s.owner) * own, tiles), o1 = min(o0 + own, tiles);
+    double goal = s.goal;
+    int last = -1;  // the last tile with any weight
+    for (int base = o0; base < o1; base += kWarps) {
+        const int t = base + warp;
+        Pairs r[2] = {};
+        if (t < o1) row.rest(s, t, lane, r);
+        Pairs sum = r[0];
+        add(sum, r[1]);
+        const double of_tile = warp_sum(sum);
+        if (lane == 0) s.tiles[warp] = of_tile;
+        __syncthreads();
+        int hit = -1;
+        if (warp == 0) {  // (in each warp's own registers the same: one does it, and tells)
+            double before = 0.0;
+            for (int k = 0; k < kWarps && hit < 0; ++k) {
+                if (!(s.tiles[k] > 0.0)) continue;
+                last = base + k;
+                if (goal < before + s.tiles[k]) hit = k;
+                else before += s.tiles[k];
+            }
+            goal -= before;
+            if (lane == 0) s.hit = hit, s.goal = goal;
+        }
+        __syncthreads();
+        if (s.hit >= 0) {
+            if (warp == s.hit) {
+                const int token = pick(r, t, lane, s.goal);
+                if (lane == 0) a.next[seq] = token;
+            }
+            return;
+        }
+        __syncthreads();  // (s.tiles and s.hit are written again)
+    }
+    if (warp == 0) {  // rounding: the last with any weight
+        Pairs r[2] = {};
+        if (last >= 0) row.rest(s, last, lane, r);
+        const int token = pick(r, last, lane, 1e300);
+        if (lane == 0) a.next[seq] = token;
+    }
 }
 
 template <bool kDrawn, bool kVec>
 cudaError_t launch(const Verify &a, cudaStream_t s) {
-    // A row's pass takes a block of a cluster of eight some 2 us, its exchange 1: as many blocks as are free at a time.
+    // As many blocks as fit the GPU at a time, two an SM: a row's pass takes four of them 4 us, its exchange 1.
     const int64_t tiles = (a.V + kTile - 1) / kTile;
     int blocks = kMost;
-    while (blocks > 1 && (blocks * a.n_seq > 2 * 152 || tiles < blocks * kWarps)) blocks /= 2;
+    while (blocks > 1 && (blocks * (int64_t)a.n_seq > 2 * 152 || tiles < blocks * kWarps / 2)) blocks /= 2;
+    if (blocks > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(k_verify<kDrawn, kVec>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     return launch_clusters(k_verify<kDrawn, kVec>, dim3(1, (unsigned)blocks, (unsigned)a.n_seq), blocks, kThreads, 0, s, a);
 }
 
