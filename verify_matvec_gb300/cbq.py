@@ -159,6 +159,7 @@ def _check(status: int, where: str):
 
 # ----------------------------------------------------------- marshalling --
 
+@functools.cache
 def _torch():
     import torch
     return torch
@@ -908,31 +909,44 @@ def cbq_kv_commit(kc, vc, table, ctx, path, count, out=None, err=None, stream=No
     return out
 
 
+@functools.cache
+def _numbers8():
+    torch = _torch()
+    return torch.float8_e4m3fn, torch.float32
+
+
 def _cache8(k8, v8, ks, vs):
     """(cbq_kv_cache8, layers, layer stride, scale layer stride) of CUDA tensors:
     k8, v8 float8_e4m3fn ([layers,] pages, page_size, kv_heads, dim); ks, vs fp32
     ([layers,] pages, page_size / block, kv_heads)."""
-    torch = _torch()
-    if any(t.dtype is not torch.float8_e4m3fn or not t.is_cuda for t in (k8, v8)):
+    f8, f32 = _numbers8()
+    if k8.dtype is not f8 or v8.dtype is not f8 or not k8.is_cuda or not v8.is_cuda:
         raise TypeError("k8 and v8 must be CUDA tensors of torch.float8_e4m3fn")
-    if any(t.dtype is not torch.float32 or not t.is_cuda for t in (ks, vs)):
+    if ks.dtype is not f32 or vs.dtype is not f32 or not ks.is_cuda or not vs.is_cuda:
         raise TypeError("ks and vs must be CUDA tensors of torch.float32")
     shape, st, scales, sst = k8.shape, k8.stride(), ks.shape, ks.stride()
-    layers, stride, scale_stride = 1, 0, 0
     if shape != v8.shape or st != v8.stride() or scales != vs.shape or sst != vs.stride():
         raise ValueError("k8 and v8, and ks and vs, must be of one shape and strides")
-    if len(shape) == 5 and len(scales) == 4 and shape[0] == scales[0]:
-        layers, stride, scale_stride = shape[0], st[0], sst[0]
-        shape, st, scales, sst = shape[1:], st[1:], scales[1:], sst[1:]
-    if len(shape) != 4 or len(scales) != 3 or scales[0] != shape[0] or scales[2] != shape[2]:
-        raise ValueError("k8 and v8 must be (pages, page_size, kv_heads, dim), ks and vs (pages, blocks, kv_heads)")
-    pages, page, heads, dim = shape
-    if st[3] != 1 and dim != 1:
+    layers = 1
+    layer = scale_layer = 0
+    if len(shape) == 4 and len(scales) == 3:
+        pages, page, heads, dim = shape
+        p, t, h, last = st
+        scale_pages, blocks, scale_heads = scales
+        sp, sb, sh = sst
+    elif len(shape) == 5 and len(scales) == 4 and shape[0] == scales[0]:
+        layers, pages, page, heads, dim = shape
+        layer, p, t, h, last = st
+        _, scale_pages, blocks, scale_heads = scales
+        scale_layer, sp, sb, sh = sst
+    else:
+        raise ValueError("k8 and v8 must be ([layers,] pages, page_size, kv_heads, dim), ks and vs ([layers,] pages, blocks, kv_heads)")
+    if scale_pages != pages or scale_heads != heads or blocks < 1 or page % blocks:
+        raise ValueError("ks and vs must have the pages and heads of k8 and v8, and a whole number of tokens to each scale")
+    if last != 1 and dim != 1:
         raise ValueError("the cache's last axis must be contiguous")
-    if scales[1] < 1 or page % scales[1]:
-        raise ValueError("a page must have a whole number of tokens to each of its scales")
-    return cbq_kv_cache8(k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(), heads, dim, page, page // scales[1],
-                         pages, *st[:3], *sst), layers, stride, scale_stride
+    return cbq_kv_cache8(k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(), heads, dim, page, page // blocks,
+                         pages, p, t, h, sp, sb, sh), layers, layer, scale_layer
 
 
 def cbq_kv_quantize(kc, vc, src, k8, v8, ks, vs, dst, err=None, stream=None):
@@ -974,13 +988,14 @@ def cbq_tree_attention8(q, k8, v8, ks, vs, table8, old, kc, vc, table, ctx, star
     shape, dev, i32 = q.shape, q.device, torch.int32
     n, heads, dim = shape
     c = _cache(kc, vc)
-    c8, layers, _, _ = _cache8(k8, v8, ks, vs)
-    if layers != 1 or k8.dim() != 4:
+    c8 = _cache8(k8, v8, ks, vs)[0]
+    if len(k8.shape) != 4:
         raise ValueError("k8 and v8 must be (pages, page_size, kv_heads, dim)")
     if q.dtype != kc.dtype or dim != c.head_dim:
         raise ValueError("q must have the cache's dtype and dim")
     n_seq, width = table.shape
-    if table8.dim() != 2 or table8.shape[0] != n_seq:
+    shape8 = table8.shape
+    if len(shape8) != 2 or shape8[0] != n_seq:
         raise ValueError("table8 must be (sequences, width)")
     if out is None:
         out = _new(shape, q.dtype, dev, stream)
@@ -997,7 +1012,7 @@ def cbq_tree_attention8(q, k8, v8, ks, vs, table8, old, kc, vc, table, ctx, star
     else:
         wp, room = _vec(workspace, torch.uint8, -1, "workspace"), workspace.numel()
     qp, qt, qh = _heads(q, "q")
-    _check(load().cbq_tree_attention8(qp, qt, qh, heads, n, c8, _vec(table8, i32, -1, "table8"), table8.shape[1],
+    _check(load().cbq_tree_attention8(qp, qt, qh, heads, n, c8, _vec(table8, i32, -1, "table8"), shape8[1],
                                       _vec(old, i32, n_seq, "old"), c, _vec(table, i32, -1, "table"), width, n_seq,
                                       _vec(ctx, i32, n_seq, "ctx"), _vec(start, i32, n_seq + 1, "start"),
                                       _vec(mask, torch.int64, n, "mask"), max_tok, max_old, max_new,

@@ -975,6 +975,24 @@ Plan plan_old(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_he
     return p;
 }
 
+// Of the same limits as the last call's (or as the size of the workspace was just asked for with): the same plan.  (It
+// takes the host 3 us to find.)
+struct OldPlan {
+    int n_seq, max_tok, q_heads, kv_heads, head_dim;
+    int64_t max_old, max_new;
+    Plan plan;
+    int n8, chunk8;
+};
+const OldPlan &plan_old_again(int n_seq, int max_tok, int64_t max_old, int64_t max_new, int q_heads, int kv_heads, int head_dim) {
+    static thread_local OldPlan last = {};
+    if (last.n_seq != n_seq || last.max_tok != max_tok || last.max_old != max_old || last.max_new != max_new || last.q_heads != q_heads ||
+        last.kv_heads != kv_heads || last.head_dim != head_dim) {
+        last = OldPlan{n_seq, max_tok, q_heads, kv_heads, head_dim, max_old, max_new, {}, 0, 0};
+        last.plan = plan_old(n_seq, max_tok, max_old, max_new, q_heads, kv_heads, head_dim, &last.n8, &last.chunk8);
+    }
+    return last;
+}
+
 // What the parts of the rows take, for the second kernel to join.
 size_t parts_room(const Plan &p, int64_t total_tok, int q_heads, int head_dim) {
     if (p.n_chunks == 1 || p.cluster) return 16;
@@ -1038,7 +1056,10 @@ template <typename T>
 cudaError_t launch_type(const TreeAttention &a, OldPlaces b, cudaStream_t s) {
     const uintptr_t ends = reinterpret_cast<uintptr_t>(b.c.k) | reinterpret_cast<uintptr_t>(b.c.v);
     if (!whole_rows(a) || ends % 16 != 0 || (b.c.page_stride | b.c.tok_stride | b.c.head_stride) % 16 != 0) return launch_general<T>(a, b, s);
-    return launch_planned<T>(a, b, plan_old(a.n_seq, a.max_tok, b.max_old, b.max_new, a.q_heads, a.c.kv_heads, a.c.head_dim, &b.n8, &b.chunk8), s);
+    const OldPlan &p = plan_old_again(a.n_seq, a.max_tok, b.max_old, b.max_new, a.q_heads, a.c.kv_heads, a.c.head_dim);
+    b.n8 = p.n8;
+    b.chunk8 = p.chunk8;
+    return launch_planned<T>(a, b, p.plan, s);
 }
 
 }  // namespace
@@ -1052,8 +1073,7 @@ size_t tree_attention_workspace(int n_seq, int64_t total_tok, int max_tok, int64
 size_t tree_attention8_workspace(int n_seq, int64_t total_tok, int max_tok, int64_t max_old, int64_t max_new, int q_heads,
                                  int kv_heads, int head_dim) {
     if (!tiled_dim(head_dim)) return 16;
-    int n8, chunk8;
-    return parts_room(plan_old(n_seq, max_tok, max_old, max_new, q_heads, kv_heads, head_dim, &n8, &chunk8), total_tok, q_heads, head_dim);
+    return parts_room(plan_old_again(n_seq, max_tok, max_old, max_new, q_heads, kv_heads, head_dim).plan, total_tok, q_heads, head_dim);
 }
 
 cudaError_t launch_tree_attention(const TreeAttention &a, cudaStream_t s) {

@@ -151,7 +151,7 @@ __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127)
 // Neighbouring units are neighbouring heads, whose rows lie side by side.
 // grid (units of a layer / units a block, layers, 2): keys, then values.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kQuantThreads) k_quantize(KvQuantize a, int warps, uint32_t units) {
+__global__ void __launch_bounds__(kQuantThreads, 3) k_quantize(KvQuantize a, int warps, uint32_t units) {
     __shared__ uint32_t of_warp[kQuantWarps];
     pdl_trigger();
     pdl_wait();

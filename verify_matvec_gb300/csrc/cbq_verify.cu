@@ -30,8 +30,27 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMost = 16;    // blocks of a cluster
 constexpr int kTile = 128;   // tokens that a warp takes at a time, four a lane side by side
 
-// Numbers as two, two at a time: v = hi + lo, |lo| at most half a unit of hi's
-// last place.  A packed instruction does the arithmetic of both.
+// A number as two: v = hi + lo, |lo| at most half a unit of hi's last place.
+struct alignas(8) Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair normal(float hi, float lo) {  // |lo| is small beside hi
+    const float s = hi + lo;
+    return Pair{s, lo - (s - hi)};
+}
+__device__ __forceinline__ Pair plus(Pair a, Pair b) {
+    const float s = a.hi + b.hi, z = s - a.hi;
+    return normal(s, ((a.hi - (s - z)) + (b.hi - z)) + (a.lo + b.lo));
+}
+__device__ __forceinline__ Pair minus(Pair a, Pair b) { return plus(a, Pair{-b.hi, -b.lo}); }
+__device__ __forceinline__ Pair times(Pair a, Pair b) {
+    const float h = a.hi * b.hi, e = __fmaf_rn(a.hi, b.hi, -h);
+    return normal(h, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.lo, e)));
+}
+__device__ __forceinline__ bool under(Pair a, Pair b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ bool some(Pair a) { return a.hi > 0.0f || (a.hi == 0.0f && a.lo > 0.0f); }
+
+// The same, two at a time: a packed instruction does the arithmetic of both.
 struct Pairs {
     float2 hi, lo;
 };
@@ -57,20 +76,20 @@ __device__ __forceinline__ Pairs left_of(float2 p, float2 q, float ch, float cl)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // v at p's place in block r's shared memory.
-__device__ __forceinline__ void peer_store(double *p, uint32_t r, double v) {
-    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.f64 [a], %2;\n}\n" ::"r"(
-                     (uint32_t)__cvta_generic_to_shared(p)), "r"(r), "d"(v) : "memory");
+__device__ __forceinline__ void peer_store(Pair *p, uint32_t r, Pair v) {
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.v2.f32 [a], {%2, %3};\n}\n" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(p)), "r"(r), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
 struct Shared {
     float u[CBQ_TREE_MAX], p[CBQ_TREE_MAX], q[CBQ_TREE_MAX];  // of each draft: its number, and its token's probabilities at its parent
     int token[CBQ_TREE_MAX], parent[CBQ_TREE_MAX], path[CBQ_TREE_MAX];
     int gone[CBQ_TREE_MAX];          // chosen drafts: the tokens taken out at this node
-    double warp[kWarps];             // sums of the warps' stretches
-    double blocks[2][kMost];         // and of the blocks', of two passes in turn
-    double tiles[kWarps];            // of the owner's tiles
-    double c, left, goal;
-    float ch, cl;                    // c as two
+    Pair warp[kWarps];               // sums of the warps' stretches
+    Pair blocks[2][kMost];           // and of the blocks', of two passes in turn
+    Pair tiles[kWarps];              // of the owner's tiles
+    Pair c, left, goal;
+    float u_next;
     int at, n_gone, next, count, owner, hit;
     bool draws, summed, some;        // the walk has ended; the sums at hand are those of this node and c; they are not zero
 };
@@ -80,35 +99,34 @@ struct Shared {
 // child was refused: then its pass was the last.)
 template <bool kDrawn>
 __device__ void walk(Shared &s, int n) {
-    double c = s.c, left = s.left;
+    Pair c = s.c, left = s.left;
     int at = s.at, i = s.next;
     for (; i < n; ++i) {
         if (s.parent[i] != at) continue;
-        const double p = s.p[i], q = s.q[i], u = s.u[i];
-        double rest = p;
+        const Pair p = {s.p[i], 0.0f}, q = {s.q[i], 0.0f}, u = {s.u[i], 0.0f};
+        Pair rest = p;
         if (kDrawn) {
-            rest = p - c * q;
+            rest = minus(p, times(c, q));
         } else {
             for (int k = 0; k < s.n_gone; ++k)
-                if (s.gone[k] == s.token[i]) rest = 0.0;
+                if (s.gone[k] == s.token[i]) rest = {0.0f, 0.0f};
         }
-        if (u * q * left < rest) {
+        if (under(times(times(u, q), left), rest)) {
             s.path[s.count++] = at = i;
-            c = 0.0, left = 1.0;
+            c = {0.0f, 0.0f}, left = {1.0f, 0.0f};
             s.n_gone = 0;
             s.summed = false;
         } else if (!kDrawn) {
-            if (rest > 0.0) s.gone[s.n_gone++] = s.token[i], left -= rest;
-        } else if (left > 0.0) {
-            c += left;
+            if (some(rest)) s.gone[s.n_gone++] = s.token[i], left = minus(left, rest);
+        } else if (some(left)) {
+            c = plus(c, left);
             s.summed = false;
             ++i;
             break;
         }
     }
     s.c = c, s.left = left, s.at = at, s.next = i;
-    s.ch = (float)c, s.cl = (float)(c - (double)s.ch);
-    s.draws = kDrawn ? s.summed || c == 0.0 : true;
+    s.draws = kDrawn ? s.summed || c.hi == 0.0f : true;
 }
 
 // Four tokens side by side, as r: those of this lane of tile t of a row.
@@ -130,12 +148,16 @@ struct Row {
         }
         return v;
     }
-    __device__ __forceinline__ void rest(const Shared &s, int t, int lane, Pairs (&r)[2]) const {
-        const float4 x = load(p, t, lane);
-        const float2 a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
+    struct Tile {
+        float4 p, q;
+    };
+    __device__ __forceinline__ Tile load(int t, int lane) const {
+        return Tile{load(p, t, lane), kDrawn && q ? load(q, t, lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    }
+    __device__ __forceinline__ void rest(const Shared &s, int t, int lane, const Tile &x, Pairs (&r)[2]) const {
+        const float2 a = make_float2(x.p.x, x.p.y), b = make_float2(x.p.z, x.p.w);
         if (kDrawn && q) {
-            const float4 y = load(q, t, lane);
-            const float2 c = make_float2(y.x, y.y), d = make_float2(y.z, y.w);
+            const float2 c = make_float2(x.q.x, x.q.y), d = make_float2(x.q.z, x.q.w);
             if (ch == 1.0f && cl == 0.0f) r[0] = left_of<true>(a, c, ch, cl), r[1] = left_of<true>(b, d, ch, cl);
             else r[0] = left_of<false>(a, c, ch, cl), r[1] = left_of<false>(b, d, ch, cl);
         } else {
@@ -156,39 +178,51 @@ struct Row {
 };
 
 // The sum of a warp's numbers, by all its lanes.
-__device__ __forceinline__ double warp_sum(Pairs s) {
-    Pairs t = {make_float2(s.hi.x, 0.0f), make_float2(s.lo.x, 0.0f)};
-    add(t, Pairs{make_float2(s.hi.y, 0.0f), make_float2(s.lo.y, 0.0f)});
+__device__ __forceinline__ Pair warp_sum(Pairs s) {
+    Pair t = plus(Pair{s.hi.x, s.lo.x}, Pair{s.hi.y, s.lo.y});
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        add(t, Pairs{make_float2(__shfl_xor_sync(~0u, t.hi.x, o), 0.0f), make_float2(__shfl_xor_sync(~0u, t.lo.x, o), 0.0f)});
-    return (double)t.hi.x + (double)t.lo.x;
+    for (int o = 16; o; o >>= 1) t = plus(t, Pair{__shfl_xor_sync(~0u, t.hi, o), __shfl_xor_sync(~0u, t.lo, o)});
+    return t;
+}
+// Inclusive sums over the lanes of a warp.
+__device__ __forceinline__ Pair scan(Pair v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair u = {__shfl_up_sync(~0u, v.hi, o), __shfl_up_sync(~0u, v.lo, o)};
+        if (lane >= o) v = plus(u, v);
+    }
+    return v;
+}
+// The first lane whose inclusive sum passes goal, of those with any weight; the
+// last of them where rounding leaves the goal behind.  *before: the sum before it.
+__device__ __forceinline__ int first_past(Pair upto, bool any, Pair goal, int lane, Pair *before) {
+    const unsigned have = __ballot_sync(~0u, any), past = __ballot_sync(~0u, any && under(goal, upto));
+    const int l = past ? __ffs(past) - 1 : have ? 31 - __clz(have) : 0;
+    const Pair ahead = {__shfl_up_sync(~0u, upto.hi, 1), __shfl_up_sync(~0u, upto.lo, 1)};
+    *before = {__shfl_sync(~0u, lane ? ahead.hi : 0.0f, l), __shfl_sync(~0u, lane ? ahead.lo : 0.0f, l)};
+    return l;
 }
 
 // The token of a tile, by the warp that has it, at which the sum passes `goal`;
 // the last with any weight where rounding leaves the goal behind it (-1: none).
-__device__ __forceinline__ int pick(const Pairs (&r)[2], int t, int lane, double goal) {
-    const float hi[4] = {r[0].hi.x, r[0].hi.y, r[1].hi.x, r[1].hi.y}, lo[4] = {r[0].lo.x, r[0].lo.y, r[1].lo.x, r[1].lo.y};
-    double upto[4], sum = 0.0;
+__device__ __forceinline__ int pick(const Pairs (&r)[2], int t, int lane, Pair goal) {
+    const Pair v[4] = {{r[0].hi.x, r[0].lo.x}, {r[0].hi.y, r[0].lo.y}, {r[1].hi.x, r[1].lo.x}, {r[1].hi.y, r[1].lo.y}};
+    Pair upto[4];
     int mine = -1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        upto[e] = sum += (double)hi[e] + (double)lo[e];
-        if (hi[e] > 0.0f || lo[e] > 0.0f) mine = t * kTile + lane * 4 + e;
+        upto[e] = e ? plus(upto[e - 1], v[e]) : normal(v[0].hi, v[0].lo);
+        if (some(v[e])) mine = t * kTile + lane * 4 + e;
     }
-    double scan = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(~0u, scan, o);
-        if (lane >= o) scan += u;
-    }
+    const Pair all = scan(upto[3], lane);
     const int last = (int)__reduce_max_sync(~0u, (unsigned)(mine + 1)) - 1;
-    const unsigned past = __ballot_sync(~0u, scan > goal && mine >= 0);
+    const unsigned past = __ballot_sync(~0u, under(goal, all) && mine >= 0);
     if (!past) return last;
+    const Pair ahead = {__shfl_up_sync(~0u, all.hi, 1), __shfl_up_sync(~0u, all.lo, 1)};
     int token = mine;  // (rounding: the lane's last)
 #pragma unroll
     for (int e = 3; e >= 0; --e)
-        if (scan - sum + upto[e] > goal && (hi[e] > 0.0f || lo[e] > 0.0f)) token = t * kTile + lane * 4 + e;
+        if (under(goal, lane ? plus(ahead, upto[e]) : upto[e]) && some(v[e])) token = t * kTile + lane * 4 + e;
     return __shfl_sync(~0u, token, __ffs(past) - 1);
 }
 
@@ -222,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
         s.q[tid] = !kDrawn ? 1.0f : real ? a.draft[(b0 + parent) * a.draft_stride + token] : 0.0f;
     }
     if (tid == 0) {
-        s.c = 0.0, s.left = 1.0, s.at = 0, s.next = 1, s.path[0] = 0, s.count = 1, s.n_gone = 0;
+        s.u_next = fminf(fmaxf(a.u_next[seq], 0.0f), 1.0f - 0x1p-24f);
+        s.c = {0.0f, 0.0f}, s.left = {1.0f, 0.0f}, s.at = 0, s.next = 1, s.path[0] = 0, s.count = 1, s.n_gone = 0;
         s.summed = false;
     }
     __syncthreads();
@@ -236,45 +271,55 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
     bool again = false;  // nothing was left: from p itself
     for (;;) {
         if (tid == 0) {
-            if (again) s.ch = s.cl = 0.0f, s.n_gone = 0, s.summed = false;
+            if (again) s.c = {0.0f, 0.0f}, s.n_gone = 0, s.summed = false;
             else walk<kDrawn>(s, n);
         }
         __syncthreads();
         const bool draws = s.draws;
         const int64_t r = b0 + s.at;
         row.p = a.probs + r * a.probs_stride;
-        row.ch = s.ch;
-        row.cl = s.cl;
+        row.ch = s.c.hi;
+        row.cl = s.c.lo;
         row.q = kDrawn && row.ch > 0.0f ? a.draft + r * a.draft_stride : nullptr;
         if (!s.summed) {
             turn ^= 1;  // (a buffer is written again two passes on: all have read it by then)
             Pairs sum = {};
-#pragma unroll 4
-            for (int t = t0; t < t1; ++t) {
-                Pairs r[2];
-                row.rest(s, t, lane, r);
-                add(sum, r[0]);
-                add(sum, r[1]);
+            // two tiles are worked on while the next two are on their way
+            typename Row<kDrawn, kVec>::Tile now[2], next[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) now[j] = row.load(t0 + j < t1 ? t0 + j : tiles, lane);  // (past the end: zeros)
+            for (int t = t0; t < t1; t += 2) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) next[j] = row.load(t + 2 + j < t1 ? t + 2 + j : tiles, lane);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    Pairs r[2];
+                    row.rest(s, t + j, lane, now[j], r);
+                    add(sum, r[0]);
+                    add(sum, r[1]);
+                    now[j] = next[j];
+                }
             }
-            const double of_warp = warp_sum(sum);
+            const Pair of_warp = warp_sum(sum);
             if (lane == 0) s.warp[warp] = of_warp;
             __syncthreads();
             if (warp == 0) {
-                double v = lane < kWarps ? s.warp[lane] : 0.0;
+                Pair v = lane < kWarps ? s.warp[lane] : Pair{0.0f, 0.0f};
 #pragma unroll
-                for (int o = kWarps / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+                for (int o = kWarps / 2; o; o >>= 1) v = plus(v, Pair{__shfl_xor_sync(~0u, v.hi, o), __shfl_xor_sync(~0u, v.lo, o)});
                 if (lane < blocks) peer_store(&s.blocks[turn][rank], lane, v);
             }
             cluster_arrive();
             cluster_wait();
         }
         // (what the walk and the draw go on with, in every block alike)
-        if (tid == 0) {
-            double total = 0.0;
-            for (int o = 0; o < blocks; ++o) total += s.blocks[turn][o];
-            s.left = total;
-            s.some = total > 0.0;
-            s.summed = true;
+        if (warp == 0) {
+            const Pair total = scan(lane < blocks ? s.blocks[turn][lane] : Pair{0.0f, 0.0f}, lane);
+            if (lane == 31) {
+                s.left = total;
+                s.some = some(total);
+                s.summed = true;
+            }
         }
         __syncthreads();
         if (!draws) continue;
@@ -283,60 +328,52 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
         __syncthreads();  // (all have read what the next round writes)
     }
 
-    const bool some = s.some;
+    const bool any = s.some;
     if (rank == 0) {
         const int count = s.count;
         for (int i = tid; i < a.max_tok; i += kThreads) path[i] = i < count ? s.path[i] : -1;
         if (tid == 0) {
             a.count[seq] = count;
-            if (!some) a.next[seq] = -1;
+            if (!any) a.next[seq] = -1;
         }
     }
-    if (!some) return;
-    if (tid == 0) {
-        const double goal = (double)fminf(fmaxf(a.u_next[seq], 0.0f), 1.0f - 0x1p-24f) * s.left;
-        double before = 0.0;
-        int o = 0;
-        for (; o < blocks - 1 && !(goal < before + s.blocks[turn][o]); ++o) before += s.blocks[turn][o];
+    if (!any) return;
+    if (warp == 0) {
+        const Pair none = {0.0f, 0.0f}, of_block = lane < blocks ? s.blocks[turn][lane] : none, of_warp = lane < kWarps ? s.warp[lane] : none;
+        const Pair goal = times(s.left, Pair{s.u_next, 0.0f});
+        Pair before;
         int w = -1;
+        const int o = first_past(scan(of_block, lane), some(of_block), goal, lane, &before);
+        Pair rest = minus(goal, before);
         if (o == rank) {
-            int last = 0;
-            for (int i = 0; i < kWarps && w < 0; ++i) {
-                if (!(s.warp[i] > 0.0)) continue;
-                last = i;
-                if (goal < before + s.warp[i]) w = i;
-                else before += s.warp[i];
-            }
-            if (w < 0) before -= s.warp[w = last];  // (rounding: the last with any weight)
+            w = first_past(scan(of_warp, lane), some(of_warp), rest, lane, &before);
+            rest = minus(rest, before);
         }
-        s.owner = w;
-        s.goal = goal - before;
+        if (lane == 0) s.owner = w, s.goal = rest;
     }
     __syncthreads();
     if (s.owner < 0) return;
     // the block shares out the tiles of the warp whose stretch it is
     const int o0 = min((rank * kWarps + s.owner) * own, tiles), o1 = min(o0 + own, tiles);
-    double goal = s.goal;
+    Pair goal = s.goal;
     int last = -1;  // the last tile with any weight
     for (int base = o0; base < o1; base += kWarps) {
         const int t = base + warp;
         Pairs r[2] = {};
-        if (t < o1) row.rest(s, t, lane, r);
+        if (t < o1) row.rest(s, t, lane, row.load(t, lane), r);
         Pairs sum = r[0];
         add(sum, r[1]);
-        const double of_tile = warp_sum(sum);
+        const Pair of_tile = warp_sum(sum);
         if (lane == 0) s.tiles[warp] = of_tile;
         __syncthreads();
-        int hit = -1;
-        if (warp == 0) {  // (in each warp's own registers the same: one does it, and tells)
-            double before = 0.0;
-            for (int k = 0; k < kWarps && hit < 0; ++k) {
-                if (!(s.tiles[k] > 0.0)) continue;
-                last = base + k;
-                if (goal < before + s.tiles[k]) hit = k;
-                else before += s.tiles[k];
-            }
-            goal -= before;
+        if (warp == 0) {
+            const Pair v = lane < kWarps ? s.tiles[lane] : Pair{0.0f, 0.0f}, upto = scan(v, lane);
+            const Pair all = {__shfl_sync(~0u, upto.hi, 31), __shfl_sync(~0u, upto.lo, 31)};
+            const unsigned have = __ballot_sync(~0u, some(v));
+            if (have) last = base + 31 - __clz(have);
+            Pair before = all;
+            const int hit = under(goal, all) ? first_past(upto, some(v), goal, lane, &before) : -1;
+            goal = minus(goal, before);
             if (lane == 0) s.hit = hit, s.goal = goal;
         }
         __syncthreads();
@@ -351,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
     }
     if (warp == 0) {  // rounding: the last with any weight
         Pairs r[2] = {};
-        if (last >= 0) row.rest(s, last, lane, r);
-        const int token = pick(r, last, lane, 1e300);
+        if (last >= 0) row.rest(s, last, lane, row.load(last, lane), r);
+        const int token = pick(r, last, lane, Pair{INFINITY, 0.0f});
         if (lane == 0) a.next[seq] = token;
     }
 }
