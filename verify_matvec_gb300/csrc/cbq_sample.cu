@@ -435,9 +435,9 @@ struct Part {
     // The index where value(two logits) of what is listed and counts(index, logit,
     // value), summed in the order of the indices over the whole row, reaches
     // need(sum); -1 in the blocks that do not hold it.  *total: the row's sum;
-    // *at: the value there.
-    template <typename V, typename C, typename G>
-    __device__ int walk(V value, C counts, G need, uint64_t *total, uint64_t *at) {
+    // *at: the value there.  kept(place in the list, value) is told each one's.
+    template <typename V, typename C, typename G, typename K>
+    __device__ int walk(V value, C counts, G need, uint64_t *total, uint64_t *at, K kept) {
         const int start = first + warp * N * 32;
         uint64_t mine = 0;
         for (int i0 = 0; i0 < listed; i0 += 128) {  // two chains of arithmetic at a time (and within the stretch)
@@ -446,8 +446,11 @@ struct Part {
                 const int i = i0 + j * 32 + lane;
                 const float la = list[i], lb = list[i + 32];
                 const Two v = value(la, lb);
-                mine += i < listed && counts(start + (whole ? i : (int)place[i]), la, v.a) ? v.a : 0;
-                mine += i + 32 < listed && counts(start + (whole ? i + 32 : (int)place[i + 32]), lb, v.b) ? v.b : 0;
+                const uint64_t a = i < listed && counts(start + (whole ? i : (int)place[i]), la, v.a) ? v.a : 0;
+                const uint64_t b = i + 32 < listed && counts(start + (whole ? i + 32 : (int)place[i + 32]), lb, v.b) ? v.b : 0;
+                kept(i, a);
+                kept(i + 32, b);
+                mine += a + b;
             }
         }
         // at most 2^50 a lane: the sum of a warp in two halves
@@ -565,6 +568,11 @@ __device__ __forceinline__ Inverse inverse(uint64_t mass) {
     const float m = (float)mass, rest = (float)(int64_t)(mass - (uint64_t)m);
     const float hi = 8388608.0f / m;
     return Inverse{hi, (__fmaf_rn(-hi, m, 8388608.0f) - hi * rest) / m};
+}
+// A weight as fp32, in units of 2^23.
+__device__ __forceinline__ float weight_f32(uint64_t w) {
+    const float h = __uint_as_float(0x4B000000u | (uint32_t)(w >> 23)) - 8388608.0f;
+    return __fmaf_rn(__uint_as_float(0x4B000000u | ((uint32_t)w & 0x7FFFFFu)) - 8388608.0f, 0x1p-23f, h);
 }
 __device__ __forceinline__ float part_of(uint64_t w, Inverse inv) {
     const float h = __uint_as_float(0x4B000000u | (uint32_t)(w >> 23)) - 8388608.0f;
@@ -800,22 +808,33 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
     uint64_t total, value;
     if (ties != ~0ull) {
         const int i = row.walk([](float, float) { return Two{1, 1}; }, [&](int, float l, uint64_t) { return l == tau; },
-                               [&](uint64_t) { return ties; }, &total, &value);
+                               [&](uint64_t) { return ties; }, &total, &value, [](int, uint64_t) {});
         last = (int)__reduce_max_sync(~0u, (uint32_t)row.tell((uint64_t)(i + 1), 0).x) - 1;
     }
     auto stays = [&](int at, float l, uint64_t v) { return (l > tau || (l == tau && at <= last)) && v >= floor_w; };
+    // The whole distribution alone: the weights take the logits' places in the list, as fp32 (a half unit of its last place
+    // off), and need no second go.  With a token to be drawn its block needs the logits again.
+    const bool alone = kDist && !a.u;
     const int i = row.walk([&](float x, float y) { return weigh(x, y, sc, s.table); }, stays,
-                           [&](uint64_t sum) { return taken(sum, u); }, &total, &value);
+                           [&](uint64_t sum) { return alone ? 0 : taken(sum, u); }, &total, &value, [&](int at, uint64_t w) {
+                               if (kDist && alone) row.list[at] = weight_f32(w);
+                           });
     if constexpr (kDist) {
         const Inverse inv = inverse(total);
         for (int i0 = 0; i0 < row.listed; i0 += 64) {
             const int i1 = i0 + lane, i2 = i1 + 32;
             const float la = row.list[i1], lb = row.list[i2];
-            const Two v = weigh(la, lb, sc, s.table);
             const int base = row.first + warp * N * 32;
             const int at1 = base + (row.whole ? i1 : (int)row.place[i1]), at2 = base + (row.whole ? i2 : (int)row.place[i2]);
-            if (row.whole ? at1 < a.V : i1 < row.listed && stays(at1, la, v.a)) dist[at1] = part_of(v.a, inv);
-            if (row.whole ? at2 < a.V : i2 < row.listed && stays(at2, lb, v.b)) dist[at2] = part_of(v.b, inv);
+            float pa = __fmaf_rn(la, inv.hi, la * inv.lo), pb = __fmaf_rn(lb, inv.hi, lb * inv.lo);
+            bool in1 = row.whole ? at1 < a.V : i1 < row.listed, in2 = row.whole ? at2 < a.V : i2 < row.listed;
+            if (!alone) {
+                const Two v = weigh(la, lb, sc, s.table);
+                pa = part_of(v.a, inv), pb = part_of(v.b, inv);
+                in1 = in1 && (row.whole || stays(at1, la, v.a)), in2 = in2 && (row.whole || stays(at2, lb, v.b));
+            }
+            if (in1) dist[at1] = pa;
+            if (in2) dist[at2] = pb;
         }
     }
     if (i >= 0 && threadIdx.x == 0 && (!kDist || a.ids)) {
