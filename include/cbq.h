@@ -554,13 +554,14 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
  * (the weights, the order and the cuts are cbq_sample's; a weight under 2^-46
  * has no mass).  T <= 0 or NaN gives 1 to the first of the order; a row of
  * nothing but -inf and NaN gives zeros.  out_dev: n x V fp32, row c at out_dev
- * + c*out_stride, not overlapping the logits; each value is within 2^-23
+ * + c*out_stride; each value is within 2^-23
  * (relative) of its quotient, and that within 2^-38 of the formula's, both
  * plus 2^-46 absolute.  u_dev and
  * ids_dev, both or neither: one token a row is drawn too, the same that
- * cbq_sample draws.  One launch.  Errors as cbq_sample, and EINVAL (out_dev
+ * cbq_sample draws.  out_dev and ids_dev overlap nothing that the call reads,
+ * nor each other.  One launch.  Errors as cbq_sample, and EINVAL (out_dev
  * null, out_stride < V with n > 1 or < 0, one of u_dev and ids_dev alone, an
- * out_dev that overlaps the logits). */
+ * output that overlaps). */
 int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
               float *out_dev, int64_t out_stride, int32_t *ids_dev, void *stream);
@@ -595,12 +596,13 @@ int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_strid
  * one whose rows leave [0, total_tok) counts as empty, and both set
  * CBQ_DEVERR_BAD_LENGTH; a node whose parent is not before it is never
  * reached.  u_dev[row] (total_tok; node 0's is not used) and u_next_dev
- * (n_seq) in [0, 1).  One launch; nothing but the rows of the nodes that the
- * walk passes is read.
+ * (n_seq) in [0, 1).  path_dev, count_dev and next_dev overlap nothing that the
+ * call reads, nor one another.  One launch; nothing but the rows of the nodes
+ * that the walk passes is read.
  * Errors: EINVAL (null; V < 1 or > CBQ_SAMPLE_MAX_V; probs_stride or
  * draft_stride < V with total_tok > 1, or < 0; total_tok < 1 or > 2^24; n_seq
  * < 1 or > 65535; max_tok outside 1..CBQ_TREE_MAX; a pointer not aligned to
- * its type), ECUDA, EDEVICE. */
+ * its type; an output that overlaps), ECUDA, EDEVICE. */
 int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_dev, int64_t draft_stride, int V,
                const int32_t *tokens_dev, const int32_t *parent_dev, int64_t total_tok, const int32_t *start_dev,
                int n_seq, int max_tok, const float *u_dev, const float *u_next_dev, int32_t *path_dev,
@@ -619,10 +621,11 @@ int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_
  * cache is not read or written and sets CBQ_DEVERR_BAD_SLOT.  ctx_out_dev is
  * written for every sequence: what counts there is how many entries of the
  * path were good.  Pages that two of the call's sequences name must not lie
- * behind their contexts.  ctx_out_dev may be NULL, and must not be ctx_dev.
+ * behind their contexts.  ctx_out_dev may be NULL, and overlaps
+ * nothing that the call reads (other sequences' blocks are still at it).
  * Errors: EINVAL (null; a bad cache; layers < 1 or > 65535; layer_stride < 0;
  * table_width < 1; n_seq < 1 or > 65535; max_tok outside 1..CBQ_TREE_MAX;
- * ctx_out_dev == ctx_dev; a pointer not aligned to its type), ECUDA, EDEVICE. */
+ * a ctx_out_dev that overlaps; a pointer not aligned to its type), ECUDA, EDEVICE. */
 int cbq_kv_commit(const cbq_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table_dev,
                   int table_width, int n_seq, const int32_t *ctx_dev, const int32_t *path_dev, int max_tok,
                   const int32_t *count_dev, int32_t *ctx_out_dev, unsigned int *err_dev, void *stream);
@@ -661,7 +664,7 @@ typedef struct cbq_kv_cache8 {
  *           would take a maximum above 448 * 2^120).
  * A scale that is a power of two costs a floating-point number no precision,
  * so the bytes do not depend on how the division rounds.  NaN and infinities
- * become NaN.  A negative entry of src_dev or dst_dev skips its pair; one
+ * become NaN.  The two caches do not overlap.  A negative entry of src_dev or dst_dev skips its pair; one
  * beyond the cache does too and sets CBQ_DEVERR_BAD_SLOT.  Two pairs with one
  * dst page race.  One launch.
  * Errors: EINVAL (null; a bad cache; heads, head_dim or page_size that differ;
@@ -751,12 +754,13 @@ int cbq_moe_debug_stall(cbq_moe *L, int mode);
 int cbq_debug_mmq_stall(cbq_weights *W, int mode);
 
 /* Give-up test mode of the calling thread's cbq_tree_attention and
- * cbq_tree_attention8 calls (0 turns it off): with mode 1 the first block of the many-row kernel copies no tile,
- * so its roles' bounded waits give up after 1 s (CBQ_DEVERR_PIPE_TIMEOUT in
- * *err_dev), and it frees its tensor memory and ends.  Such a call returns
- * after about a second, sets only that bit, leaves that block's rows (of the
- * first sequence and kv head) undefined and the others as they would be; the
- * next call is correct.  Calls that the other kernels take are not touched.
+ * cbq_tree_attention8 calls (0 turns it off): with mode 1 the first block of
+ * the many-row kernel copies no tile, so its roles' bounded waits give up after
+ * 1 s (CBQ_DEVERR_PIPE_TIMEOUT in *err_dev), and it frees its tensor memory and
+ * ends.  Such a call returns after about a second, sets only that bit, leaves
+ * that block's rows (of the first sequence and kv head) undefined and the
+ * others as they would be; the next call is correct.  Calls that the other
+ * kernels take are not touched.
  * Errors: EINVAL (mode outside 0..1). */
 int cbq_debug_tree_stall(int mode);
 

@@ -904,6 +904,31 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
 
 // ----------------------------------- behind the logits, and the cache ------
 
+namespace {
+
+struct Span {
+    const void *p;  // null: nothing
+    uint64_t bytes;
+};
+// No output overlaps an input or another output: blocks of several rows or
+// sequences read and write at the same time.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto meet = [](const Span &a, const Span &b) {
+        const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (const Span &o : outs) {
+        for (const Span &i : ins)
+            if (meet(o, i)) return false;
+        for (const Span &other : outs)
+            if (&o < &other && meet(o, other)) return false;
+    }
+    return true;
+}
+uint64_t rows_bytes(int64_t n, int64_t stride, int V, size_t size) { return ((uint64_t)stride * (n - 1) + V) * size; }
+
+}  // namespace
+
 int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,
               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
               float *out_dev, int64_t out_stride, int32_t *ids_dev, void *stream) {
@@ -913,9 +938,11 @@ int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_strid
         !aligned_to(top_p_dev, 4) || !aligned_to(min_p_dev, 4) || !aligned_to(u_dev, 4) || !aligned_to(ids_dev, 4) ||
         !aligned_to(out_dev, 4))
         return CBQ_EINVAL;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(logits_dev), y = reinterpret_cast<uintptr_t>(out_dev);
-    const uintptr_t x_bytes = ((uintptr_t)row_stride * (n - 1) + V) * dtype_bytes(dtype), y_bytes = ((uintptr_t)out_stride * (n - 1) + V) * 4;
-    if (x < y + y_bytes && y < x + x_bytes) return CBQ_EINVAL;
+    const uint64_t each = (uint64_t)n * 4;
+    if (!apart({{out_dev, rows_bytes(n, out_stride, V, 4)}, {ids_dev, each}},
+               {{logits_dev, rows_bytes(n, row_stride, V, dtype_bytes(dtype))}, {temperature_dev, each}, {top_k_dev, each},
+                {top_p_dev, each}, {min_p_dev, each}, {u_dev, each}}))
+        return CBQ_EINVAL;
     int dev = 0;
     const int rc = check_device(&dev);
     if (rc != CBQ_OK) return rc;
@@ -939,6 +966,11 @@ int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_
                           (const void *)u_next_dev, (const void *)path_dev, (const void *)count_dev,
                           (const void *)next_dev, (const void *)err_dev})
         if (!aligned_to(p, 4)) return CBQ_EINVAL;
+    const uint64_t nodes = (uint64_t)total_tok * 4, each = (uint64_t)n_seq * 4;
+    if (!apart({{path_dev, each * max_tok}, {count_dev, each}, {next_dev, each}},
+               {{probs_dev, rows_bytes(total_tok, probs_stride, V, 4)}, {draft_dev, rows_bytes(total_tok, draft_stride, V, 4)},
+                {tokens_dev, nodes}, {parent_dev, nodes}, {start_dev, each + 4}, {u_dev, nodes}, {u_next_dev, each}}))
+        return CBQ_EINVAL;
     int dev = 0;
     const int rc = check_device(&dev);
     if (rc != CBQ_OK) return rc;
@@ -953,8 +985,11 @@ int cbq_kv_commit(const cbq_kv_cache *cache, int layers, int64_t layer_stride, c
                   const int32_t *count_dev, int32_t *ctx_out_dev, unsigned int *err_dev, void *stream) {
     if (!good_cache(cache) || layers < 1 || layers > 65535 || layer_stride < 0 || !table_dev || table_width < 1 ||
         n_seq < 1 || n_seq > 65535 || !ctx_dev || !path_dev || max_tok < 1 || max_tok > CBQ_TREE_MAX || !count_dev ||
-        ctx_out_dev == ctx_dev || !aligned_to(table_dev, 4) || !aligned_to(ctx_dev, 4) || !aligned_to(path_dev, 4) ||
+        !aligned_to(table_dev, 4) || !aligned_to(ctx_dev, 4) || !aligned_to(path_dev, 4) ||
         !aligned_to(count_dev, 4) || !aligned_to(ctx_out_dev, 4) || !aligned_to(err_dev, 4))
+        return CBQ_EINVAL;
+    const uint64_t each = (uint64_t)n_seq * 4;
+    if (!apart({{ctx_out_dev, each}}, {{table_dev, each * table_width}, {ctx_dev, each}, {path_dev, each * max_tok}, {count_dev, each}}))
         return CBQ_EINVAL;
     int dev = 0;
     const int rc = check_device(&dev);
