@@ -1,6 +1,7 @@
 """One verify step of speculative decoding through the library: a tree of
-drafted tokens goes through one decoder layer and the output head, and a token
-is drawn at each of them.
+drafted tokens goes through one decoder layer and the output head, and either a
+token is drawn at each of them, or the tree is verified against what its drafts
+were drawn from and the cache brought up to date.
 
     x (tokens x hidden)
       -> cbq_matvec            q, k, v of the drafts (codebook-4bit weights)
@@ -10,6 +11,10 @@ is drawn at each of them.
       -> cbq_moe_matvec_logits routed experts, residual
       -> cbq_matvec            logits
       -> cbq_sample            one token a draft
+    or
+      -> cbq_probs             the target's and the drafter's distributions
+      -> cbq_verify            the accepted drafts and the token behind them
+      -> cbq_kv_commit         their keys and values to the end of the context
 
 Run it: python examples/verify_step.py  (random weights; needs the GPU).
 """
@@ -79,6 +84,22 @@ def accepted(ids, drafts, parents):
             return path
 
 
+def settle(layer, ctx, parents, table, tokens, logits, drafter, temperature, top_k, top_p, u, u_next):
+    """What stays of a step's drafts, so that what comes out is distributed as
+    the target's own tokens: logits (nodes, V) of the step, drafter (nodes, V)
+    the logits from which each node's children were drawn, with the same
+    temperature and cuts, tokens (nodes) int32 the drafts (node 0's is settled
+    already).  The cache keeps the accepted nodes behind the context.  Returns
+    path and count (the accepted nodes), the next token and the new length."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=logits.device)  # noqa: E731
+    n = logits.shape[0]
+    probs = cbq.cbq_probs(logits, temperature, top_k, top_p, None)
+    draft = cbq.cbq_probs(drafter, temperature, top_k, top_p, None)
+    path, count, token = cbq.cbq_verify(probs, draft, tokens, i32(parents), i32([0, n]), u, u_next, n)
+    length = cbq.cbq_kv_commit(layer.kc, layer.vc, table, i32([ctx]), path, count)
+    return {"path": path, "count": count, "token": token, "length": length, "probs": probs, "draft": draft}
+
+
 def main():
     layer = Layer()
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -96,6 +117,16 @@ def main():
     drafts = [0, ids[0], ids[1], 7, 9]  # (as if the drafter had guessed the first branch)
     print("drawn", ids, "probabilities", [round(p, 3) for p in r["probs"].tolist()])
     print("accepted drafts", accepted(ids, drafts, parents))
+    # the same step's tree as a drafter's own draws: its logits are near the target's
+    drafter = r["logits"] + 0.3 * torch.randn(r["logits"].shape, generator=g, device="cuda")
+    cuts = (f(0.8, torch.float32), f(50, torch.int32), f(0.95, torch.float32))
+    drawn = torch.zeros(n, dtype=torch.int32, device="cuda")
+    for i, p in enumerate(parents):
+        if p >= 0:
+            drawn[i] = cbq.cbq_sample(drafter[p:p + 1], *(c[:1] for c in cuts), None, torch.rand(1, generator=g, device="cuda"))[0][0]
+    s = settle(layer, ctx, parents, table, drawn, r["logits"], drafter, *cuts, torch.rand(n, generator=g, device="cuda"),
+               torch.rand(1, generator=g, device="cuda"))
+    print("verified: nodes", s["path"][0].tolist(), "next token", s["token"].item(), "context", s["length"].item())
 
 
 if __name__ == "__main__":
