@@ -15,7 +15,14 @@
 // What a sum can hide decides here (a token is the answer or it is not), so
 // terms and sums are pairs of fp32 numbers, some 2^-48 of their size off: 64-bit
 // arithmetic is a sixty-fourth as wide on this GPU and would be the bound, pairs
-// cost 20 instructions a token and are not.
+// cost some 15 instructions a token and are near it.
+//
+// 64 trees of 12 drafts over 129,280 tokens take 32 us (the slowest of them four
+// passes, each some 10,000 clocks of loads and sums in a quarter of the row, 3,000
+// of exchange and 2,000 of walk, and a draw of 6,000), 200 of 6 70 us, one of 5
+// 7 us.  (With two tiles less ahead where only p is read, and three operations a pair
+// of tokens more in the differences: 37, 81 and 7.2.  With bulk copies into a
+// ring of each warp's own, of 1 KB: 46 and 108.)
 #include <algorithm>
 
 #include "cbq_device.cuh"
@@ -56,6 +63,11 @@ struct Pairs {
 };
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 less(float2 a, float2 b) { return __ffma2_rn(b, both(-1.0f), a); }  // a - b
+__device__ __forceinline__ void add(Pairs &s, float2 x) {
+    const float2 t = __fadd2_rn(s.hi, x), z = less(t, s.hi);
+    s.lo = __fadd2_rn(s.lo, __fadd2_rn(less(s.hi, less(t, z)), less(x, z)));
+    s.hi = t;
+}
 __device__ __forceinline__ void add(Pairs &s, Pairs x) {
     const float2 t = __fadd2_rn(s.hi, x.hi), z = less(t, s.hi);
     s.lo = __fadd2_rn(s.lo, __fadd2_rn(__fadd2_rn(less(s.hi, less(t, z)), less(x.hi, z)), x.lo));
@@ -63,12 +75,19 @@ __device__ __forceinline__ void add(Pairs &s, Pairs x) {
 }
 
 // What is left of p at two tokens: max(p - c q, 0), c = ch + cl; NaN gives 0.
+// Only where c q <= p does the rounding of the difference count, and there it is
+// (p - t) - c q.
 template <bool kOne>  // c is 1
 __device__ __forceinline__ Pairs left_of(float2 p, float2 q, float ch, float cl) {
-    const float2 h = kOne ? q : __fmul2_rn(q, both(ch));
-    const float2 t = less(p, h), z = less(t, p);
-    float2 low = less(less(p, less(t, z)), __fadd2_rn(h, z));                                    // t + low = p - h
-    if (!kOne) low = __ffma2_rn(q, both(-cl), __fadd2_rn(low, __ffma2_rn(q, both(-ch), h)));     // h + the rest = ch q
+    if (kOne) {  // p less the smaller of the two
+        p = make_float2(fmaxf(p.x, 0.0f), fmaxf(p.y, 0.0f));
+        q = make_float2(fminf(p.x, q.x), fminf(p.y, q.y));
+        const float2 t = less(p, q);
+        return Pairs{t, less(less(p, t), q)};
+    }
+    const float2 h = __fmul2_rn(q, both(ch)), t = less(p, h);
+    // t + low = p - h, h + the rest = ch q
+    const float2 low = __ffma2_rn(q, both(-cl), __fadd2_rn(less(less(p, t), h), __ffma2_rn(q, both(-ch), h)));
     auto kept = [](float t, float low) { return t > 0.0f ? low : t == 0.0f ? fmaxf(low, 0.0f) : 0.0f; };
     return Pairs{make_float2(fmaxf(t.x, 0.0f), fmaxf(t.y, 0.0f)), make_float2(kept(t.x, low.x), kept(t.y, low.y))};
 }
@@ -177,6 +196,34 @@ struct Row {
     }
 };
 
+// The sums of a lane's tokens of tiles t0 .. t1 - 1: kAhead tiles are worked on
+// while the next as many are on their way.
+template <int kAhead, bool kBoth, bool kDrawn, bool kVec>
+__device__ __forceinline__ void sum_of(const Row<kDrawn, kVec> &row, const Shared &s, int t0, int t1, int tiles, int lane, Pairs &sum) {
+    float4 p[2][kAhead], q[2][kAhead];
+    auto take = [&](int to, int t) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = t + j < t1 ? t + j : tiles;  // (past the end: zeros)
+            p[to][j] = row.load(row.p, i, lane);
+            if (kBoth) q[to][j] = row.load(row.q, i, lane);
+        }
+    };
+    take(0, t0);
+    for (int t = t0; t < t1; t += kAhead) {
+        take(1, t + kAhead);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            Pairs r[2];
+            row.rest(s, t + j, lane, {p[0][j], kBoth ? q[0][j] : float4{}}, r);
+            if (kBoth) add(sum, r[0]), add(sum, r[1]);
+            else add(sum, r[0].hi), add(sum, r[1].hi);
+            p[0][j] = p[1][j];
+            if (kBoth) q[0][j] = q[1][j];
+        }
+    }
+}
+
 // The sum of a warp's numbers, by all its lanes.
 __device__ __forceinline__ Pair warp_sum(Pairs s) {
     Pair t = plus(Pair{s.hi.x, s.lo.x}, Pair{s.hi.y, s.lo.y});
@@ -284,22 +331,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
         if (!s.summed) {
             turn ^= 1;  // (a buffer is written again two passes on: all have read it by then)
             Pairs sum = {};
-            // two tiles are worked on while the next two are on their way
-            typename Row<kDrawn, kVec>::Tile now[2], next[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) now[j] = row.load(t0 + j < t1 ? t0 + j : tiles, lane);  // (past the end: zeros)
-            for (int t = t0; t < t1; t += 2) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) next[j] = row.load(t + 2 + j < t1 ? t + 2 + j : tiles, lane);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    Pairs r[2];
-                    row.rest(s, t + j, lane, now[j], r);
-                    add(sum, r[0]);
-                    add(sum, r[1]);
-                    now[j] = next[j];
-                }
-            }
+            if (kDrawn && row.q) sum_of<2, true>(row, s, t0, t1, tiles, lane, sum);
+            else sum_of<kDrawn ? 4 : 2, false>(row, s, t0, t1, tiles, lane, sum);
             const Pair of_warp = warp_sum(sum);
             if (lane == 0) s.warp[warp] = of_warp;
             __syncthreads();
@@ -396,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
 
 template <bool kDrawn, bool kVec>
 cudaError_t launch(const Verify &a, cudaStream_t s) {
-    // As many blocks as fit the GPU at a time, two an SM: a row's pass takes four of them 4 us, its exchange 1.
+    // As many blocks as fit the GPU at a time, two an SM: a row's pass takes four of them 5 us, its exchange 1.5.
     const int64_t tiles = (a.V + kTile - 1) / kTile;
     int blocks = kMost;
     while (blocks > 1 && (blocks * (int64_t)a.n_seq > 2 * 152 || tiles < blocks * kWarps / 2)) blocks /= 2;
