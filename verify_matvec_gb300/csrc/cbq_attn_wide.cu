@@ -17,7 +17,7 @@
 // follow its mask there, and a value row with NaN or infinities, which some
 // rows may not see (0 * v would be NaN), is zeroed in shared memory by the
 // copying warp and added by hand to the rows that see it.
-// Roles: warps 0..3 and 4..7 the two groups, 8 and 9 the copies, 10 the scores'
+// Roles (places of 16 bits): warps 0..3 and 4..7 the two groups, 8 and 9 the copies, 10 the scores'
 // products and 11 the sums' (waiting, issuing and committing takes a warp as
 // long as the products themselves: one warp for both was the bound).
 // Tiles lie in shared memory in halves of 64 columns, 128 bytes a row, the 16-
@@ -33,6 +33,19 @@
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
 // MB) take 60 us: some 5 us a block beside its keys, an uneven last wave, and
 // 1,120 of 1,440 blocks without keys that take their turn on an SM all the same.
+//
+// Old places in 8 bits are blocks of their own.  Their numbers become fp16 on
+// the way (the tensor cores want both operands of one kind, and the weights need
+// more than 4 bits), their scales go to the scores and the weights.  Roles: warps
+// 0..7 as above, 8..11 widen the tiles, 12 and 13 the products, 14 and 15 copy.
+// 8 sequences of 64 drafts over 16,000 keys in 8 bits (282 MB) and 64 behind them take
+// 355 to 410 us, by the scales (750 to 650 TFLOP/s).  Issue slots are the bound:
+// the warps that widen and those that weigh want 47% of them, with 1.4 waits for
+// an instruction to each (16 bits: 41%, 0.6), as eight copies of long unrolled
+// loops share the caches for instructions.  24 ragged sequences of up to 78 rows
+// (76 MB) take 103 us: starts and ends of blocks, as above, of both kinds.  (Keys
+// as they are, the query as a sum of e4m3 and e5m2 parts: two or three products
+// where one is, and 8 x 64 drafts 358 -> 392 us in bf16, 437 in fp16.)
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
