@@ -19,10 +19,11 @@
 //
 // 64 trees of 12 drafts over 129,280 tokens take 32 us (the slowest of them four
 // passes, each some 10,000 clocks of loads and sums in a quarter of the row, 3,000
-// of exchange and 2,000 of walk, and a draw of 6,000), 200 of 6 70 us, one of 5
-// 7 us.  (With two tiles less ahead where only p is read, and three operations a pair
-// of tokens more in the differences: 37, 81 and 7.2.  With bulk copies into a
-// ring of each warp's own, of 1 KB: 46 and 108.)
+// of exchange and 2,000 of walk, and a draw of 6,000), 200 of 6 57 us, one of 5
+// 7 us: latencies, with issue slots 14% and memory 15% busy.  (With two tiles less
+// ahead where only p is read, and three operations a pair of tokens more in the
+// differences, the 64 trees took 37 us; with bulk copies into a ring of each
+// warp's own, of 1 KB, 46.)
 #include <algorithm>
 
 #include "cbq_device.cuh"
@@ -429,10 +430,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
 
 template <bool kDrawn, bool kVec>
 cudaError_t launch(const Verify &a, cudaStream_t s) {
-    // As many blocks as fit the GPU at a time, two an SM: a row's pass takes four of them 5 us, its exchange 1.5.
-    const int64_t tiles = (a.V + kTile - 1) / kTile;
-    int blocks = kMost;
-    while (blocks > 1 && (blocks * (int64_t)a.n_seq > 2 * 152 || tiles < blocks * kWarps / 2)) blocks /= 2;
+    // Blocks of a sequence: what a pass costs beside the rows (walk, exchange, draw) is some 1,260 tiles' worth, and the GPU
+    // takes two blocks an SM at a time.  64 trees: 4 blocks 32 us, 8 40; 200: 1 block 70, 2 58 (chosen drafts: 41 and 43).
+    const int64_t tiles = (a.V + kTile - 1) / kTile, rows = kDrawn ? 2 : 1;
+    int blocks = 1;
+    double least = 0.0;
+    for (int b = 1; b <= kMost && (b == 1 || tiles >= b * kWarps / 2); b *= 2) {
+        const double t = std::max(1.0, (double)b * a.n_seq / (2 * 152)) * (1260.0 + (double)(tiles * rows) / b);
+        if (b == 1 || t < least) least = t, blocks = b;
+    }
     if (blocks > 8) {
         const cudaError_t e = cudaFuncSetAttribute(k_verify<kDrawn, kVec>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
