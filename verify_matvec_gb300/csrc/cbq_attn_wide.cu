@@ -43,9 +43,11 @@
 // the warps that widen and those that weigh want 47% of them, with 1.4 waits for
 // an instruction to each (16 bits: 41%, 0.6), as eight copies of long unrolled
 // loops share the caches for instructions.  24 ragged sequences of up to 78 rows
-// (76 MB) take 103 us: starts and ends of blocks, as above, of both kinds.  (Keys
+// (76 MB) take 95 us: starts and ends of blocks, as above, of both kinds.  (Keys
 // as they are, the query as a sum of e4m3 and e5m2 parts: two or three products
 // where one is, and 8 x 64 drafts 358 -> 392 us in bf16, 437 in fp16.)
+#include <algorithm>
+
 #include "cbq_pipe.cuh"
 #include "step/cbq_attn.cuh"
 
@@ -56,7 +58,9 @@ namespace {
 constexpr int kGroup = 128;                   // rows of a group
 constexpr int kTile = 64;                     // keys of a tile
 constexpr int kStages = 5;
-constexpr int kOldStages = 3, kRaw = 4;       // old places: of their tiles as fp16, and as they are in memory
+constexpr int kRaw = 4;                       // old places: of their tiles as they are in memory
+template <int D>
+constexpr int kOldStages = D == 64 ? 5 : 3;   // and as fp16 (24 sequences of 78 rows, heads of 64: 5 78 us, 3 85)
 constexpr int kCopyWarp = 8;                  // behind the weights' warps
 // The other roles.  With old places four more warps turn their tiles into fp16,
 // and the registers that a block of 16 warps is launched with (128 a thread) are
@@ -98,13 +102,13 @@ struct WideShared {
 
 // Of a tile of old places: the scales of each 16 keys, where those are equal (of
 // the keys, log2 of the values', one over that, and 1), and of each key.
+template <int kStages8>
 struct OldShared {
     struct alignas(16) Tile {
         float4 group[4];
         float ks[kTile], vs[kTile];
-    } tile[kOldStages];
+    } tile[kStages8];
 };
-static_assert(sizeof(WideShared) + sizeof(OldShared) <= 3072, "beside the tiles no more is left");
 struct NoOldShared {};
 
 // Descriptor of a tile in shared memory with 128-byte rows, swizzled: eight
@@ -244,12 +248,12 @@ struct OldTiles {
     const TreeAttention &a;
     const OldPlaces &b;
     WideShared &sh;
-    OldShared &old;
+    OldShared<kOldStages<D>> &old;
     uint8_t *ring;
     int lane, w;  // which of the warps of its role
     int begin, end, tiles, kvh, s;
 
-    __device__ __forceinline__ uint8_t *raw(int slot) const { return ring + kOldStages * 2 * kTileBytes + slot * 2 * kRawBytes; }
+    __device__ __forceinline__ uint8_t *raw(int slot) const { return ring + kOldStages<D> * 2 * kTileBytes + slot * 2 * kRawBytes; }
 
     // Keys are looked up in order: the next tile's key is some pages and tokens on (no divisions).
     struct Keys {
@@ -389,7 +393,7 @@ struct OldTiles {
             after = look_on();
         }
         Place put;
-        put.stages = kOldStages;
+        put.stages = kOldStages<D>;
         for (int t = 0; t < tiles; ++t, put.step(1)) {
             Rows f;
             if constexpr (kWhole) {
@@ -404,7 +408,7 @@ struct OldTiles {
             }
             const int slot = t % kRaw;
             if (!warp_wait(sh, sh.raw_full[slot], t / kRaw & 1, a.err)) break;
-            if (t >= kOldStages && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
+            if (t >= kOldStages<D> && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
             uint8_t *to = ring + put.slot * 2 * kTileBytes;
             if (f.bits == 0xFFFFu) turn<false>(raw(slot), to, f.bits);
             else turn<true>(raw(slot), to, f.bits);
@@ -413,7 +417,7 @@ struct OldTiles {
             const float k0 = kWhole ? f.ks : __shfl_sync(~0u, f.ks, lead), v0 = kWhole ? f.vs : __shfl_sync(~0u, f.vs, lead);
             bool one = k0 >= 0x1p-100f && v0 >= 0x1p-80f && v0 <= 0x1p112f;
             if constexpr (!kWhole) one = __all_sync(~0u, one && (!(f.bits >> (lane & 15) & 1) || lane >= kRows || (f.ks == k0 && f.vs == v0)));
-            OldShared::Tile &tile = old.tile[put.slot];
+            auto &tile = old.tile[put.slot];
             if (lane < kRows) {
                 tile.ks[w * kRows + lane] = f.ks;
                 tile.vs[w * kRows + lane] = f.vs;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
     constexpr int kQBytes = kGroup * D * 2, kTileBytes = kTile * D * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WideShared sh;
-    __shared__ std::conditional_t<kOld, OldShared, NoOldShared> old;
+    __shared__ std::conditional_t<kOld, OldShared<kOldStages<D>>, NoOldShared> old;
     pdl_wait();
     pdl_trigger();  // (after the wait: the join reads what this call was given before it waits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         asm volatile("bar.sync 2, %0;" ::"n"(kOthers) : "memory");
     }
 
-    const int stages = is8 ? kOldStages : kStages;
+    const int stages = is8 ? kOldStages<D> : kStages;
     if (warp >= kCopyWarp) {
     if constexpr (kOld) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (is8 && !multiplies) {
@@ -1024,10 +1028,12 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
 
 template <typename T, int D, typename Old>
 cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
-    constexpr size_t kSmem = 2 * kGroup * D * 2 + kStages * 2 * kTile * D * 2;
-    static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
-    static_assert(kOldStages * 2 + kRaw <= kStages * 2, "and so do the old places' tiles, of 16 bits and of 8");
     constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
+    constexpr int kRing = kStages * 2 * kTile * D * 2, kOldRing = kOldStages<D> * 2 * kTile * D * 2 + kRaw * 2 * kTile * D;
+    constexpr size_t kSmem = 2 * kGroup * D * 2 + (kOld ? std::max(kRing, kOldRing) : kRing);
+    static_assert(kGroup * (D + 4) * 4 <= kStages * 2 * kTile * D * 2, "group 1's part fits the ring");
+    static_assert(kOldStages<D> <= kStages, "places of the barriers");
+    static_assert(kSmem + sizeof(WideShared) + (kOld ? sizeof(OldShared<kOldStages<D>>) : 0) <= 227 * 1024, "a block's shared memory");
     const unsigned x = (unsigned)(a.c.kv_heads * row_tiles);
     return launch_dependent(k_tree_wide<T, D, Old>, kOld ? dim3(x, (unsigned)a.n_seq, (unsigned)n_chunks) : dim3(x, (unsigned)n_chunks, (unsigned)a.n_seq),
                             Roles<kOld>::kThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
