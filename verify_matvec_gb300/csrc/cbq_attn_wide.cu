@@ -413,14 +413,18 @@ struct OldTiles {
             if (f.bits == 0xFFFFu) turn<false>(raw(slot), to, f.bits);
             else turn<true>(raw(slot), to, f.bits);
             // one pair of scales for the 16 keys, if it is one (and no number that the weights' warps could not take so)
-            const int lead = f.bits ? __ffs(f.bits) - 1 : 0;
-            const float k0 = kWhole ? f.ks : __shfl_sync(~0u, f.ks, lead), v0 = kWhole ? f.vs : __shfl_sync(~0u, f.vs, lead);
-            bool one = k0 >= 0x1p-100f && v0 >= 0x1p-80f && v0 <= 0x1p112f;
-            if constexpr (!kWhole) one = __all_sync(~0u, one && (!(f.bits >> (lane & 15) & 1) || lane >= kRows || (f.ks == k0 && f.vs == v0)));
+            float k0 = f.ks, v0 = f.vs;
+            bool one = true;
             auto &tile = old.tile[put.slot];
-            if (lane < kRows) {
-                tile.ks[w * kRows + lane] = f.ks;
-                tile.vs[w * kRows + lane] = f.vs;
+            if constexpr (!kWhole) {
+                const int lead = f.bits ? __ffs(f.bits) - 1 : 0;
+                k0 = __shfl_sync(~0u, f.ks, lead), v0 = __shfl_sync(~0u, f.vs, lead);
+                one = __all_sync(~0u, k0 >= 0x1p-100f && v0 >= 0x1p-80f && v0 <= 0x1p112f &&
+                                          (!(f.bits >> (lane & 15) & 1) || lane >= kRows || (f.ks == k0 && f.vs == v0)));
+                if (lane < kRows) {
+                    tile.ks[w * kRows + lane] = f.ks;
+                    tile.vs[w * kRows + lane] = f.vs;
+                }
             }
             if (lane == 0) {
                 tile.group[w] = make_float4(k0, log2_of(v0), 1.0f / v0, one ? 1.0f : 0.0f);
@@ -437,7 +441,10 @@ struct OldTiles {
     }
 };
 
-template <typename T, int D, typename Old>
+// kWhole (of old places): see above.  A kernel of its own, as what scales of each
+// key take is not only more work: in the same kernel it cost the others, by its
+// place among the instructions, 10 to 20% (8 x 64 drafts 329 us for 356).
+template <typename T, int D, typename Old, bool kWhole>
 __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThreads, 1)
     k_tree_wide(const __grid_constant__ TreeAttention a, const __grid_constant__ Old b, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
     constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
@@ -561,15 +568,9 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
     if (is8 && !multiplies) {
         if constexpr (kOld) {
             const int w = copies ? warp - kCopy : warp - kCopyWarp;
-            if (b.c.page_size % 16 == 0 && b.c.block % 16 == 0) {
-                const OldTiles<D, true> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
-                if (copies) tiles_of.copy();
-                else tiles_of.widen();
-            } else {
-                const OldTiles<D, false> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
-                if (copies) tiles_of.copy();
-                else tiles_of.widen();
-            }
+            const OldTiles<D, kWhole> tiles_of = {a, b, sh, old, smem + 2 * kQBytes, lane, w, begin, end, tiles, kvh, s};
+            if (copies) tiles_of.copy();
+            else tiles_of.widen();
         }
     } else if (copies) {
         // copies: the two warps take tiles in turn (what a tile costs a warp is mostly waits and look-ups); lane l keeps
@@ -782,16 +783,17 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             float of_group[4] = {of_row, of_row, of_row, of_row}, lv[4] = {}, per_v[4] = {1.0f, 1.0f, 1.0f, 1.0f};
             if constexpr (kOld) {
                 if (is8) {
-                    float all = 1.0f;
+                    [[maybe_unused]] float all = 1.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float4 y = old.tile[slot].group[k];
-                        of_group[k] = fmaxf(of_row * y.x, 1e-45f), lv[k] = y.y, per_v[k] = y.z;
+                        const float f = of_row * y.x;
+                        of_group[k] = f < 1e-45f ? 1e-45f : f, lv[k] = y.y, per_v[k] = y.z;  // (a scale of NaN stays)
                         all *= y.w;
                     }
-                    each = all == 0.0f;
+                    if constexpr (!kWhole) each = all == 0.0f;
                 }
-                if (each) {
+                if constexpr (!kWhole) if (each) {
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
                         const float4 ks = *reinterpret_cast<const float4 *>(&old.tile[slot].ks[j]);
@@ -818,7 +820,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             float now;
             if constexpr (!kOld) {
                 now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc - kLower;
-            } else if (!each) {
+            } else if (kWhole || !each) {
                 now = fmaxf(fmaxf(top[0] * of_group[0] + lv[0], top[1] * of_group[1] + lv[1]), fmaxf(top[2] * of_group[2] + lv[2], top[3] * of_group[3] + lv[3])) - kLower;
             } else {  // each key's score with its value's scale
                 float most = -INFINITY;
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
                         weigh_one(k * 8 + i / 4, of_group[k], lv[k], sum[k]);
                     }
                 };
-                if (each)
+                if (!kWhole && each)
                     all([&](int j, float f, float add, float2 &to) {
                         weigh<__half>(x, j, f, add, to, p, reinterpret_cast<const float2 *>(old.tile[slot].vs));
                     });
@@ -1026,7 +1028,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
 }
 
-template <typename T, int D, typename Old>
+template <typename T, int D, bool kWhole, typename Old>
 cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
     constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
     constexpr int kRing = kStages * 2 * kTile * D * 2, kOldRing = kOldStages<D> * 2 * kTile * D * 2 + kRaw * 2 * kTile * D;
@@ -1035,28 +1037,29 @@ cudaError_t launch_wide(const TreeAttention &a, const Old &b, int chunk, int n_c
     static_assert(kOldStages<D> <= kStages, "places of the barriers");
     static_assert(kSmem + sizeof(WideShared) + (kOld ? sizeof(OldShared<kOldStages<D>>) : 0) <= 227 * 1024, "a block's shared memory");
     const unsigned x = (unsigned)(a.c.kv_heads * row_tiles);
-    return launch_dependent(k_tree_wide<T, D, Old>, kOld ? dim3(x, (unsigned)a.n_seq, (unsigned)n_chunks) : dim3(x, (unsigned)n_chunks, (unsigned)a.n_seq),
+    return launch_dependent(k_tree_wide<T, D, Old, kWhole>, kOld ? dim3(x, (unsigned)a.n_seq, (unsigned)n_chunks) : dim3(x, (unsigned)n_chunks, (unsigned)a.n_seq),
                             Roles<kOld>::kThreads, kSmem, s, a, b, chunk, row_tiles, part_o, part_ml);
 }
 
-template <typename Old>
+template <bool kWhole, typename Old>
 cudaError_t launch_any(const TreeAttention &a, const Old &b, int chunk, int n_chunks, int row_tiles, float *part_o, float2 *part_ml, cudaStream_t s) {
     if (a.c.dtype == CBQ_BF16)
-        return a.c.head_dim == 64 ? launch_wide<__nv_bfloat16, 64>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
-                                  : launch_wide<__nv_bfloat16, 128>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
-    return a.c.head_dim == 64 ? launch_wide<__half, 64>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
-                              : launch_wide<__half, 128>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+        return a.c.head_dim == 64 ? launch_wide<__nv_bfloat16, 64, kWhole>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
+                                  : launch_wide<__nv_bfloat16, 128, kWhole>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+    return a.c.head_dim == 64 ? launch_wide<__half, 64, kWhole>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s)
+                              : launch_wide<__half, 128, kWhole>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_wide(const TreeAttention &a, NoOldPlaces b, int chunk, int n_chunks, int row_tiles, float *part_o,
                              float2 *part_ml, cudaStream_t s) {
-    return launch_any(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+    return launch_any<true>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
 }
 cudaError_t launch_tree_wide(const TreeAttention &a, const OldPlaces &b, int chunk, int n_chunks, int row_tiles, float *part_o,
                              float2 *part_ml, cudaStream_t s) {
-    return launch_any(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+    if (b.c.page_size % 16 == 0 && b.c.block % 16 == 0) return launch_any<true>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
+    return launch_any<false>(a, b, chunk, n_chunks, row_tiles, part_o, part_ml, s);
 }
 
 }  // namespace cbq
