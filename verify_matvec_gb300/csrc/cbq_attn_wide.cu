@@ -109,7 +109,9 @@ struct OldShared {
         float ks[kTile], vs[kTile];
     } tile[kStages8];
 };
-struct NoOldShared {};
+struct NoOldShared {
+    static constexpr const OldShared<1>::Tile *tile = nullptr;  // (named where nothing is made of it)
+};
 
 // Descriptor of a tile in shared memory with 128-byte rows, swizzled: eight
 // rows are 1024 bytes; `lead` bytes to the next 64 columns where rows are the
@@ -750,8 +752,6 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         // weights: thread = row of its group
         const int g = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-        const bool half = std::is_same_v<T, __half> || is8;  // what the weights are for the product with v
-        const float kLower = half ? 10.0f : 0.0f, kGrow = half ? 5.0f : 8.0f;
         float m = -INFINITY, l = 0.0f;  // weights are 2^(x - m): m is the maximum less kLower, or up to kGrow below that
         const int row_in = (split ? 0 : g * kGroup) + r;
         const bool live = row_in < rows;
@@ -765,6 +765,9 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         if constexpr (kOld)
             if (is8) of_row = sh.of_row[live ? row_in : 0];
         if (split && g) at.step(1);
+        auto weigh_all = [&](auto of_old) {  // (apart, for the instructions' sake)
+        constexpr bool k8 = decltype(of_old)::value, half = std::is_same_v<T, __half> || k8;  // half: the weights' type in the product with v
+        constexpr float kLower = half ? 10.0f : 0.0f, kGrow = half ? 5.0f : 8.0f;
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
             ok = warp_wait(sh, sh.scored[g][n & 1], n >> 1 & 1, a.err);
@@ -781,18 +784,16 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             // old places: the factors on the scores of each 16 keys, log2 of those on their weights, and one over those
             bool each = false;  // each key has scales of its own
             float of_group[4] = {of_row, of_row, of_row, of_row}, lv[4] = {}, per_v[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-            if constexpr (kOld) {
-                if (is8) {
-                    [[maybe_unused]] float all = 1.0f;
+            if constexpr (k8) {
+                [[maybe_unused]] float all = 1.0f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 y = old.tile[slot].group[k];
-                        const float f = of_row * y.x;
-                        of_group[k] = f < 1e-45f ? 1e-45f : f, lv[k] = y.y, per_v[k] = y.z;  // (a scale of NaN stays)
-                        all *= y.w;
-                    }
-                    if constexpr (!kWhole) each = all == 0.0f;
+                for (int k = 0; k < 4; ++k) {
+                    const float4 y = old.tile[slot].group[k];
+                    const float f = of_row * y.x;
+                    of_group[k] = f < 1e-45f ? 1e-45f : f, lv[k] = y.y, per_v[k] = y.z;  // (a scale of NaN stays)
+                    all *= y.w;
                 }
+                if constexpr (!kWhole) each = all == 0.0f;
                 if constexpr (!kWhole) if (each) {
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
@@ -814,11 +815,11 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const int k = i & 3, j = kOld ? k * 16 + i / 4 * 2 : i * 2;  // (with old places the tops of each 16)
+                const int k = i & 3, j = k8 ? k * 16 + i / 4 * 2 : i * 2;  // (of old places the tops of each 16)
                 top[k] = max3(top[k], __uint_as_float(x[j >> 5][j & 31]), __uint_as_float(x[j >> 5][(j & 31) + 1]));
             }
             float now;
-            if constexpr (!kOld) {
+            if constexpr (!k8) {
                 now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc - kLower;
             } else if (kWhole || !each) {
                 now = fmaxf(fmaxf(top[0] * of_group[0] + lv[0], top[1] * of_group[1] + lv[1]), fmaxf(top[2] * of_group[2] + lv[2], top[3] * of_group[3] + lv[3])) - kLower;
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             }
             const float less = m == -INFINITY ? 0.0f : -m;
             uint32_t p[32];
-            if constexpr (!kOld) {
+            if constexpr (!k8) {
                 float2 sum[2] = {};
 #pragma unroll
                 for (int j = 0; j < 32; ++j) weigh<T>(x, j, sc, less, sum[j & 1], p);
@@ -878,8 +879,8 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
                     all([&](int j, float f, float add, float2 &to) {
                         weigh<__half>(x, j, f, add, to, p, reinterpret_cast<const float2 *>(old.tile[slot].vs));
                     });
-                else if (is8) all([&](int j, float f, float add, float2 &to) { weigh<__half>(x, j, f, add, to, p); });
-                else all([&](int j, float f, float add, float2 &to) { weigh<T>(x, j, f, add, to, p); });
+                else
+                    all([&](int j, float f, float add, float2 &to) { weigh<__half>(x, j, f, add, to, p); });
                 l += ((sum[0].x + sum[0].y) * per_v[0] + (sum[1].x + sum[1].y) * per_v[1]) + ((sum[2].x + sum[2].y) * per_v[2] + (sum[3].x + sum[3].y) * per_v[3]);
             }
             tm_st(s_at, p);
@@ -887,6 +888,13 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.weighed[g][n & 1]));
+        }
+        };
+        if constexpr (kOld) {
+            if (is8) weigh_all(std::true_type{});
+            else weigh_all(std::false_type{});
+        } else {
+            weigh_all(std::false_type{});
         }
         if (l != l) m = 0.0f;  // (no maximum keeps a NaN: what joins the parts must not take them for empty)
         if (ok && n > 0) ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
