@@ -326,9 +326,8 @@ struct OldTiles {
         copy_wait<0>();
     }
 
-    // This warp's rows of a tile as it is to those of a tile as fp16; kSome: those that are not there become zeros.
-    template <bool kSome>
-    __device__ __forceinline__ void turn(const uint8_t *from, uint8_t *to, uint32_t bits) const {
+    // This warp's rows of a tile as it is to those of a tile as fp16.  (Those that are not there were copied as zeros.)
+    __device__ __forceinline__ void turn(const uint8_t *from, uint8_t *to) const {
         constexpr int kSets = 2 * (D / 64);  // keys and values; the halves of their columns
         const int r0 = w * kRows + lane / 4, odd = lane / 4 & 1;
         uint4 x[kSets][2];
@@ -346,8 +345,7 @@ struct OldTiles {
                 uint32_t y[8];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t two = c == 0 ? x[k][i].x : c == 1 ? x[k][i].y : c == 2 ? x[k][i].z : x[k][i].w;
-                    if (kSome && !(bits >> (i * 8 + lane / 4) & 1)) two = 0;
+                    const uint32_t two = c == 0 ? x[k][i].x : c == 1 ? x[k][i].y : c == 2 ? x[k][i].z : x[k][i].w;
                     y[2 * c] = e4m3_f16x2((uint16_t)two);
                     y[2 * c + 1] = e4m3_f16x2((uint16_t)(two >> 16));
                 }
@@ -412,8 +410,7 @@ struct OldTiles {
             if (!warp_wait(sh, sh.raw_full[slot], t / kRaw & 1, a.err)) break;
             if (t >= kOldStages<D> && !warp_wait(sh, sh.empty[put.slot], (put.round - 1) & 1, a.err)) break;
             uint8_t *to = ring + put.slot * 2 * kTileBytes;
-            if (f.bits == 0xFFFFu) turn<false>(raw(slot), to, f.bits);
-            else turn<true>(raw(slot), to, f.bits);
+            turn(raw(slot), to);
             // one pair of scales for the 16 keys, if it is one (and no number that the weights' warps could not take so)
             float k0 = f.ks, v0 = f.vs;
             bool one = true;
