@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
                 ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
                 if (!ok) break;
                 fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32];
                     tm_ld(lanes + Cols<D>::o(g) + d, o);
