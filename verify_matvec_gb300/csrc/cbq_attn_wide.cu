@@ -39,11 +39,12 @@
 // more than 4 bits), their scales go to the scores and the weights.  Roles: warps
 // 0..7 as above, 8..11 widen the tiles, 12 and 13 the products, 14 and 15 copy.
 // 8 sequences of 64 drafts over 16,000 keys in 8 bits (282 MB) and 64 behind them take
-// 355 to 410 us, by the scales (750 to 650 TFLOP/s).  Issue slots are the bound:
-// the warps that widen and those that weigh want 47% of them, with 1.4 waits for
-// an instruction to each (16 bits: 41%, 0.6), as eight copies of long unrolled
-// loops share the caches for instructions.  24 ragged sequences of up to 78 rows
-// (76 MB) take 95 us: starts and ends of blocks, as above, of both kinds.  (Keys
+// 318 us (850 TFLOP/s).  Issue slots are the bound: the warps that widen and those
+// that weigh want 46% of them, with 0.74 waits for an instruction to each (16
+// bits: 41%, 0.51), as long unrolled loops share the caches for instructions: what
+// is rare is in a kernel, a loop or a branch of its own for that reason (with all
+// of it in the way, 1.4 waits and 407 us).  24 ragged sequences of up to 78 rows
+// (76 MB) take 80 us: starts and ends of blocks, as above, of both kinds.  (Keys
 // as they are, the query as a sum of e4m3 and e5m2 parts: two or three products
 // where one is, and 8 x 64 drafts 358 -> 392 us in bf16, 437 in fp16.)
 #include <algorithm>
@@ -442,7 +443,7 @@ struct OldTiles {
 
 // kWhole (of old places): see above.  A kernel of its own, as what scales of each
 // key take is not only more work: in the same kernel it cost the others, by its
-// place among the instructions, 10 to 20% (8 x 64 drafts 329 us for 356).
+// place among the instructions, 10 to 20% (8 x 64 drafts 343 us for 407).
 template <typename T, int D, typename Old, bool kWhole>
 __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThreads, 1)
     k_tree_wide(const __grid_constant__ TreeAttention a, const __grid_constant__ Old b, int chunk, int row_tiles, float *part_o, float2 *part_ml) {
