@@ -692,7 +692,8 @@ int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const i
  * (what is below 2^-30 of the row's largest loses bits), and the weights times
  * the values' scales rounded to fp16 relative to the row's largest: those
  * below 2^-24 of it lose bits.  Scales may be any positive numbers from 2^-80 to
- * 2^112 (of values above 2^120, which take larger ones, small weights are lost).
+ * 2^112, both ends in one row too (of values above 2^120, which take larger
+ * ones, small weights are lost).
  * old->kv_heads and head_dim are the cache's.  max_old = 0 with old_dev all
  * zero is cbq_tree_attention.  Speed: heads of 64, 128 and 256 with k, v, out
  * and all rows of both caches on 16 bytes take the tensor cores; every other

@@ -199,8 +199,10 @@ struct OldShared {
 // to 2^15 by its own power of two 2^k; the scale of a key comes to its score and
 // that of a value to its weight.  The maximum is of what the weights are with
 // their scales, so they stay within fp16 (and as in the kernel below, 2^10 above
-// the running maximum's); l may be larger than that by a block's scale, and
-// fp32 has the room: 2^-80 <= vs.
+// the running maximum's).  l, without them, may be larger or smaller than that by
+// a block's scale, and fp32 has the room for 2^-80 <= vs <= 2^112; but not for
+// the factor from one maximum to the next, 2^-192 at the least, which therefore
+// goes on l in two halves here and where parts are joined (part_sum()).
 // Fragments: the order of the summed axis is free as long as both sides have it,
 // so a lane takes 16 bytes side by side of a key's row for four products, and
 // the same 16 values of q; and the values come through a transposing load of
@@ -360,6 +362,7 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
             top[half] = fmaxf(top[half], __shfl_xor_sync(~0u, top[half], 2));
             const float now = fmaxf(m[half], top[half] - kLower), shift = now == -INFINITY ? 0.0f : now;
             const float keep = pow2(m[half] - shift);
+            const float before = keep > 0.0f ? l[half] * keep : part_sum<true>(l[half], m[half] - shift);
             m[half] = now;
             float sum = 0.0f;
 #pragma unroll
@@ -370,7 +373,7 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
                     sum += w;
                     x[j][half * 2 + e] = w * (e ? vs[j].y : vs[j].x);
                 }
-            l[half] = l[half] * keep + sum;
+            l[half] = before + sum;
 #pragma unroll
             for (int d = 0; d < D / 8; ++d) {
                 o[d][half * 2] *= keep;
@@ -728,7 +731,7 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < S::kParts; ++w) {
-            if (top != -INFINITY) sum += ml[w][r].y * pow2(ml[w][r].x - top);
+            if (top != -INFINITY) sum += part_sum<kOld>(ml[w][r].y, ml[w][r].x - top);
             const float4 y = *reinterpret_cast<const float4 *>(res + (w * S::kRows + r) * D + d);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
@@ -766,7 +769,8 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
             if (o >= parts) continue;
             const float4 y = peer_load4(peer(res + r * D + d, rank_of(o)));
             const float f = top == -INFINITY ? 0.0f : pow2(m_of[o].x - top);
-            sum += m_of[o].y * f;
+            if (kOld) sum += top == -INFINITY ? 0.0f : part_sum<true>(m_of[o].y, m_of[o].x - top);
+            else sum += m_of[o].y * f;
             v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
         }
         put(row_of(r), d, v, top, sum);
@@ -784,6 +788,7 @@ __global__ void __launch_bounds__(128, blocks_an_sm(D))
 // chunk).  grid (ceil(q_heads * W / 8), max_tok, n_seq).
 template <typename T, int D, int W, typename Old>
 __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, Old b, int chunk, bool wide, const float *part_o, const float2 *part_ml) {
+    constexpr bool kOld = std::is_same_v<Old, OldPlaces>;
     constexpr int kEach = D / 32;  // values of a lane, side by side
     struct alignas(kEach * 4 < 16 ? kEach * 4 : 16) Values {
         float v[kEach];
@@ -820,13 +825,13 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, Old b, int c
         for (int j = 0; j < 8; ++j) now = fmaxf(now, p[j].x);
         if (now == -INFINITY) continue;
         const float keep = pow2(top - now);
-        sum *= keep;
+        sum = kOld ? part_sum<true>(sum, top - now) : sum * keep;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) v.v[e] *= keep;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float f = pow2(p[j].x - now);
-            sum += p[j].y * f;
+            sum += kOld ? part_sum<true>(p[j].y, p[j].x - now) : p[j].y * f;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) v.v[e] += f * y[j].v[e];
         }
@@ -846,7 +851,7 @@ __global__ void __launch_bounds__(256) k_tree_join(TreeAttention a, Old b, int c
             for (int o = 0; o < W; ++o) {
                 const float f = pow2(tops[o] - top);
                 const Values y = vals[o][lane];
-                sum += f * sums[o];
+                sum += kOld ? part_sum<true>(sums[o], tops[o] - top) : f * sums[o];
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) v.v[e] += f * y.v[e];
             }

@@ -102,7 +102,7 @@ struct WideShared {
 };
 
 // Of a tile of old places: the scales of each 16 keys, where those are equal (of
-// the keys, log2 of the values', one over that, and 1), and of each key.
+// the keys, log2 of the values', one over that, and two bits), and of each key.
 template <int kStages8>
 struct OldShared {
     struct alignas(16) Tile {
@@ -110,6 +110,9 @@ struct OldShared {
         float ks[kTile], vs[kTile];
     } tile[kStages8];
 };
+// Those bits: the 16 keys' scales are not equal; one of the values' scales of these or
+// of the like 16 of the tiles before is not within 2^-38 .. 2^38.
+constexpr int kEachKey = 1, kFar = 2;
 struct NoOldShared {
     static constexpr const OldShared<1>::Tile *tile = nullptr;  // (named where nothing is made of it)
 };
@@ -393,6 +396,7 @@ struct OldTiles {
             next = ask(look_on());
             after = look_on();
         }
+        bool far = false;
         Place put;
         put.stages = kOldStages<D>;
         for (int t = 0; t < tiles; ++t, put.step(1)) {
@@ -426,8 +430,10 @@ struct OldTiles {
                     tile.vs[w * kRows + lane] = f.vs;
                 }
             }
+            const bool wide = !(f.vs >= 0x1p-38f && f.vs <= 0x1p38f);
+            far |= kWhole ? wide : (bool)__any_sync(~0u, wide);
             if (lane == 0) {
-                tile.group[w] = make_float4(k0, log2_of(v0), 1.0f / v0, one ? 1.0f : 0.0f);
+                tile.group[w] = make_float4(k0, log2_of(v0), 1.0f / v0, __int_as_float((one ? 0 : kEachKey) | (far ? kFar : 0)));
                 reinterpret_cast<uint16_t *>(sh.valid[put.slot])[w] = (uint16_t)f.bits;
             }
             // One word for the warp (arrivals of 32 lanes at one place follow one another).  The writes are handed to the
@@ -766,6 +772,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
         auto weigh_all = [&](auto of_old) {  // (apart, for the instructions' sake)
         constexpr bool k8 = decltype(of_old)::value, half = std::is_same_v<T, __half> || k8;  // half: the weights' type in the product with v
         constexpr float kLower = half ? 10.0f : 0.0f, kGrow = half ? 5.0f : 8.0f;
+        [[maybe_unused]] constexpr float kApart = 90.0f;  // weights 2^-36 of a top of 2^-90 are still normal numbers
         for (int i = g; i < items; i += 2, ++n, at.step(split ? 2 : 1)) {
             const int slot = at.slot;
             ok = warp_wait(sh, sh.scored[g][n & 1], n >> 1 & 1, a.err);
@@ -781,17 +788,19 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             if (!ok) break;
             // old places: the factors on the scores of each 16 keys, log2 of those on their weights, and one over those
             bool each = false;  // each key has scales of its own
+            [[maybe_unused]] bool far = false;
             float of_group[4] = {of_row, of_row, of_row, of_row}, lv[4] = {}, per_v[4] = {1.0f, 1.0f, 1.0f, 1.0f};
             if constexpr (k8) {
-                [[maybe_unused]] float all = 1.0f;
+                int all = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 y = old.tile[slot].group[k];
                     const float f = of_row * y.x;
                     of_group[k] = f < 1e-45f ? 1e-45f : f, lv[k] = y.y, per_v[k] = y.z;  // (a scale of NaN stays)
-                    all *= y.w;
+                    all |= __float_as_int(y.w);
                 }
-                if constexpr (!kWhole) each = all == 0.0f;
+                if constexpr (!kWhole) each = all & kEachKey;
+                far = all & kFar;
                 if constexpr (!kWhole) if (each) {
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
@@ -838,9 +847,11 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
                 for (int k = 0; k < 4; ++k) of_group[k] = of_row, lv[k] = 0.0f, per_v[k] = 1.0f;
             }
             const bool grown = now > m + kGrow || (m == -INFINITY && now > -INFINITY);
-            const float keep = grown ? pow2(m - now) : 1.0f;
-            if (grown) m = now, l *= keep;
+            float keep = grown ? pow2(k8 ? 0.5f * (m - now) : m - now) : 1.0f;  // (old places: in two halves, see part_sum())
+            if (grown) m = now;
+            if constexpr (!k8) l *= keep;
             if (n > 0 && __any_sync(~0u, grown)) {
+                if constexpr (k8) l = l * keep * keep, keep *= keep;  // (before the first item l is 0)
                 // O is scaled, once the products before are in it
                 ok = warp_wait(sh, sh.summed[g][(n - 1) & 1], (n - 1) >> 1 & 1, a.err);
                 if (!ok) break;
@@ -865,6 +876,16 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) lv[k] += less;
+                if ((kWhole || !each) && far) {
+                    // Far below others' (weight times scale), 16 keys still count for l where their scale is as far below: they
+                    // are weighed 2^-30 of their own top, which is nothing in O, and l makes up for it.  (With all scales within
+                    // 2^-38 .. 2^38, what is lost so is some 2^-60 of l.  8 x 64 drafts 318 -> 322 us.)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x_top = top[k] * of_group[k];
+                        if (x_top + lv[k] < -kApart && x_top > -INFINITY) lv[k] = -30.0f - x_top, per_v[k] = pow2(x_top - m + 30.0f);
+                    }
+                }
                 float2 sum[4] = {};
                 auto all = [&](auto weigh_one) {
 #pragma unroll
@@ -943,7 +964,8 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
             if (split && items > 1) other = sh.ml[r];
             const float top = fmaxf(m, other.x);
             const float f0 = n == 0 || top == -INFINITY ? 0.0f : pow2(m - top), f1 = top == -INFINITY ? 0.0f : pow2(other.x - top);
-            const float sum = l * f0 + other.y * f1;
+            float sum = l * f0 + other.y * f1;
+            if (kOld) sum = top == -INFINITY ? 0.0f : part_sum<true>(n == 0 ? 0.0f : l, m - top) + part_sum<true>(other.y, other.x - top);
             const float inv = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t part = (int64_t)c * a.total_tok * a.q_heads + row;
             const int64_t to_row = (alone ? row : part) * D;

@@ -89,6 +89,17 @@ __device__ __forceinline__ float pow2(float x) {
     return r;
 }
 
+// A part's sum of weights l under its own maximum m, under the maximum m - d of
+// all (d <= 0).  kFar: the maxima hold the values' scales, which the sums do not,
+// so what counts of a sum may be 2^192 of such steps away: by two halves, as
+// 2^d alone would be 0 below 2^-126.
+template <bool kFar>
+__device__ __forceinline__ float part_sum(float l, float d) {
+    if (!kFar) return l * pow2(d);
+    const float half = pow2(0.5f * d);
+    return l * half * half;
+}
+
 __device__ __forceinline__ float log2_of(float x) {
     float r;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
