@@ -351,7 +351,7 @@ __device__ __forceinline__ void old_places(const TreeAttention &a, const OldPlac
             const float lv[2] = {scale_log2(vs[j].x), scale_log2(vs[j].y)};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[j][e] *= of_row[e / 2] * (e % 2 ? ks.y : ks.x);
+                x[j][e] = x[j][e] * of_row[e / 2] * (e % 2 ? ks.y : ks.x);  // (in this order a score of 0 stays 0)
                 if (there != kAll && !(sh.valid[slot][key / S::kCopied8] >> ((key + e % 2) % S::kCopied8) & 1)) x[j][e] = -INFINITY;
                 top[e / 2] = fmaxf(top[e / 2], x[j][e] + lv[e % 2]);
             }

@@ -185,6 +185,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// A factor on scores that is neither 0 (-inf times that would be NaN) nor infinite
+// (so would a score of 0 be); NaN stays.
+__device__ __forceinline__ float finite_factor(float f) {
+    float r;
+    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, 0f00000001;\n min.NaN.f32 %0, t, 0f7F7FFFFF;\n}\n" : "=f"(r) : "f"(f));
+    return r;
+}
 // log2 of a scale within a tenth, for a maximum: its bits are that, but for the
 // curve between two powers of two.
 __device__ __forceinline__ float near_log2(float v) {
@@ -795,8 +802,7 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 y = old.tile[slot].group[k];
-                    const float f = of_row * y.x;
-                    of_group[k] = f < 1e-45f ? 1e-45f : f, lv[k] = y.y, per_v[k] = y.z;  // (a scale of NaN stays)
+                    of_group[k] = finite_factor(of_row * y.x), lv[k] = y.y, per_v[k] = y.z;
                     all |= __float_as_int(y.w);
                 }
                 if constexpr (!kWhole) each = all & kEachKey;
