@@ -587,9 +587,11 @@ int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_strid
  * S < r(x), otherwise x is taken out of r and S = S - r(x).  A token outside
  * [0, V) is never accepted.  If nothing is left of r (the draft equals the
  * target, and rounding refused it) the token is drawn from p; from a row of
- * zeros next is -1.  NaN counts as 0.  c, S, products, differences and sums
- * are carried as two fp32 numbers each (within 2^-46 of their terms), and
- * summed in an order that does not depend on timing.
+ * zeros next is -1.  In a row of probs or draft NaN counts as 0, and so does
+ * what is below 0; a u of NaN accepts nothing, and u_next is held in [0, 1) with
+ * NaN as 0.  c, S, products, differences and sums are carried as two fp32
+ * numbers each (within 2^-46 of their terms), and summed in an order that does
+ * not depend on timing.
  * path_dev: n_seq x max_tok int32, the accepted nodes from node 0 on,
  * ascending, then -1; count_dev[s]: how many; next_dev[s]: the token.  A
  * sequence of no nodes gives 0 and -1.  One longer than max_tok is cut to it,

@@ -75,7 +75,10 @@ __device__ __forceinline__ void add(Pairs &s, Pairs x) {
     s.hi = t;
 }
 
-// What is left of p at two tokens: max(p - c q, 0), c = ch + cl; NaN gives 0.
+// NaN in a row, and what is below 0, count as 0.
+__device__ __forceinline__ float number(float x) { return fmaxf(x, 0.0f); }
+
+// What is left of p at two tokens: max(p - c q, 0), c = ch + cl; NaN in p gives 0, q has none.
 // Only where c q <= p does the rounding of the difference count, and there it is
 // (p - t) - c q.
 template <bool kOne>  // c is 1
@@ -177,7 +180,7 @@ struct Row {
     __device__ __forceinline__ void rest(const Shared &s, int t, int lane, const Tile &x, Pairs (&r)[2]) const {
         const float2 a = make_float2(x.p.x, x.p.y), b = make_float2(x.p.z, x.p.w);
         if (kDrawn && q) {
-            const float2 c = make_float2(x.q.x, x.q.y), d = make_float2(x.q.z, x.q.w);
+            const float2 c = make_float2(number(x.q.x), number(x.q.y)), d = make_float2(number(x.q.z), number(x.q.w));
             if (ch == 1.0f && cl == 0.0f) r[0] = left_of<true>(a, c, ch, cl), r[1] = left_of<true>(b, d, ch, cl);
             else r[0] = left_of<false>(a, c, ch, cl), r[1] = left_of<false>(b, d, ch, cl);
         } else {
@@ -300,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
         s.token[tid] = real ? token : -1;
         s.parent[tid] = behind ? parent : -1;
         s.u[tid] = a.u[b0 + tid];
-        s.p[tid] = real ? a.probs[(b0 + parent) * a.probs_stride + token] : 0.0f;
-        s.q[tid] = !kDrawn ? 1.0f : real ? a.draft[(b0 + parent) * a.draft_stride + token] : 0.0f;
+        s.p[tid] = real ? number(a.probs[(b0 + parent) * a.probs_stride + token]) : 0.0f;
+        s.q[tid] = !kDrawn ? 1.0f : real ? number(a.draft[(b0 + parent) * a.draft_stride + token]) : 0.0f;
     }
     if (tid == 0) {
         s.u_next = fminf(fmaxf(a.u_next[seq], 0.0f), 1.0f - 0x1p-24f);
