@@ -559,7 +559,8 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
  * plus 2^-46 absolute.  u_dev and
  * ids_dev, both or neither: one token a row is drawn too, the same that
  * cbq_sample draws.  out_dev and ids_dev overlap nothing that the call reads,
- * nor each other.  One launch.  Errors as cbq_sample, and EINVAL (out_dev
+ * nor each other (rows that lie in turn, the halves of one tensor's, share no
+ * byte and do not).  One launch.  Errors as cbq_sample, and EINVAL (out_dev
  * null, out_stride < V with n > 1 or < 0, one of u_dev and ids_dev alone, an
  * output that overlaps). */
 int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_stride, const float *temperature_dev,

@@ -906,17 +906,28 @@ int cbq_sample(const void *logits_dev, int dtype, int n, int V, int64_t row_stri
 
 namespace {
 
+// Rows of `bytes` bytes, `stride` bytes from one to the next (at least as many).
 struct Span {
     const void *p;  // null: nothing
     uint64_t bytes;
+    int64_t rows = 1;
+    uint64_t stride = 0;
 };
+bool meet(const Span &a, const Span &b) {
+    if (!a.p || !b.p) return false;
+    uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (x + (a.rows - 1) * a.stride + a.bytes <= y || y + (b.rows - 1) * b.stride + b.bytes <= x) return false;
+    // one lies within the other, or the rows of the two lie in turn: the row that ends first is passed
+    for (int64_t i = 0, j = 0; i < a.rows && j < b.rows;) {
+        if (x < y + b.bytes && y < x + a.bytes) return true;
+        if (x < y) ++i, x += a.stride;
+        else ++j, y += b.stride;
+    }
+    return false;
+}
 // No output overlaps an input or another output: blocks of several rows or
 // sequences read and write at the same time.
 bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-    auto meet = [](const Span &a, const Span &b) {
-        const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-        return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
-    };
     for (const Span &o : outs) {
         for (const Span &i : ins)
             if (meet(o, i)) return false;
@@ -925,7 +936,7 @@ bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     }
     return true;
 }
-uint64_t rows_bytes(int64_t n, int64_t stride, int V, size_t size) { return ((uint64_t)stride * (n - 1) + V) * size; }
+Span rows_of(const void *p, int64_t n, int64_t stride, int V, size_t size) { return Span{p, (uint64_t)V * size, n, (uint64_t)stride * size}; }
 
 }  // namespace
 
@@ -939,8 +950,8 @@ int cbq_probs(const void *logits_dev, int dtype, int n, int V, int64_t row_strid
         !aligned_to(out_dev, 4))
         return CBQ_EINVAL;
     const uint64_t each = (uint64_t)n * 4;
-    if (!apart({{out_dev, rows_bytes(n, out_stride, V, 4)}, {ids_dev, each}},
-               {{logits_dev, rows_bytes(n, row_stride, V, dtype_bytes(dtype))}, {temperature_dev, each}, {top_k_dev, each},
+    if (!apart({rows_of(out_dev, n, out_stride, V, 4), {ids_dev, each}},
+               {rows_of(logits_dev, n, row_stride, V, dtype_bytes(dtype)), {temperature_dev, each}, {top_k_dev, each},
                 {top_p_dev, each}, {min_p_dev, each}, {u_dev, each}}))
         return CBQ_EINVAL;
     int dev = 0;
@@ -968,7 +979,7 @@ int cbq_verify(const float *probs_dev, int64_t probs_stride, const float *draft_
         if (!aligned_to(p, 4)) return CBQ_EINVAL;
     const uint64_t nodes = (uint64_t)total_tok * 4, each = (uint64_t)n_seq * 4;
     if (!apart({{path_dev, each * max_tok}, {count_dev, each}, {next_dev, each}},
-               {{probs_dev, rows_bytes(total_tok, probs_stride, V, 4)}, {draft_dev, rows_bytes(total_tok, draft_stride, V, 4)},
+               {rows_of(probs_dev, total_tok, probs_stride, V, 4), rows_of(draft_dev, total_tok, draft_stride, V, 4),
                 {tokens_dev, nodes}, {parent_dev, nodes}, {start_dev, each + 4}, {u_dev, nodes}, {u_next_dev, each}}))
         return CBQ_EINVAL;
     int dev = 0;
