@@ -28,10 +28,10 @@
 // copies were the bound: 2,100 clocks a tile for 1,700.)
 //
 // 8 sequences of 64 drafts x 8 heads a kv head over 16,000 keys (270 GFLOP, 543
-// MB) take 254 us, 1,060 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
+// MB) take 251 us, 1,074 TFLOP/s, in 128 blocks on 152 SMs.  An item takes its
 // SM 1,020 clocks, of which the products take 594 (S 8 x 46, both operands from
 // shared memory; O 4 x 57).  24 ragged sequences of 78 rows and 64 a head (149
-// MB) take 60 us: some 5 us a block beside its keys, an uneven last wave, and
+// MB) take 57 us: some 5 us a block beside its keys, an uneven last wave, and
 // 1,120 of 1,440 blocks without keys that take their turn on an SM all the same.
 //
 // Old places in 8 bits are blocks of their own.  Their numbers become fp16 on
@@ -517,8 +517,10 @@ __global__ void __launch_bounds__(Roles<std::is_same_v<Old, OldPlaces>>::kThread
     const uint32_t q_at = smem_addr(smem), ring = q_at + 2 * kQBytes;
     const int32_t *table = a.table + (int64_t)s * a.table_width;
 
-    const bool multiplies = warp == kScoreWarp || warp == kSumWarp, copies = warp >= kCopy && warp < kCopy + 2;
-    if (warp < kCopyWarp || multiplies) {
+    // (Without old places, ranges: with the products' warps told one by one, 8 x 64 drafts took 261 us for 251.)
+    const bool multiplies = kOld ? warp == kScoreWarp || warp == kSumWarp : warp >= kScoreWarp;
+    const bool copies = warp >= kCopy && !multiplies;
+    if (kOld ? warp < kCopyWarp || multiplies : !copies) {
         // q of the rows, the sign of the scale with it; absent rows are zero
         const bool q_whole = (reinterpret_cast<uintptr_t>(a.q) % 16 | (a.q_tok | a.q_head) % 8) == 0;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
