@@ -512,7 +512,7 @@ struct Part {
 
     // The rest for those n in one block, without another word from the others: for each, what comes before it in the
     // order, and, of what is kept, before it by index.  want(mass of the first k): what top-p's must reach.
-    template <typename F, typename G, typename H>
+    template <bool kAlways, typename F, typename G, typename H>
     __device__ void settle(int n, int k, F mass, G want, uint64_t least, float u, int32_t *id, float *prob, H keeps) {
         uint64_t *key = reinterpret_cast<uint64_t *>(s.gather), *w = key + kSettle, *kept = w + kSettle;
         static_assert(sizeof(s.gather) >= 3 * kSettle * sizeof(uint64_t), "three numbers each");
@@ -552,7 +552,7 @@ struct Part {
         }
         const uint64_t goal = taken(total, u);
         if (stays && q == 0) keeps((int)~(uint32_t)mine, own, total);
-        if (id && stays && q == 0 && upto - own < goal && upto >= goal) {
+        if ((kAlways || id) && stays && q == 0 && upto - own < goal && upto >= goal) {
             *id = (int32_t)~(uint32_t)mine;
             if (prob) *prob = (float)((double)own / (double)total);
         }
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) k_sample(Sample a) {
         const int n = row.collect();
         if (n <= kSettle) {
             if (row.rank == 0)
-                row.settle(n, by_k ? k : a.V, mass, [&](uint64_t m) { return !by_p ? ~0ull : weighed ? want : goal(m); }, floor_w, u,
+                row.template settle<!kDist>(n, by_k ? k : a.V, mass, [&](uint64_t m) { return !by_p ? ~0ull : weighed ? want : goal(m); }, floor_w, u,
                            !kDist || a.ids ? a.ids + c : nullptr, a.probs ? a.probs + c : nullptr, [&](int at, uint64_t w, uint64_t sum) {
                                if constexpr (kDist) dist[at] = part_of(w, inverse(sum));
                            });
