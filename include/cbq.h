@@ -700,8 +700,11 @@ int cbq_kv_quantize(const cbq_kv_cache *from, int64_t from_layer_stride, const i
  * old->kv_heads and head_dim are the cache's.  max_old = 0 with old_dev all
  * zero is cbq_tree_attention.  Speed: heads of 64, 128 and 256 with k, v, out
  * and all rows of both caches on 16 bytes take the tensor cores; every other
- * layout a warp a row, one key after another.  With many rows a kv head, 8-bit
- * pages and blocks of whole 16 tokens are faster.  ws_dev, out_dtype, lse_dev,
+ * layout a warp a row, one key after another.  With many rows a kv head an 8-bit
+ * cache saves room but takes longer than one of 16 bits (8 trees of 64 drafts
+ * over 16,000 keys 324 us for 252; few rows over long contexts take less, 106 for
+ * 175), and twice that where pages and blocks are not of whole 16 tokens.
+ * ws_dev, out_dtype, lse_dev,
  * err_dev and the other arguments as cbq_tree_attention.
  * Errors: those of cbq_tree_attention, and EINVAL (a bad 8-bit cache; max_old
  * outside 0..CBQ_TREE_MAX_LEN; max_new outside 1..CBQ_TREE_MAX_LEN; their sum

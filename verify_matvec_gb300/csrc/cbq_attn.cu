@@ -22,7 +22,7 @@
 // 0 .. n8 - 1 of old places, then those of 16 bits).  Half the bytes, and the
 // products are the bound: mma.sync takes 512 multiplications a clock of an SM,
 // and 16 rows are padded where there are fewer.  Two sequences of 131,000 keys
-// (538 MB) take 105 us, 5.1 TB/s, where 16 bits take 169 to 179; 32 rows 154.
+// (538 MB) take 106 us, 5.1 TB/s, where 16 bits take 169 to 179; 32 rows 153.
 // 300 keys 6.3 us.  (A maximum that follows late, a branch where 16 keys have
 // one scale, or three blocks an SM: 105, 116, 108.)
 #include <algorithm>

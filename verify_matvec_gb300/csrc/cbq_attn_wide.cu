@@ -39,12 +39,13 @@
 // more than 4 bits), their scales go to the scores and the weights.  Roles: warps
 // 0..7 as above, 8..11 widen the tiles, 12 and 13 the products, 14 and 15 copy.
 // 8 sequences of 64 drafts over 16,000 keys in 8 bits (282 MB) and 64 behind them take
-// 318 us (850 TFLOP/s).  Issue slots are the bound: the warps that widen and those
-// that weigh want 46% of them, with 0.74 waits for an instruction to each (16
-// bits: 41%, 0.51), as long unrolled loops share the caches for instructions: what
-// is rare is in a kernel, a loop or a branch of its own for that reason (with all
-// of it in the way, 1.4 waits and 407 us).  24 ragged sequences of up to 78 rows
-// (76 MB) take 80 us: starts and ends of blocks, as above, of both kinds.  (Keys
+// 324 us (832 TFLOP/s), 695 with scales of 4 tokens.  Issue slots are the bound: the
+// warps that widen and those that weigh want 47% of them, with 0.76 waits for an
+// instruction to each (16 bits: 42%, 0.44), as long unrolled loops share the caches
+// for instructions: what is rare is in a kernel, a loop or a branch of its own for
+// that reason (with all of it in the way, 1.4 waits and 407 us).  24 ragged sequences
+// of up to 78 rows (76 MB) take 82 us: starts and ends of blocks, as above, of both
+// kinds.  (Keys
 // as they are, the query as a sum of e4m3 and e5m2 parts: two or three products
 // where one is, and 8 x 64 drafts 358 -> 392 us in bf16, 437 in fp16.)
 #include <algorithm>
@@ -254,7 +255,7 @@ __device__ __forceinline__ bool warp_wait(WideShared &s, uint64_t &bar, uint32_t
 // page and one pair of scales.  Scales go to the weights' warps, for each 16
 // keys: there they cost next to nothing, while a scale a key costs as much again
 // as the weights themselves.  (Multiplied into the fp16 numbers here they made
-// 343 us of 8 trees of 64 drafts 458.)
+// 343 us of 8 trees of 64 drafts 458; both before later steps.)
 template <int D, bool kWhole>
 struct OldTiles {
     static constexpr int kTileBytes = kTile * D * 2, kHalf = kTile * 128, kRawBytes = kTile * D, kPieces = D / 16, kRows = 16;

@@ -23,9 +23,9 @@ constexpr int kAtOnce = 8;  // tokens whose loads are under way together
 // needs no other's word and no room in between.
 //
 // Bound by latency (table, path, load, store one after another): 2.5 us for one
-// sequence's accepted drafts in 32 layers, 7.2 for 64 sequences' of large trees
-// (32 MB, of which memory would take 5.1).  (The layers after one another: 15 us
-// more.)
+// sequence's accepted drafts in 32 layers, 7.3 for 64 sequences' of large trees
+// while their 32 MB are in L2, 11.1 from memory, which would take 5.1 at its
+// rate.  (The layers after one another: 15 us more.)
 //
 // grid (blocks of a slice of the layers' rows, keys' and values'; slices; n_seq).
 template <typename V>
@@ -154,8 +154,8 @@ __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127)
 // A unit is a block of tokens of one head: `warps` warps take it (1, 2, 4 or
 // 8), each value read once as long as it fits their registers, which 16,384 do.
 // Neighbouring units are neighbouring heads, whose rows lie side by side.
-// Bound by memory: 341 pages of 48 tokens in 4 layers (402 MB read and written) 68
-// us, 5.9 TB/s; a page of 64 in 32 layers (12.6 MB) 4.7.  A thread's pieces follow one
+// Bound by memory: 341 pages of 48 tokens in 4 layers (402 MB read and written) 67.5
+// us, 6.0 TB/s; a page of 64 in 32 layers (12.6 MB, in L2) 4.7.  A thread's pieces follow one
 // another without divisions, and magnitudes are compared as integers, two at a
 // time; with 96 registers a thread, two blocks an SM, 81 us.
 // grid (units of a layer / units a block, layers, 2): keys, then values.

@@ -23,7 +23,7 @@
 // block, 38% over the launch).  129,280 fp32 logits: a row with top-p alone 11 us
 // where that keeps few, 19 with thousands, 29 with half of the row; five rows
 // with all cuts 14.4 us (the general way, without one block that settles few:
-// 20.9), 256 rows of all kinds 121.  Their distributions (cbq_probs) 145: 132 MB
+// 20.9), 256 rows of all kinds 120.  Their distributions (cbq_probs) 144: 132 MB
 // more to write, of which the zeros are on their way while the cuts are found.
 #include <cfloat>
 

@@ -17,13 +17,14 @@
 // arithmetic is a sixty-fourth as wide on this GPU and would be the bound, pairs
 // cost some 15 instructions a token and are near it.
 //
-// 64 trees of 12 drafts over 129,280 tokens take 32 us (the slowest of them four
-// passes, each some 10,000 clocks of loads and sums in a quarter of the row, 3,000
-// of exchange and 2,000 of walk, and a draw of 6,000), 200 of 6 57 us, one of 5
-// 7 us: latencies, with issue slots 14% and memory 15% busy.  (With two tiles less
-// ahead where only p is read, and three operations a pair of tokens more in the
-// differences, the 64 trees took 37 us; with bulk copies into a ring of each
-// warp's own, of 1 KB, 46.)
+// 64 binary trees of 12 over 129,280 tokens, with a drafter near the target, take
+// 32 us with warm caches (the slowest of them four passes, each some 10,000 clocks
+// of loads and sums in a quarter of the row, 3,000 of exchange and 2,000 of walk,
+// and a draw of 6,000), 200 of 6 58 us, one of 5 7 us; trees of up to 12 whose
+// drafter is farther off, and refused more often, 41, and 49 cold: latencies, with
+// issue slots 15% and memory 15% busy.  (With two tiles less ahead where only p is
+// read, and three operations a pair of tokens more in the differences, the 32 us
+// were 37; with bulk copies into a ring of each warp's own, of 1 KB, 46.)
 #include <algorithm>
 
 #include "cbq_device.cuh"
@@ -434,7 +435,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(Verify a) {
 template <bool kDrawn, bool kVec>
 cudaError_t launch(const Verify &a, cudaStream_t s) {
     // Blocks of a sequence: what a pass costs beside the rows (walk, exchange, draw) is some 1,260 tiles' worth, and the GPU
-    // takes two blocks an SM at a time.  64 trees: 4 blocks 32 us, 8 40; 200: 1 block 70, 2 58 (chosen drafts: 41 and 43).
+    // takes two blocks an SM at a time.  64 trees: 4 blocks 32 us, 8 40; 200: 1 block 71, 2 58, 4 57 (chosen drafts: 41, 41
+    // and 44).  With a drafter that is refused more often, passes are more and trees end farther apart: 64: 46 and 44, 200:
+    // 130, 89 and 81.
     const int64_t tiles = (a.V + kTile - 1) / kTile, rows = kDrawn ? 2 : 1;
     int blocks = 1;
     double least = 0.0;
